@@ -271,11 +271,11 @@ def _own(st, op):
     from paged_kv_cache_273_gb300 import pkv
     if op == "tables" and st["case"]["what"] == "reserve":
         pkv.kv_device_reserve(st["pool"], st["free_ids"], st["free_in"], st["lens"], st["block_tables"], st["slots"],
-                              num_new=st["new"], free_out=st["free_out"], lens_out=st["lens_out"], q_start=st["q_start"])
+                              num_new=st["new"], free_out=st["free_out"], seq_lens_out=st["lens_out"], q_start=st["q_start"])
         return {"slots": st["slots"], "tables": st["block_tables"], "lens": st["lens_out"], "q_start": st["q_start"], "free": st["free_out"][:1]}
     if op == "tables":
         pkv.kv_device_release(st["pool"], st["free_ids"], st["free_in"], st["lens"], st["done"], st["block_tables"],
-                              free_out=st["free_out"], lens_out=st["lens_out"])
+                              free_out=st["free_out"], seq_lens_out=st["lens_out"])
         return {"free_ids": st["free_ids"], "lens": st["lens_out"], "free": st["free_out"][:1]}
     if op == "append":
         pkv.kv_append(st["pool"], st["k_new"], st["v_new"], st["slots"], st["k_cache"], st["v_cache"], st["k_scales"], st["v_scales"])
