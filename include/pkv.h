@@ -18,8 +18,9 @@
  * Layouts (all row-major, all device buffers owned by the caller):
  *   k_cache, v_cache   [NB][Hkv][bs][D]  element type = the pool's kv_dtype.
  *                      Each (block, KV head) tile of bs*D elements is contiguous.
- *   k_scales, v_scales [NB][Hkv][bs]     fp16, int8 pools only (one scale per
- *                      cached token per KV head); NULL otherwise.
+ *   k_scales, v_scales [NB][Hkv][bs]     fp16, int8 and int4 pools (one scale
+ *                      per cached token per KV head); [NB][Hkv] fp32, F8 pools
+ *                      (one power of two per block and KV head); NULL otherwise.
  *   q                  [B][Hq][D]        q_dtype.
  *   out                [B][Hq][D]        fp32.
  *   block_tables       [B][max_blocks_per_seq] int32: entry j of row b is the
@@ -62,7 +63,8 @@ typedef enum {
     PKV_F16 = 1,
     PKV_BF16 = 2,
     PKV_I8 = 3,
-    PKV_I4 = 4
+    PKV_I4 = 4,
+    PKV_F8 = 5
 } pkv_dtype;
 
 typedef enum {
@@ -93,11 +95,13 @@ const char *pkv_status_string(int status);
  *   out          receives the new pool (owned by the caller; free with
  *                kv_block_pool_destroy).
  *   num_blocks   NB >= 1; NB * block_size must be < 2^31.
- *   block_size   power of two, 1..256 (>= 8 for int8 pools).
+ *   block_size   power of two, 4..256 (>= 8 for pools with scales).
  *   num_kv_heads Hkv >= 1.
  *   head_dim     64 or 128.
- *   kv_dtype     element type of the cache: F32, F16, BF16, or I8 (int8 codes
- *                with per-token-per-head fp16 scales).
+ *   kv_dtype     element type of the cache: F32, F16, BF16, I8 or I4 (integer
+ *                codes with per-token-per-head fp16 scales; I4: head_dim 128),
+ *                or F8 (e4m3 codes with one power-of-two fp32 scale for each
+ *                block and KV head of K and of V).
  *
  * The pool keeps a free list (all NB blocks free at start), one reference
  * count per block, and a 4-byte device error word on the current device.  It
@@ -116,7 +120,8 @@ void kv_block_pool_destroy(pkv_pool *pool);
 /* Bytes of one of k_cache / v_cache: NB * Hkv * bs * D * sizeof(kv_dtype). */
 size_t kv_cache_bytes(const pkv_pool *pool);
 
-/* Bytes of one of k_scales / v_scales: NB * Hkv * bs * 2 for int8 pools, else 0. */
+/* Bytes of one of k_scales / v_scales: NB * Hkv * bs * 2 for int8 and int4
+ * pools, NB * Hkv * 4 for F8 pools, else 0. */
 size_t kv_scales_bytes(const pkv_pool *pool);
 
 /* Number of blocks currently on the free list. */
@@ -227,6 +232,22 @@ int kv_slot_mapping(const int32_t *block_tables, int max_blocks_per_seq, int blo
  * and s is stored as that token's scale.  Inputs must be finite with
  * |x| <= 65504.  A slot outside [0, NB*bs) sets PKV_ERR_BAD_INDEX in the
  * error word and that token is skipped.  num_tokens == 0 is a no-op.
+ *
+ * F8 pools ([NOTES] "Quantized KV cache"): in_dtype F16, BF16 or F32, any
+ * finite value.  A run is the call's new rows of one block that are neighbours
+ * in slot_mapping with slots ascending by one, as kv_reserve_slots,
+ * kv_slot_mapping and kv_device_reserve write them; a block gets at most one
+ * run a call (the result of several is undefined).  For each run, KV head, and
+ * K and V, with amax the run's largest |x|,
+ *   e = the least integer >= -96 with amax <= 448 * 2^e   (-96 for amax = 0),
+ *   E = e if the run starts the block (offset 0), else max(e, the block's E),
+ *   code = e4m3_round_nearest_even(x * 2^-E),
+ * the block's rows before the run are brought to a larger E first (code =
+ * e4m3_round_nearest_even(code * 2^(old E - E)), exact but for the smallest
+ * codes), and 2^E is stored as the block's scale.  Rows behind the run are left
+ * as they are; an append that goes back in a block (rejected draft tokens)
+ * keeps the block's E.  Of values that are not finite only the memory safety
+ * is promised.
  */
 int kv_append(const pkv_pool *pool, const void *k_new, const void *v_new, pkv_dtype in_dtype,
               const int32_t *slot_mapping, int num_tokens, void *k_cache, void *v_cache,
@@ -271,7 +292,7 @@ size_t paged_decode_workspace_bytes(const pkv_pool *pool, int batch, int num_q_h
  * code * scale.  scale is normally 1/sqrt(D).
  *
  *   q          device [B][Hq][D]; q_dtype = kv_dtype for fp pools, F16 or
- *              BF16 for int8 pools.
+ *              BF16 for int8, int4 and F8 pools.
  *   num_q_heads  Hq, a multiple of Hkv with G in {1, 2, 4, 8}.
  *   block_tables, seq_lens  device int32 (see conventions).  A length of 0
  *              gives a zero output row; a length above
@@ -525,6 +546,143 @@ int paged_decode_attention_noalloc(const pkv_pool *pool, const void *q, pkv_dtyp
                                    float scale, float *out, pkv_stream_t stream);
 
 /*
+ * kv_device_reserve — kv_reserve_slots on the device, for loops that never wait
+ * for the host ([VIS] "PagedAttention: the cache in blocks": a sequence gains a
+ * block only when its tokens need one).  The free blocks are a stack in device
+ * memory that the caller fills once, with ids taken from the pool by
+ * kv_block_alloc; those blocks are then handed out and taken back here and in
+ * kv_device_release alone, and are not shared.
+ *
+ *   free_ids       device int32 [free_capacity], the stack; read only.
+ *   free_in        device int32 [2]: [0] the number of free ids.
+ *   free_out       device int32 [2]: [0] receives the number left; [1] is a
+ *                  counter that must be zero before the first call, which every
+ *                  call leaves zero.  free_out may be free_in.
+ *   seq_lens       device int32 [batch], rows cached before the call (L).
+ *   num_new        device int32 [batch], new tokens (n); NULL means 1 each.
+ *   block_tables   device int32 [batch][max_blocks_per_seq]; row b holds the
+ *                  ceil(L / bs) blocks of sequence b and receives the new ones.
+ *   slot_mapping   device int32 [max_tokens]: the new tokens' slots, sequence
+ *                  after sequence, then -1 (which kv_append skips) to the end.
+ *   q_start        device int32 [batch + 1] or NULL: the new tokens' offsets,
+ *                  as paged_prefill_attention takes them.
+ *   seq_lens_out   device int32 [batch], receives L + n; may be seq_lens.
+ *
+ * New blocks are the top ones of the stack, in sequence order: the k-th is
+ * free_ids[count - 1 - k], what kv_reserve_slots takes off a pool whose free
+ * list ends in these ids.  All or nothing: if the stack has too few, the next
+ * pkv_check_error returns PKV_ERR_NO_BLOCKS; if a length, a count or the number
+ * of new tokens (more than max_tokens) is out of range, PKV_ERR_BAD_INDEX.  The
+ * call then changes no table, copies the lengths and the free count, and fills
+ * slot_mapping with -1 and q_start with 0.  An id outside the pool, on the stack
+ * or in a table row, is recorded (PKV_ERR_BAD_INDEX) and its tokens' slots are
+ * -1.  Apart from the pairs named here the arrays must not overlap.  batch <= 4096; batch == 0
+ * is a no-op.  One kernel.  PKV_ERR_INVALID also if the pool's device is not the
+ * current one.
+ */
+int kv_device_reserve(const pkv_pool *pool, const int32_t *free_ids, int free_capacity,
+                      const int32_t *free_in, int32_t *free_out, const int32_t *seq_lens,
+                      const int32_t *num_new, int batch, int32_t *block_tables,
+                      int max_blocks_per_seq, int32_t *slot_mapping, int max_tokens,
+                      int32_t *q_start, int32_t *seq_lens_out, pkv_stream_t stream);
+
+/*
+ * kv_device_release — the blocks of finished sequences back to the device's free
+ * stack ([GUIDE] "Paging: borrow the trick operating systems already use").
+ * For every b with done[b] != 0 the ceil(seq_lens[b] / bs) blocks of row b go on
+ * the stack, sequence after sequence, and seq_lens_out[b] = 0; the other lengths
+ * are copied.  The rows themselves are left as they are.
+ *
+ *   done           device int32 [batch].
+ *   free_ids       device int32 [free_capacity]; entries from free_in[0] on are
+ *                  written.
+ *   free_in, free_out, seq_lens, seq_lens_out, block_tables, limits  as for
+ *                  kv_device_reserve (block_tables is read only here).
+ *
+ * All or nothing: a length out of range or a stack that would outgrow
+ * free_capacity gives PKV_ERR_BAD_INDEX at the next pkv_check_error, and the
+ * call only copies the lengths and the count.  A block that two rows hold, or
+ * one that is on the stack already, is not noticed.  One kernel.
+ */
+int kv_device_release(const pkv_pool *pool, int32_t *free_ids, int free_capacity,
+                      const int32_t *free_in, int32_t *free_out, const int32_t *seq_lens,
+                      const int32_t *done, int batch, const int32_t *block_tables,
+                      int max_blocks_per_seq, int32_t *seq_lens_out, pkv_stream_t stream);
+
+/*
+ * kv_bounds_append — keep, beside a K cache of any type, lower and upper bounds
+ * of each block's keys, channel by channel: what paged_decode_attention_sparse
+ * scores blocks by.  Called with the same k_new and slot_mapping as kv_append.
+ *
+ *   k_new        device [T][Hkv][D] of in_dtype (F16, BF16 or F32), finite,
+ *                |x| <= 127 * 2^120.
+ *   slot_mapping device [T] int32, runs as for kv_append on F8 pools.
+ *   bounds       device int8 [NB][Hkv][2][D]: the minima, then the maxima.
+ *   bound_exps   device int32 [NB][Hkv].
+ *
+ * For each run and KV head, with amax the run's largest |x|:
+ *   e = the least integer >= -96 with amax <= 127 * 2^e    (-96 for amax = 0),
+ *   E = e if the run starts the block, else max(e, the block's E),
+ *   lower[d] = floor(min x_d * 2^-E), upper[d] = ceil(max x_d * 2^-E),
+ * joined with the block's bounds of its earlier rows, rounded down (up) to the
+ * new E.  The bounds of a block do not depend on how its rows were split over
+ * calls.  A slot out of range sets PKV_ERR_BAD_INDEX and its token is skipped.
+ * num_tokens == 0 is a no-op.  PKV_ERR_INVALID also if the pool's device is not
+ * the current one.
+ */
+int kv_bounds_append(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype,
+                     const int32_t *slot_mapping, int num_tokens, int8_t *bounds,
+                     int32_t *bound_exps, pkv_stream_t stream);
+
+/*
+ * paged_sparse_workspace_bytes — bytes of the workspace of
+ * paged_decode_attention_sparse: the decode workspace, then a counter and
+ * max_selected block ids for each (sequence, KV head), and a score for each
+ * block of a sequence of max_seq_len tokens.  0 on bad arguments.
+ */
+size_t paged_sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
+                                    int max_seq_len, int max_selected);
+
+/*
+ * paged_decode_attention_sparse — paged_decode_attention over at most
+ * max_selected blocks of each sequence, chosen for each query and KV head by the
+ * keys' bounds: the softmax of [NOTES] "Concept" over the chosen blocks' rows.
+ * [VIS] "What the page leaves out" names attention variants that read less of
+ * the cache; this one reads every block's bounds (2 D + 4 bytes) and the rows of
+ * the chosen blocks.
+ *
+ * Choice, for sequence b and KV head kvh with n = ceil(seq_lens[b] / bs) blocks:
+ * all of them if n <= max_selected; else the newest block (n - 1) and the
+ * max_selected - 1 others of largest score, the lower index first among equal
+ * scores.  With eq the least integer >= -96 such that the group's G queries have
+ * |q| <= 127 * 2^eq, and qi = round_half_even(q * 2^-eq), block j's score is
+ *   max over the group's heads of
+ *     sum_d (max(qi_d, 0) * upper_d + min(qi_d, 0) * lower_d)
+ *       * 2^(the block's bound exponent),
+ * an upper bound of q . k over the block's keys, up to the rounding of q, in
+ * units of 2^eq; it is computed exactly (within fp32's exponents).
+ *
+ *   bounds, bound_exps  as kv_bounds_append keeps them.
+ *   selected     device int32 [B][Hkv][max_selected], receives the chosen blocks'
+ *                indices in the sequence (0-based, ascending), then -1.
+ *   workspace    device scratch of at least paged_sparse_workspace_bytes(),
+ *                zeroed once by the caller like paged_decode_attention's.
+ * Pools: F16, BF16 and F8 (others PKV_ERR_UNSUPPORTED).  All other arguments,
+ * limits and errors are those of paged_decode_attention; a block id outside the
+ * pool sets PKV_ERR_BAD_INDEX, counts as the lowest score and is read as zeros.
+ * Two kernels.  PKV_ERR_INVALID also for max_selected < 1, and if the pool's
+ * device is not the current one.
+ */
+int paged_decode_attention_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
+                                  int num_q_heads, const void *k_cache, const void *v_cache,
+                                  const void *k_scales, const void *v_scales,
+                                  const int8_t *bounds, const int32_t *bound_exps,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *seq_lens, int batch, int max_seq_len,
+                                  int max_selected, float scale, float *out, int32_t *selected,
+                                  void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/*
  * pkv_selftest_wait_timeout — a check of the failure path of the library's
  * bounded device waits (not part of the method).  Launches one kernel whose
  * single waiting thread waits, the way every mbarrier wait in this library
@@ -538,7 +696,8 @@ int pkv_selftest_wait_timeout(const pkv_pool *pool, pkv_stream_t stream);
 
 /*
  * pkv_check_error — synchronise the stream, read and clear the pool's device
- * error word.  Returns PKV_OK, PKV_ERR_BAD_INDEX, PKV_ERR_TIMEOUT (a bounded
+ * error word.  Returns PKV_OK, PKV_ERR_BAD_INDEX, PKV_ERR_NO_BLOCKS (only a
+ * device reservation found too few free blocks), PKV_ERR_TIMEOUT (a bounded
  * wait inside a kernel gave up; the kernel returned without finishing), or
  * PKV_ERR_CUDA.
  */

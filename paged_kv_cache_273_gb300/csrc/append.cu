@@ -418,7 +418,10 @@ int launch_block_copy(const pkv_pool *pool, const int32_t *src, const int32_t *d
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t rows = (int64_t)pool->num_kv_heads * pool->block_size;
     const int64_t chunks = rows * row_bytes(pool->kv_dtype, pool->head_dim) / 16;
-    const int64_t scales = quantized_dtype(pool->kv_dtype) ? rows : 0;
+    // 2-byte units: a row's fp16 scale, or a (block, head)'s fp32 scale
+    const int64_t scales = pool->kv_dtype == PKV_F8        ? 2 * pool->num_kv_heads
+                           : quantized_dtype(pool->kv_dtype) ? rows
+                                                             : 0;
     const int threads = 256;
     const int64_t total = (int64_t)n * (2 * chunks + 2 * scales);
     launch_pdl(block_copy_kernel, dim3(grid_for(total, threads, pool->num_sms)), dim3(threads), 0,
@@ -435,6 +438,9 @@ int launch_append(const pkv_pool *pool, const void *k_new, const void *v_new, pk
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int H = pool->num_kv_heads, D = pool->head_dim, bs = pool->block_size;
     const int64_t num_slots = (int64_t)pool->num_blocks * bs;
+    if (pool->kv_dtype == PKV_F8)
+        return launch_append_f8(pool, k_new, v_new, in_dtype, slot_mapping, num_tokens, k_cache,
+                                v_cache, k_scales, v_scales, stream);
     if (pool->kv_dtype == PKV_I4) {
         const int64_t rows = (int64_t)num_tokens * H;
         const int threads = 256;

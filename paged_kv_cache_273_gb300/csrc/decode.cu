@@ -106,6 +106,10 @@ int launch_decode(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
                   const int32_t *seq_prefix, const float *prefix_part)
 {
     (void)workspace_bytes;
+    if (pool->kv_dtype == PKV_F8)
+        return launch_decode_f8(pool, q, q_dtype, num_q_heads, k_cache, v_cache, k_scales,
+                                v_scales, block_tables, max_blocks_per_seq, seq_lens, batch,
+                                max_seq_len, window, scale, out, workspace, stream);
     const int Hkv = pool->num_kv_heads;
     const int G = num_q_heads / Hkv;
     // tiles, and their cost for the split over CTAs, must count in 31 bits
@@ -153,6 +157,7 @@ int launch_decode(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     case PKV_BF16: return kern::launch_d<PKV_BF16>(pool, G, prm, batch, max_seq_len, s);
     case PKV_I8: return kern::launch_d<PKV_I8>(pool, G, prm, batch, max_seq_len, s);
     case PKV_I4: return kern::launch_d<PKV_I4>(pool, G, prm, batch, max_seq_len, s);
+    case PKV_F8: break;   // above
     }
     return PKV_ERR_UNSUPPORTED;
 }

@@ -17,6 +17,7 @@ enum : unsigned int {
     PKV_EBIT_BLOCK = 2u,     // attention, block copy: block id outside [0, NB)
     PKV_EBIT_SEQLEN = 4u,    // attention: seq_len < 0 or beyond its block table row
     PKV_EBIT_TIMEOUT = 8u,   // a bounded mbarrier wait gave up
+    PKV_EBIT_NO_BLOCKS = 16u,  // device reservation: the free list is too short
 };
 
 struct pkv_pool {
@@ -44,7 +45,7 @@ inline int dtype_bytes(pkv_dtype t)
     switch (t) {
     case PKV_F32: return 4;
     case PKV_F16: case PKV_BF16: return 2;
-    case PKV_I8: return 1;
+    case PKV_I8: case PKV_F8: return 1;
     case PKV_I4: return 0;      // two per byte: use row_bytes()
     }
     return 0;
@@ -56,8 +57,25 @@ inline int64_t row_bytes(pkv_dtype t, int head_dim)
     return t == PKV_I4 ? head_dim / 2 : (int64_t)head_dim * dtype_bytes(t);
 }
 
-// Caches with one fp16 scale per cached row.
-inline bool quantized_dtype(pkv_dtype t) { return t == PKV_I8 || t == PKV_I4; }
+// Caches with scales: one fp16 scale per cached row (int8, int4), or one fp32
+// power of two per (block, KV head) (8-bit float).
+inline bool quantized_dtype(pkv_dtype t)
+{
+    return t == PKV_I8 || t == PKV_I4 || t == PKV_F8;
+}
+
+// Exponents of a block's scale and of its key bounds: 2^-96 for a block of
+// zeros; at most 2^120 (the largest fp32 value is below 448 * 2^120).  Both
+// keep 2^e and 2^-e normal fp32 numbers.
+constexpr int BLOCK_MIN_EXP = -96, BLOCK_MAX_EXP = 120;
+
+inline int log2_of(int pow2)
+{
+    int lg = 0;
+    while ((1 << lg) < pow2)
+        ++lg;
+    return lg;
+}
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -87,6 +105,42 @@ int launch_block_copy(const pkv_pool *pool, const int32_t *src, const int32_t *d
 int launch_append(const pkv_pool *pool, const void *k_new, const void *v_new, pkv_dtype in_dtype,
                   const int32_t *slot_mapping, int num_tokens, void *k_cache, void *v_cache,
                   void *k_scales, void *v_scales, pkv_stream_t stream);
+
+// kv_append on an 8-bit float pool, and the key bounds (append_blocks.cu).
+int launch_append_f8(const pkv_pool *pool, const void *k_new, const void *v_new,
+                     pkv_dtype in_dtype, const int32_t *slots, int num_tokens, void *k_cache,
+                     void *v_cache, void *k_scales, void *v_scales, pkv_stream_t stream);
+int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype,
+                         const int32_t *slots, int num_tokens, int8_t *bounds, int32_t *exps,
+                         pkv_stream_t stream);
+
+// Decode attention over an 8-bit float cache (decode_f8.cu).
+int launch_decode_f8(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num_q_heads,
+                     const void *k_cache, const void *v_cache, const void *k_scales,
+                     const void *v_scales, const int32_t *tables, int max_blocks,
+                     const int32_t *seq_lens, int batch, int max_seq_len, int window, float scale,
+                     float *out, void *workspace, pkv_stream_t stream);
+
+// Block choice and the attention over the chosen blocks (select.cu).
+size_t sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_len,
+                              int budget);
+int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num_q_heads,
+                  const void *k_cache, const void *v_cache, const void *k_scales,
+                  const void *v_scales, const int8_t *bounds, const int32_t *exps,
+                  const int32_t *tables, int max_blocks, const int32_t *seq_lens, int batch,
+                  int max_seq_len, int budget, float scale, float *out, int32_t *selected,
+                  void *workspace, pkv_stream_t stream);
+
+// Block tables and slots on the device (tables.cu).
+int launch_device_reserve(const pkv_pool *pool, const int32_t *free_ids, int free_capacity,
+                          const int32_t *free_in, int32_t *free_out, const int32_t *lens,
+                          const int32_t *num_new, int batch, int32_t *tables, int max_blocks,
+                          int32_t *slots, int max_tokens, int32_t *q_start, int32_t *lens_out,
+                          pkv_stream_t stream);
+int launch_device_release(const pkv_pool *pool, int32_t *free_ids, int free_capacity,
+                          const int32_t *free_in, int32_t *free_out, const int32_t *lens,
+                          const int32_t *done, int batch, const int32_t *tables, int max_blocks,
+                          int32_t *lens_out, pkv_stream_t stream);
 
 size_t decode_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads);
 

@@ -62,7 +62,7 @@ int kv_block_pool_init(pkv_pool **out, int num_blocks, int block_size, int num_k
     if ((int64_t)num_blocks * block_size >= ((int64_t)1 << 31))
         return PKV_ERR_INVALID;
     if (kv_dtype != PKV_F32 && kv_dtype != PKV_F16 && kv_dtype != PKV_BF16 &&
-        kv_dtype != PKV_I8 && kv_dtype != PKV_I4)
+        kv_dtype != PKV_I8 && kv_dtype != PKV_I4 && kv_dtype != PKV_F8)
         return PKV_ERR_INVALID;
     if (head_dim != 64 && head_dim != 128)
         return PKV_ERR_UNSUPPORTED;
@@ -127,6 +127,8 @@ size_t kv_scales_bytes(const pkv_pool *pool)
 {
     if (!pool || !pkv::quantized_dtype(pool->kv_dtype))
         return 0;
+    if (pool->kv_dtype == PKV_F8)
+        return (size_t)pool->num_blocks * pool->num_kv_heads * 4;
     return (size_t)pool->num_blocks * pool->num_kv_heads * pool->block_size * 2;
 }
 
@@ -790,6 +792,155 @@ int paged_prefill_attention(const pkv_pool *pool, const void *q, int num_q_heads
                                out, stream);
 }
 
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// PKV_OK when the pool's device is there and current (a launch goes to the
+// current device, whose kernels cannot reach another device's error word).
+int device_check(const pkv_pool *pool)
+{
+    if (!pool->has_device)
+        return PKV_ERR_CUDA;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    return dev == pool->device ? PKV_OK : PKV_ERR_INVALID;
+}
+
+// The arguments kv_device_reserve and kv_device_release share.
+int tables_check(const pkv_pool *pool, const int32_t *free_ids, int free_capacity,
+                 const int32_t *free_in, const int32_t *free_out, const int32_t *seq_lens,
+                 const int32_t *seq_lens_out, int batch, const int32_t *block_tables,
+                 int max_blocks_per_seq)
+{
+    if (!pool || batch < 0 || max_blocks_per_seq < 1 || free_capacity < 0)
+        return PKV_ERR_INVALID;
+    if (batch > 4096)
+        return PKV_ERR_UNSUPPORTED;
+    if (batch == 0)
+        return PKV_OK;
+    if (!free_in || !free_out || !seq_lens || !seq_lens_out || !block_tables ||
+        (free_capacity > 0 && !free_ids))
+        return PKV_ERR_INVALID;
+    if (!aligned4(free_ids) || !aligned4(free_in) || !aligned4(free_out) || !aligned4(seq_lens) ||
+        !aligned4(seq_lens_out) || !aligned4(block_tables))
+        return PKV_ERR_INVALID;
+    return PKV_OK;
+}
+
+}  // namespace
+
+int kv_device_reserve(const pkv_pool *pool, const int32_t *free_ids, int free_capacity,
+                      const int32_t *free_in, int32_t *free_out, const int32_t *seq_lens,
+                      const int32_t *num_new, int batch, int32_t *block_tables,
+                      int max_blocks_per_seq, int32_t *slot_mapping, int max_tokens,
+                      int32_t *q_start, int32_t *seq_lens_out, pkv_stream_t stream)
+{
+    Range range("pkv.kv_device_reserve");
+    const int rc = tables_check(pool, free_ids, free_capacity, free_in, free_out, seq_lens,
+                                seq_lens_out, batch, block_tables, max_blocks_per_seq);
+    if (rc != PKV_OK)
+        return rc;
+    if (max_tokens < 0 || (max_tokens > 0 && !slot_mapping) || !aligned4(slot_mapping) ||
+        !aligned4(num_new) || !aligned4(q_start))
+        return PKV_ERR_INVALID;
+    if (batch == 0)
+        return PKV_OK;
+    const int dc = device_check(pool);
+    if (dc != PKV_OK)
+        return dc;
+    return pkv::launch_device_reserve(pool, free_ids, free_capacity, free_in, free_out, seq_lens,
+                                      num_new, batch, block_tables, max_blocks_per_seq,
+                                      slot_mapping, max_tokens, q_start, seq_lens_out, stream);
+}
+
+int kv_device_release(const pkv_pool *pool, int32_t *free_ids, int free_capacity,
+                      const int32_t *free_in, int32_t *free_out, const int32_t *seq_lens,
+                      const int32_t *done, int batch, const int32_t *block_tables,
+                      int max_blocks_per_seq, int32_t *seq_lens_out, pkv_stream_t stream)
+{
+    Range range("pkv.kv_device_release");
+    const int rc = tables_check(pool, free_ids, free_capacity, free_in, free_out, seq_lens,
+                                seq_lens_out, batch, block_tables, max_blocks_per_seq);
+    if (rc != PKV_OK || batch == 0)
+        return rc;
+    if (!done || !aligned4(done))
+        return PKV_ERR_INVALID;
+    const int dc = device_check(pool);
+    if (dc != PKV_OK)
+        return dc;
+    return pkv::launch_device_release(pool, free_ids, free_capacity, free_in, free_out, seq_lens,
+                                      done, batch, block_tables, max_blocks_per_seq, seq_lens_out,
+                                      stream);
+}
+
+int kv_bounds_append(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype,
+                     const int32_t *slot_mapping, int num_tokens, int8_t *bounds,
+                     int32_t *bound_exps, pkv_stream_t stream)
+{
+    Range range("pkv.kv_bounds_append");
+    if (!pool || num_tokens < 0)
+        return PKV_ERR_INVALID;
+    if (in_dtype != PKV_F16 && in_dtype != PKV_BF16 && in_dtype != PKV_F32)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0)
+        return PKV_OK;
+    if (!k_new || !slot_mapping || !bounds || !bound_exps)
+        return PKV_ERR_INVALID;
+    if (!pkv::aligned16(k_new) || !pkv::aligned16(bounds) || !aligned4(bound_exps) ||
+        !aligned4(slot_mapping))
+        return PKV_ERR_INVALID;
+    const int dc = device_check(pool);
+    if (dc != PKV_OK)
+        return dc;
+    return pkv::launch_append_bounds(pool, k_new, in_dtype, slot_mapping, num_tokens, bounds,
+                                     bound_exps, stream);
+}
+
+size_t paged_sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
+                                    int max_seq_len, int max_selected)
+{
+    if (!pool || batch < 0 || num_q_heads < 1 || num_q_heads % pool->num_kv_heads != 0 ||
+        max_seq_len < 0 || max_selected < 1)
+        return 0;
+    return pkv::sparse_workspace_bytes(pool, batch, num_q_heads, max_seq_len, max_selected);
+}
+
+int paged_decode_attention_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
+                                  int num_q_heads, const void *k_cache, const void *v_cache,
+                                  const void *k_scales, const void *v_scales,
+                                  const int8_t *bounds, const int32_t *bound_exps,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *seq_lens, int batch, int max_seq_len,
+                                  int max_selected, float scale, float *out, int32_t *selected,
+                                  void *workspace, size_t workspace_bytes, pkv_stream_t stream)
+{
+    Range range("pkv.paged_decode_attention_sparse");
+    if (!pool || max_selected < 1)
+        return PKV_ERR_INVALID;
+    if (pool->kv_dtype != PKV_F16 && pool->kv_dtype != PKV_BF16 && pool->kv_dtype != PKV_F8)
+        return PKV_ERR_UNSUPPORTED;
+    const int rc = decode_check(pool, q, q_dtype, num_q_heads, k_cache, v_cache, k_scales,
+                                v_scales, block_tables, max_blocks_per_seq, seq_lens, batch,
+                                max_seq_len, 0, out, workspace, workspace_bytes);
+    if (rc != PKV_OK || batch == 0)
+        return rc;
+    if (!bounds || !bound_exps || !selected || !pkv::aligned16(bounds) || !aligned4(bound_exps) ||
+        !aligned4(selected))
+        return PKV_ERR_INVALID;
+    if (workspace_bytes <
+        pkv::sparse_workspace_bytes(pool, batch, num_q_heads, max_seq_len, max_selected))
+        return PKV_ERR_INVALID;
+    const int dc = device_check(pool);
+    if (dc != PKV_OK)
+        return dc;
+    return pkv::launch_sparse(pool, q, q_dtype, num_q_heads, k_cache, v_cache, k_scales, v_scales,
+                              bounds, bound_exps, block_tables, max_blocks_per_seq, seq_lens,
+                              batch, max_seq_len, max_selected, scale, out, selected, workspace,
+                              stream);
+}
+
 int pkv_selftest_wait_timeout(const pkv_pool *pool, pkv_stream_t stream)
 {
     if (!pool)
@@ -818,7 +969,7 @@ int pkv_check_error(const pkv_pool *pool, pkv_stream_t stream)
         return PKV_ERR_CUDA;
     if (h & PKV_EBIT_TIMEOUT)
         return PKV_ERR_TIMEOUT;
-    return PKV_ERR_BAD_INDEX;
+    return h == PKV_EBIT_NO_BLOCKS ? PKV_ERR_NO_BLOCKS : PKV_ERR_BAD_INDEX;
 }
 
 }  // extern "C"

@@ -5,8 +5,9 @@ kernels.  PyTorch supplies device memory and streams.  If libpkv.so has not
 been built, importing the library raises; there is no CPU fallback.
 
 Device tensors follow the layouts of ``include/pkv.h``:
-  k_cache, v_cache   [NB, Hkv, bs, D]   (float32 | float16 | bfloat16 | int8)
-  k_scales, v_scales [NB, Hkv, bs]      float16 (int8 pools only)
+  k_cache, v_cache   [NB, Hkv, bs, D]   (float32 | float16 | bfloat16 | int8 | float8_e4m3fn)
+  k_scales, v_scales [NB, Hkv, bs]      float16 (int8 and int4 pools)
+                     [NB, Hkv]          float32 (float8 pools)
   q                  [B, Hq, D];  out [B, Hq, D] float32
   block_tables       [B, max_blocks_per_seq] int32;  seq_lens [B] int32
   slot_mapping       [T] int32
@@ -23,7 +24,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
-PKV_F32, PKV_F16, PKV_BF16, PKV_I8, PKV_I4 = 0, 1, 2, 3, 4
+PKV_F32, PKV_F16, PKV_BF16, PKV_I8, PKV_I4, PKV_F8 = 0, 1, 2, 3, 4, 5
 PKV_OK = 0
 PKV_ERR_INVALID = -1
 PKV_ERR_NO_BLOCKS = -2
@@ -37,6 +38,8 @@ TORCH_DTYPE = {PKV_F32: torch.float32, PKV_F16: torch.float16, PKV_BF16: torch.b
 PKV_DTYPE = {v: k for k, v in TORCH_DTYPE.items()}
 # 4-bit caches are held as bytes, two codes each: [NB, Hkv, bs, D/2] uint8.
 TORCH_DTYPE[PKV_I4] = torch.uint8
+# 8-bit float caches: e4m3 codes.
+TORCH_DTYPE[PKV_F8] = torch.float8_e4m3fn
 
 # Every symbol the header declares (checked by the tests).
 SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "kv_cache_bytes",
@@ -45,8 +48,9 @@ SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "
            "kv_slot_mapping", "kv_append", "kv_block_copy", "paged_decode_workspace_bytes", "paged_decode_attention",
            "paged_decode_attention_window", "paged_prefill_attention", "kv_prefix_groups",
            "paged_decode_cascade_workspace_bytes", "paged_decode_attention_cascade",
-           "paged_decode_attention_noalloc", "paged_decode_step", "pkv_selftest_wait_timeout",
-           "pkv_check_error")
+           "paged_decode_attention_noalloc", "paged_decode_step", "kv_device_reserve",
+           "kv_device_release", "kv_bounds_append", "paged_sparse_workspace_bytes",
+           "paged_decode_attention_sparse", "pkv_selftest_wait_timeout", "pkv_check_error")
 
 
 class StepLayout(ctypes.Structure):
@@ -134,6 +138,17 @@ def load() -> ctypes.CDLL:
         lib.paged_decode_step.argtypes = [P, P, P, SZ, ctypes.POINTER(StepLayout), I, I, I, P, P,
                                           P, P, P, I, I, I, F, P, P, P, SZ, P]
         lib.paged_decode_step.restype = I
+        lib.kv_device_reserve.argtypes = [P, P, I, P, P, P, P, I, P, I, P, I, P, P, P]
+        lib.kv_device_reserve.restype = I
+        lib.kv_device_release.argtypes = [P, P, I, P, P, P, P, I, P, I, P, P]
+        lib.kv_device_release.restype = I
+        lib.kv_bounds_append.argtypes = [P, P, I, P, I, P, P, P]
+        lib.kv_bounds_append.restype = I
+        lib.paged_sparse_workspace_bytes.argtypes = [P, I, I, I, I]
+        lib.paged_sparse_workspace_bytes.restype = SZ
+        lib.paged_decode_attention_sparse.argtypes = [P, P, I, I, P, P, P, P, P, P, P, I, P, I, I,
+                                                      I, F, P, P, P, SZ, P]
+        lib.paged_decode_attention_sparse.restype = I
         lib.pkv_selftest_wait_timeout.argtypes = [P, P]
         lib.pkv_selftest_wait_timeout.restype = I
         lib.pkv_check_error.argtypes = [P, P]
@@ -210,6 +225,9 @@ class Pool:
             shape = shape[:3] + (self.head_dim // 2,)
         k = torch.zeros(shape, dtype=dt, device=device)
         v = torch.zeros(shape, dtype=dt, device=device)
+        if self.kv_dtype == PKV_F8:
+            return (k, v, torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                    torch.zeros(shape[:2], dtype=torch.float32, device=device))
         if self.kv_dtype in (PKV_I8, PKV_I4):
             sshape = shape[:3]
             return (k, v, torch.zeros(sshape, dtype=torch.float16, device=device),
@@ -551,6 +569,135 @@ def paged_decode_step(pool: Pool, host_in, dev_in, layout: StepLayout, in_dtype,
     DecodeStep(pool, dev_in, layout, in_dtype, q_dtype, num_q_heads, k_cache, v_cache,
                block_tables, batch, max_seq_len, scale, out, workspace, k_scales, v_scales,
                stream)(host_in, host_out)
+
+
+# ------------------------------------------------------------- device-resident step
+def _shaped(name: str, t, dtype, shape) -> None:
+    """Raise unless t is a CUDA tensor of this type and shape (None in shape: any size)."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, ["*" if n is None else n for n in shape], list(t.shape)))
+
+
+def alloc_device_free_list(ids, device="cuda"):
+    """The device's free stack for kv_device_reserve and kv_device_release, holding the block
+    ids `ids` (taken from the pool by kv_block_alloc; the last one is handed out first).
+    Returns (free_ids int32 [n], free_state int32 [2]: the count, and a counter kept zero)."""
+    ids = _i32(ids)
+    state = torch.tensor([ids.size, 0], dtype=torch.int32, device=device)
+    return torch.from_numpy(ids.copy()).to(device), state
+
+
+def kv_device_reserve(pool: Pool, free_ids, free_in, seq_lens, block_tables, slot_mapping,
+                      num_new=None, free_out=None, seq_lens_out=None, q_start=None,
+                      stream=None) -> None:
+    """kv_reserve_slots on the device (see include/pkv.h): the new tokens' blocks off the free
+    stack into block_tables, their slots into slot_mapping (-1 behind the last).  free_out and
+    seq_lens_out default to free_in and seq_lens, updated in place."""
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    free_out = free_in if free_out is None else free_out
+    B = seq_lens.numel()
+    _shaped("free_ids", free_ids, torch.int32, (None,))
+    _shaped("free_in", free_in, torch.int32, (2,))
+    _shaped("free_out", free_out, torch.int32, (2,))
+    _shaped("seq_lens", seq_lens, torch.int32, (B,))
+    _shaped("seq_lens_out", seq_lens_out, torch.int32, (B,))
+    _shaped("block_tables", block_tables, torch.int32, (B, None))
+    _shaped("slot_mapping", slot_mapping, torch.int32, (None,))
+    if num_new is not None:
+        _shaped("num_new", num_new, torch.int32, (B,))
+    if q_start is not None:
+        _shaped("q_start", q_start, torch.int32, (B + 1,))
+    _check(load().kv_device_reserve(
+        pool.handle, _dptr(free_ids), free_ids.numel(), _dptr(free_in), _dptr(free_out),
+        _dptr(seq_lens), _dptr(num_new), B, _dptr(block_tables), block_tables.shape[1],
+        _dptr(slot_mapping), slot_mapping.numel(), _dptr(q_start), _dptr(seq_lens_out),
+        _stream(stream)), "kv_device_reserve")
+
+
+def kv_device_release(pool: Pool, free_ids, free_in, seq_lens, done, block_tables, free_out=None,
+                      seq_lens_out=None, stream=None) -> None:
+    """The blocks of the sequences with done[b] != 0 back on the free stack, their lengths to 0
+    (see include/pkv.h).  free_out and seq_lens_out default to in place."""
+    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    free_out = free_in if free_out is None else free_out
+    B = seq_lens.numel()
+    _shaped("free_ids", free_ids, torch.int32, (None,))
+    _shaped("free_in", free_in, torch.int32, (2,))
+    _shaped("free_out", free_out, torch.int32, (2,))
+    _shaped("seq_lens", seq_lens, torch.int32, (B,))
+    _shaped("seq_lens_out", seq_lens_out, torch.int32, (B,))
+    _shaped("done", done, torch.int32, (B,))
+    _shaped("block_tables", block_tables, torch.int32, (B, None))
+    _check(load().kv_device_release(
+        pool.handle, _dptr(free_ids), free_ids.numel(), _dptr(free_in), _dptr(free_out),
+        _dptr(seq_lens), _dptr(done), B, _dptr(block_tables), block_tables.shape[1],
+        _dptr(seq_lens_out), _stream(stream)), "kv_device_release")
+
+
+def alloc_bounds(pool: Pool, device="cuda"):
+    """Key bounds of every block: int8 [NB, Hkv, 2, D] and their exponents int32 [NB, Hkv]."""
+    head = (pool.num_blocks, pool.num_kv_heads)
+    return (torch.zeros(head + (2, pool.head_dim), dtype=torch.int8, device=device),
+            torch.zeros(head, dtype=torch.int32, device=device))
+
+
+def kv_bounds_append(pool: Pool, k_new, slot_mapping, bounds, bound_exps, stream=None) -> None:
+    """Join the new keys to their blocks' bounds (see include/pkv.h)."""
+    if k_new.dtype not in PKV_DTYPE:
+        raise ValueError("unsupported k_new dtype %s" % k_new.dtype)
+    T, head = k_new.shape[0], (pool.num_blocks, pool.num_kv_heads)
+    _shaped("k_new", k_new, k_new.dtype, (T, pool.num_kv_heads, pool.head_dim))
+    _shaped("slot_mapping", slot_mapping, torch.int32, (T,))
+    _shaped("bounds", bounds, torch.int8, head + (2, pool.head_dim))
+    _shaped("bound_exps", bound_exps, torch.int32, head)
+    _check(load().kv_bounds_append(pool.handle, _dptr(k_new), PKV_DTYPE[k_new.dtype],
+                                   _dptr(slot_mapping), T, _dptr(bounds), _dptr(bound_exps),
+                                   _stream(stream)), "kv_bounds_append")
+
+
+def paged_sparse_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_seq_len: int,
+                                 max_selected: int) -> int:
+    return int(load().paged_sparse_workspace_bytes(pool.handle, batch, num_q_heads, max_seq_len,
+                                                   max_selected))
+
+
+def alloc_sparse_workspace(pool: Pool, batch: int, num_q_heads: int, max_seq_len: int,
+                           max_selected: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for paged_decode_attention_sparse."""
+    n = paged_sparse_workspace_bytes(pool, batch, num_q_heads, max_seq_len, max_selected)
+    if n == 0:
+        raise PkvError(PKV_ERR_INVALID, "paged_sparse_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_decode_attention_sparse(pool: Pool, q, k_cache, v_cache, bounds, bound_exps,
+                                  block_tables, seq_lens, scale: float, out, selected, workspace,
+                                  max_seq_len: int, k_scales=None, v_scales=None,
+                                  stream=None) -> None:
+    """paged_decode_attention over the newest block and the blocks of largest score, at most
+    selected.shape[2] a sequence (see include/pkv.h); `selected` [B, Hkv, max_selected] int32
+    receives the choice."""
+    if q.dtype not in PKV_DTYPE:
+        raise ValueError("unsupported q dtype %s" % q.dtype)
+    B, Hq, _ = q.shape
+    head = (pool.num_blocks, pool.num_kv_heads)
+    _shaped("q", q, q.dtype, (B, Hq, pool.head_dim))
+    _shaped("out", out, torch.float32, (B, Hq, pool.head_dim))
+    _shaped("bounds", bounds, torch.int8, head + (2, pool.head_dim))
+    _shaped("bound_exps", bound_exps, torch.int32, head)
+    _shaped("block_tables", block_tables, torch.int32, (B, None))
+    _shaped("seq_lens", seq_lens, torch.int32, (B,))
+    _shaped("selected", selected, torch.int32, (B, pool.num_kv_heads, None))
+    _check(load().paged_decode_attention_sparse(
+        pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
+        _dptr(k_scales), _dptr(v_scales), _dptr(bounds), _dptr(bound_exps), _dptr(block_tables),
+        block_tables.shape[1], _dptr(seq_lens), B, int(max_seq_len), selected.shape[2],
+        float(scale), _dptr(out), _dptr(selected), _dptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)),
+        "paged_decode_attention_sparse")
 
 
 def pkv_selftest_wait_timeout(pool: Pool, stream=None) -> None:
