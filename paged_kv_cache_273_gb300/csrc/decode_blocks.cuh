@@ -30,8 +30,7 @@
 //    far.  So a weight needs no multiplication by its scale and stays in
 //    fp16's range whatever the scales are, both sums come from the same
 //    rounded x - m, and every rescaling is by a power of two.  Weights are
-//    split into a high and a low fp16 part (2^-22 relative; bf16 caches: two
-//    bf16 parts, 2^-18).
+//    split into two fp16 or three bf16 parts.
 //  * Rows outside the attended range are filled with zeros by the copies, so
 //    that whatever they hold (NaN codes of an earlier owner) is never read.
 #pragma once
@@ -49,6 +48,8 @@ constexpr int MAX_BATCH = 4096;
 // Tiles a warp is given at least, where the batch has fewer than one share of
 // that for every warp of the GPU.
 constexpr int MIN_TILES = 2;
+// Tiles a warp takes of a piece that is not worth joining across CTAs.
+constexpr int SHORT_TILES = 16;
 
 template <int D, int G, int KV>
 struct Cfg {
@@ -60,11 +61,11 @@ struct Cfg {
     static constexpr int TILE_BYTES = TILE * ROWB;
     static constexpr int SC_BYTES = F8 ? 2 * TILE * 4 : 0;   // each row's K scale, then V scale
     static constexpr int STAGE = 2 * TILE_BYTES + SC_BYTES;
-    static constexpr int W = 8;                     // warps
+    static constexpr int W = F8 ? (D == 64 ? 16 : 12) : 8;   // warps
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
     // ring stages that fit beside the states and the tile prefix, at most 6
-    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 8 + 256;
+    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 6 * 16 + W * 16 + 256;
     static constexpr int FIT = (232448 - FIXED) / (W * STAGE);
     static constexpr int NST = FIT > 6 ? 6 : FIT;
     static_assert(NST >= 2, "ring");
@@ -97,21 +98,24 @@ struct Params {
     float scale_log2;
 };
 
-// Shared memory: the rings, the warps' first states, the tile prefix, the
-// states' pieces.
+// Shared memory: the rings, the warps' first states, what the rings' tiles
+// are, the tile prefix (and, for up to half the largest batch, the sequences'
+// lengths), the states' pieces.
 template <int D, int G, int KV>
 struct Smem {
     using C = Cfg<D, G, KV>;
     static constexpr int RING = 0;
     static constexpr int STATES = C::W * C::NST * C::STAGE;
-    static constexpr int TSTART = STATES + C::W * C::STATE * 4;
+    static constexpr int INFO = round_up(STATES + C::W * C::STATE * 4, 16);
+    static constexpr int TSTART = INFO + C::W * C::NST * 16;
+    __host__ __device__ static bool has_lens(int batch) { return 2 * batch <= MAX_BATCH; }
     __host__ __device__ static int meta(int batch)
     {
-        return round_up(TSTART + (batch + 1) * 4, 16);
+        return round_up(TSTART + ((has_lens(batch) ? 2 : 1) * batch + 1) * 4, 16);
     }
     __host__ __device__ static int total(int batch)
     {
-        return meta(batch) + (2 * C::W + C::W + 8) * 4;
+        return meta(batch) + (2 * C::W + 2 * C::W + 16) * 4;
     }
 };
 
@@ -164,103 +168,104 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A position in the tile list.
-struct Pos {
-    int b, kvh, ti;      // sequence, KV head, 16-row tile of the sequence
-    int L, lo;           // rows attended: [lo, L)
-    int end;             // one past the piece's last tile
+// A tile of the list: what a lane holds of each of the warp's next 32 tiles.
+struct Tile {
+    int id[4];           // block of each quarter of the rows (blocks of >= 16 rows: all in id[0])
+    int b, kvh;
+    int bits;            // rows in the sequence (1..16), first attended row << 5, first / last
+                         // tile of the piece << 10 / 11, first row's place in its block << 12
 };
+constexpr int FIRST = 1 << 10, LAST = 1 << 11;
+
+__device__ __forceinline__ int rows_of(int bits) { return bits & 31; }
+__device__ __forceinline__ int skip_of(int bits) { return (bits >> 5) & 31; }
 
 template <int D, int G, int KV>
-__device__ __forceinline__ Pos pos_at(const Params &p, const int *tstart, int x)
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *tstart, int x)
 {
-    Pos s;
-    s.b = kern::find_seq(tstart, p.batch, x);
-    s.L = seq_len(p, s.b);
-    s.lo = first_row(p, s.L);
-    const int nt = num_tiles(s.L, s.lo);
-    const int off = x - tstart[s.b];
-    s.kvh = off / nt;
-    s.ti = off - s.kvh * nt + s.lo / TILE;
-    s.end = s.lo / TILE + nt;
-    return s;
-}
-
-// To the next tile (only called when the list has one).
-__device__ __forceinline__ void advance(const Params &p, const int *tstart, Pos &s)
-{
-    if (++s.ti < s.end)
-        return;
-    if (++s.kvh == p.num_kv_heads) {
-        s.kvh = 0;
-        do
-            ++s.b;
-        while (tstart[s.b + 1] == tstart[s.b]);
-        s.L = seq_len(p, s.b);
-        s.lo = first_row(p, s.L);
-        s.end = (s.L + TILE - 1) / TILE;
+    Tile t;
+    t.b = kern::find_seq(tstart, p.batch, x);
+    const int L = Smem<D, G, KV>::has_lens(p.batch) ? tstart[p.batch + 1 + t.b] : seq_len(p, t.b);
+    const int lo = first_row(p, L);
+    const int nt = num_tiles(L, lo);
+    const int off = x - tstart[t.b];
+    t.kvh = off / nt;
+    const int i = off - t.kvh * nt;
+    const int t0 = TILE * (lo / TILE + i);
+    t.bits = min(TILE, L - t0) | max(0, lo - t0) << 5 | (i == 0 ? FIRST : 0) |
+             (i + 1 == nt ? LAST : 0) | (t0 & (p.block_size - 1)) << 12;
+    const int32_t *row =
+        p.tables + (p.per_head ? (int64_t)t.b * p.num_kv_heads + t.kvh : (int64_t)t.b) *
+                       p.table_stride;
+    // blocks that hold attended rows (no other entry is looked at)
+    const int n = p.block_size >= TILE ? 1 : TILE >> p.bs_log2;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int r0 = u << p.bs_log2;
+        t.id[u] = -1;
+        if (u < n && (n == 1 || (r0 < rows_of(t.bits) &&
+                                 r0 + p.block_size > skip_of(t.bits)))) {
+            const int id = __ldg(row + ((t0 >> p.bs_log2) + u));
+            if (id < 0 || id >= p.num_blocks)
+                atomicOr(p.err, PKV_EBIT_BLOCK);
+            else
+                t.id[u] = id;
+        }
     }
-    s.ti = s.lo / TILE;
+    return t;
 }
 
-// Copies of one tile into a stage, one commit group.
+// Copies of the tile that lane j describes into a stage, one commit group.
 template <int D, int G, int KV>
-__device__ __forceinline__ void issue_tile(const Params &p, const Pos &s, unsigned char *stage,
-                                           int lane)
+__device__ __forceinline__ void issue_tile(const Params &p, const Tile &d, int j,
+                                           unsigned char *stage, int4 *info, int lane)
 {
     using C = Cfg<D, G, KV>;
     const int r0 = lane / C::CH, c = lane % C::CH;
-    const int bs = p.block_size;
-    const int32_t *row =
-        p.tables + (p.per_head ? (int64_t)s.b * p.num_kv_heads + s.kvh : (int64_t)s.b) *
-                       p.table_stride;
-    const int t0 = TILE * s.ti;
-    auto block_of = [&](int t, bool &ok) {
-        int id = ok ? __ldg(row + (t >> p.bs_log2)) : 0;
-        if (id < 0 || id >= p.num_blocks) {
-            atomicOr(p.err, PKV_EBIT_BLOCK);
-            id = 0;
-            ok = false;
-        }
-        return id;
-    };
+    const int bits = __shfl_sync(FULL_MASK, d.bits, j), kvh = __shfl_sync(FULL_MASK, d.kvh, j);
+    const int b = __shfl_sync(FULL_MASK, d.b, j), id0 = __shfl_sync(FULL_MASK, d.id[0], j);
+    const int rows = rows_of(bits), skip = skip_of(bits), bs = p.block_size;
+    if (lane == 0)
+        *info = make_int4(bits, b, kvh, 0);
     if (bs >= TILE) {
-        // the tile lies in one block (its first attended row says which)
-        bool ok = true;
-        const int id = block_of(t0, ok);
-        const int64_t head = (int64_t)id * p.num_kv_heads + s.kvh;
-        const int64_t base = (head * bs + (t0 & (bs - 1)) + r0) * C::ROWB + c * 16;
+        const int64_t head = (int64_t)max(id0, 0) * p.num_kv_heads + kvh;
+        const int64_t base = (head * bs + (bits >> 12) + r0) * C::ROWB + c * 16;
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) {
             const int r = r0 + i * C::RPI;
-            const bool v = ok && t0 + r < s.L && t0 + r >= s.lo;
+            const bool v = id0 >= 0 && r < rows && r >= skip;
             const uint32_t dst = kern::swz_off(r * C::ROWB + c * 16, true);
             cp16_zfill(stage + dst, p.k_cache + base + i * C::RPI * C::ROWB, v);
             cp16_zfill(stage + C::TILE_BYTES + dst, p.v_cache + base + i * C::RPI * C::ROWB, v);
         }
         if constexpr (C::F8)
             cp4_zfill(stage + 2 * C::TILE_BYTES + lane * 4,
-                      (lane < TILE ? p.k_scales : p.v_scales) + head, ok);
+                      (lane < TILE ? p.k_scales : p.v_scales) + head, id0 >= 0);
     } else {
+        const int id1 = __shfl_sync(FULL_MASK, d.id[1], j);
+        const int id2 = __shfl_sync(FULL_MASK, d.id[2], j);
+        const int id3 = __shfl_sync(FULL_MASK, d.id[3], j);
+        auto head_of = [&](int r, bool &v) -> int64_t {
+            const int u = r >> p.bs_log2;
+            const int id = u == 0 ? id0 : u == 1 ? id1 : u == 2 ? id2 : id3;
+            v = id >= 0 && r < rows && r >= skip;
+            return (int64_t)max(id, 0) * p.num_kv_heads + kvh;
+        };
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) {
-            const int r = r0 + i * C::RPI, t = t0 + r;
-            bool v = t < s.L && t >= s.lo;
-            const int id = block_of(t, v);
-            const int64_t off =
-                (((int64_t)id * p.num_kv_heads + s.kvh) * bs + (t & (bs - 1))) * C::ROWB + c * 16;
+            const int r = r0 + i * C::RPI;
+            bool v;
+            const int64_t head = head_of(r, v);
+            const int64_t off = (head * bs + (r & (bs - 1))) * C::ROWB + c * 16;
             const uint32_t dst = kern::swz_off(r * C::ROWB + c * 16, true);
             cp16_zfill(stage + dst, p.k_cache + off, v);
             cp16_zfill(stage + C::TILE_BYTES + dst, p.v_cache + off, v);
         }
         if constexpr (C::F8) {
-            const int t = t0 + (lane & (TILE - 1));
-            bool v = t < s.L && t >= s.lo;
-            const int id = block_of(t, v);
+            bool v;
+            const int64_t head = head_of(lane & (TILE - 1), v);
             cp4_zfill(stage + 2 * C::TILE_BYTES + lane * 4,
-                      (lane < TILE ? p.k_scales : p.v_scales) +
-                          ((int64_t)id * p.num_kv_heads + s.kvh),
-                      v);
+                      (lane < TILE ? p.k_scales : p.v_scales) + head, v);
         }
     }
 }
@@ -270,26 +275,32 @@ struct State : kern::MmaState<D, G, KV, false> {
     float n[2];          // whole numbers >= x + ev of heads 2 tig, 2 tig + 1 (m: >= x)
 };
 
-// q of the G heads of (b, kvh) -> B fragments of the score MMAs (the head
-// columns beyond G repeat the heads, as in the other kernel), and the factors
-// that turn an MMA sum over the lane's two heads into a log2-domain score.
-template <int D, int G, int KV>
-__device__ __forceinline__ void load_q(State<D, G, KV> &st, float (&qscale)[2], const Params &p,
-                                       int b, int kvh, int lane)
+// The lane's quarter of q's row for its head column (head gid mod G: the
+// columns beyond G repeat the heads, as in the other kernel), raw.
+template <int D, int G>
+__device__ __forceinline__ void fetch_q(uint32_t (&w)[D / 8], const Params &p, int b, int kvh,
+                                        int lane)
 {
-    constexpr bool F8 = KV == PKV_F8;
-    constexpr int NQ = D / 32;                       // 16-byte chunks of the lane's quarter row
     const int gid = lane >> 2, tig = lane & 3;
-    const int head = gid % G;
     const uint4 *src = reinterpret_cast<const uint4 *>(
         static_cast<const uint16_t *>(p.q) +
-        ((int64_t)b * p.num_q_heads + kvh * G + head) * D + tig * (D / 4));
-    uint32_t w[NQ * 4];
+        ((int64_t)b * p.num_q_heads + kvh * G + gid % G) * D + tig * (D / 4));
 #pragma unroll
-    for (int c = 0; c < NQ; ++c) {
+    for (int c = 0; c < D / 32; ++c) {
         const uint4 x = __ldg(src + c);
         w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
     }
+}
+
+// Raw q -> B fragments of the score MMAs, and the factors that turn an MMA sum
+// over the lane's two heads into a log2-domain score.
+template <int D, int G, int KV>
+__device__ __forceinline__ void use_q(State<D, G, KV> &st, float (&qscale)[2],
+                                      uint32_t (&w)[D / 8], const Params &p, int lane)
+{
+    constexpr bool F8 = KV == PKV_F8;
+    constexpr int NQ = D / 32;                       // 16-byte chunks of the lane's quarter row
+    const int tig = lane & 3;
     float unscale = p.scale_log2;
     if (F8 && p.q_dtype == PKV_BF16) {
         // fp16 has bf16's 8 significant bits but not its exponents: bring the
@@ -330,6 +341,131 @@ __device__ __forceinline__ void load_q(State<D, G, KV> &st, float (&qscale)[2], 
     // the heads of columns 2 tig, 2 tig + 1 (lane 4 n holds column n's head)
     qscale[0] = __shfl_sync(FULL_MASK, unscale, 8 * tig);
     qscale[1] = __shfl_sync(FULL_MASK, unscale, 8 * tig + 4);
+}
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        x += __shfl_xor_sync(FULL_MASK, x, m);
+    return x;
+}
+
+// Parts a weight is split into, each of the MMA's type: two of fp16 leave
+// 2^-22 of it, three of bf16 2^-27 (two would leave 2^-18).
+template <int KV>
+__host__ __device__ constexpr int weight_parts() { return KV == PKV_BF16 ? 3 : 2; }
+
+// O^T += V^T P^T of one tile.  The MMA's 8 head columns take 8 / G parts of the
+// weights at a time: column c holds part c / G of head c mod G (the columns
+// repeat the heads), so that G < 8 needs one or two MMAs for all parts.  The
+// tile's sum starts at zero and is added to the running one in fp32: an MMA
+// truncates what it adds to its accumulator, and over a long run of tiles that
+// would show (3e-6 of the result at 230 tiles a warp).
+template <int D, int G, int KV>
+__device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
+                                        const uint32_t (&vw)[4][kern::VFrag<D, KV>::VW], float p0,
+                                        float p1, float p2, float p3, int lane)
+{
+    constexpr bool BF = kern::MmaBf16<KV>::v;
+    constexpr int NP = weight_parts<KV>();
+    constexpr int NB = (NP * G + 7) / 8;          // MMAs for all parts
+    const int tig = lane & 3;
+    uint32_t part[2][NP];                         // heads 2 tig, 2 tig + 1 of token gid | gid + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float x = h ? p2 : p0, y = h ? p3 : p1;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            if constexpr (BF) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                x -= __low2float(v);
+                y -= __high2float(v);
+                part[h][i] = *reinterpret_cast<const uint32_t *>(&v);
+            } else {
+                const __half2 v = __floats2half2_rn(x, y);
+                x -= __low2float(v);
+                y -= __high2float(v);
+                part[h][i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+    }
+    uint32_t bf[NB][2];
+#pragma unroll
+    for (int m = 0; m < NB; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v = 0u;
+            if constexpr (G == 1) {
+                // columns 2 tig, 2 tig + 1 are parts 2 tig, 2 tig + 1 of the one head
+                if (tig == 0)
+                    v = __byte_perm(part[h][0], part[h][1], 0x7610u);
+                else if (tig == 1 && NP > 2)
+                    v = part[h][NP - 1] & 0xffffu;
+            } else {
+                const int mine = (2 * tig) / G + m * (8 / G);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    if (mine == i)
+                        v = part[h][i];
+            }
+            bf[m][h] = kern::transpose8x8(v);
+        }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (KV == PKV_F8) {
+            const int w = j >> 1;
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            f8x4_to_half2(__byte_perm(vw[0][w], vw[1][w], sel), a0, a1);
+            f8x4_to_half2(__byte_perm(vw[2][w], vw[3][w], sel), a2, a3);
+        } else {
+            a0 = __byte_perm(vw[0][j], vw[1][j], 0x5410u);
+            a1 = __byte_perm(vw[0][j], vw[1][j], 0x7632u);
+            a2 = __byte_perm(vw[2][j], vw[3][j], 0x5410u);
+            a3 = __byte_perm(vw[2][j], vw[3][j], 0x7632u);
+        }
+        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int m = 0; m < NB; ++m)
+            kern::mma_16816<BF>(t, a0, a1, a2, a3, bf[m][0], bf[m][1]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            st.acc[j][u] += t[u];
+    }
+}
+
+// At a piece's end: the sums of a head's parts, in the head's own columns.
+template <int D, int G, int KV>
+__device__ __forceinline__ void join_parts(State<D, G, KV> &st)
+{
+    constexpr int NP = weight_parts<KV>();
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        if constexpr (G == 1) {
+            st.acc[j][0] += st.acc[j][1];
+            st.acc[j][2] += st.acc[j][3];
+            if constexpr (NP > 2) {
+                st.acc[j][0] += __shfl_down_sync(FULL_MASK, st.acc[j][0], 1);
+                st.acc[j][2] += __shfl_down_sync(FULL_MASK, st.acc[j][2], 1);
+            }
+        } else if constexpr (G < 8) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x = st.acc[j][u];
+                st.acc[j][u] += __shfl_down_sync(FULL_MASK, x, G / 2);
+                if constexpr (G == 2 && NP > 2)
+                    st.acc[j][u] += __shfl_down_sync(FULL_MASK, x, 2);
+            }
+        }
+    }
 }
 
 // One tile: scores, online softmax, weighted V (see the head of the file).
@@ -417,7 +553,7 @@ __device__ __forceinline__ void tile(State<D, G, KV> &st, const float (&qscale)[
         p2 = kern::exp2_approx(x2 + (f1 - d0));
         p3 = kern::exp2_approx(x3 + (f1 - d1));
     }
-    kern::mma_pv<D, G, KV, false>(st, vw, p0, p1, p2, p3, lane);
+    weigh_v<D, G, KV>(st, vw, p0, p1, p2, p3, lane);
 }
 
 template <int D, int G, int KV>
@@ -431,8 +567,9 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     float *states = reinterpret_cast<float *>(smem + S::STATES);
     int *tstart = reinterpret_cast<int *>(smem + S::TSTART);
     int *meta = reinterpret_cast<int *>(smem + S::meta(p.batch));   // [W][2] pieces, -1 = none
-    int *scan = meta + 2 * W;                                       // [W] warp sums
-    int *flag = scan + W;                                           // [2] pieces to join here
+    int *scan = meta + 2 * W;                                       // [W] warp sums, [W] maxima
+    int *flag = scan + 2 * W;                                       // [2] pieces to join here
+    int *edge = flag + 2;        // the CTA's first and last piece: index, its first and last CTA
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = p.batch, Hkv = p.num_kv_heads, Hq = p.num_q_heads;
     const int cta = blockIdx.x;
@@ -444,14 +581,20 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     {
         const int per = (B + NT - 1) / NT;
         const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-        int n = 0;
+        int n = 0, most = 0;
         for (int b = b0; b < b1; ++b) {
             const int raw = __ldg(p.seq_lens + b);
             if ((raw < 0 || raw > p.len_cap) && cta == 0)
                 atomicOr(p.err, PKV_EBIT_SEQLEN);
-            const int L = seq_len(p, b);
-            n += num_tiles(L, first_row(p, L)) * Hkv;
+            const int L = raw < 0 || raw > p.len_cap ? 0 : attended_len(p, raw);
+            if (S::has_lens(B))
+                tstart[B + 1 + b] = L;
+            const int nt = num_tiles(L, first_row(p, L));
+            n += nt * Hkv;
+            // (a sequence without tiles counts as one too long for the even split)
+            most = max(most, nt > 0 ? nt : INT_MAX);
         }
+        most = __reduce_max_sync(FULL_MASK, most);
         int inc = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -459,8 +602,10 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
             if (lane >= off)
                 inc += x;
         }
-        if (lane == 31)
+        if (lane == 31) {
             scan[warp] = inc;
+            scan[W + warp] = most;
+        }
         if (tid < 2 * W)
             meta[tid] = -1;
         if (tid < 2)
@@ -473,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 at += scan[w];
         for (int b = b0; b < b1; ++b) {
             tstart[b] = at;
-            const int L = seq_len(p, b);
+            const int L = S::has_lens(B) ? tstart[B + 1 + b] : seq_len(p, b);
             at += num_tiles(L, first_row(p, L)) * Hkv;
         }
         if (tid == NT - 1)
@@ -481,31 +626,65 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         __syncthreads();
     }
     const int T = tstart[B];
-    // CTAs that share the list: no more than leave every warp MIN_TILES
-    const int P = max(1, min((int)gridDim.x, T / (W * MIN_TILES)));
-
-    // rows of sequences without a row to attend: zeros
-    for (int b = cta; b < B; b += gridDim.x)
-        if (tstart[b + 1] == tstart[b])
-            for (int i = tid; i < Hq * D; i += NT)
-                p.out[(int64_t)b * Hq * D + i] = 0.0f;
-    if (cta >= P || T == 0)
-        return;
-
-    const int c0 = (int)((int64_t)cta * T / P), c1 = (int)((int64_t)(cta + 1) * T / P);
+    // ---- this CTA's tiles [c0, c1), and how many CTAs have any (P).  Where the
+    // sequences are about as long as one another, a CTA takes `each` whole
+    // pieces, so that none is joined across CTAs: if that leaves at most a
+    // fifth of the CTAs idle (fewer SMs still draw the memory's full rate), or
+    // if the pieces are so short that joining costs more than it spreads.
+    // Else every CTA takes an equal part of the list, but no fewer than
+    // MIN_TILES tiles a warp.
+    int most = scan[W];
+#pragma unroll
+    for (int w = 1; w < W; ++w)
+        most = max(most, scan[W + w]);
+    const int pieces = B * Hkv;
+    const int each = (pieces + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int whole_ctas = (pieces + each - 1) / each;
+    const bool even = (int64_t)most * pieces <= (int64_t)T + T / 8 &&
+                      (whole_ctas * 5 >= (int)gridDim.x * 4 || most <= SHORT_TILES * W);
+    const int P = even ? whole_ctas : max(1, min((int)gridDim.x, T / (W * MIN_TILES)));
+    auto bound = [&](int c) {
+        if (c >= P)
+            return T;
+        if (!even)
+            return (int)((int64_t)c * T / P);
+        const int b = c * each / Hkv;
+        return tstart[b] + (c * each - b * Hkv) * ((tstart[b + 1] - tstart[b]) / Hkv);
+    };
+    const int c0 = bound(cta), c1 = bound(cta + 1);
     const int r0 = c0 + (int)((int64_t)warp * (c1 - c0) / W);
     const int r1 = c0 + (int)((int64_t)(warp + 1) * (c1 - c0) / W);
+    auto tiles_of = [&](int seg, int &x0, int &x1) {
+        const int b = seg / Hkv, kvh = seg - b * Hkv;
+        const int nt = (tstart[b + 1] - tstart[b]) / Hkv;
+        x0 = tstart[b] + kvh * nt;
+        x1 = x0 + nt;
+    };
+    auto piece_of = [&](int x) {
+        const int b = kern::find_seq(tstart, B, x);
+        return b * Hkv + (x - tstart[b]) / ((tstart[b + 1] - tstart[b]) / Hkv);
+    };
     unsigned char *ring = smem + S::RING + warp * NST * C::STAGE;
+    int4 *info = reinterpret_cast<int4 *>(smem + S::INFO) + warp * NST;
     if (r0 < r1) {
         const int n = r1 - r0;
-        Pos cs = pos_at<D, G, KV>(p, tstart, r0);
-        Pos is = cs;
+        // the lanes describe the run's tiles 32 at a time: one round trip to the
+        // block tables for all of them
+        int base = 0;
+        Tile d = tile_at<D, G, KV>(p, tstart, min(r0 + lane, r1 - 1));
+        uint32_t qraw[D / 8];
+        fetch_q<D, G>(qraw, p, __shfl_sync(FULL_MASK, d.b, 0), __shfl_sync(FULL_MASK, d.kvh, 0),
+                      lane);
         int issued = 0;
         auto issue = [&]() {
             if (issued < n) {
-                issue_tile<D, G, KV>(p, is, ring + (issued % NST) * C::STAGE, lane);
-                if (++issued < n)
-                    advance(p, tstart, is);
+                if (issued - base == 32) {
+                    base = issued;
+                    d = tile_at<D, G, KV>(p, tstart, min(r0 + base + lane, r1 - 1));
+                }
+                issue_tile<D, G, KV>(p, d, issued - base, ring + (issued % NST) * C::STAGE,
+                                     info + issued % NST, lane);
+                ++issued;
             }
             cp_commit();
         };
@@ -513,14 +692,30 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         for (int i = 0; i < NST - 1; ++i)
             issue();
 
+        if (warp == W - 1 && lane < 2 && !even) {
+            // (the last warp has tiles wherever the CTA has) the CTAs of the
+            // first and the last piece, worked out while the first tiles arrive
+            const int seg = piece_of(lane ? c1 - 1 : c0);
+            int x0, x1;
+            tiles_of(seg, x0, x1);
+            edge[3 * lane] = seg;
+            edge[3 * lane + 1] = kern::owner_of(x0, T, P);
+            edge[3 * lane + 2] = kern::owner_of(x1 - 1, T, P);
+        }
+
         State<D, G, KV> st;
         float qscale[2];
         bool fresh = true;
-        bool whole = cs.ti == cs.lo / TILE;       // the piece began in this run
+        bool whole = true;                 // the piece began in this run
         const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll 1
         for (int k = 0; k < n; ++k) {
+            cp_wait<NST - 2>();
+            __syncwarp();              // the lanes' copies have landed, the last tile is read
+            const int4 it = info[k % NST];
             if (fresh) {
-                load_q<D, G, KV>(st, qscale, p, cs.b, cs.kvh, lane);
+                whole = (it.x & FIRST) != 0;
+                use_q<D, G, KV>(st, qscale, qraw, p, lane);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     st.m[r] = st.n[r] = -INFINITY;
@@ -533,12 +728,16 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                         st.acc[j][u] = 0.0f;
                 fresh = false;
             }
-            cp_wait<NST - 2>();
-            __syncwarp();              // the lanes' copies have landed, the last tile is read
             issue();
-            tile<D, G, KV>(st, qscale, ring + (k % NST) * C::STAGE, cs.L - TILE * cs.ti,
-                           cs.lo - TILE * cs.ti, lane);
-            const bool ends = cs.ti + 1 == cs.end;
+            const bool ends = (it.x & LAST) != 0;
+            if (ends && k + 1 < n) {
+                // q of the next piece, on its way while this piece's last tile is computed
+                __syncwarp();
+                const int4 next = info[(k + 1) % NST];
+                fetch_q<D, G>(qraw, p, next.y, next.z, lane);
+            }
+            tile<D, G, KV>(st, qscale, ring + (k % NST) * C::STAGE, rows_of(it.x), skip_of(it.x),
+                           lane);
             if (ends || k + 1 == n) {
                 // ---- the piece's end, or the run's
 #pragma unroll
@@ -546,35 +745,20 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 #pragma unroll
                     for (int mask = 4; mask < 32; mask <<= 1)
                         st.l[r] += __shfl_xor_sync(FULL_MASK, st.l[r], mask);
-                if constexpr (G == 1) {
-                    // column 1 holds the low-part sums of column 0's head
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        st.acc[j][0] += st.acc[j][1];
-                        st.acc[j][2] += st.acc[j][3];
-                    }
-                } else if constexpr (G < 8) {
-                    // columns 2 tig + G, + 1 (lane + G / 2) hold the low-part
-                    // sums of the lane's heads
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            st.acc[j][u] += __shfl_down_sync(FULL_MASK, st.acc[j][u], G / 2);
-                }
+                join_parts<D, G, KV>(st);
                 const bool out_now = whole && ends;
                 if (!out_now)
                     __syncwarp();      // the ring may be overwritten
                 float *dst;
                 if (out_now) {
-                    dst = p.out + ((int64_t)cs.b * Hq + cs.kvh * G) * D;
+                    dst = p.out + ((int64_t)it.y * Hq + it.z * G) * D;
                 } else {
                     // a piece that began before the run is its first one and
                     // has a place of its own; one that goes on behind it is
                     // its last one and takes the drained ring's
                     dst = whole ? reinterpret_cast<float *>(ring) : states + warp * C::STATE;
                     if (lane == 0)
-                        meta[2 * warp + (whole ? 1 : 0)] = cs.b * Hkv + cs.kvh;
+                        meta[2 * warp + (whole ? 1 : 0)] = it.y * Hkv + it.z;
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -596,114 +780,159 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                     }
                 }
                 fresh = true;
-                whole = true;
             }
-            if (k + 1 < n)
-                advance(p, tstart, cs);
         }
         cp_wait<0>();
     }
+
+    // rows of sequences without a row to attend: zeros
+    for (int b = cta; b < B; b += gridDim.x)
+        if (tstart[b + 1] == tstart[b])
+            for (int i = tid; i < Hq * D; i += NT)
+                p.out[(int64_t)b * Hq * D + i] = 0.0f;
+    if (c0 >= c1)
+        return;
     __syncthreads();
 
     // ---- join the warps' states of each piece (they lie in list order)
-    auto state_of = [&](int f) {
-        return f & 1 ? reinterpret_cast<const float *>(smem + S::RING +
-                                                       (f >> 1) * NST * C::STAGE)
-                     : states + (f >> 1) * C::STATE;
-    };
-    auto tiles_of = [&](int seg, int &x0, int &x1) {
-        const int b = seg / Hkv, kvh = seg - b * Hkv;
-        const int nt = (tstart[b + 1] - tstart[b]) / Hkv;
-        x0 = tstart[b] + kvh * nt;
-        x1 = x0 + nt;
-    };
+    // lane f: state f (warp f / 2's first or last piece)
+    static_assert(2 * W <= 32, "a lane a state");
+    const float *mine_state = lane & 1 ? reinterpret_cast<const float *>(
+                                             smem + S::RING + (lane >> 1) % W * NST * C::STAGE)
+                                       : states + (lane >> 1) % W * C::STATE;
+    const int mine_seg = lane < 2 * W ? meta[lane] : -1;
+    const unsigned valid = __ballot_sync(FULL_MASK, mine_seg >= 0);
+    const unsigned before = valid & ((1u << lane) - 1u);
+    const int prev_seg = __shfl_sync(FULL_MASK, mine_seg, before ? 31 - __clz(before) : 0);
+    unsigned starts = __ballot_sync(FULL_MASK,
+                                    mine_seg >= 0 && (before == 0 || prev_seg != mine_seg));
+    constexpr int MO = (G * D + NT - 1) / NT;   // elements of a piece's output a thread joins
     int shared_pieces = 0;
-    for (int f = 0; f < 2 * W;) {
-        const int seg = meta[f];
-        if (seg < 0) {
-            ++f;
-            continue;
-        }
-        int e = f + 1;
-        while (e < 2 * W && (meta[e] == seg || meta[e] < 0))
-            ++e;
-        int x0, x1;
-        tiles_of(seg, x0, x1);
-        const bool mine = x0 >= c0 && x1 <= c1;
+    while (starts) {
+        const int f = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const unsigned members =
+            valid & ~((1u << f) - 1u) & (starts ? (starts & (~starts + 1u)) - 1u : ~0u);
+        const int seg = __shfl_sync(FULL_MASK, mine_seg, f);
+        // shared with other CTAs: 1 as this CTA's first piece, 2 as its last
+        int edges = 0;
+        if (!even)
+            for (int t = 0; t < 2; ++t)
+                if (edge[3 * t] == seg && edge[3 * t + 1] != edge[3 * t + 2])
+                    edges = t + 1;
+        const bool mine = edges == 0;
         float *dst = mine ? p.out + ((int64_t)(seg / Hkv) * Hq + (seg % Hkv) * G) * D
                           : p.partials + (int64_t)(cta + seg) * C::STATE;
-        for (int i = tid; i < G * D; i += NT) {
-            const int g = i / D;
-            float M = -INFINITY;
-            for (int u = f; u < e; ++u)
-                if (meta[u] >= 0)
-                    M = fmaxf(M, state_of(u)[G * D + g]);
-            float num = 0.0f, den = 0.0f;
-            for (int u = f; u < e; ++u)
-                if (meta[u] >= 0) {
-                    const float *sp = state_of(u);
-                    const float w = kern::exp2_approx(sp[G * D + g] - M);
-                    num = fmaf(w, sp[i], num);
-                    den = fmaf(w, sp[G * D + G + g], den);
+        const bool member = (members >> lane) & 1u;
+        // a warp's 32 elements belong to one head: the lanes weigh the states
+        float w[MO], den[MO], top[MO], num[MO];
+#pragma unroll
+        for (int o = 0; o < MO; ++o) {
+            const int g = min((o * NT + tid) / D, G - 1);
+            const float m = member ? mine_state[G * D + g] : -INFINITY;
+            const float l = member ? mine_state[G * D + G + g] : 0.0f;
+            top[o] = warp_max(m);
+            w[o] = member ? kern::exp2_approx(m - top[o]) : 0.0f;
+            den[o] = warp_sum(w[o] * l);
+            num[o] = 0.0f;
+        }
+#pragma unroll 1
+        for (unsigned left = members; left;) {
+            // four states at a time; past the last one it is read again, with weight 0
+            int u[4];
+            float v[4][MO];
+            bool there[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                there[t] = left != 0u;
+                u[t] = there[t] ? __ffs(left) - 1 : u[0];
+                left &= left - 1u;
+                const float *sp = (u[t] & 1 ? reinterpret_cast<const float *>(
+                                                  smem + S::RING + (u[t] >> 1) * NST * C::STAGE)
+                                            : states + (u[t] >> 1) * C::STATE) + tid;
+#pragma unroll
+                for (int o = 0; o < MO; ++o)
+                    v[t][o] = tid + o * NT < G * D ? sp[o * NT] : 0.0f;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int o = 0; o < MO; ++o) {
+                    const float wu = __shfl_sync(FULL_MASK, w[o], u[t]);
+                    num[o] = fmaf(there[t] ? wu : 0.0f, v[t][o], num[o]);
                 }
-            if (mine) {
-                dst[i] = num / den;
-            } else {
-                dst[i] = num;
-                if (i % D == 0) {
-                    dst[G * D + g] = M;
-                    dst[G * D + G + g] = den;
+        }
+#pragma unroll
+        for (int o = 0; o < MO; ++o) {
+            const int i = o * NT + tid, g = i / D;
+            if (i < G * D) {
+                dst[i] = mine ? num[o] / den[o] : num[o];
+                if (!mine && i % D == 0) {
+                    dst[G * D + g] = top[o];
+                    dst[G * D + G + g] = den[o];
                 }
             }
         }
-        if (!mine) {
-            if (tid == 0)
-                scan[shared_pieces] = seg;
-            ++shared_pieces;           // at most two: the CTA's first and last piece
-        }
-        f = e;
+        shared_pieces |= edges;        // bit t: the piece edge[3 t] is
     }
     if (shared_pieces == 0)
         return;
     __syncthreads();
-    if (tid == 0) {
-        __threadfence();               // every thread's partials, ordered before the counts
-        for (int i = 0; i < shared_pieces; ++i) {
-            const int seg = scan[i];
-            int x0, x1;
-            tiles_of(seg, x0, x1);
-            const int others = kern::owner_of(x1 - 1, T, P) - kern::owner_of(x0, T, P);
-            if (atomicAdd(p.counters + seg, 1) == others) {
-                flag[i] = seg;
-                p.counters[seg] = 0;
-            }
+    if (tid < 2 && (shared_pieces >> tid & 1)) {
+        const int seg = edge[3 * tid];
+        __threadfence();               // every thread's partials, ordered before the count
+        if (atomicAdd(p.counters + seg, 1) == edge[3 * tid + 2] - edge[3 * tid + 1]) {
+            flag[tid] = seg;
+            p.counters[seg] = 0;
+            __threadfence();
         }
-        __threadfence();
     }
     __syncthreads();
+#pragma unroll 1
     for (int j = 0; j < 2; ++j) {
         const int seg = flag[j];
         if (seg < 0)
             continue;
-        int x0, x1;
-        tiles_of(seg, x0, x1);
-        const int o0 = kern::owner_of(x0, T, P), o1 = kern::owner_of(x1 - 1, T, P);
-        for (int i = tid; i < G * D; i += NT) {
-            const int g = i / D;
-            float m = -INFINITY, num = 0.0f, den = 0.0f;
-#pragma unroll 4
-            for (int c = o0; c <= o1; ++c) {
-                const float *sp = p.partials + (int64_t)(c + seg) * C::STATE;
-                const float mp = __ldcg(sp + G * D + g), np = __ldcg(sp + i),
-                            dp = __ldcg(sp + G * D + G + g);
-                const float mn = fmaxf(m, mp);
-                const float a = kern::exp2_approx(m - mn), w = kern::exp2_approx(mp - mn);
-                num = fmaf(num, a, np * w);
-                den = fmaf(den, a, dp * w);
-                m = mn;
-            }
-            p.out[((int64_t)(seg / Hkv) * Hq + (seg % Hkv) * G) * D + i] = num / den;
+        const int o0 = edge[3 * j + 1], o1 = edge[3 * j + 2];
+        const float *part = p.partials + (int64_t)(o0 + seg) * C::STATE;
+        const int np = o1 - o0 + 1;
+        float num[MO], den[MO], top[MO];
+#pragma unroll
+        for (int o = 0; o < MO; ++o) {
+            num[o] = den[o] = 0.0f;
+            top[o] = -INFINITY;
         }
+#pragma unroll 1
+        for (int q0 = 0; q0 < np; q0 += 32) {
+            const int qn = min(32, np - q0);
+            const bool in = lane < qn;
+            float w[MO];
+#pragma unroll
+            for (int o = 0; o < MO; ++o) {
+                const int g = min((o * NT + tid) / D, G - 1);
+                const float *sp = part + (int64_t)(q0 + min(lane, qn - 1)) * C::STATE + G * D + g;
+                const float m = in ? __ldcg(sp) : -INFINITY, l = in ? __ldcg(sp + G) : 0.0f;
+                const float mn = fmaxf(top[o], warp_max(m));
+                const float a = kern::exp2_approx(top[o] - mn);
+                w[o] = in ? kern::exp2_approx(m - mn) : 0.0f;
+                den[o] = fmaf(den[o], a, warp_sum(w[o] * l));
+                num[o] *= a;
+                top[o] = mn;
+            }
+#pragma unroll 4
+            for (int u = 0; u < qn; ++u) {
+                const float *sp = part + (int64_t)(q0 + u) * C::STATE + tid;
+#pragma unroll
+                for (int o = 0; o < MO; ++o)
+                    num[o] = fmaf(__shfl_sync(FULL_MASK, w[o], u),
+                                  tid + o * NT < G * D ? __ldcg(sp + o * NT) : 0.0f, num[o]);
+            }
+        }
+#pragma unroll
+        for (int o = 0; o < MO; ++o)
+            if (tid + o * NT < G * D)
+                p.out[((int64_t)(seg / Hkv) * Hq + (seg % Hkv) * G) * D + o * NT + tid] =
+                    num[o] / den[o];
     }
 }
 
@@ -719,7 +948,10 @@ int launch_t(const pkv_pool *pool, const Params &prm, cudaStream_t stream, int64
     if (cudaFuncSetAttribute(decode_blocks_kernel<D, G, KV>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return PKV_ERR_CUDA;
+    // a CTA for each piece, or one for the least its warps take
     int64_t P = max_tiles / (C::W * MIN_TILES);
+    if (P < (int64_t)prm.batch * prm.num_kv_heads)
+        P = (int64_t)prm.batch * prm.num_kv_heads;
     if (P > pool->num_sms)
         P = pool->num_sms;
     if (P < 1)

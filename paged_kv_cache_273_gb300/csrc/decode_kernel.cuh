@@ -932,11 +932,7 @@ __device__ __forceinline__ void mma_pv(MmaState<D, G, KV, QS> &st,
     split_pair<BF>(p2, p3, ph1, pl1);
     constexpr bool PACK = G < 8;
     uint32_t bh0, bh1, bl0 = 0u, bl1 = 0u;
-    if constexpr (G == 1) {
-        // column 0 the high part, column 1 the low part of the one head
-        bh0 = transpose8x8(tig == 0 ? __byte_perm(ph0, pl0, 0x7610u) : 0u);
-        bh1 = transpose8x8(tig == 0 ? __byte_perm(ph1, pl1, 0x7610u) : 0u);
-    } else if constexpr (PACK) {
+    if constexpr (PACK) {
         const bool hi_cols = 2 * tig < G, lo_cols = !hi_cols && 2 * tig < 2 * G;
         bh0 = transpose8x8(hi_cols ? ph0 : (lo_cols ? pl0 : 0u));
         bh1 = transpose8x8(hi_cols ? ph1 : (lo_cols ? pl1 : 0u));
@@ -969,12 +965,6 @@ __device__ __forceinline__ void mma_pv(MmaState<D, G, KV, QS> &st,
             a1 = i8pair_to_half2<0x4342u>(tab);
             a2 = i8pair_to_half2<0x4140u>(tcd);
             a3 = i8pair_to_half2<0x4342u>(tcd);
-        } else if constexpr (KV == PKV_F8) {
-            // bytes 2j, 2j+1 of the token's eighth, the two tokens' interleaved
-            const int w = j >> 1;
-            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-            f8x4_to_half2(__byte_perm(vw[0][w], vw[1][w], sel), a0, a1);
-            f8x4_to_half2(__byte_perm(vw[2][w], vw[3][w], sel), a2, a3);
         } else {
             // codes 2j, 2j+1 of the token's eighth (16 codes in two words)
             // are byte j of it: that byte of the two tokens goes to bytes 0

@@ -11,11 +11,15 @@
 // exact in fp32: which blocks are chosen does not depend on the order of any
 // sum.  2^eq is common to the blocks and left out.
 //
-// Work.  Bounds are read once, 2 D + 4 bytes a (block, KV head): a CTA scores
-// a chunk of one (sequence, KV head)'s blocks, 16 bytes a lane, with dp4a;
-// the last CTA of that (sequence, KV head) finds the budget-th largest score
-// by a search over the bits of the (order-preserving) score keys, held in
-// registers, and writes the chosen blocks in ascending order.
+// Work.  Bounds are read once, 2 D + 4 bytes a (block, KV head), 16 bytes a
+// lane, and multiplied with dp4a; every warp scores whole groups of 32 blocks
+// with its own copy of the query values in registers, so scoring needs no
+// barrier.  The last CTA of a (sequence, KV head) then finds the budget-th
+// largest score key (an order-preserving map of the score) digit by digit: the
+// keys, staged in shared memory, are counted by 8-bit digits of their
+// distance to the smallest, counted from the top bit that any of them has, so
+// that the first digit already spreads them; and it writes the chosen
+// blocks in ascending order.
 #include <algorithm>
 
 #include "decode_blocks.cuh"
@@ -35,9 +39,9 @@ namespace {
 
 using namespace dev;
 
-constexpr int NT = 512;              // threads of a CTA
+constexpr int NT = 256;              // threads of a CTA
 constexpr int NW = NT / 32;
-constexpr int MAX_KEYS = 32;         // keys a thread holds in registers (16384 blocks in all)
+constexpr int SMEM_KEYS = 49152;     // score keys that are staged in shared memory
 
 struct SelectArgs {
     const void *q;
@@ -53,6 +57,7 @@ struct SelectArgs {
     int batch, num_kv_heads, num_blocks, block_size, bs_log2, max_blocks, len_cap;
     int max_n;                       // blocks of the longest sequence allowed
     int chunk, chunks;               // blocks a CTA scores; CTAs a (sequence, KV head)
+    int stage;                       // shared memory holds a (sequence, KV head)'s keys
     int budget, q_dtype;
 };
 
@@ -63,141 +68,150 @@ __device__ __forceinline__ uint32_t sort_key(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ int block_sum(int x, int *scratch)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    x = __reduce_add_sync(FULL_MASK, x);
-    __syncthreads();
-    if (lane == 0)
-        scratch[warp] = x;
-    __syncthreads();
-    return __reduce_add_sync(FULL_MASK, lane < NW ? scratch[lane] : 0);
-}
-
 // The `want` largest of n keys (ties: lowest index first), 0 < want < n: their
-// indices, ascending, to sel / phys.  Key i is held by thread i % NT.
-template <int K>
-__device__ __forceinline__ void pick(const SelectArgs &a, const volatile uint32_t *keys, int n,
-                                     int want, int32_t *sel, int32_t *phys, const int32_t *row,
-                                     int *scratch)
+// indices, ascending, to sel / phys.  `keys` may be staged or in the workspace.
+struct Pick {
+    int hist[256];
+    uint32_t lo[NW], hi[NW];
+    int gt[NW], eq[NW];
+    int bin, left;
+};
+
+__device__ __forceinline__ void pick(const volatile uint32_t *keys, int n, int want, int32_t *sel,
+                                     int32_t *phys, const int32_t *row, Pick &s)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t key[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j)
-        key[j] = tid + j * NT < n ? keys[tid + j * NT] : 0u;
-    // t = the want-th largest key: the largest t that at least `want` reach
-    uint32_t t = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t cand = t | (1u << bit);
-        int c = 0;
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-            c += key[j] >= cand;
-        if (block_sum(c, scratch) >= want)
-            t = cand;
+    // the keys' range
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll 4
+    for (int i = tid; i < n; i += NT) {
+        const uint32_t k = keys[i];
+        lo = min(lo, k);
+        hi = max(hi, k);
     }
-    int above = 0;
+    lo = __reduce_min_sync(FULL_MASK, lo);
+    hi = __reduce_max_sync(FULL_MASK, hi);
+    if (lane == 0) {
+        s.lo[warp] = lo;
+        s.hi[warp] = hi;
+    }
+    s.hist[tid] = 0;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-        above += key[j] > t;
-    const int ties = want - block_sum(above, scratch);     // equal keys to take, lowest index first
-    // ranks in index order (index i = j * NT + tid)
-    int base_gt = 0, base_eq = 0;
-#pragma unroll 1
-    for (int j = 0; j < K; ++j) {
-        if (j * NT >= n)
-            break;
-        const int i = j * NT + tid;
-        uint32_t kj = 0;
-#pragma unroll
-        for (int u = 0; u < K; ++u)
-            if (u == j)
-                kj = key[u];
-        const bool gt = i < n && kj > t, eq = i < n && kj == t;
-        const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
+    for (int w = 0; w < NW; ++w) {
+        lo = min(lo, s.lo[w]);
+        hi = max(hi, s.hi[w]);
+    }
+    // t, relative to lo: the want-th largest key, a digit of up to 8 bits at a
+    // time; `left` of the keys that share t's digits so far are still to take
+    int top = hi > lo ? 32 - __clz(hi - lo) : 0;      // bits not decided yet
+    uint32_t t = 0;
+    int left = want;
+    while (top > 0) {
+        const int shift = max(top - 8, 0);
+#pragma unroll 4
+        for (int i = tid; i < n; i += NT) {
+            const uint32_t k = keys[i] - lo;
+            if (top >= 32 || (k >> top) == (t >> top))
+                atomicAdd(&s.hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1);
+        }
         __syncthreads();
-        if (lane == 0)
-            scratch[warp] = __popc(mg) | (__popc(me) << 16);
-        __syncthreads();
-        int bg = 0, be = 0, tg = 0, te = 0;
+        if (warp == 0) {
+            // bins from the top: lane l holds bins 255 - 8 l .. 248 - 8 l
+            int c[8], sum = 0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const int v = scratch[w];
-            if (w < warp) {
-                bg += v & 0xffff;
-                be += v >> 16;
+            for (int u = 0; u < 8; ++u) {
+                c[u] = s.hist[255 - 8 * lane - u];
+                sum += c[u];
             }
-            tg += v & 0xffff;
-            te += v >> 16;
+            int inc = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(FULL_MASK, inc, off);
+                if (lane >= off)
+                    inc += x;
+            }
+            int above = inc - sum;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (above < left && above + c[u] >= left) {
+                    s.bin = 255 - 8 * lane - u;
+                    s.left = left - above;
+                }
+                above += c[u];
+            }
         }
-        const unsigned below = (1u << lane) - 1u;
-        const int rg = base_gt + bg + __popc(mg & below), re = base_eq + be + __popc(me & below);
-        if (gt || (eq && re < ties)) {
-            const int at = rg + min(re, ties);
-            sel[at] = i;
-            phys[at] = __ldg(row + i);
+        __syncthreads();
+        t |= (uint32_t)s.bin << shift;
+        left = s.left;
+        top = shift;
+        s.hist[tid] = 0;
+        __syncthreads();
+    }
+    t += lo;
+    // keys above t, and the first `left` equal ones, in index order: each warp
+    // ranks a contiguous run of indices, 32 at a time
+    const int per = ((n + NW - 1) / NW + 31) & ~31;
+    const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
+    const unsigned below = (1u << lane) - 1u;
+    int g = 0, e = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
+        g += __popc(__ballot_sync(FULL_MASK, i + lane < i1 && k > t));
+        e += __popc(__ballot_sync(FULL_MASK, i + lane < i1 && k == t));
+    }
+    if (lane == 0) {
+        s.gt[warp] = g;
+        s.eq[warp] = e;
+    }
+    __syncthreads();
+    g = e = 0;
+    for (int w = 0; w < warp; ++w) {
+        g += s.gt[w];
+        e += s.eq[w];
+    }
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
+        const bool gt = i + lane < i1 && k > t, eq = i + lane < i1 && k == t;
+        const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
+        const int rg = g + __popc(mg & below), re = e + __popc(me & below);
+        if (gt || (eq && re < left)) {
+            const int at = rg + min(re, left);
+            sel[at] = i + lane;
+            phys[at] = __ldg(row + i + lane);
         }
-        base_gt += tg;
-        base_eq += te;
+        g += __popc(mg);
+        e += __popc(me);
     }
 }
 
-// The same for more keys than registers hold: the keys are read again for
-// every bit.
-__device__ __forceinline__ void pick_many(const SelectArgs &a, const volatile uint32_t *keys,
-                                          int n, int want, int32_t *sel, int32_t *phys,
-                                          const int32_t *row, int *scratch)
+// The largest over the G heads of s[g] summed over the LPB lanes of a block.
+// While a lane holds several heads, each level of the sum halves them (the
+// lane whose mask bit is set keeps the upper half); the remaining levels add.
+template <int G, int LPB>
+__device__ __forceinline__ int sum_heads(int (&s)[G], int lane)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t t = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t cand = t | (1u << bit);
-        int c = 0;
-#pragma unroll 4
-        for (int i = tid; i < n; i += NT)
-            c += keys[i] >= cand;
-        if (block_sum(c, scratch) >= want)
-            t = cand;
-    }
-    int above = 0;
-#pragma unroll 4
-    for (int i = tid; i < n; i += NT)
-        above += keys[i] > t;
-    const int ties = want - block_sum(above, scratch);
-    int base_gt = 0, base_eq = 0;
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += NT) {
-        const int i = i0 + tid;
-        const uint32_t kj = i < n ? keys[i] : 0u;
-        const bool gt = i < n && kj > t, eq = i < n && kj == t;
-        const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
-        __syncthreads();
-        if (lane == 0)
-            scratch[warp] = __popc(mg) | (__popc(me) << 16);
-        __syncthreads();
-        int bg = 0, be = 0;
-        for (int w = 0; w < NW; ++w) {
-            const int v = scratch[w];
-            if (w < warp) {
-                bg += v & 0xffff;
-                be += v >> 16;
-            }
-        }
-        const unsigned below = (1u << lane) - 1u;
-        const int rg = base_gt + bg + __popc(mg & below), re = base_eq + be + __popc(me & below);
-        if (gt || (eq && re < ties)) {
-            const int at = rg + min(re, ties);
-            sel[at] = i;
-            phys[at] = __ldg(row + i);
-        }
-        for (int w = 0; w < NW; ++w) {
-            base_gt += scratch[w] & 0xffff;
-            base_eq += scratch[w] >> 16;
+    int mask = LPB / 2;
+#pragma unroll
+    for (int h = G / 2; h >= 1; h >>= 1, mask >>= 1) {
+        const bool up = (lane & mask) != 0;
+#pragma unroll
+        for (int g = 0; g < h; ++g) {
+            const int send = up ? s[g] : s[g + h], keep = up ? s[g + h] : s[g];
+            s[g] = keep + __shfl_xor_sync(FULL_MASK, send, mask);
         }
     }
+    const int below = mask;
+#pragma unroll
+    for (; mask >= 1; mask >>= 1)
+        s[0] += __shfl_xor_sync(FULL_MASK, s[0], mask);
+    int best = s[0];
+#pragma unroll
+    for (int m = LPB / 2; m > below; m >>= 1)
+        best = max(best, __shfl_xor_sync(FULL_MASK, best, m));
+    return best;
 }
 
 template <int D, int G>
@@ -205,10 +219,10 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
 {
     constexpr int LPB = 2 * D / 16;          // lanes that read one block's bounds
     constexpr int BPW = 32 / LPB;            // blocks a warp reads at once
-    __shared__ __align__(16) int8_t s_q[2][G][D];   // negative parts, positive parts
+    extern __shared__ uint32_t s_keys[];
     __shared__ int s_part[32 * NW];          // a warp's 32 block sums
-    __shared__ int scratch[NW + 1];
-    __shared__ float s_max[NW];
+    __shared__ Pick s_pick;
+    __shared__ int s_last;
     grid_dependency_wait();
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -242,45 +256,57 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
     if (a.budget == 1)
         return;
 
-    // ---- the group's query values in whole steps of 2^eq
-    const uint16_t *qsrc =
-        static_cast<const uint16_t *>(a.q) + ((int64_t)b * H + kvh) * G * D;
-    auto q_at = [&](int i) {
-        const uint16_t w = __ldg(qsrc + i);
-        return a.q_dtype == PKV_BF16 ? bf16lo(w) : __half2float(__ushort_as_half(w));
-    };
-    float amax = 0.0f;
-    for (int i = tid; i < G * D; i += NT)
-        amax = fmaxf(amax, fabsf(q_at(i)));
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, m));
-    if (lane == 0)
-        s_max[warp] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-        amax = fmaxf(amax, s_max[w]);
-    const float f = pow2_f32(-int8_exponent(amax));
-    for (int i = tid; i < G * D; i += NT) {
-        const int v = max(-127, min(127, __float2int_rn(q_at(i) * f)));
-        s_q[0][i / D][i % D] = (int8_t)min(v, 0);
-        s_q[1][i / D][i % D] = (int8_t)max(v, 0);
-    }
-    __syncthreads();
-    // the lane's 16 channels of the lower (first half of the lanes) or upper bounds
+    // ---- the group's query values in whole steps of 2^eq: the lane's 16
+    // channels, negative parts for the lanes of the lower bounds, positive for
+    // the upper
     const int c = lane % LPB, sub = lane / LPB;
+    const bool upper = c >= LPB / 2;
     int qr[G][4];
+    {
+        const uint4 *qsrc = reinterpret_cast<const uint4 *>(
+            static_cast<const uint16_t *>(a.q) + ((int64_t)b * H + kvh) * G * D +
+            (c % (LPB / 2)) * 16);
+        uint32_t raw[G][8];
+        float amax = 0.0f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int4 w = *reinterpret_cast<const int4 *>(
-            &s_q[c / (LPB / 2)][g][(c % (LPB / 2)) * 16]);
-        qr[g][0] = w.x; qr[g][1] = w.y; qr[g][2] = w.z; qr[g][3] = w.w;
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 x = __ldg(qsrc + g * (D / 8) + h);
+                raw[g][4 * h] = x.x; raw[g][4 * h + 1] = x.y;
+                raw[g][4 * h + 2] = x.z; raw[g][4 * h + 3] = x.w;
+            }
+        auto pair = [&](uint32_t w) {
+            return a.q_dtype == PKV_BF16 ? make_float2(bf16lo(w), bf16hi(w)) : half2_to_float2(w);
+        };
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 x = pair(raw[g][i]);
+                amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, m));
+        const float f = pow2_f32(-int8_exponent(amax));
+        auto step = [&](float x) {
+            const int v = max(-127, min(127, __float2int_rn(x * f)));
+            return (upper ? max(v, 0) : min(v, 0)) & 0xff;
+        };
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = pair(raw[g][2 * i]), y = pair(raw[g][2 * i + 1]);
+                qr[g][i] = step(x.x) | step(x.y) << 8 | step(y.x) << 16 | step(y.y) << 24;
+            }
     }
 
     // ---- scores of this CTA's blocks (the newest one is not scored): 32
     // blocks a warp at a time
     uint32_t *keys = a.keys + (int64_t)seg * a.max_n;
+    const int parts = (n + a.chunk - 1) / a.chunk;
     const int j_end = min(n - 1, j_begin + a.chunk);
     for (int j0 = j_begin + warp * 32; j0 < j_end; j0 += NW * 32) {
         const int j = j0 + lane;
@@ -291,7 +317,8 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
             id = 0;
         }
         const int e = __ldg(a.exps + (int64_t)id * H + kvh);
-        constexpr int STEP = 4;              // blocks' loads in flight: STEP * BPW
+        constexpr int STEP = 8;              // loads of a lane in flight
+        static_assert(LPB % STEP == 0, "whole steps");
 #pragma unroll 1
         for (int u0 = 0; u0 < LPB; u0 += STEP) {
             uint4 x[STEP];
@@ -303,7 +330,6 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
             }
 #pragma unroll
             for (int u = 0; u < STEP; ++u) {
-                int best = INT_MIN;
                 int s[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
@@ -312,13 +338,9 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
                     v = __dp4a((int)x[u].z, qr[g][2], v);
                     s[g] = __dp4a((int)x[u].w, qr[g][3], v);
                 }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-#pragma unroll
-                    for (int m = LPB / 2; m >= 1; m >>= 1)
-                        s[g] += __shfl_xor_sync(FULL_MASK, s[g], m);
-                    best = max(best, s[g]);
-                }
+                // sums over the block's lanes: halving the heads a lane keeps
+                // at each level until one is left, then its largest head
+                int best = sum_heads<G, LPB>(s, lane);
                 if (c == 0)
                     s_part[warp * 32 + (u0 + u) * BPW + sub] = best;
             }
@@ -326,34 +348,38 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
         __syncwarp();
         if (j < j_end) {
             const int ec = min(max(e, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
-            keys[j] = ok ? sort_key((float)s_part[warp * 32 + lane] * pow2_f32(ec)) : 0u;
+            const uint32_t k = ok ? sort_key((float)s_part[warp * 32 + lane] * pow2_f32(ec)) : 0u;
+            if (parts == 1 && a.stage)
+                s_keys[j] = k;
+            else
+                keys[j] = k;
         }
         __syncwarp();
     }
 
     // ---- the last CTA of this (sequence, KV head) chooses
-    const int parts = (n + a.chunk - 1) / a.chunk;
     __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        const int old = parts > 1 ? atomicAdd(a.counters + seg, 1) : 0;
-        scratch[NW] = old == parts - 1;
-        if (old == parts - 1 && parts > 1)
-            a.counters[seg] = 0;
-        __threadfence();
+    if (parts > 1) {
+        if (tid == 0) {
+            __threadfence();
+            const int old = atomicAdd(a.counters + seg, 1);
+            s_last = old == parts - 1;
+            if (old == parts - 1) {
+                a.counters[seg] = 0;
+                __threadfence();
+            }
+        }
+        __syncthreads();
+        if (!s_last)
+            return;
+        if (a.stage) {
+#pragma unroll 4
+            for (int i = tid; i < n - 1; i += NT)
+                s_keys[i] = __ldcg(keys + i);
+            __syncthreads();
+        }
     }
-    __syncthreads();
-    if (!scratch[NW])
-        return;
-    const int m = n - 1, want = a.budget - 1;
-    if (m <= 4 * NT)
-        pick<4>(a, keys, m, want, sel, phys, row, scratch);
-    else if (m <= 8 * NT)
-        pick<8>(a, keys, m, want, sel, phys, row, scratch);
-    else if (m <= MAX_KEYS * NT)
-        pick<MAX_KEYS>(a, keys, m, want, sel, phys, row, scratch);
-    else
-        pick_many(a, keys, m, want, sel, phys, row, scratch);
+    pick(a.stage ? s_keys : keys, n - 1, a.budget - 1, sel, phys, row, s_pick);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -375,14 +401,26 @@ Regions regions(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_le
     return r;
 }
 
+template <int D, int G>
+cudaError_t launch_select_t(const SelectArgs &a, unsigned grid, size_t smem, cudaStream_t s)
+{
+    if (smem > 40000) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            select_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_pdl(select_kernel<D, G>, dim3(grid), dim3(NT), smem, s, a);
+}
+
 template <int D>
-cudaError_t launch_select(const SelectArgs &a, int G, unsigned grid, cudaStream_t s)
+cudaError_t launch_select(const SelectArgs &a, int G, unsigned grid, size_t smem, cudaStream_t s)
 {
     switch (G) {
-    case 1: return launch_pdl(select_kernel<D, 1>, dim3(grid), dim3(NT), 0, s, a);
-    case 2: return launch_pdl(select_kernel<D, 2>, dim3(grid), dim3(NT), 0, s, a);
-    case 4: return launch_pdl(select_kernel<D, 4>, dim3(grid), dim3(NT), 0, s, a);
-    default: return launch_pdl(select_kernel<D, 8>, dim3(grid), dim3(NT), 0, s, a);
+    case 1: return launch_select_t<D, 1>(a, grid, smem, s);
+    case 2: return launch_select_t<D, 2>(a, grid, smem, s);
+    case 4: return launch_select_t<D, 4>(a, grid, smem, s);
+    default: return launch_select_t<D, 8>(a, grid, smem, s);
     }
 }
 
@@ -426,12 +464,14 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     a.max_n = (int)((max_seq_len + (int64_t)bs - 1) / bs);
     a.budget = budget;
     a.q_dtype = q_dtype;
-    // a CTA's chunk: whole warps' groups of 32 blocks, a few CTAs a SM over the batch
+    // a CTA's chunk: whole groups of 32 blocks for its warps, four CTAs a SM over the batch
     const int64_t segs = (int64_t)batch * H, n = (cap + bs - 1) / bs;
     const int64_t per = (segs * n + (int64_t)pool->num_sms * 4 - 1) / ((int64_t)pool->num_sms * 4);
     const int64_t span = 32 * NW;
     a.chunk = (int)std::max<int64_t>(span, (per + span - 1) / span * span);
     a.chunks = (int)std::max<int64_t>(1, (n + a.chunk - 1) / a.chunk);
+    a.stage = n <= SMEM_KEYS;
+    const size_t smem = a.stage ? (size_t)n * 4 : 0;
     const int64_t tiles_a_head =
         (std::min<int64_t>(cap, (int64_t)budget * bs) + blk::TILE - 1) / blk::TILE;
     const int64_t max_tiles = segs * tiles_a_head;
@@ -440,8 +480,8 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(segs * a.chunks);
     const int G = num_q_heads / H;
-    const cudaError_t e = pool->head_dim == 64 ? launch_select<64>(a, G, grid, s)
-                                               : launch_select<128>(a, G, grid, s);
+    const cudaError_t e = pool->head_dim == 64 ? launch_select<64>(a, G, grid, smem, s)
+                                               : launch_select<128>(a, G, grid, smem, s);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess)
         return PKV_ERR_CUDA;
     blk::Params p = block_params(pool, q, q_dtype, num_q_heads, k_cache, v_cache, k_scales,
