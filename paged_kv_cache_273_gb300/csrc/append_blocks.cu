@@ -41,18 +41,100 @@ __device__ __forceinline__ float warp_max(float x)
     return x;
 }
 
-// E consecutive input values of a row, raw, and as floats.
-template <typename T, int E>
-struct alignas(sizeof(T) * E) Raw {
-    T v[E];
+// 16 bytes of a row: 8 (16-bit types) or 4 (fp32) consecutive values.
+template <typename T>
+struct Row16;
+
+// 16-bit types two to a word, minima and maxima on the packed pairs.
+template <typename T2, bool BF>
+struct Row16Pairs {
+    static constexpr int N = 8;
+    uint4 w;
+    __device__ __forceinline__ static T2 as(uint32_t x) { return *reinterpret_cast<T2 *>(&x); }
+    __device__ __forceinline__ static uint32_t bits(T2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+    __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) { return bits(__hmax2(as(a), as(b))); }
+    __device__ __forceinline__ static uint32_t min2(uint32_t a, uint32_t b) { return bits(__hmin2(as(a), as(b))); }
+    __device__ __forceinline__ static float2 pair(uint32_t x)
+    {
+        return BF ? make_float2(bf16lo(x), bf16hi(x)) : half2_to_float2(x);
+    }
+    __device__ __forceinline__ float amax() const
+    {
+        const uint32_t m = max2(max2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                max2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        const float2 f = pair(m);
+        return fmaxf(f.x, f.y);
+    }
+    __device__ __forceinline__ void lower(const Row16Pairs &o)
+    {
+        w = make_uint4(min2(w.x, o.w.x), min2(w.y, o.w.y), min2(w.z, o.w.z), min2(w.w, o.w.w));
+    }
+    __device__ __forceinline__ void raise(const Row16Pairs &o)
+    {
+        w = make_uint4(max2(w.x, o.w.x), max2(w.y, o.w.y), max2(w.z, o.w.z), max2(w.w, o.w.w));
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const
+    {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = pair(v[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
+template <> struct Row16<__half> : Row16Pairs<__half2, false> {};
+template <> struct Row16<__nv_bfloat16> : Row16Pairs<__nv_bfloat162, true> {};
+
+template <>
+struct Row16<float> {
+    static constexpr int N = 4;
+    uint4 w;
+    __device__ __forceinline__ void get(float (&x)[N]) const
+    {
+        x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+    }
+    __device__ __forceinline__ float amax() const
+    {
+        float x[4];
+        get(x);
+        return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    }
+    __device__ __forceinline__ static uint32_t lo(uint32_t a, uint32_t b)
+    {
+        return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    __device__ __forceinline__ static uint32_t hi(uint32_t a, uint32_t b)
+    {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    __device__ __forceinline__ void lower(const Row16 &o)
+    {
+        w = make_uint4(lo(w.x, o.w.x), lo(w.y, o.w.y), lo(w.z, o.w.z), lo(w.w, o.w.w));
+    }
+    __device__ __forceinline__ void raise(const Row16 &o)
+    {
+        w = make_uint4(hi(w.x, o.w.x), hi(w.y, o.w.y), hi(w.z, o.w.z), hi(w.w, o.w.w));
+    }
 };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ uint4 shfl_xor4(uint4 x, int m)
+{
+    return make_uint4(__shfl_xor_sync(FULL_MASK, x.x, m), __shfl_xor_sync(FULL_MASK, x.y, m),
+                      __shfl_xor_sync(FULL_MASK, x.z, m), __shfl_xor_sync(FULL_MASK, x.w, m));
+}
 
-// Rows of a run that are held in registers at once.
-constexpr int ROWS = 16;
+// How a warp reads rows: LPR lanes a row, 16 bytes each, RPI rows at once;
+// NR such reads hold the 16 rows that stay in registers.
+template <typename T, int D>
+struct Rows {
+    static constexpr int LPR = D * (int)sizeof(T) / 16;
+    static constexpr int RPI = 32 / LPR;
+    static constexpr int ROWS = 16;
+    static constexpr int NR = ROWS / RPI;
+};
 
 // For every run that starts at a token of [t0, t0 + C) (C <= 32), in order:
 // f(first token, block, first offset in the block, rows).  All lanes call f
@@ -94,213 +176,215 @@ __device__ __forceinline__ void for_runs(const int32_t *slots, int64_t t0, int C
 }
 
 // One warp per (chunk of C tokens, K or V, head).
-template <typename T, int E>
-__global__ void __launch_bounds__(256) append_f8_kernel(
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) append_f8_kernel(
     const T *__restrict__ k_new, const T *__restrict__ v_new, const int32_t *__restrict__ slots,
     int64_t num_tokens, int C, int num_kv_heads, int block_size, int64_t num_slots,
     uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache, float *__restrict__ k_scales,
     float *__restrict__ v_scales, unsigned int *__restrict__ err)
 {
-    constexpr int D = 32 * E;
-    using R = Raw<T, E>;
+    using A = Rows<T, D>;
+    using X = Row16<T>;
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31;
+    const int r0 = lane / A::LPR, c = lane % A::LPR;
     const int H = num_kv_heads;
     const int64_t chunks = (num_tokens + C - 1) / C;
-    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < chunks * 2 * H;
-         w += nwarps) {
-        const int64_t chunk = w / (2 * H);
-        const int r = (int)(w - chunk * 2 * H);
-        const bool is_v = r >= H;
-        const int h = is_v ? r - H : r;
-        const T *src = (is_v ? v_new : k_new);
-        uint8_t *cache = is_v ? v_cache : k_cache;
-        float *scales = is_v ? v_scales : k_scales;
-        auto encode = [&](const float (&x)[E], uint8_t *dst) {
-            uint32_t word = f8_pack(x[0], x[1]);
-            if constexpr (E == 4) {
-                word |= (uint32_t)f8_pack(x[2], x[3]) << 16;
-                *reinterpret_cast<uint32_t *>(dst) = word;
+    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t chunk = w / (2 * H);
+    if (chunk >= chunks)
+        return;
+    const int r = (int)(w - chunk * 2 * H);
+    const bool is_v = r >= H;
+    const int h = is_v ? r - H : r;
+    const T *src = is_v ? v_new : k_new;
+    uint8_t *cache = is_v ? v_cache : k_cache;
+    float *scales = is_v ? v_scales : k_scales;
+    for_runs(slots, chunk * C, C, num_tokens, block_size, num_slots, r == 0, err,
+             [&](int64_t t, int blk, int off, int n) {
+        const uint4 *in = reinterpret_cast<const uint4 *>(src + (t * H + h) * D) + c;
+        const int64_t step = (int64_t)H * A::LPR;          // uint4s from row to row
+        const int64_t head = (int64_t)blk * H + h;
+        uint8_t *rows = cache + head * block_size * D;
+        const int e_old = off > 0 ? block_exponent(scales[head]) : BLOCK_MIN_EXP;
+        X x[A::NR];
+        float amax = 0.0f;
+        // the largest magnitude of the run; its first rows stay in x
+        for (int k0 = n > A::ROWS ? (n - 1) / A::ROWS * A::ROWS : 0; k0 >= 0; k0 -= A::ROWS) {
+#pragma unroll
+            for (int i = 0; i < A::NR; ++i) {
+                const int k = k0 + i * A::RPI + r0;
+                x[i].w = k < n ? __ldg(in + k * step) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < A::NR; ++i)
+                amax = fmaxf(amax, x[i].amax());
+        }
+        int e = code_exponent(warp_max(amax));
+        if (off > 0) {
+            if (e > e_old) {
+                // the block's older rows at its new scale, 16 codes a lane
+                const float f = pow2_f32(max(e_old - e, -126));
+                uint4 *p = reinterpret_cast<uint4 *>(rows);
+                for (int i = lane; i < off * (D / 16); i += 32) {
+                    const uint4 old = p[i];
+                    uint32_t v[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float y[4];
+                        f8_unpack(v[u] & 0xffffu, y[0], y[1]);
+                        f8_unpack(v[u] >> 16, y[2], y[3]);
+                        v[u] = f8_pack(y[0] * f, y[1] * f) | f8_pack(y[2] * f, y[3] * f) << 16;
+                    }
+                    p[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
             } else {
-                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)word;
+                e = e_old;
             }
-        };
-        for_runs(slots, chunk * C, C, num_tokens, block_size, num_slots, r == 0, err,
-                 [&](int64_t t, int blk, int off, int n) {
-            const R *in = reinterpret_cast<const R *>(src + (t * H + h) * D) + lane;
-            const int64_t step = (int64_t)H * 32;              // R's from row to row
-            const int64_t head = (int64_t)blk * H + h;
-            uint8_t *rows = cache + head * block_size * D + lane * E;
-            R x[ROWS];
-            float amax = 0.0f;
-            // the largest magnitude of the run; its first ROWS rows stay in x
-            for (int k0 = n > ROWS ? (n - 1) / ROWS * ROWS : 0; k0 >= 0; k0 -= ROWS) {
+        }
+        __syncwarp();                                      // every lane has read the scale
+        if (lane == 0)
+            scales[head] = pow2_f32(e);
+        const float f = pow2_f32(-e);
+        for (int k0 = 0; k0 < n; k0 += A::ROWS) {
+            if (k0 > 0) {
 #pragma unroll
-                for (int k = 0; k < ROWS; ++k)
-                    if (k0 + k < n)
-                        x[k] = in[(k0 + k) * step];
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k)
-                    if (k0 + k < n)
-#pragma unroll
-                        for (int u = 0; u < E; ++u)
-                            amax = fmaxf(amax, fabsf(to_f(x[k].v[u])));
-            }
-            int e = code_exponent(warp_max(amax));
-            if (off > 0) {
-                const int e_old = block_exponent(scales[head]);
-                if (e > e_old) {
-                    // the block's older rows at its new scale
-                    const float f = pow2_f32(max(e_old - e, -126));
-                    for (int k = 0; k < off; ++k) {
-                        uint8_t *p = rows + k * D;
-                        float y[E];
-                        if constexpr (E == 4) {
-                            const uint32_t word = *reinterpret_cast<const uint32_t *>(p);
-                            f8_unpack(word & 0xffffu, y[0], y[1]);
-                            f8_unpack(word >> 16, y[2], y[3]);
-                        } else {
-                            f8_unpack(*reinterpret_cast<const uint16_t *>(p), y[0], y[1]);
-                        }
-#pragma unroll
-                        for (int u = 0; u < E; ++u)
-                            y[u] *= f;
-                        encode(y, p);
-                    }
-                } else {
-                    e = e_old;
+                for (int i = 0; i < A::NR; ++i) {
+                    const int k = k0 + i * A::RPI + r0;
+                    if (k < n)
+                        x[i].w = __ldg(in + k * step);
                 }
             }
-            __syncwarp();                                      // every lane has read the scale
-            if (lane == 0)
-                scales[head] = pow2_f32(e);
-            const float f = pow2_f32(-e);
-            for (int k0 = 0; k0 < n; k0 += ROWS) {
-                if (k0 > 0) {
 #pragma unroll
-                    for (int k = 0; k < ROWS; ++k)
-                        if (k0 + k < n)
-                            x[k] = in[(k0 + k) * step];
+            for (int i = 0; i < A::NR; ++i) {
+                const int k = k0 + i * A::RPI + r0;
+                if (k < n) {
+                    float y[X::N];
+                    x[i].get(y);
+                    uint32_t v[X::N / 4];
+#pragma unroll
+                    for (int u = 0; u < X::N / 4; ++u)
+                        v[u] = f8_pack(y[4 * u] * f, y[4 * u + 1] * f) |
+                               f8_pack(y[4 * u + 2] * f, y[4 * u + 3] * f) << 16;
+                    uint8_t *dst = rows + (off + k) * D + c * X::N;
+                    if constexpr (X::N == 8)
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(v[0], v[1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(dst) = v[0];
                 }
-#pragma unroll
-                for (int k = 0; k < ROWS; ++k)
-                    if (k0 + k < n) {
-                        float y[E];
-#pragma unroll
-                        for (int u = 0; u < E; ++u)
-                            y[u] = to_f(x[k].v[u]) * f;
-                        encode(y, rows + (off + k0 + k) * D);
-                    }
             }
-        });
-    }
+        }
+    });
 }
 
 // One warp per (chunk of C tokens, head).  bounds [NB][Hkv][2][D]: the
 // minima rounded down, then the maxima rounded up, in units of 2^exps.
-template <typename T, int E>
+template <typename T, int D>
 __global__ void __launch_bounds__(256) append_bounds_kernel(
     const T *__restrict__ k_new, const int32_t *__restrict__ slots, int64_t num_tokens, int C,
     int num_kv_heads, int block_size, int64_t num_slots, int8_t *__restrict__ bounds,
     int32_t *__restrict__ exps, unsigned int *__restrict__ err)
 {
-    constexpr int D = 32 * E;
-    using R = Raw<T, E>;
-    using C8 = Raw<int8_t, E>;
+    using A = Rows<T, D>;
+    using X = Row16<T>;
     grid_dependency_wait();
     grid_dependents_launch();
     const int lane = threadIdx.x & 31;
+    const int r0 = lane / A::LPR, c = lane % A::LPR;
     const int H = num_kv_heads;
     const int64_t chunks = (num_tokens + C - 1) / C;
-    const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < chunks * H;
-         w += nwarps) {
-        const int64_t chunk = w / H;
-        const int h = (int)(w - chunk * H);
-        for_runs(slots, chunk * C, C, num_tokens, block_size, num_slots, h == 0, err,
-                 [&](int64_t t, int blk, int off, int n) {
-            const R *in = reinterpret_cast<const R *>(k_new + (t * H + h) * D) + lane;
-            const int64_t step = (int64_t)H * 32;
-            const int64_t head = (int64_t)blk * H + h;
-            C8 *lo_p = reinterpret_cast<C8 *>(bounds + head * 2 * D) + lane;
-            C8 *hi_p = lo_p + 32;
-            float lo[E], hi[E];
+    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t chunk = w / H;
+    if (chunk >= chunks)
+        return;
+    const int h = (int)(w - chunk * H);
+    for_runs(slots, chunk * C, C, num_tokens, block_size, num_slots, h == 0, err,
+             [&](int64_t t, int blk, int off, int n) {
+        const uint4 *in = reinterpret_cast<const uint4 *>(k_new + (t * H + h) * D) + c;
+        const int64_t step = (int64_t)H * A::LPR;
+        const int64_t head = (int64_t)blk * H + h;
+        // a lane group's bounds: N channels, r0 picks the lower or the upper ones
+        int8_t *mine = bounds + (head * 2) * D + c * X::N;
+        int e_old = 0;
+        if (off > 0)
+            e_old = min(max(exps[head], BLOCK_MIN_EXP), BLOCK_MAX_EXP);
+        X lo, hi;
+        for (int k0 = 0; k0 < n; k0 += A::ROWS) {
+            X x[A::NR];
 #pragma unroll
-            for (int u = 0; u < E; ++u) {
-                lo[u] = INFINITY;
-                hi[u] = -INFINITY;
+            for (int i = 0; i < A::NR; ++i)
+                // (past the run's end its last row again: loads that no test holds back)
+                x[i].w = __ldg(in + min(k0 + i * A::RPI + r0, n - 1) * step);
+            if (k0 == 0)
+                lo = hi = x[0];
+#pragma unroll
+            for (int i = 0; i < A::NR; ++i) {
+                lo.lower(x[i]);
+                hi.raise(x[i]);
             }
-            for (int k0 = 0; k0 < n; k0 += 8) {
-                R x[8];
+        }
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k0 + k < n)
-                        x[k] = in[(k0 + k) * step];
+        for (int m = A::LPR; m < 32; m <<= 1) {
+            X l, u;
+            l.w = shfl_xor4(lo.w, m);
+            u.w = shfl_xor4(hi.w, m);
+            lo.lower(l);
+            hi.raise(u);
+        }
+        int e = int8_exponent(warp_max(fmaxf(lo.amax(), hi.amax())));
+        if (off > 0)
+            e = max(e, e_old);
+        __syncwarp();
+        if (lane == 0)
+            exps[head] = e;
+        if (r0 != 0)
+            return;
+        const float f = pow2_f32(-e);
+        float l[X::N], u[X::N];
+        lo.get(l);
+        hi.get(u);
+        int il[X::N], iu[X::N];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k0 + k < n)
+        for (int i = 0; i < X::N; ++i) {
+            il[i] = __float2int_rd(l[i] * f);
+            iu[i] = __float2int_ru(u[i] * f);
+        }
+        if (off > 0) {
+            const int down = min(e - e_old, 31);
 #pragma unroll
-                        for (int u = 0; u < E; ++u) {
-                            const float y = to_f(x[k].v[u]);
-                            lo[u] = fminf(lo[u], y);
-                            hi[u] = fmaxf(hi[u], y);
-                        }
-            }
-            float amax = 0.0f;
+            for (int q = 0; q < X::N / 4; ++q) {
+                const uint32_t wl = reinterpret_cast<const uint32_t *>(mine)[q];
+                const uint32_t wu = reinterpret_cast<const uint32_t *>(mine + D)[q];
 #pragma unroll
-            for (int u = 0; u < E; ++u)
-                amax = fmaxf(amax, fmaxf(fabsf(lo[u]), fabsf(hi[u])));
-            int e = int8_exponent(warp_max(amax));
-            int e_old = e;
-            if (off > 0) {
-                e_old = min(max(exps[head], BLOCK_MIN_EXP), BLOCK_MAX_EXP);
-                e = max(e, e_old);
-            }
-            __syncwarp();
-            if (lane == 0)
-                exps[head] = e;
-            const float f = pow2_f32(-e);
-            C8 l8, h8;
-            int il[E], ih[E];
-#pragma unroll
-            for (int u = 0; u < E; ++u) {
-                il[u] = __float2int_rd(lo[u] * f);
-                ih[u] = __float2int_ru(hi[u] * f);
-            }
-            if (off > 0) {
-                const C8 lw = *lo_p, hw = *hi_p;
-                const int down = min(e - e_old, 31);
-#pragma unroll
-                for (int u = 0; u < E; ++u) {
-                    il[u] = min(il[u], (int)lw.v[u] >> down);
-                    ih[u] = max(ih[u], -((-(int)hw.v[u]) >> down));
+                for (int i = 0; i < 4; ++i) {
+                    const int ol = (int8_t)(wl >> (8 * i)), ou = (int8_t)(wu >> (8 * i));
+                    il[4 * q + i] = min(il[4 * q + i], ol >> down);
+                    iu[4 * q + i] = max(iu[4 * q + i], -((-ou) >> down));
                 }
             }
+        }
 #pragma unroll
-            for (int u = 0; u < E; ++u) {
-                l8.v[u] = (int8_t)max(il[u], -128);
-                h8.v[u] = (int8_t)min(ih[u], 127);
+        for (int q = 0; q < X::N / 4; ++q) {
+            uint32_t wl = 0u, wu = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wl |= (uint32_t)(max(il[4 * q + i], -128) & 0xff) << (8 * i);
+                wu |= (uint32_t)(min(iu[4 * q + i], 127) & 0xff) << (8 * i);
             }
-            *lo_p = l8;
-            *hi_p = h8;
-        });
-    }
+            reinterpret_cast<uint32_t *>(mine)[q] = wl;
+            reinterpret_cast<uint32_t *>(mine + D)[q] = wu;
+        }
+    });
 }
 
 // Tokens a warp looks for runs in: one while that keeps every SM's warps few
 // (a decode step: every token is a run of its own), else 32, so that a bulk
-// write's warps find a whole block's run each and few find none.
+// write's warps find a run or two each and few find none (131k rows of 8 heads:
+// 128 us at 32, 139 at 16).
 int chunk_tokens(int64_t warps_at_one, int num_sms)
 {
     return warps_at_one <= (int64_t)num_sms * 64 ? 1 : 32;
-}
-
-int grid_for(int64_t warps, int num_sms)
-{
-    const int64_t blocks = (warps + 7) / 8, cap = (int64_t)num_sms * 8;
-    return (int)(blocks < 1 ? 1 : blocks > cap ? cap : blocks);
 }
 
 }  // namespace
@@ -312,21 +396,23 @@ int launch_append_f8(const pkv_pool *pool, const void *k_new, const void *v_new,
     const int H = pool->num_kv_heads, bs = pool->block_size;
     const int64_t T = num_tokens, num_slots = (int64_t)pool->num_blocks * bs;
     const int C = chunk_tokens(T * 2 * H, pool->num_sms);
-    const int grid = grid_for((T + C - 1) / C * 2 * H, pool->num_sms);
+    const int64_t grid = ((T + C - 1) / C * 2 * H + 7) / 8;     // 8 warps a CTA
+    if (grid > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define PKV_A8(T_, E)                                                                            \
-    launch_pdl(append_f8_kernel<T_, E>, dim3(grid), dim3(256), 0, s,                              \
+#define PKV_A8(T_, D)                                                                            \
+    launch_pdl(append_f8_kernel<T_, D>, dim3((unsigned)grid), dim3(256), 0, s,                              \
                static_cast<const T_ *>(k_new), static_cast<const T_ *>(v_new), slots, T, C, H,    \
                bs, num_slots, static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache),   \
                static_cast<float *>(k_scales), static_cast<float *>(v_scales), pool->d_err)
     if (pool->head_dim == 128) {
-        if (in_dtype == PKV_F16) PKV_A8(__half, 4);
-        else if (in_dtype == PKV_BF16) PKV_A8(__nv_bfloat16, 4);
-        else PKV_A8(float, 4);
+        if (in_dtype == PKV_F16) PKV_A8(__half, 128);
+        else if (in_dtype == PKV_BF16) PKV_A8(__nv_bfloat16, 128);
+        else PKV_A8(float, 128);
     } else {
-        if (in_dtype == PKV_F16) PKV_A8(__half, 2);
-        else if (in_dtype == PKV_BF16) PKV_A8(__nv_bfloat16, 2);
-        else PKV_A8(float, 2);
+        if (in_dtype == PKV_F16) PKV_A8(__half, 64);
+        else if (in_dtype == PKV_BF16) PKV_A8(__nv_bfloat16, 64);
+        else PKV_A8(float, 64);
     }
 #undef PKV_A8
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -339,20 +425,22 @@ int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_d
     const int H = pool->num_kv_heads, bs = pool->block_size;
     const int64_t T = num_tokens, num_slots = (int64_t)pool->num_blocks * bs;
     const int C = chunk_tokens(T * H, pool->num_sms);
-    const int grid = grid_for((T + C - 1) / C * H, pool->num_sms);
+    const int64_t grid = ((T + C - 1) / C * H + 7) / 8;
+    if (grid > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define PKV_B8(T_, E)                                                                            \
-    launch_pdl(append_bounds_kernel<T_, E>, dim3(grid), dim3(256), 0, s,                          \
+#define PKV_B8(T_, D)                                                                            \
+    launch_pdl(append_bounds_kernel<T_, D>, dim3((unsigned)grid), dim3(256), 0, s,                          \
                static_cast<const T_ *>(k_new), slots, T, C, H, bs, num_slots, bounds, exps,       \
                pool->d_err)
     if (pool->head_dim == 128) {
-        if (in_dtype == PKV_F16) PKV_B8(__half, 4);
-        else if (in_dtype == PKV_BF16) PKV_B8(__nv_bfloat16, 4);
-        else PKV_B8(float, 4);
+        if (in_dtype == PKV_F16) PKV_B8(__half, 128);
+        else if (in_dtype == PKV_BF16) PKV_B8(__nv_bfloat16, 128);
+        else PKV_B8(float, 128);
     } else {
-        if (in_dtype == PKV_F16) PKV_B8(__half, 2);
-        else if (in_dtype == PKV_BF16) PKV_B8(__nv_bfloat16, 2);
-        else PKV_B8(float, 2);
+        if (in_dtype == PKV_F16) PKV_B8(__half, 64);
+        else if (in_dtype == PKV_BF16) PKV_B8(__nv_bfloat16, 64);
+        else PKV_B8(float, 64);
     }
 #undef PKV_B8
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

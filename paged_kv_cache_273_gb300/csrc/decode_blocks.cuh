@@ -49,7 +49,7 @@ constexpr int MAX_BATCH = 4096;
 // that for every warp of the GPU.
 constexpr int MIN_TILES = 2;
 // Tiles a warp takes of a piece that is not worth joining across CTAs.
-constexpr int SHORT_TILES = 16;
+constexpr int SHORT_TILES = 8;
 
 template <int D, int G, int KV>
 struct Cfg {

@@ -11,10 +11,14 @@
 // exact in fp32: which blocks are chosen does not depend on the order of any
 // sum.  2^eq is common to the blocks and left out.
 //
-// Work.  Bounds are read once, 2 D + 4 bytes a (block, KV head), 16 bytes a
-// lane, and multiplied with dp4a; every warp scores whole groups of 32 blocks
-// with its own copy of the query values in registers, so scoring needs no
-// barrier.  The last CTA of a (sequence, KV head) then finds the budget-th
+// Work.  Bounds are read once, 2 D + 4 bytes a (block, KV head).  The scores
+// of 16 blocks and all heads of the group are warp-level MMAs on fp16 (int8
+// values and their sums below 2^24 are exact there; an int8 MMA of this GPU
+// takes 65 clocks to the fp16 one's 8, and dp4a with its sums over lanes made
+// the kernel issue-bound: 18 us of scoring on 16 x 2048 blocks x 8 heads
+// where the bytes take 10).  Every warp scores whole groups of 32 blocks with
+// its own copy of the query values in registers, so scoring needs no barrier.
+// The last CTA of a (sequence, KV head) then finds the budget-th
 // largest score key (an order-preserving map of the score) digit by digit: the
 // keys, staged in shared memory, are counted by 8-bit digits of their
 // distance to the smallest, counted from the top bit that any of them has, so
@@ -41,7 +45,7 @@ using namespace dev;
 
 constexpr int NT = 256;              // threads of a CTA
 constexpr int NW = NT / 32;
-constexpr int SMEM_KEYS = 49152;     // score keys that are staged in shared memory
+constexpr int SMEM_KEYS = 24576;     // score keys that are staged in shared memory, with their ids
 
 struct SelectArgs {
     const void *q;
@@ -57,7 +61,7 @@ struct SelectArgs {
     int batch, num_kv_heads, num_blocks, block_size, bs_log2, max_blocks, len_cap;
     int max_n;                       // blocks of the longest sequence allowed
     int chunk, chunks;               // blocks a CTA scores; CTAs a (sequence, KV head)
-    int stage;                       // shared memory holds a (sequence, KV head)'s keys
+    int stage;                       // keys (and as many ids) staged in shared memory, or 0
     int budget, q_dtype;
 };
 
@@ -69,26 +73,44 @@ __device__ __forceinline__ uint32_t sort_key(float x)
 }
 
 // The `want` largest of n keys (ties: lowest index first), 0 < want < n: their
-// indices, ascending, to sel / phys.  `keys` may be staged or in the workspace.
+// indices, ascending, to sel, their ids to phys.  Keys and ids may be staged, or in
+// the workspace and the block table.
 struct Pick {
     int hist[256];
+    uint32_t cand[NT];                   // the keys that the digits so far leave open
     uint32_t lo[NW], hi[NW];
     int gt[NW], eq[NW];
-    int bin, left;
+    int ncand, left;
+    uint32_t t;
 };
 
-__device__ __forceinline__ void pick(const volatile uint32_t *keys, int n, int want, int32_t *sel,
-                                     int32_t *phys, const int32_t *row, Pick &s)
+template <bool STAGED>
+__device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, int n, int want,
+                                     int32_t *sel, int32_t *phys, Pick &s)
 {
+    constexpr int BATCH = 8;             // keys a thread loads before it uses them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto key = [&](int i) { return STAGED ? keys[i] : __ldcg(keys + i); };
+    // f(key) for every key, in no particular order
+    auto for_keys = [&](auto f) {
+#pragma unroll 1
+        for (int i0 = tid; i0 < n; i0 += NT * BATCH) {
+            uint32_t k[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                k[u] = key(min(i0 + u * NT, n - 1));
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                if (i0 + u * NT < n)
+                    f(k[u]);
+        }
+    };
     // the keys' range
     uint32_t lo = 0xffffffffu, hi = 0u;
-#pragma unroll 4
-    for (int i = tid; i < n; i += NT) {
-        const uint32_t k = keys[i];
+    for_keys([&](uint32_t k) {
         lo = min(lo, k);
         hi = max(hi, k);
-    }
+    });
     lo = __reduce_min_sync(FULL_MASK, lo);
     hi = __reduce_max_sync(FULL_MASK, hi);
     if (lane == 0) {
@@ -102,51 +124,87 @@ __device__ __forceinline__ void pick(const volatile uint32_t *keys, int n, int w
         lo = min(lo, s.lo[w]);
         hi = max(hi, s.hi[w]);
     }
-    // t, relative to lo: the want-th largest key, a digit of up to 8 bits at a
-    // time; `left` of the keys that share t's digits so far are still to take
+    // t, relative to lo: the want-th largest key, by digits of up to 8 bits; `left`
+    // of the keys that share t's digits so far are still to take.  Once no more
+    // than a thread each are open, their ranks among one another say the rest.
     int top = hi > lo ? 32 - __clz(hi - lo) : 0;      // bits not decided yet
     uint32_t t = 0;
-    int left = want;
-    while (top > 0) {
+    int left = want, open = n;
+#pragma unroll 1
+    while (top > 0 && open > NT) {
         const int shift = max(top - 8, 0);
-#pragma unroll 4
-        for (int i = tid; i < n; i += NT) {
-            const uint32_t k = keys[i] - lo;
+        const uint32_t mask = (1u << (top - shift)) - 1u;
+        for_keys([&](uint32_t k) {
+            k -= lo;
             if (top >= 32 || (k >> top) == (t >> top))
-                atomicAdd(&s.hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1);
-        }
+                atomicAdd(&s.hist[(k >> shift) & mask], 1);
+        });
         __syncthreads();
-        if (warp == 0) {
-            // bins from the top: lane l holds bins 255 - 8 l .. 248 - 8 l
-            int c[8], sum = 0;
+        // every warp finds the digit for itself, bins from the top: lane l
+        // holds bins 255 - 8 l .. 248 - 8 l
+        int c[8], sum = 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                c[u] = s.hist[255 - 8 * lane - u];
-                sum += c[u];
-            }
-            int inc = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int x = __shfl_up_sync(FULL_MASK, inc, off);
-                if (lane >= off)
-                    inc += x;
-            }
-            int above = inc - sum;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (above < left && above + c[u] >= left) {
-                    s.bin = 255 - 8 * lane - u;
-                    s.left = left - above;
-                }
-                above += c[u];
-            }
+        for (int u = 0; u < 8; ++u) {
+            c[u] = s.hist[255 - 8 * lane - u];
+            sum += c[u];
         }
-        __syncthreads();
-        t |= (uint32_t)s.bin << shift;
-        left = s.left;
+        int inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(FULL_MASK, inc, off);
+            if (lane >= off)
+                inc += x;
+        }
+        const int l = __ffs(__ballot_sync(FULL_MASK, inc >= left)) - 1;
+        int above = inc - sum, bin = 0, rest = 0, in = 0;
+        bool found = false;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (!found && above + c[u] >= left) {
+                found = true;
+                bin = 255 - 8 * lane - u;
+                rest = left - above;
+                in = c[u];
+            }
+            above += c[u];
+        }
+        t |= (uint32_t)__shfl_sync(FULL_MASK, bin, l) << shift;
+        left = __shfl_sync(FULL_MASK, rest, l);
+        open = __shfl_sync(FULL_MASK, in, l);
         top = shift;
+        __syncthreads();                 // the counts are read
         s.hist[tid] = 0;
         __syncthreads();
+    }
+    if (top > 0) {
+        if (tid == 0)
+            s.ncand = 0;
+        __syncthreads();
+        for_keys([&](uint32_t k) {
+            k -= lo;
+            if (top >= 32 || (k >> top) == (t >> top))
+                s.cand[atomicAdd(&s.ncand, 1)] = k;
+        });
+        __syncthreads();
+        if (tid < open) {
+            // keys above this one, and as large: it is the one sought if the
+            // left-th largest falls among the latter
+            const uint32_t mine = s.cand[tid];
+            int gt = 0, ge = 0;
+#pragma unroll 8
+            for (int i = 0; i < open; ++i) {
+                const uint32_t k = s.cand[i];
+                gt += k > mine;
+                ge += k >= mine;
+            }
+            if (gt < left && left <= ge) {   // (equal keys write the same)
+                s.t = mine;
+                s.left = left - gt;
+            }
+        }
+        __syncthreads();
+        t = s.t;
+        left = s.left;
     }
     t += lo;
     // keys above t, and the first `left` equal ones, in index order: each warp
@@ -154,73 +212,55 @@ __device__ __forceinline__ void pick(const volatile uint32_t *keys, int n, int w
     const int per = ((n + NW - 1) / NW + 31) & ~31;
     const int i0 = min(n, warp * per), i1 = min(n, i0 + per);
     const unsigned below = (1u << lane) - 1u;
+    // f(index, key) for the warp's run, 32 indices at a time in order
+    auto for_run = [&](auto f) {
+#pragma unroll 1
+        for (int i = i0; i < i1; i += 32 * BATCH) {
+            uint32_t k[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                k[u] = key(min(i + 32 * u + lane, i1 - 1));
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+                f(i + 32 * u + lane, k[u]);
+        }
+    };
     int g = 0, e = 0;
-#pragma unroll 4
-    for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
-        g += __popc(__ballot_sync(FULL_MASK, i + lane < i1 && k > t));
-        e += __popc(__ballot_sync(FULL_MASK, i + lane < i1 && k == t));
-    }
+    for_run([&](int i, uint32_t k) {
+        g += __popc(__ballot_sync(FULL_MASK, i < i1 && k > t));
+        e += __popc(__ballot_sync(FULL_MASK, i < i1 && k == t));
+    });
     if (lane == 0) {
         s.gt[warp] = g;
         s.eq[warp] = e;
     }
     __syncthreads();
     g = e = 0;
-    for (int w = 0; w < warp; ++w) {
-        g += s.gt[w];
-        e += s.eq[w];
-    }
-#pragma unroll 1
-    for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
-        const bool gt = i + lane < i1 && k > t, eq = i + lane < i1 && k == t;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        if (w < warp) {
+            g += s.gt[w];
+            e += s.eq[w];
+        }
+    for_run([&](int i, uint32_t k) {
+        const bool gt = i < i1 && k > t, eq = i < i1 && k == t;
         const unsigned mg = __ballot_sync(FULL_MASK, gt), me = __ballot_sync(FULL_MASK, eq);
-        const int rg = g + __popc(mg & below), re = e + __popc(me & below);
+        const int re = e + __popc(me & below);
         if (gt || (eq && re < left)) {
-            const int at = rg + min(re, left);
-            sel[at] = i + lane;
-            phys[at] = __ldg(row + i + lane);
+            const int at = g + __popc(mg & below) + min(re, left);
+            sel[at] = i;
+            phys[at] = ids[i];
         }
         g += __popc(mg);
         e += __popc(me);
-    }
-}
-
-// The largest over the G heads of s[g] summed over the LPB lanes of a block.
-// While a lane holds several heads, each level of the sum halves them (the
-// lane whose mask bit is set keeps the upper half); the remaining levels add.
-template <int G, int LPB>
-__device__ __forceinline__ int sum_heads(int (&s)[G], int lane)
-{
-    int mask = LPB / 2;
-#pragma unroll
-    for (int h = G / 2; h >= 1; h >>= 1, mask >>= 1) {
-        const bool up = (lane & mask) != 0;
-#pragma unroll
-        for (int g = 0; g < h; ++g) {
-            const int send = up ? s[g] : s[g + h], keep = up ? s[g + h] : s[g];
-            s[g] = keep + __shfl_xor_sync(FULL_MASK, send, mask);
-        }
-    }
-    const int below = mask;
-#pragma unroll
-    for (; mask >= 1; mask >>= 1)
-        s[0] += __shfl_xor_sync(FULL_MASK, s[0], mask);
-    int best = s[0];
-#pragma unroll
-    for (int m = LPB / 2; m > below; m >>= 1)
-        best = max(best, __shfl_xor_sync(FULL_MASK, best, m));
-    return best;
+    });
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
+__global__ void __launch_bounds__(NT, 2) select_kernel(const SelectArgs a)
 {
-    constexpr int LPB = 2 * D / 16;          // lanes that read one block's bounds
-    constexpr int BPW = 32 / LPB;            // blocks a warp reads at once
-    extern __shared__ uint32_t s_keys[];
-    __shared__ int s_part[32 * NW];          // a warp's 32 block sums
+    constexpr int NC = D / 32;               // 16-byte chunks a lane reads of a block's bounds
+    extern __shared__ uint32_t s_keys[];     // keys, then (from a.stage on) ids
     __shared__ Pick s_pick;
     __shared__ int s_last;
     grid_dependency_wait();
@@ -256,50 +296,51 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
     if (a.budget == 1)
         return;
 
-    // ---- the group's query values in whole steps of 2^eq: the lane's 16
-    // channels, negative parts for the lanes of the lower bounds, positive for
-    // the upper
-    const int c = lane % LPB, sub = lane / LPB;
-    const bool upper = c >= LPB / 2;
-    int qr[G][4];
+    // ---- the group's query values in whole steps of 2^eq, as B fragments: lane
+    // (gid, tig) holds head gid mod G and the channels of its chunks 4 c + tig of
+    // the bounds: negative parts for the lower bounds (c < NC / 2), positive
+    // parts for the upper ones
+    const int gid = lane >> 2, tig = lane & 3;
+    uint32_t qf[4 * NC][2];
     {
         const uint4 *qsrc = reinterpret_cast<const uint4 *>(
-            static_cast<const uint16_t *>(a.q) + ((int64_t)b * H + kvh) * G * D +
-            (c % (LPB / 2)) * 16);
-        uint32_t raw[G][8];
+            static_cast<const uint16_t *>(a.q) + (((int64_t)b * H + kvh) * G + gid % G) * D) +
+            2 * tig;
+        uint32_t raw[NC / 2][8];
         float amax = 0.0f;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 x = __ldg(qsrc + g * (D / 8) + h);
-                raw[g][4 * h] = x.x; raw[g][4 * h + 1] = x.y;
-                raw[g][4 * h + 2] = x.z; raw[g][4 * h + 3] = x.w;
-            }
         auto pair = [&](uint32_t w) {
             return a.q_dtype == PKV_BF16 ? make_float2(bf16lo(w), bf16hi(w)) : half2_to_float2(w);
         };
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int c = 0; c < NC / 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 x = __ldg(qsrc + 8 * c + h);
+                raw[c][4 * h] = x.x; raw[c][4 * h + 1] = x.y;
+                raw[c][4 * h + 2] = x.z; raw[c][4 * h + 3] = x.w;
+            }
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 x = pair(raw[g][i]);
+                const float2 x = pair(raw[c][i]);
                 amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
             }
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1)
             amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, m));
         const float f = pow2_f32(-int8_exponent(amax));
-        auto step = [&](float x) {
-            const int v = max(-127, min(127, __float2int_rn(x * f)));
-            return (upper ? max(v, 0) : min(v, 0)) & 0xff;
-        };
+        auto step = [&](float x) { return fminf(fmaxf(rintf(x * f), -127.0f), 127.0f); };
+        const __half2 zero = __floats2half2_rn(0.0f, 0.0f);
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int c = 0; c < NC / 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = pair(raw[g][2 * i]), y = pair(raw[g][2 * i + 1]);
-                qr[g][i] = step(x.x) | step(x.y) << 8 | step(y.x) << 16 | step(y.y) << 24;
+            for (int i = 0; i < 8; ++i) {
+                const float2 x = pair(raw[c][i]);
+                const __half2 v = __floats2half2_rn(step(x.x), step(x.y));
+                const __half2 neg = __hmin2(v, zero), pos = __hmax2(v, zero);
+                qf[4 * c + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t *>(&neg);
+                qf[4 * (c + NC / 2) + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t *>(&pos);
             }
     }
 
@@ -308,53 +349,96 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
     uint32_t *keys = a.keys + (int64_t)seg * a.max_n;
     const int parts = (n + a.chunk - 1) / a.chunk;
     const int j_end = min(n - 1, j_begin + a.chunk);
-    for (int j0 = j_begin + warp * 32; j0 < j_end; j0 += NW * 32) {
-        const int j = j0 + lane;
-        int id = j < j_end ? __ldg(row + j) : 0;
-        const bool ok = id >= 0 && id < a.num_blocks;
-        if (!ok) {
-            atomicOr(a.err, PKV_EBIT_BLOCK);
-            id = 0;
+    constexpr int STEP = NW * 32;
+    // the block ids of the lane's block of a group, its exponent, and the
+    // bounds of rows gid, gid + 8 of a 16-block tile (the lane's chunks)
+    auto load_id = [&](int j0) {
+        return j0 + lane < j_end ? __ldg(row + j0 + lane) : 0;
+    };
+    auto valid_id = [&](int id) {
+        if (id >= 0 && id < a.num_blocks)
+            return id;
+        atomicOr(a.err, PKV_EBIT_BLOCK);
+        return 0;
+    };
+    auto load_tile = [&](uint4 (&x)[2][NC], int id, int t) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int id_r = __shfl_sync(FULL_MASK, id, 16 * t + 8 * r + gid);
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                a.bounds + ((int64_t)id_r * H + kvh) * 2 * D) + tig;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                x[r][c] = __ldg(src + 4 * c);
         }
-        const int e = __ldg(a.exps + (int64_t)id * H + kvh);
-        constexpr int STEP = 8;              // loads of a lane in flight
-        static_assert(LPB % STEP == 0, "whole steps");
+    };
+    // a tile's scores: lane l gets that of row l mod 16
+    auto score_tile = [&](const uint4 (&x)[2][NC]) {
+        float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t u[4] = {x[0][c].x, x[0][c].y, x[0][c].z, x[0][c].w};
+            const uint32_t v[4] = {x[1][c].x, x[1][c].y, x[1][c].z, x[1][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t ub = u[i] ^ 0x80808080u, vb = v[i] ^ 0x80808080u;
+                kern::mma_16816<false>(s[i & 1], kern::i8pair_to_half2<0x4140u>(ub),
+                                       kern::i8pair_to_half2<0x4140u>(vb),
+                                       kern::i8pair_to_half2<0x4342u>(ub),
+                                       kern::i8pair_to_half2<0x4342u>(vb), qf[4 * c + i][0],
+                                       qf[4 * c + i][1]);
+            }
+        }
+        // rows gid and gid + 8: the largest over the columns (heads)
+        float m0 = fmaxf(s[0][0] + s[1][0], s[0][1] + s[1][1]);
+        float m1 = fmaxf(s[0][2] + s[1][2], s[0][3] + s[1][3]);
+#pragma unroll
+        for (int m = 1; m < 4; m <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(FULL_MASK, m0, m));
+            m1 = fmaxf(m1, __shfl_xor_sync(FULL_MASK, m1, m));
+        }
+        const float r0 = __shfl_sync(FULL_MASK, m0, 4 * (lane & 7));
+        const float r1 = __shfl_sync(FULL_MASK, m1, 4 * (lane & 7));
+        return lane & 8 ? r1 : r0;
+    };
+    int j0 = j_begin + warp * 32;
+    if (j0 < j_end) {
+        // a tile's bounds are on their way while the one before is scored
+        int raw = load_id(j0), raw_next = load_id(j0 + STEP);
+        int id = valid_id(raw);
+        int e = __ldg(a.exps + (int64_t)id * H + kvh);
+        uint4 x0[2][NC], x1[2][NC];
+        load_tile(x0, id, 0);
 #pragma unroll 1
-        for (int u0 = 0; u0 < LPB; u0 += STEP) {
-            uint4 x[STEP];
-#pragma unroll
-            for (int u = 0; u < STEP; ++u) {
-                const int id_u = __shfl_sync(FULL_MASK, id, (u0 + u) * BPW + sub);
-                x[u] = __ldg(reinterpret_cast<const uint4 *>(
-                                 a.bounds + ((int64_t)id_u * H + kvh) * 2 * D) + c);
+        for (;;) {
+            load_tile(x1, id, 1);
+            const float even = score_tile(x0);
+            const bool ok = raw == id;
+            const int raw_now = raw, e_now = e, j = j0 + lane;
+            j0 += STEP;
+            const bool more = j0 < j_end;
+            if (more) {
+                raw = raw_next;
+                id = valid_id(raw);
+                raw_next = load_id(j0 + STEP);
+                e = __ldg(a.exps + (int64_t)id * H + kvh);
+                load_tile(x0, id, 0);
             }
-#pragma unroll
-            for (int u = 0; u < STEP; ++u) {
-                int s[G];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    int v = __dp4a((int)x[u].x, qr[g][0], 0);
-                    v = __dp4a((int)x[u].y, qr[g][1], v);
-                    v = __dp4a((int)x[u].z, qr[g][2], v);
-                    s[g] = __dp4a((int)x[u].w, qr[g][3], v);
+            const float odd = score_tile(x1);
+            if (j < j_end) {
+                const int ec = min(max(e_now, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
+                const uint32_t k =
+                    ok ? sort_key((lane < 16 ? even : odd) * pow2_f32(ec)) : 0u;
+                if (parts == 1 && a.stage) {
+                    s_keys[j] = k;
+                    s_keys[a.stage + j] = raw_now;
+                } else {
+                    keys[j] = k;
                 }
-                // sums over the block's lanes: halving the heads a lane keeps
-                // at each level until one is left, then its largest head
-                int best = sum_heads<G, LPB>(s, lane);
-                if (c == 0)
-                    s_part[warp * 32 + (u0 + u) * BPW + sub] = best;
             }
+            if (!more)
+                break;
         }
-        __syncwarp();
-        if (j < j_end) {
-            const int ec = min(max(e, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
-            const uint32_t k = ok ? sort_key((float)s_part[warp * 32 + lane] * pow2_f32(ec)) : 0u;
-            if (parts == 1 && a.stage)
-                s_keys[j] = k;
-            else
-                keys[j] = k;
-        }
-        __syncwarp();
     }
 
     // ---- the last CTA of this (sequence, KV head) chooses
@@ -374,12 +458,18 @@ __global__ void __launch_bounds__(NT) select_kernel(const SelectArgs a)
             return;
         if (a.stage) {
 #pragma unroll 4
-            for (int i = tid; i < n - 1; i += NT)
+            for (int i = tid; i < n - 1; i += NT) {
                 s_keys[i] = __ldcg(keys + i);
+                s_keys[a.stage + i] = __ldg(row + i);
+            }
             __syncthreads();
         }
     }
-    pick(a.stage ? s_keys : keys, n - 1, a.budget - 1, sel, phys, row, s_pick);
+    if (a.stage)
+        pick<true>(s_keys, reinterpret_cast<const int32_t *>(s_keys + a.stage), n - 1,
+                   a.budget - 1, sel, phys, s_pick);
+    else
+        pick<false>(keys, row, n - 1, a.budget - 1, sel, phys, s_pick);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -464,14 +554,14 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     a.max_n = (int)((max_seq_len + (int64_t)bs - 1) / bs);
     a.budget = budget;
     a.q_dtype = q_dtype;
-    // a CTA's chunk: whole groups of 32 blocks for its warps, four CTAs a SM over the batch
+    // a CTA's chunk: whole groups of 32 blocks for its warps, two CTAs a SM (as many as are resident)
     const int64_t segs = (int64_t)batch * H, n = (cap + bs - 1) / bs;
-    const int64_t per = (segs * n + (int64_t)pool->num_sms * 4 - 1) / ((int64_t)pool->num_sms * 4);
+    const int64_t per = (segs * n + (int64_t)pool->num_sms * 2 - 1) / ((int64_t)pool->num_sms * 2);
     const int64_t span = 32 * NW;
     a.chunk = (int)std::max<int64_t>(span, (per + span - 1) / span * span);
     a.chunks = (int)std::max<int64_t>(1, (n + a.chunk - 1) / a.chunk);
-    a.stage = n <= SMEM_KEYS;
-    const size_t smem = a.stage ? (size_t)n * 4 : 0;
+    a.stage = n <= SMEM_KEYS ? (int)n : 0;
+    const size_t smem = (size_t)a.stage * 8;
     const int64_t tiles_a_head =
         (std::min<int64_t>(cap, (int64_t)budget * bs) + blk::TILE - 1) / blk::TILE;
     const int64_t max_tiles = segs * tiles_a_head;

@@ -90,6 +90,8 @@ __device__ __forceinline__ bool last_cta(int32_t *ticket)
 {
     __shared__ int last;
     __syncthreads();
+    if (gridDim.x == 1)
+        return true;
     if (threadIdx.x == 0) {
         __threadfence();
         last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
@@ -174,11 +176,8 @@ __global__ void __launch_bounds__(NT) reserve_kernel(TableArgs a, const int32_t 
         }
         return id;
     };
-    for (int k = first; k < NB; k += stride) {
-        const int b = find(s_blk, B, k);
-        const int old = (int)(((long long)a.lens[b] + bs - 1) >> lg);
-        tables[(int64_t)b * a.max_blocks + old + (k - s_blk[b])] = fresh(k);
-    }
+    // (the first new block's id is on its way while the slots are worked out)
+    int id = first < NB ? fresh(first) : 0;
     // four consecutive tokens a thread: one search, then along the batch
     for (int64_t i4 = (int64_t)first * 4; i4 < max_tokens; i4 += (int64_t)stride * 4) {
         int b = i4 < T ? find(s_tok, B, (int)i4) : B;
@@ -194,18 +193,18 @@ __global__ void __launch_bounds__(NT) reserve_kernel(TableArgs a, const int32_t 
                 const int pos = L + (int)(i - s_tok[b]);
                 const int old = (int)(((long long)L + bs - 1) >> lg);
                 const int j = pos >> lg;
-                int id;
+                int blk;
                 if (j >= old) {
-                    id = fresh(s_blk[b] + j - old);
+                    blk = fresh(s_blk[b] + j - old);
                 } else {
-                    id = tables[(int64_t)b * a.max_blocks + j];
-                    if (id < 0 || id >= a.num_blocks) {
+                    blk = tables[(int64_t)b * a.max_blocks + j];
+                    if (blk < 0 || blk >= a.num_blocks) {
                         atomicOr(a.err, PKV_EBIT_BLOCK);
-                        id = -1;
+                        blk = -1;
                     }
                 }
-                if (id >= 0)
-                    v[u] = id * bs + (pos & (bs - 1));
+                if (blk >= 0)
+                    v[u] = blk * bs + (pos & (bs - 1));
             }
         }
         if (i4 + 4 <= max_tokens && (reinterpret_cast<uintptr_t>(slots) & 15u) == 0) {
@@ -216,6 +215,13 @@ __global__ void __launch_bounds__(NT) reserve_kernel(TableArgs a, const int32_t 
                 if (i4 + u < max_tokens)
                     slots[i4 + u] = v[u];
         }
+    }
+    for (int k = first; k < NB; k += stride) {
+        const int b = find(s_blk, B, k);
+        const int old = (int)(((long long)a.lens[b] + bs - 1) >> lg);
+        if (k != first)
+            id = fresh(k);
+        tables[(int64_t)b * a.max_blocks + old + (k - s_blk[b])] = id;
     }
     if (q_start)
         for (int b = first; b <= B; b += stride)
@@ -303,10 +309,13 @@ TableArgs table_args(const pkv_pool *pool, const int32_t *free_in, int32_t *free
     return a;
 }
 
+// CTAs for this many threads' work, at most three a SM (what their shared
+// memory and threads let be resident): a thread then has one or two rounds of
+// dependent loads.
 int grid_for(int64_t items, int num_sms)
 {
-    const int64_t g = (items + NT - 1) / NT;
-    return (int)(g < 1 ? 1 : g > num_sms ? num_sms : g);
+    const int64_t g = (items + NT - 1) / NT, cap = (int64_t)num_sms * 3;
+    return (int)(g < 1 ? 1 : g > cap ? cap : g);
 }
 
 }  // namespace

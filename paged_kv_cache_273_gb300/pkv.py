@@ -73,6 +73,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libpkv.so (built by ``paged_kv_cache_273_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -185,13 +187,20 @@ def _dptr(t: torch.Tensor | None):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# The current stream's handle without building a Stream object (a third of a
+# small call's host time), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 class Pool:
@@ -572,13 +581,28 @@ def paged_decode_step(pool: Pool, host_in, dev_in, layout: StepLayout, in_dtype,
 
 
 # ------------------------------------------------------------- device-resident step
+_I32, _F32, _I8 = torch.int32, torch.float32, torch.int8
+
+
 def _shaped(name: str, t, dtype, shape) -> None:
-    """Raise unless t is a CUDA tensor of this type and shape (None in shape: any size)."""
-    if t.dtype != dtype:
+    """Raise unless t is a tensor of this type and shape (None in shape: any size)."""
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or
+                         any(n is not None and n != m for n, m in zip(shape, got))):
         raise ValueError("%s must have shape %s, got %s"
-                         % (name, ["*" if n is None else n for n in shape], list(t.shape)))
+                         % (name, ["*" if n is None else n for n in shape], list(got)))
+
+
+def _vector(name: str, t) -> None:
+    if t.dtype is not _I32 or t.dim() != 1:
+        _shaped(name, t, _I32, (None,))
+
+
+def _rows(name: str, t, rows: int) -> None:
+    if t.dtype is not _I32 or t.dim() != 2 or t.shape[0] != rows:
+        _shaped(name, t, _I32, (rows, None))
 
 
 def alloc_device_free_list(ids, device="cuda"):
@@ -596,24 +620,27 @@ def kv_device_reserve(pool: Pool, free_ids, free_in, seq_lens, block_tables, slo
     """kv_reserve_slots on the device (see include/pkv.h): the new tokens' blocks off the free
     stack into block_tables, their slots into slot_mapping (-1 behind the last).  free_out and
     seq_lens_out default to free_in and seq_lens, updated in place."""
-    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
-    free_out = free_in if free_out is None else free_out
     B = seq_lens.numel()
-    _shaped("free_ids", free_ids, torch.int32, (None,))
-    _shaped("free_in", free_in, torch.int32, (2,))
-    _shaped("free_out", free_out, torch.int32, (2,))
-    _shaped("seq_lens", seq_lens, torch.int32, (B,))
-    _shaped("seq_lens_out", seq_lens_out, torch.int32, (B,))
-    _shaped("block_tables", block_tables, torch.int32, (B, None))
-    _shaped("slot_mapping", slot_mapping, torch.int32, (None,))
+    row = (B,)
+    _vector("free_ids", free_ids)
+    _shaped("free_in", free_in, _I32, (2,))
+    _shaped("seq_lens", seq_lens, _I32, row)
+    _rows("block_tables", block_tables, B)
+    _vector("slot_mapping", slot_mapping)
     if num_new is not None:
-        _shaped("num_new", num_new, torch.int32, (B,))
+        _shaped("num_new", num_new, _I32, row)
+    if free_out is not None:
+        _shaped("free_out", free_out, _I32, (2,))
+    if seq_lens_out is not None:
+        _shaped("seq_lens_out", seq_lens_out, _I32, row)
     if q_start is not None:
-        _shaped("q_start", q_start, torch.int32, (B + 1,))
+        _shaped("q_start", q_start, _I32, (B + 1,))
+    state, lens = _dptr(free_in), _dptr(seq_lens)
     _check(load().kv_device_reserve(
-        pool.handle, _dptr(free_ids), free_ids.numel(), _dptr(free_in), _dptr(free_out),
-        _dptr(seq_lens), _dptr(num_new), B, _dptr(block_tables), block_tables.shape[1],
-        _dptr(slot_mapping), slot_mapping.numel(), _dptr(q_start), _dptr(seq_lens_out),
+        pool.handle, _dptr(free_ids), free_ids.shape[0], state,
+        state if free_out is None else _dptr(free_out), lens, _dptr(num_new), B,
+        _dptr(block_tables), block_tables.shape[1], _dptr(slot_mapping), slot_mapping.shape[0],
+        _dptr(q_start), lens if seq_lens_out is None else _dptr(seq_lens_out),
         _stream(stream)), "kv_device_reserve")
 
 
@@ -621,20 +648,24 @@ def kv_device_release(pool: Pool, free_ids, free_in, seq_lens, done, block_table
                       seq_lens_out=None, stream=None) -> None:
     """The blocks of the sequences with done[b] != 0 back on the free stack, their lengths to 0
     (see include/pkv.h).  free_out and seq_lens_out default to in place."""
-    seq_lens_out = seq_lens if seq_lens_out is None else seq_lens_out
-    free_out = free_in if free_out is None else free_out
     B = seq_lens.numel()
-    _shaped("free_ids", free_ids, torch.int32, (None,))
-    _shaped("free_in", free_in, torch.int32, (2,))
-    _shaped("free_out", free_out, torch.int32, (2,))
-    _shaped("seq_lens", seq_lens, torch.int32, (B,))
-    _shaped("seq_lens_out", seq_lens_out, torch.int32, (B,))
-    _shaped("done", done, torch.int32, (B,))
-    _shaped("block_tables", block_tables, torch.int32, (B, None))
+    row = (B,)
+    _vector("free_ids", free_ids)
+    _shaped("free_in", free_in, _I32, (2,))
+    _shaped("seq_lens", seq_lens, _I32, row)
+    _shaped("done", done, _I32, row)
+    _rows("block_tables", block_tables, B)
+    if free_out is not None:
+        _shaped("free_out", free_out, _I32, (2,))
+    if seq_lens_out is not None:
+        _shaped("seq_lens_out", seq_lens_out, _I32, row)
+    state, lens = _dptr(free_in), _dptr(seq_lens)
     _check(load().kv_device_release(
-        pool.handle, _dptr(free_ids), free_ids.numel(), _dptr(free_in), _dptr(free_out),
-        _dptr(seq_lens), _dptr(done), B, _dptr(block_tables), block_tables.shape[1],
-        _dptr(seq_lens_out), _stream(stream)), "kv_device_release")
+        pool.handle, _dptr(free_ids), free_ids.shape[0], state,
+        state if free_out is None else _dptr(free_out), lens, _dptr(done), B,
+        _dptr(block_tables), block_tables.shape[1],
+        lens if seq_lens_out is None else _dptr(seq_lens_out), _stream(stream)),
+        "kv_device_release")
 
 
 def alloc_bounds(pool: Pool, device="cuda"):
@@ -650,9 +681,9 @@ def kv_bounds_append(pool: Pool, k_new, slot_mapping, bounds, bound_exps, stream
         raise ValueError("unsupported k_new dtype %s" % k_new.dtype)
     T, head = k_new.shape[0], (pool.num_blocks, pool.num_kv_heads)
     _shaped("k_new", k_new, k_new.dtype, (T, pool.num_kv_heads, pool.head_dim))
-    _shaped("slot_mapping", slot_mapping, torch.int32, (T,))
-    _shaped("bounds", bounds, torch.int8, head + (2, pool.head_dim))
-    _shaped("bound_exps", bound_exps, torch.int32, head)
+    _shaped("slot_mapping", slot_mapping, _I32, (T,))
+    _shaped("bounds", bounds, _I8, head + (2, pool.head_dim))
+    _shaped("bound_exps", bound_exps, _I32, head)
     _check(load().kv_bounds_append(pool.handle, _dptr(k_new), PKV_DTYPE[k_new.dtype],
                                    _dptr(slot_mapping), T, _dptr(bounds), _dptr(bound_exps),
                                    _stream(stream)), "kv_bounds_append")
@@ -685,12 +716,12 @@ def paged_decode_attention_sparse(pool: Pool, q, k_cache, v_cache, bounds, bound
     B, Hq, _ = q.shape
     head = (pool.num_blocks, pool.num_kv_heads)
     _shaped("q", q, q.dtype, (B, Hq, pool.head_dim))
-    _shaped("out", out, torch.float32, (B, Hq, pool.head_dim))
-    _shaped("bounds", bounds, torch.int8, head + (2, pool.head_dim))
-    _shaped("bound_exps", bound_exps, torch.int32, head)
-    _shaped("block_tables", block_tables, torch.int32, (B, None))
-    _shaped("seq_lens", seq_lens, torch.int32, (B,))
-    _shaped("selected", selected, torch.int32, (B, pool.num_kv_heads, None))
+    _shaped("out", out, _F32, (B, Hq, pool.head_dim))
+    _shaped("bounds", bounds, _I8, head + (2, pool.head_dim))
+    _shaped("bound_exps", bound_exps, _I32, head)
+    _rows("block_tables", block_tables, B)
+    _shaped("seq_lens", seq_lens, _I32, (B,))
+    _shaped("selected", selected, _I32, (B, pool.num_kv_heads, None))
     _check(load().paged_decode_attention_sparse(
         pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
         _dptr(k_scales), _dptr(v_scales), _dptr(bounds), _dptr(bound_exps), _dptr(block_tables),
