@@ -95,6 +95,8 @@ struct Params {
     int per_head;                // tables rows are lists of chosen blocks
     int budget;                  // per_head: entries of a list
     int q_dtype;
+    int pieces_each;             // even split: (sequence, KV head)s a CTA, and the CTAs
+    int whole_ctas;
     float scale_log2;
 };
 
@@ -168,6 +170,16 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// x / d of non-negative ints; a fraction of an integer division's latency where
+// both the quotient's distance to the next whole number, at least 1 / (2 d), and
+// fp32's error in it, at most (x / d) 2^-22, leave no doubt: x < 2^20.
+static __device__ __noinline__ int long_quotient(int x, int d) { return x / d; }
+
+__device__ __forceinline__ int quotient(int x, int d)
+{
+    return x < (1 << 20) ? (int)__fdividef((float)x + 0.5f, (float)d) : long_quotient(x, d);
+}
+
 // A tile of the list: what a lane holds of each of the warp's next 32 tiles.
 struct Tile {
     int id[4];           // block of each quarter of the rows (blocks of >= 16 rows: all in id[0])
@@ -189,7 +201,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *tstart, int 
     const int lo = first_row(p, L);
     const int nt = num_tiles(L, lo);
     const int off = x - tstart[t.b];
-    t.kvh = off / nt;
+    t.kvh = quotient(off, nt);
     const int i = off - t.kvh * nt;
     const int t0 = TILE * (lo / TILE + i);
     t.bits = min(TILE, L - t0) | max(0, lo - t0) << 5 | (i == 0 ? FIRST : 0) |
@@ -251,7 +263,7 @@ __device__ __forceinline__ void issue_tile(const Params &p, const Tile &d, int j
             v = id >= 0 && r < rows && r >= skip;
             return (int64_t)max(id, 0) * p.num_kv_heads + kvh;
         };
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < C::NI; ++i) {
             const int r = r0 + i * C::RPI;
             bool v;
@@ -582,6 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         const int per = (B + NT - 1) / NT;
         const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
         int n = 0, most = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int raw = __ldg(p.seq_lens + b);
             if ((raw < 0 || raw > p.len_cap) && cta == 0)
@@ -616,6 +629,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         for (int w = 0; w < W; ++w)
             if (w < warp)
                 at += scan[w];
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             tstart[b] = at;
             const int L = S::has_lens(B) ? tstart[B + 1 + b] : seq_len(p, b);
@@ -637,33 +651,37 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 #pragma unroll
     for (int w = 1; w < W; ++w)
         most = max(most, scan[W + w]);
-    const int pieces = B * Hkv;
-    const int each = (pieces + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int whole_ctas = (pieces + each - 1) / each;
-    const bool even = (int64_t)most * pieces <= (int64_t)T + T / 8 &&
-                      (whole_ctas * 5 >= (int)gridDim.x * 4 || most <= SHORT_TILES * W);
-    const int P = even ? whole_ctas : max(1, min((int)gridDim.x, T / (W * MIN_TILES)));
-    auto bound = [&](int c) {
-        if (c >= P)
-            return T;
-        if (!even)
-            return (int)((int64_t)c * T / P);
-        const int b = c * each / Hkv;
-        return tstart[b] + (c * each - b * Hkv) * ((tstart[b + 1] - tstart[b]) / Hkv);
+    const bool even = (int64_t)most * B * Hkv <= (int64_t)T + T / 8 &&
+                      (p.whole_ctas * 5 >= (int)gridDim.x * 4 || most <= SHORT_TILES * W);
+    const int P = even ? p.whole_ctas : max(1, min((int)gridDim.x, T / (W * MIN_TILES)));
+    // tiles of one KV head of sequence b
+    auto tiles_a_head = [&](int b) { return quotient(tstart[b + 1] - tstart[b], Hkv); };
+    // an uneven split's boundaries, floor(c T / P), and the CTA with tile x
+    // (cut(c) is at least c TP, and more than that by less than c)
+    const int TP = T / P, TR = T - TP * P;
+    auto cut = [&](int c) { return c * TP + quotient(c * TR, P); };
+    auto owner = [&](int x) {
+        int c = min(P - 1, quotient(x, TP));
+        while (cut(c) > x)
+            --c;
+        return c;
     };
-    const int c0 = bound(cta), c1 = bound(cta + 1);
+    int c0 = T, c1 = T;
+    if (cta < P) {
+        if (even) {
+            int b = quotient(cta * p.pieces_each, Hkv);
+            c0 = tstart[b] + (cta * p.pieces_each - b * Hkv) * tiles_a_head(b);
+            if (cta + 1 < P) {
+                b = quotient((cta + 1) * p.pieces_each, Hkv);
+                c1 = tstart[b] + ((cta + 1) * p.pieces_each - b * Hkv) * tiles_a_head(b);
+            }
+        } else {
+            c0 = cut(cta);
+            c1 = cut(cta + 1);
+        }
+    }
     const int r0 = c0 + (int)((int64_t)warp * (c1 - c0) / W);
     const int r1 = c0 + (int)((int64_t)(warp + 1) * (c1 - c0) / W);
-    auto tiles_of = [&](int seg, int &x0, int &x1) {
-        const int b = seg / Hkv, kvh = seg - b * Hkv;
-        const int nt = (tstart[b + 1] - tstart[b]) / Hkv;
-        x0 = tstart[b] + kvh * nt;
-        x1 = x0 + nt;
-    };
-    auto piece_of = [&](int x) {
-        const int b = kern::find_seq(tstart, B, x);
-        return b * Hkv + (x - tstart[b]) / ((tstart[b + 1] - tstart[b]) / Hkv);
-    };
     unsigned char *ring = smem + S::RING + warp * NST * C::STAGE;
     int4 *info = reinterpret_cast<int4 *>(smem + S::INFO) + warp * NST;
     if (r0 < r1) {
@@ -691,17 +709,6 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 #pragma unroll
         for (int i = 0; i < NST - 1; ++i)
             issue();
-
-        if (warp == W - 1 && lane < 2 && !even) {
-            // (the last warp has tiles wherever the CTA has) the CTAs of the
-            // first and the last piece, worked out while the first tiles arrive
-            const int seg = piece_of(lane ? c1 - 1 : c0);
-            int x0, x1;
-            tiles_of(seg, x0, x1);
-            edge[3 * lane] = seg;
-            edge[3 * lane + 1] = kern::owner_of(x0, T, P);
-            edge[3 * lane + 2] = kern::owner_of(x1 - 1, T, P);
-        }
 
         State<D, G, KV> st;
         float qscale[2];
@@ -784,10 +791,21 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         }
         cp_wait<0>();
     }
+    if (warp == W - 1 && lane < 2 && !even && c0 < c1) {
+        // the CTAs of this one's first and last piece
+        const int x = lane ? c1 - 1 : c0;
+        const int b = kern::find_seq(tstart, B, x), nt = tiles_a_head(b);
+        const int kvh = quotient(x - tstart[b], nt), x0 = tstart[b] + kvh * nt;
+        edge[3 * lane] = b * Hkv + kvh;
+        edge[3 * lane + 1] = owner(x0);
+        edge[3 * lane + 2] = owner(x0 + nt - 1);
+    }
 
     // rows of sequences without a row to attend: zeros
+#pragma unroll 1
     for (int b = cta; b < B; b += gridDim.x)
         if (tstart[b + 1] == tstart[b])
+#pragma unroll 1
             for (int i = tid; i < Hq * D; i += NT)
                 p.out[(int64_t)b * Hq * D + i] = 0.0f;
     if (c0 >= c1)
@@ -821,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 if (edge[3 * t] == seg && edge[3 * t + 1] != edge[3 * t + 2])
                     edges = t + 1;
         const bool mine = edges == 0;
-        float *dst = mine ? p.out + ((int64_t)(seg / Hkv) * Hq + (seg % Hkv) * G) * D
+        float *dst = mine ? p.out + (int64_t)seg * G * D
                           : p.partials + (int64_t)(cta + seg) * C::STATE;
         const bool member = (members >> lane) & 1u;
         // a warp's 32 elements belong to one head: the lanes weigh the states
@@ -931,7 +949,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 #pragma unroll
         for (int o = 0; o < MO; ++o)
             if (tid + o * NT < G * D)
-                p.out[((int64_t)(seg / Hkv) * Hq + (seg % Hkv) * G) * D + o * NT + tid] =
+                p.out[(int64_t)seg * G * D + o * NT + tid] =
                     num[o] / den[o];
     }
 }
@@ -939,8 +957,9 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 // ---- host side ---------------------------------------------------------------
 
 template <int D, int G, int KV>
-int launch_t(const pkv_pool *pool, const Params &prm, cudaStream_t stream, int64_t max_tiles)
+int launch_t(const pkv_pool *pool, const Params &base, cudaStream_t stream, int64_t max_tiles)
 {
+    Params prm = base;
     using C = Cfg<D, G, KV>;
     const int smem = Smem<D, G, KV>::total(prm.batch);
     if (smem > pool->max_smem_optin)
@@ -956,6 +975,9 @@ int launch_t(const pkv_pool *pool, const Params &prm, cudaStream_t stream, int64
         P = pool->num_sms;
     if (P < 1)
         P = 1;
+    const int64_t pieces = (int64_t)prm.batch * prm.num_kv_heads;
+    prm.pieces_each = (int)((pieces + P - 1) / P);
+    prm.whole_ctas = (int)((pieces + prm.pieces_each - 1) / prm.pieces_each);
     if (launch_pdl(decode_blocks_kernel<D, G, KV>, dim3((unsigned)P), dim3(C::NT), (size_t)smem,
                    stream, prm) != cudaSuccess)
         return PKV_ERR_CUDA;
