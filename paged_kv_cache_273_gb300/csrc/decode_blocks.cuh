@@ -920,30 +920,38 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
             num[o] = den[o] = 0.0f;
             top[o] = -INFINITY;
         }
+        // 16 partials at a time, all their loads on the way together
+        constexpr int BATCH = 16;
 #pragma unroll 1
-        for (int q0 = 0; q0 < np; q0 += 32) {
-            const int qn = min(32, np - q0);
-            const bool in = lane < qn;
-            float w[MO];
+        for (int q0 = 0; q0 < np; q0 += BATCH) {
+            const int qn = min(BATCH, np - q0);
+            float v[BATCH][MO], m[MO], l[MO];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const float *sp = part + (int64_t)(q0 + min(u, qn - 1)) * C::STATE + tid;
+#pragma unroll
+                for (int o = 0; o < MO; ++o)
+                    v[u][o] = tid + o * NT < G * D ? __ldcg(sp + o * NT) : 0.0f;
+            }
 #pragma unroll
             for (int o = 0; o < MO; ++o) {
                 const int g = min((o * NT + tid) / D, G - 1);
                 const float *sp = part + (int64_t)(q0 + min(lane, qn - 1)) * C::STATE + G * D + g;
-                const float m = in ? __ldcg(sp) : -INFINITY, l = in ? __ldcg(sp + G) : 0.0f;
-                const float mn = fmaxf(top[o], warp_max(m));
+                m[o] = __ldcg(sp);
+                l[o] = __ldcg(sp + G);
+            }
+#pragma unroll
+            for (int o = 0; o < MO; ++o) {
+                const bool in = lane < qn;
+                const float mn = fmaxf(top[o], warp_max(in ? m[o] : -INFINITY));
                 const float a = kern::exp2_approx(top[o] - mn);
-                w[o] = in ? kern::exp2_approx(m - mn) : 0.0f;
-                den[o] = fmaf(den[o], a, warp_sum(w[o] * l));
+                const float w = in ? kern::exp2_approx(m[o] - mn) : 0.0f;
+                den[o] = fmaf(den[o], a, warp_sum(in ? w * l[o] : 0.0f));
                 num[o] *= a;
                 top[o] = mn;
-            }
-#pragma unroll 4
-            for (int u = 0; u < qn; ++u) {
-                const float *sp = part + (int64_t)(q0 + u) * C::STATE + tid;
 #pragma unroll
-                for (int o = 0; o < MO; ++o)
-                    num[o] = fmaf(__shfl_sync(FULL_MASK, w[o], u),
-                                  tid + o * NT < G * D ? __ldcg(sp + o * NT) : 0.0f, num[o]);
+                for (int u = 0; u < BATCH; ++u)
+                    num[o] = fmaf(__shfl_sync(FULL_MASK, w, u), v[u][o], num[o]);
             }
         }
 #pragma unroll

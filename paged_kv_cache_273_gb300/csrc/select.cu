@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t sort_key(float x)
 // indices, ascending, to sel, their ids to phys.  Keys and ids may be staged, or in
 // the workspace and the block table.
 struct Pick {
-    int hist[256];
+    int hist[3][256];                    // counts of digit d in d mod 3
     uint32_t cand[NT];                   // the keys that the digits so far leave open
     uint32_t lo[NW], hi[NW];
     int gt[NW], eq[NW];
@@ -117,7 +117,9 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
         s.lo[warp] = lo;
         s.hi[warp] = hi;
     }
-    s.hist[tid] = 0;
+    s.hist[0][tid] = s.hist[1][tid] = 0;
+    if (tid == 0)
+        s.ncand = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -131,21 +133,25 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
     uint32_t t = 0;
     int left = want, open = n;
 #pragma unroll 1
-    while (top > 0 && open > NT) {
+    for (int d = 0; top > 0 && open > NT; ++d) {
+        int *hist = s.hist[d % 3];
         const int shift = max(top - 8, 0);
         const uint32_t mask = (1u << (top - shift)) - 1u;
         for_keys([&](uint32_t k) {
             k -= lo;
             if (top >= 32 || (k >> top) == (t >> top))
-                atomicAdd(&s.hist[(k >> shift) & mask], 1);
+                atomicAdd(&hist[(k >> shift) & mask], 1);
         });
+        // the next digit's counts at zero; digit d - 2's, in the same place, were
+        // read before the last barrier
+        s.hist[(d + 1) % 3][tid] = 0;
         __syncthreads();
         // every warp finds the digit for itself, bins from the top: lane l
         // holds bins 255 - 8 l .. 248 - 8 l
         int c[8], sum = 0;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            c[u] = s.hist[255 - 8 * lane - u];
+            c[u] = hist[255 - 8 * lane - u];
             sum += c[u];
         }
         int inc = sum;
@@ -172,14 +178,8 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
         left = __shfl_sync(FULL_MASK, rest, l);
         open = __shfl_sync(FULL_MASK, in, l);
         top = shift;
-        __syncthreads();                 // the counts are read
-        s.hist[tid] = 0;
-        __syncthreads();
     }
     if (top > 0) {
-        if (tid == 0)
-            s.ncand = 0;
-        __syncthreads();
         for_keys([&](uint32_t k) {
             k -= lo;
             if (top >= 32 || (k >> top) == (t >> top))

@@ -281,6 +281,26 @@ def test_sparse_exponents_far_apart():
 
 
 @pytest.mark.gpu
+def test_sparse_scores_crowded_in_a_few_digits():
+    # a few blocks far off, so that the thousands of others share the first digits of the search
+    # for the last one chosen; many of them equal
+    s = Sparse("f16", 400, 2, 4, 64, seed=16)
+    s.he[:] = -3
+    s.hb[:] = np.random.default_rng(3).integers(-2, 3, (1, 2, 2, 64))
+    s.hb[:, :, 1] = np.maximum(s.hb[:, :, 0], s.hb[:, :, 1])
+    s.hb[:, :, 1, 0] = np.maximum(s.hb[:, :, 0, 0], np.arange(400)[:, None] % 50)
+    s.he[7], s.he[8], s.he[9] = 40, -90, 90
+    s.hb[9, :, 0], s.hb[9, :, 1] = -100, -99             # far below all others or far above
+    s.sync()
+    lens = [4 * 6000 + 1, 4 * 3000, 4 * 20000]
+    tables = _tables(400, lens, 4, 7)
+    q = _rows(1, (3, 8, 64), "f16")
+    for budget in (2, 300, 1500):
+        out, sel, _ = s.call(q, tables, lens, budget, 0.125)
+        s.check(q, tables, lens, budget, 0.125, out, sel)
+
+
+@pytest.mark.gpu
 def test_sparse_with_room_for_all_is_the_dense_call():
     s = Sparse("f8", 100, 4, 16, 128, seed=8)
     lens = [1000, 3, 0, 16, 777]
