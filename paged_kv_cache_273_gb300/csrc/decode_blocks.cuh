@@ -191,6 +191,7 @@ constexpr int FIRST = 1 << 10, LAST = 1 << 11;
 
 __device__ __forceinline__ int rows_of(int bits) { return bits & 31; }
 __device__ __forceinline__ int skip_of(int bits) { return (bits >> 5) & 31; }
+__device__ __forceinline__ bool is_full(int bits) { return (bits & 1023) == TILE; }
 
 template <int D, int G, int KV>
 __device__ __forceinline__ Tile tile_at(const Params &p, const int *tstart, int x)
@@ -239,16 +240,29 @@ __device__ __forceinline__ void issue_tile(const Params &p, const Tile &d, int j
     const int rows = rows_of(bits), skip = skip_of(bits), bs = p.block_size;
     if (lane == 0)
         *info = make_int4(bits, b, kvh, 0);
+    // copy i goes 512 bytes behind copy i - 1, and the swizzle's row bits flip one
+    // bit of the chunk from copy to copy
+    const uint32_t dst0 = kern::swz_off(r0 * C::ROWB + c * 16, true);
+    auto dst_of = [&](int i) { return (dst0 ^ ((i & 1) * 0x40u)) + i * 512u; };
+    static_assert(C::RPI * C::ROWB == 512, "a warp's copy");
     if (bs >= TILE) {
         const int64_t head = (int64_t)max(id0, 0) * p.num_kv_heads + kvh;
         const int64_t base = (head * bs + (bits >> 12) + r0) * C::ROWB + c * 16;
+        const unsigned char *k = p.k_cache + base, *v = p.v_cache + base;
+        if (is_full(bits) && id0 >= 0) {
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) {
-            const int r = r0 + i * C::RPI;
-            const bool v = id0 >= 0 && r < rows && r >= skip;
-            const uint32_t dst = kern::swz_off(r * C::ROWB + c * 16, true);
-            cp16_zfill(stage + dst, p.k_cache + base + i * C::RPI * C::ROWB, v);
-            cp16_zfill(stage + C::TILE_BYTES + dst, p.v_cache + base + i * C::RPI * C::ROWB, v);
+            for (int i = 0; i < C::NI; ++i) {
+                cp_async_16b(stage + dst_of(i), k + i * 512);
+                cp_async_16b(stage + C::TILE_BYTES + dst_of(i), v + i * 512);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < C::NI; ++i) {
+                const int r = r0 + i * C::RPI;
+                const bool in = id0 >= 0 && r < rows && r >= skip;
+                cp16_zfill(stage + dst_of(i), k + i * 512, in);
+                cp16_zfill(stage + C::TILE_BYTES + dst_of(i), v + i * 512, in);
+            }
         }
         if constexpr (C::F8)
             cp4_zfill(stage + 2 * C::TILE_BYTES + lane * 4,
@@ -269,9 +283,8 @@ __device__ __forceinline__ void issue_tile(const Params &p, const Tile &d, int j
             bool v;
             const int64_t head = head_of(r, v);
             const int64_t off = (head * bs + (r & (bs - 1))) * C::ROWB + c * 16;
-            const uint32_t dst = kern::swz_off(r * C::ROWB + c * 16, true);
-            cp16_zfill(stage + dst, p.k_cache + off, v);
-            cp16_zfill(stage + C::TILE_BYTES + dst, p.v_cache + off, v);
+            cp16_zfill(stage + dst_of(i), p.k_cache + off, v);
+            cp16_zfill(stage + C::TILE_BYTES + dst_of(i), p.v_cache + off, v);
         }
         if constexpr (C::F8) {
             bool v;
@@ -483,7 +496,8 @@ __device__ __forceinline__ void join_parts(State<D, G, KV> &st)
 // One tile: scores, online softmax, weighted V (see the head of the file).
 template <int D, int G, int KV>
 __device__ __forceinline__ void tile(State<D, G, KV> &st, const float (&qscale)[2],
-                                     const unsigned char *stage, int nvalid, int tlo, int lane)
+                                     const unsigned char *stage, int bits, bool one_block,
+                                     int lane)
 {
     using C = Cfg<D, G, KV>;
     const int gid = lane >> 2;
@@ -492,24 +506,35 @@ __device__ __forceinline__ void tile(State<D, G, KV> &st, const float (&qscale)[
     kern::mma_scores<D, G, KV, false>(s, st, sK, lane, true);
     uint32_t vw[4][kern::VFrag<D, KV>::VW];
     kern::load_v_frag<D, KV>(vw, sV, lane, true);
-    const bool v0 = gid < nvalid && gid >= tlo;
-    const bool v1 = gid + 8 < nvalid && gid + 8 >= tlo;
-    float x0, x1, x2, x3, f0 = 0.0f, f1 = 0.0f;
+    float f0 = 0.0f, f1 = 0.0f;
     if constexpr (C::F8) {
+        // the K scales, and the exponents of the V scales, of tokens gid, gid + 8
+        // (of one block, unless blocks are smaller than a tile)
         const float *sc = reinterpret_cast<const float *>(stage + 2 * C::TILE_BYTES);
-        const float k0 = pow2_f32(block_exponent(sc[gid]));
-        const float k1 = pow2_f32(block_exponent(sc[gid + 8]));
-        f0 = (float)block_exponent(sc[TILE + gid]);
-        f1 = (float)block_exponent(sc[TILE + gid + 8]);
+        const float k0 = sc[gid];
+        float k1 = k0;
+        f0 = exponent_f32(sc[TILE + gid]);
+        f1 = f0;
+        if (!one_block) {
+            k1 = sc[gid + 8];
+            f1 = exponent_f32(sc[TILE + gid + 8]);
+        }
         s[0] *= k0;
         s[1] *= k0;
         s[2] *= k1;
         s[3] *= k1;
     }
-    x0 = v0 ? s[0] * qscale[0] : -INFINITY;       // token gid, head 2 tig
-    x1 = v0 ? s[1] * qscale[1] : -INFINITY;       // token gid, head 2 tig + 1
-    x2 = v1 ? s[2] * qscale[0] : -INFINITY;       // token gid + 8, head 2 tig
-    x3 = v1 ? s[3] * qscale[1] : -INFINITY;       // token gid + 8, head 2 tig + 1
+    float x0 = s[0] * qscale[0];                  // token gid, head 2 tig
+    float x1 = s[1] * qscale[1];                  // token gid, head 2 tig + 1
+    float x2 = s[2] * qscale[0];                  // token gid + 8, head 2 tig
+    float x3 = s[3] * qscale[1];                  // token gid + 8, head 2 tig + 1
+    if (!is_full(bits)) {
+        const int rows = rows_of(bits), skip = skip_of(bits);
+        if (gid >= rows || gid < skip)
+            x0 = x1 = -INFINITY;
+        if (gid + 8 >= rows || gid + 8 < skip)
+            x2 = x3 = -INFINITY;
+    }
     float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
     float my0 = mx0, my1 = mx1;
     bool above = mx0 > st.m[0] || mx1 > st.m[1];
@@ -743,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 const int4 next = info[(k + 1) % NST];
                 fetch_q<D, G>(qraw, p, next.y, next.z, lane);
             }
-            tile<D, G, KV>(st, qscale, ring + (k % NST) * C::STAGE, rows_of(it.x), skip_of(it.x),
+            tile<D, G, KV>(st, qscale, ring + (k % NST) * C::STAGE, it.x, p.block_size >= TILE,
                            lane);
             if (ends || k + 1 == n) {
                 // ---- the piece's end, or the run's
