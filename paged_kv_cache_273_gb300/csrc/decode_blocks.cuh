@@ -61,13 +61,22 @@ struct Cfg {
     static constexpr int TILE_BYTES = TILE * ROWB;
     static constexpr int SC_BYTES = F8 ? 2 * TILE * 4 : 0;   // each row's K scale, then V scale
     static constexpr int STAGE = 2 * TILE_BYTES + SC_BYTES;
-    static constexpr int W = F8 ? (D == 64 ? 16 : 12) : 8;   // warps
+    // warps: a multiple of the SM's four partitions, as many as the registers
+    // allow (8-bit rows of 128, 16 x 4096 tokens, 32 / 8 heads: 29 us with 12
+    // warps, 30 to 35 us with 9 to 11 or 13 to 15)
+    static constexpr int W = F8 ? (D == 64 ? 16 : 12) : 8;
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
-    // ring stages that fit beside the states and the tile prefix, at most 6
-    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 6 * 16 + W * 16 + 256;
-    static constexpr int FIT = (232448 - FIXED) / (W * STAGE);
-    static constexpr int NST = FIT > 6 ? 6 : FIT;
+    // ring stages that fit beside the states and the tile prefix, at most 4,
+    // with 20 KB of the SM's shared memory left if that costs no stage that is
+    // needed: room for a CTA of the kernel launched next, whose start then
+    // overlaps this one's end (with all of it taken, the choice of blocks
+    // followed by the attention over them took 57 instead of 50 us on 16
+    // sequences of 2048 blocks).
+    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 4 * 16 + W * 16 + 256;
+    static constexpr int FIT20 = (212448 - FIXED) / (W * STAGE);
+    static constexpr int FIT = FIT20 >= (F8 ? 3 : 2) ? FIT20 : (232448 - FIXED) / (W * STAGE);
+    static constexpr int NST = FIT > 4 ? 4 : FIT;
     static_assert(NST >= 2, "ring");
     static_assert(NST * STAGE >= STATE * 4, "a warp's last state takes its ring's place");
     static_assert(TILE_BYTES % 1024 == 0 || STAGE % 128 == 0, "swizzle period");
