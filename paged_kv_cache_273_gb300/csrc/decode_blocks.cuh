@@ -65,6 +65,11 @@ struct Cfg {
     // allow (8-bit rows of 128, 16 x 4096 tokens, 32 / 8 heads: 29 us with 12
     // warps, 30 to 35 us with 9 to 11 or 13 to 15)
     static constexpr int W = F8 ? (D == 64 ? 16 : 12) : 8;
+    // two tiles of a piece computed together: where the registers allow it
+    // beside as many warps (rows of 64: 34.6 instead of 35.5 us on 64
+    // sequences of up to 2048 tokens, 12 heads; rows of 128 in pairs, with 8
+    // warps for the registers, 31 instead of 29 us on the shape above)
+    static constexpr bool PAIR = F8 && D == 64;
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
     // ring stages that fit beside the states and the tile prefix, at most 4,
@@ -73,11 +78,11 @@ struct Cfg {
     // overlaps this one's end (with all of it taken, the choice of blocks
     // followed by the attention over them took 57 instead of 50 us on 16
     // sequences of 2048 blocks).
-    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 4 * 16 + W * 16 + 256;
+    static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 6 * 16 + W * 16 + 256;
     static constexpr int FIT20 = (212448 - FIXED) / (W * STAGE);
     static constexpr int FIT = FIT20 >= (F8 ? 3 : 2) ? FIT20 : (232448 - FIXED) / (W * STAGE);
-    static constexpr int NST = FIT > 4 ? 4 : FIT;
-    static_assert(NST >= 2, "ring");
+    static constexpr int NST = FIT > 6 ? 6 : FIT;
+    static_assert(NST >= (PAIR ? 3 : 2), "ring");
     static_assert(NST * STAGE >= STATE * 4, "a warp's last state takes its ring's place");
     static_assert(TILE_BYTES % 1024 == 0 || STAGE % 128 == 0, "swizzle period");
 };
@@ -397,20 +402,18 @@ __device__ __forceinline__ float warp_sum(float x)
 template <int KV>
 __host__ __device__ constexpr int weight_parts() { return KV == PKV_BF16 ? 3 : 2; }
 
-// O^T += V^T P^T of one tile.  The MMA's 8 head columns take 8 / G parts of the
-// weights at a time: column c holds part c / G of head c mod G (the columns
-// repeat the heads), so that G < 8 needs one or two MMAs for all parts.  The
-// tile's sum starts at zero and is added to the running one in fp32: an MMA
-// truncates what it adds to its accumulator, and over a long run of tiles that
-// would show (3e-6 of the result at 230 tiles a warp).
-template <int D, int G, int KV>
-__device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
-                                        const uint32_t (&vw)[4][kern::VFrag<D, KV>::VW], float p0,
-                                        float p1, float p2, float p3, int lane)
+// The B fragments of a tile's weights.  The MMA's 8 head columns take 8 / G
+// parts of the weights at a time: column c holds part c / G of head c mod G (the
+// columns repeat the heads), so that G < 8 needs one or two MMAs for all parts.
+template <int KV, int G>
+__host__ __device__ constexpr int weight_mmas() { return (weight_parts<KV>() * G + 7) / 8; }
+
+template <int G, int KV>
+__device__ __forceinline__ void split_weights(uint32_t (&bf)[weight_mmas<KV, G>()][2], float p0,
+                                              float p1, float p2, float p3, int lane)
 {
     constexpr bool BF = kern::MmaBf16<KV>::v;
     constexpr int NP = weight_parts<KV>();
-    constexpr int NB = (NP * G + 7) / 8;          // MMAs for all parts
     const int tig = lane & 3;
     uint32_t part[2][NP];                         // heads 2 tig, 2 tig + 1 of token gid | gid + 8
 #pragma unroll
@@ -431,9 +434,8 @@ __device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
             }
         }
     }
-    uint32_t bf[NB][2];
 #pragma unroll
-    for (int m = 0; m < NB; ++m)
+    for (int m = 0; m < weight_mmas<KV, G>(); ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t v = 0u;
@@ -452,24 +454,38 @@ __device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
             }
             bf[m][h] = kern::transpose8x8(v);
         }
+}
+
+// O^T += V^T P^T of NS tiles.  Their sum starts at zero and is added to the
+// running one in fp32: an MMA truncates what it adds to its accumulator, and
+// over a long run of tiles that would show (3e-6 of the result at 230 tiles a
+// warp).
+template <int D, int G, int KV, int NS>
+__device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
+                                        const uint32_t (&vw)[NS][4][kern::VFrag<D, KV>::VW],
+                                        const uint32_t (&bf)[NS][weight_mmas<KV, G>()][2])
+{
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-        uint32_t a0, a1, a2, a3;
-        if constexpr (KV == PKV_F8) {
-            const int w = j >> 1;
-            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-            f8x4_to_half2(__byte_perm(vw[0][w], vw[1][w], sel), a0, a1);
-            f8x4_to_half2(__byte_perm(vw[2][w], vw[3][w], sel), a2, a3);
-        } else {
-            a0 = __byte_perm(vw[0][j], vw[1][j], 0x5410u);
-            a1 = __byte_perm(vw[0][j], vw[1][j], 0x7632u);
-            a2 = __byte_perm(vw[2][j], vw[3][j], 0x5410u);
-            a3 = __byte_perm(vw[2][j], vw[3][j], 0x7632u);
-        }
         float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < NB; ++m)
-            kern::mma_16816<BF>(t, a0, a1, a2, a3, bf[m][0], bf[m][1]);
+        for (int n = 0; n < NS; ++n) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (KV == PKV_F8) {
+                const int w = j >> 1;
+                const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                f8x4_to_half2(__byte_perm(vw[n][0][w], vw[n][1][w], sel), a0, a1);
+                f8x4_to_half2(__byte_perm(vw[n][2][w], vw[n][3][w], sel), a2, a3);
+            } else {
+                a0 = __byte_perm(vw[n][0][j], vw[n][1][j], 0x5410u);
+                a1 = __byte_perm(vw[n][0][j], vw[n][1][j], 0x7632u);
+                a2 = __byte_perm(vw[n][2][j], vw[n][3][j], 0x5410u);
+                a3 = __byte_perm(vw[n][2][j], vw[n][3][j], 0x7632u);
+            }
+#pragma unroll
+            for (int m = 0; m < weight_mmas<KV, G>(); ++m)
+                kern::mma_16816<kern::MmaBf16<KV>::v>(t, a0, a1, a2, a3, bf[n][m][0], bf[n][m][1]);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             st.acc[j][u] += t[u];
@@ -502,56 +518,61 @@ __device__ __forceinline__ void join_parts(State<D, G, KV> &st)
     }
 }
 
-// One tile: scores, online softmax, weighted V (see the head of the file).
-template <int D, int G, int KV>
-__device__ __forceinline__ void tile(State<D, G, KV> &st, const float (&qscale)[2],
-                                     const unsigned char *stage, int bits, bool one_block,
-                                     int lane)
+// NS tiles of a piece: scores, online softmax, weighted V (see the head of the
+// file).
+template <int D, int G, int KV, int NS>
+__device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)[2],
+                                      const unsigned char *const (&stage)[NS],
+                                      const int (&bits)[NS], bool one_block, int lane)
 {
     using C = Cfg<D, G, KV>;
     const int gid = lane >> 2;
-    const unsigned char *sK = stage, *sV = stage + C::TILE_BYTES;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    kern::mma_scores<D, G, KV, false>(s, st, sK, lane, true);
-    uint32_t vw[4][kern::VFrag<D, KV>::VW];
-    kern::load_v_frag<D, KV>(vw, sV, lane, true);
-    float f0 = 0.0f, f1 = 0.0f;
-    if constexpr (C::F8) {
-        // the K scales, and the exponents of the V scales, of tokens gid, gid + 8
-        // (of one block, unless blocks are smaller than a tile)
-        const float *sc = reinterpret_cast<const float *>(stage + 2 * C::TILE_BYTES);
-        const float k0 = sc[gid];
-        float k1 = k0;
-        f0 = exponent_f32(sc[TILE + gid]);
-        f1 = f0;
-        if (!one_block) {
-            k1 = sc[gid + 8];
-            f1 = exponent_f32(sc[TILE + gid + 8]);
+    uint32_t vw[NS][4][kern::VFrag<D, KV>::VW];
+    float x[NS][4], f[NS][2];          // (token gid | gid + 8, heads 2 tig, 2 tig + 1); V exponents
+    float mx0 = -INFINITY, mx1 = -INFINITY, my0 = -INFINITY, my1 = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        kern::mma_scores<D, G, KV, false>(s, st, stage[n], lane, true);
+        kern::load_v_frag<D, KV>(vw[n], stage[n] + C::TILE_BYTES, lane, true);
+        f[n][0] = f[n][1] = 0.0f;
+        if constexpr (C::F8) {
+            // the K scales, and the exponents of the V scales, of tokens gid,
+            // gid + 8 (of one block, unless blocks are smaller than a tile)
+            const float *sc = reinterpret_cast<const float *>(stage[n] + 2 * C::TILE_BYTES);
+            const float k0 = sc[gid];
+            float k1 = k0;
+            f[n][0] = f[n][1] = exponent_f32(sc[TILE + gid]);
+            if (!one_block) {
+                k1 = sc[gid + 8];
+                f[n][1] = exponent_f32(sc[TILE + gid + 8]);
+            }
+            s[0] *= k0;
+            s[1] *= k0;
+            s[2] *= k1;
+            s[3] *= k1;
         }
-        s[0] *= k0;
-        s[1] *= k0;
-        s[2] *= k1;
-        s[3] *= k1;
+        x[n][0] = s[0] * qscale[0];
+        x[n][1] = s[1] * qscale[1];
+        x[n][2] = s[2] * qscale[0];
+        x[n][3] = s[3] * qscale[1];
+        if (!is_full(bits[n])) {
+            const int rows = rows_of(bits[n]), skip = skip_of(bits[n]);
+            if (gid >= rows || gid < skip)
+                x[n][0] = x[n][1] = -INFINITY;
+            if (gid + 8 >= rows || gid + 8 < skip)
+                x[n][2] = x[n][3] = -INFINITY;
+        }
+        mx0 = fmaxf(mx0, fmaxf(x[n][0], x[n][2]));
+        mx1 = fmaxf(mx1, fmaxf(x[n][1], x[n][3]));
+        if constexpr (C::F8) {
+            my0 = fmaxf(my0, fmaxf(x[n][0] + f[n][0], x[n][2] + f[n][1]));
+            my1 = fmaxf(my1, fmaxf(x[n][1] + f[n][0], x[n][3] + f[n][1]));
+        }
     }
-    float x0 = s[0] * qscale[0];                  // token gid, head 2 tig
-    float x1 = s[1] * qscale[1];                  // token gid, head 2 tig + 1
-    float x2 = s[2] * qscale[0];                  // token gid + 8, head 2 tig
-    float x3 = s[3] * qscale[1];                  // token gid + 8, head 2 tig + 1
-    if (!is_full(bits)) {
-        const int rows = rows_of(bits), skip = skip_of(bits);
-        if (gid >= rows || gid < skip)
-            x0 = x1 = -INFINITY;
-        if (gid + 8 >= rows || gid + 8 < skip)
-            x2 = x3 = -INFINITY;
-    }
-    float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
-    float my0 = mx0, my1 = mx1;
     bool above = mx0 > st.m[0] || mx1 > st.m[1];
-    if constexpr (C::F8) {
-        my0 = fmaxf(x0 + f0, x2 + f1);
-        my1 = fmaxf(x1 + f0, x3 + f1);
+    if constexpr (C::F8)
         above |= my0 > st.n[0] || my1 > st.n[1];
-    }
     if (__any_sync(FULL_MASK, above)) {
 #pragma unroll
         for (int mask = 4; mask < 32; mask <<= 1) {
@@ -584,22 +605,25 @@ __device__ __forceinline__ void tile(State<D, G, KV> &st, const float (&qscale)[
             st.acc[j][3] *= a1;
         }
     }
-    x0 -= st.m[0];
-    x1 -= st.m[1];
-    x2 -= st.m[0];
-    x3 -= st.m[1];
-    float p0 = kern::exp2_approx(x0), p1 = kern::exp2_approx(x1);
-    float p2 = kern::exp2_approx(x2), p3 = kern::exp2_approx(x3);
-    st.l[0] += p0 + p2;
-    st.l[1] += p1 + p3;
-    if constexpr (C::F8) {
-        const float d0 = st.n[0] - st.m[0], d1 = st.n[1] - st.m[1];
-        p0 = kern::exp2_approx(x0 + (f0 - d0));
-        p1 = kern::exp2_approx(x1 + (f0 - d1));
-        p2 = kern::exp2_approx(x2 + (f1 - d0));
-        p3 = kern::exp2_approx(x3 + (f1 - d1));
+    uint32_t bf[NS][weight_mmas<KV, G>()][2];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const float x0 = x[n][0] - st.m[0], x1 = x[n][1] - st.m[1];
+        const float x2 = x[n][2] - st.m[0], x3 = x[n][3] - st.m[1];
+        float p0 = kern::exp2_approx(x0), p1 = kern::exp2_approx(x1);
+        float p2 = kern::exp2_approx(x2), p3 = kern::exp2_approx(x3);
+        st.l[0] += p0 + p2;
+        st.l[1] += p1 + p3;
+        if constexpr (C::F8) {
+            const float d0 = st.n[0] - st.m[0], d1 = st.n[1] - st.m[1];
+            p0 = kern::exp2_approx(x0 + (f[n][0] - d0));
+            p1 = kern::exp2_approx(x1 + (f[n][0] - d1));
+            p2 = kern::exp2_approx(x2 + (f[n][1] - d0));
+            p3 = kern::exp2_approx(x3 + (f[n][1] - d1));
+        }
+        split_weights<G, KV>(bf[n], p0, p1, p2, p3, lane);
     }
-    weigh_v<D, G, KV>(st, vw, p0, p1, p2, p3, lane);
+    weigh_v<D, G, KV, NS>(st, vw, bf);
 }
 
 template <int D, int G, int KV>
@@ -750,10 +774,18 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         bool whole = true;                 // the piece began in this run
         const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll 1
-        for (int k = 0; k < n; ++k) {
-            cp_wait<NST - 2>();
-            __syncwarp();              // the lanes' copies have landed, the last tile is read
+        for (int k = 0, step = 1; k < n; k += step) {
+            __syncwarp();              // the last tiles are read; this one's info is there
             const int4 it = info[k % NST];
+            // two tiles of the piece at a time, while it has them
+            const bool two = C::PAIR && !(it.x & LAST) && k + 1 < n;
+            step = two ? 2 : 1;
+            if (two)
+                cp_wait<C::PAIR ? NST - 3 : 0>();
+            else
+                cp_wait<NST - 2>();
+            __syncwarp();              // the lanes' copies have landed
+            const int bits1 = two ? info[(k + 1) % NST].x : it.x;
             if (fresh) {
                 whole = (it.x & FIRST) != 0;
                 use_q<D, G, KV>(st, qscale, qraw, p, lane);
@@ -770,16 +802,29 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 fresh = false;
             }
             issue();
-            const bool ends = (it.x & LAST) != 0;
-            if (ends && k + 1 < n) {
+            const bool ends = (bits1 & LAST) != 0;
+            if (ends && k + step < n) {
                 // q of the next piece, on its way while this piece's last tile is computed
                 __syncwarp();
-                const int4 next = info[(k + 1) % NST];
+                const int4 next = info[(k + step) % NST];
                 fetch_q<D, G>(qraw, p, next.y, next.z, lane);
             }
-            tile<D, G, KV>(st, qscale, ring + (k % NST) * C::STAGE, it.x, p.block_size >= TILE,
-                           lane);
-            if (ends || k + 1 == n) {
+            const unsigned char *s0 = ring + (k % NST) * C::STAGE;
+            const bool one_block = p.block_size >= TILE;
+            if (two) {
+                if constexpr (C::PAIR) {
+                    const unsigned char *const st2[2] = {s0, ring + ((k + 1) % NST) * C::STAGE};
+                    const int b2[2] = {it.x, bits1};
+                    tiles<D, G, KV, 2>(st, qscale, st2, b2, one_block, lane);
+                    __syncwarp();      // the first tile's stage may be filled again
+                    issue();
+                }
+            } else {
+                const unsigned char *const st1[1] = {s0};
+                const int b1[1] = {it.x};
+                tiles<D, G, KV, 1>(st, qscale, st1, b1, one_block, lane);
+            }
+            if (ends || k + step == n) {
                 // ---- the piece's end, or the run's
 #pragma unroll
                 for (int r = 0; r < 2; ++r)

@@ -203,6 +203,15 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _check_scales(pool: "Pool", *scales) -> None:
+    """8-bit float pools: one float32 scale for each (block, KV head)."""
+    if pool.kv_dtype == PKV_F8:
+        for s in scales:
+            if s is None or s.dtype is not torch.float32 or \
+                    s.numel() != pool.num_blocks * pool.num_kv_heads:
+                raise ValueError("scales must be float32 [num_blocks, num_kv_heads]")
+
+
 class Pool:
     """Handle of a ``pkv_pool`` (host bookkeeping of one shared block pool)."""
 
@@ -351,6 +360,7 @@ def kv_append(pool: Pool, k_new, v_new, slot_mapping, k_cache, v_cache, k_scales
     if slot_mapping.dtype != torch.int32:
         raise ValueError("slot_mapping must be int32")
     T = k_new.shape[0]
+    _check_scales(pool, k_scales, v_scales)
     _check(load().kv_append(pool.handle, _dptr(k_new), _dptr(v_new), PKV_DTYPE[k_new.dtype],
                             _dptr(slot_mapping), T, _dptr(k_cache), _dptr(v_cache),
                             _dptr(k_scales), _dptr(v_scales), _stream(stream)), "kv_append")
@@ -361,6 +371,7 @@ def kv_block_copy(pool: Pool, src, dst, k_cache, v_cache, k_scales=None, v_scale
     """Copy blocks src[i] -> dst[i] (device int32 tensors) in the caches."""
     if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.numel() != dst.numel():
         raise ValueError("src and dst must be int32 tensors of equal length")
+    _check_scales(pool, k_scales, v_scales)
     _check(load().kv_block_copy(pool.handle, _dptr(src), _dptr(dst), src.numel(),
                                 _dptr(k_cache), _dptr(v_cache), _dptr(k_scales),
                                 _dptr(v_scales), _stream(stream)), "kv_block_copy")
@@ -388,6 +399,7 @@ def paged_decode_attention(pool: Pool, q, k_cache, v_cache, block_tables, seq_le
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
     B, Hq, _ = q.shape
+    _check_scales(pool, k_scales, v_scales)
     _check(load().paged_decode_attention(
         pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
         _dptr(k_scales), _dptr(v_scales), _dptr(block_tables), block_tables.shape[1],
@@ -406,6 +418,7 @@ def paged_decode_attention_window(pool: Pool, q, k_cache, v_cache, block_tables,
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
     B, Hq, _ = q.shape
+    _check_scales(pool, k_scales, v_scales)
     _check(load().paged_decode_attention_window(
         pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
         _dptr(k_scales), _dptr(v_scales), _dptr(block_tables), block_tables.shape[1],
@@ -509,6 +522,7 @@ def paged_decode_attention_noalloc(pool: Pool, q, k_cache, v_cache, block_tables
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
     B, Hq, _ = q.shape
+    _check_scales(pool, k_scales, v_scales)
     _check(load().paged_decode_attention_noalloc(
         pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
         _dptr(k_scales), _dptr(v_scales), _dptr(block_tables), block_tables.shape[1],
@@ -548,6 +562,7 @@ class DecodeStep:
             raise ValueError("block_tables must be int32")
         if dev_in.dtype != torch.uint8:
             raise ValueError("dev_in must be a uint8 tensor")
+        _check_scales(pool, k_scales, v_scales)
         self.pool = pool
         self.layout = layout
         self.in_bytes = dev_in.numel()
@@ -722,6 +737,7 @@ def paged_decode_attention_sparse(pool: Pool, q, k_cache, v_cache, bounds, bound
     _rows("block_tables", block_tables, B)
     _shaped("seq_lens", seq_lens, _I32, (B,))
     _shaped("selected", selected, _I32, (B, pool.num_kv_heads, None))
+    _check_scales(pool, k_scales, v_scales)
     _check(load().paged_decode_attention_sparse(
         pool.handle, _dptr(q), PKV_DTYPE[q.dtype], Hq, _dptr(k_cache), _dptr(v_cache),
         _dptr(k_scales), _dptr(v_scales), _dptr(bounds), _dptr(bound_exps), _dptr(block_tables),

@@ -73,6 +73,22 @@ def test_refusals():
                                               None) == uns
 
 
+def test_binding_refuses_other_scales():
+    pool = pkv.kv_block_pool_init(8, 16, 2, 64, pkv.PKV_F8)
+    k, v, ks, vs = pool.alloc_cache(device="cpu")
+    x, s = torch.zeros(1, 2, 64, dtype=torch.float16), torch.zeros(1, dtype=torch.int32)
+    for bad in (None, ks.half(), torch.zeros(8, 2, 16), torch.zeros(8)):
+        with pytest.raises(ValueError):
+            pkv.kv_append(pool, x, x, s, k, v, bad, vs)
+        with pytest.raises(ValueError):
+            pkv.kv_append(pool, x, x, s, k, v, ks, bad)
+        with pytest.raises(ValueError):
+            pkv.paged_decode_attention(pool, torch.zeros(1, 4, 64, dtype=torch.float16), k, v,
+                                       torch.zeros(1, 2, dtype=torch.int32), s, 1.0,
+                                       torch.zeros(1, 4, 64), torch.zeros(64, dtype=torch.uint8),
+                                       32, bad, vs)
+
+
 # ------------------------------------------------------------------------ append, GPU
 class Cache:
     """An F8 pool with random codes and scales in every block, and its host copy."""
@@ -325,6 +341,28 @@ def test_decode_largest_batch():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G", [1, 8])
+def test_decode_of_empty_sequences_only(G):
+    c = Cache(4, 2, 16, 128, seed=1)
+    q = _rows(1, (7, 2 * G, 128), "bf16")
+    out = _attend(c, q, np.zeros((7, 1), np.int32), [0] * 7, 0.1)
+    assert not out.any().item()
+    assert pkv.pkv_check_error(c.pool) == pkv.PKV_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[1], [5] * 9, [16] * 200, [300] * 152, [300] * 153, [2000] * 19,
+                                  [2000] * 20 + [1900], [513] * 40 + [0], [97] * 3 + [4000]])
+def test_decode_splits(lens):
+    # whole pieces a CTA, shared ones, and the borders between the two
+    c = Cache(500, 1, 16, 128, seed=7, exp=(-9, -6))
+    tables = _batch(c, lens, 3)
+    q = _rows(2, (len(lens), 4, 128), "bf16", 1.5)
+    out = _attend(c, q, tables, lens, 0.09)
+    _check(c, q, tables, lens, 0.09, out, seqs=range(0, len(lens), max(1, len(lens) // 7)))
+
+
+@pytest.mark.gpu
 def test_decode_bad_inputs_are_recorded():
     c = Cache(8, 2, 16, 64, seed=2, exp=(-9, -6))
     q = _rows(3, (4, 4, 64), "f16")
@@ -384,6 +422,56 @@ def test_step_and_noalloc_take_f8_pools():
     pkv.paged_decode_attention_noalloc(c.pool, q, c.k, c.v, tables_d,
                                        torch.from_numpy(lens).to(DEV), 0.09, out2, 64, c.ks, c.vs)
     assert torch.equal(out, out2)
+
+
+@pytest.mark.gpu
+def test_caches_beyond_4_gib():
+    # the last blocks of caches of 5 GB: append, bounds, attention, attention over chosen blocks
+    NB, H, bs, D, G = 310000, 8, 16, 128, 4
+    pool = pkv.kv_block_pool_init(NB, bs, H, D, pkv.PKV_F8)
+    assert pkv.kv_cache_bytes(pool) > 2 ** 32
+    k, v, ks, vs = pool.alloc_cache(DEV)
+    bounds, exps = pkv.alloc_bounds(pool, DEV)
+    ids = np.array([NB - 1, 5, NB - 3, NB - 2, NB - 7], np.int32)
+    n = 75
+    slots = [int(ids[p // bs]) * bs + p % bs for p in range(n)]
+    kn, vn = _rows(1, (n, H, D), "bf16"), _rows(2, (n, H, D), "bf16", 2.0)
+    sd = torch.tensor(slots, dtype=torch.int32, device=DEV)
+    pkv.kv_append(pool, kn, vn, sd, k, v, ks, vs)
+    pkv.kv_bounds_append(pool, kn, sd, bounds, exps)
+    # the same in a pool of the five blocks alone
+    small = Cache(5, H, bs, D)
+    where = {int(b): i for i, b in enumerate(ids)}
+    small.append(kn, vn, [where[s // bs] * bs + s % bs for s in slots])
+    idl = torch.from_numpy(ids.astype(np.int64)).to(DEV)
+    got = k.view(torch.uint8)[idl].cpu().numpy()
+    off = n % bs                                          # the last block's unwritten rows differ
+    assert np.array_equal(got[:4], small.hk[:4]) and np.array_equal(got[4, :, :off],
+                                                                    small.hk[4, :, :off])
+    assert np.array_equal(ks[idl].double().cpu().numpy(), small.hks)
+    hb, he = np.zeros((5, H, 2, D), np.int8), np.zeros((5, H), np.int32)
+    R.append_bounds(kn.double().cpu().numpy(), [where[s // bs] * bs + s % bs for s in slots], bs,
+                    hb, he)
+    assert np.array_equal(bounds[idl].cpu().numpy(), hb)
+    assert np.array_equal(exps[idl].cpu().numpy(), he)
+    q = _rows(3, (1, H * G, D), "bf16", 1.5)
+    out = torch.zeros(1, H * G, D, device=DEV)
+    td, ld = torch.from_numpy(ids[None]).to(DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    pkv.paged_decode_attention(pool, q, k, v, td, ld, 0.09, out, pkv.alloc_workspace(pool, 1, H * G),
+                               n, ks, vs)
+    _check(small, q, np.arange(5, dtype=np.int32)[None], [n], 0.09, out)
+    sel = torch.zeros(1, H, 2, dtype=torch.int32, device=DEV)
+    pkv.paged_decode_attention_sparse(pool, q, k, v, bounds, exps, td, ld, 0.09, out, sel,
+                                      pkv.alloc_sparse_workspace(pool, 1, H * G, n, 2), n, ks, vs)
+    qh, sh, oh = q.double().cpu().numpy(), sel.cpu().numpy(), out.double().cpu().numpy()
+    for h in range(H):
+        want = R.choose(qh[0, h * G:(h + 1) * G], np.arange(5), hb, he, h, 2)
+        assert sh[0, h].tolist() == want.tolist()
+        m = len(want) * bs - (5 * bs - n)
+        o, tol = R.attend(qh[0, h * G:(h + 1) * G], small.rows(want, h, m, "k"),
+                          small.rows(want, h, m, "v"), float(np.float32(0.09)))
+        assert np.abs(oh[0, h * G:(h + 1) * G] - o).max() <= tol
+    assert pkv.pkv_check_error(pool) == pkv.PKV_OK
 
 
 @pytest.mark.gpu
