@@ -644,8 +644,13 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     const int B = p.batch, Hkv = p.num_kv_heads, Hq = p.num_q_heads;
     const int cta = blockIdx.x;
 
-    grid_dependency_wait();
-    grid_dependents_launch();
+    // Over chosen blocks the kernel before this one is the one that chose them: it
+    // writes their list alone, and it let this kernel start only after all before
+    // it had completed, so that lengths and q may be read ahead of the wait.
+    if (!p.per_head) {
+        grid_dependency_wait();
+        grid_dependents_launch();
+    }
 
     // ---- exclusive prefix of the sequences' tiles (all KV heads')
     {
@@ -740,6 +745,10 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     }
     const int r0 = c0 + (int)((int64_t)warp * (c1 - c0) / W);
     const int r1 = c0 + (int)((int64_t)(warp + 1) * (c1 - c0) / W);
+    if (p.per_head) {
+        grid_dependency_wait();
+        grid_dependents_launch();
+    }
     unsigned char *ring = smem + S::RING + warp * NST * C::STAGE;
     int4 *info = reinterpret_cast<int4 *>(smem + S::INFO) + warp * NST;
     if (r0 < r1) {
