@@ -277,7 +277,9 @@ int kv_block_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, 
  * paged_decode_attention needs for a batch of `batch` sequences and
  * num_q_heads query heads on the pool's device.  The workspace holds
  * per-piece partial softmax states and one counter per (sequence, KV head).
- * Returns 0 for invalid arguments.
+ * For F8 pools the counters are those of the largest batch (4096), so that one
+ * workspace, zeroed once, serves calls of any batch that it is large enough
+ * for, one after another.  Returns 0 for invalid arguments.
  */
 size_t paged_decode_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads);
 
@@ -636,9 +638,13 @@ int kv_bounds_append(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype
 
 /*
  * paged_sparse_workspace_bytes — bytes of the workspace of
- * paged_decode_attention_sparse: the decode workspace, then a counter and
- * max_selected block ids for each (sequence, KV head), and a score for each
- * block of a sequence of max_seq_len tokens.  0 on bad arguments.
+ * paged_decode_attention_sparse: a counter for each KV head of 4096 sequences,
+ * partial softmax states, max_selected block ids for each (sequence, KV head),
+ * and a score for each block of a sequence of max_seq_len tokens.  One workspace,
+ * zeroed once, serves calls of any batch, length and max_selected that it is
+ * large enough for, one after another; it is not shared with
+ * paged_decode_attention's of F16 and BF16 pools, nor with pools of another
+ * number of KV heads.  0 on bad arguments.
  */
 size_t paged_sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
                                     int max_seq_len, int max_selected);

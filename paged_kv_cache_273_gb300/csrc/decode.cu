@@ -90,6 +90,8 @@ bool encode_gather_row_map(CUtensorMap *map, const void *base, int row_bytes, in
 
 size_t decode_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads)
 {
+    if (pool->kv_dtype == PKV_F8)
+        return block_workspace_bytes(pool, batch, num_q_heads);
     const int G = num_q_heads / pool->num_kv_heads;
     const size_t counters = align_up((size_t)batch * pool->num_kv_heads * sizeof(int), 256);
     const size_t entries = (size_t)std::max(pool->num_sms, 1) + (size_t)batch * pool->num_kv_heads;

@@ -389,6 +389,13 @@ __device__ __forceinline__ float warp_max(float x)
     return y;
 }
 
+// 2^(m - top), the weight of a state in a join; 0 where neither has seen a score
+// above -inf.
+__device__ __forceinline__ float join_weight(float m, float top)
+{
+    return top == -INFINITY ? 0.0f : kern::exp2_approx(m - top);
+}
+
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll
@@ -583,10 +590,12 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
                 my1 = fmaxf(my1, __shfl_xor_sync(FULL_MASK, my1, mask));
             }
         }
-        const float m0 = fmaxf(st.m[0], ceilf(mx0)), m1 = fmaxf(st.m[1], ceilf(mx1));
-        const float c0 = kern::exp2_approx(st.m[0] - m0), c1 = kern::exp2_approx(st.m[1] - m1);
-        st.m[0] = m0;
-        st.m[1] = m1;
+        const float t0 = fmaxf(st.m[0], ceilf(mx0)), t1 = fmaxf(st.m[1], ceilf(mx1));
+        // (a head whose scores are all -inf so far has nothing to rescale)
+        const float c0 = !C::F8 && t0 == -INFINITY ? 1.0f : kern::exp2_approx(st.m[0] - t0);
+        const float c1 = !C::F8 && t1 == -INFINITY ? 1.0f : kern::exp2_approx(st.m[1] - t1);
+        st.m[0] = t0;
+        st.m[1] = t1;
         st.l[0] *= c0;
         st.l[1] *= c1;
         float a0 = c0, a1 = c1;
@@ -605,11 +614,15 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
             st.acc[j][3] *= a1;
         }
     }
+    // (keys of 16-bit caches may hold infinities: no weight, rather than inf - inf,
+    // for scores of -inf while there has been no other)
+    const float m0 = !C::F8 && st.m[0] == -INFINITY ? 0.0f : st.m[0];
+    const float m1 = !C::F8 && st.m[1] == -INFINITY ? 0.0f : st.m[1];
     uint32_t bf[NS][weight_mmas<KV, G>()][2];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        const float x0 = x[n][0] - st.m[0], x1 = x[n][1] - st.m[1];
-        const float x2 = x[n][2] - st.m[0], x3 = x[n][3] - st.m[1];
+        const float x0 = x[n][0] - m0, x1 = x[n][1] - m1;
+        const float x2 = x[n][2] - m0, x3 = x[n][3] - m1;
         float p0 = kern::exp2_approx(x0), p1 = kern::exp2_approx(x1);
         float p2 = kern::exp2_approx(x2), p3 = kern::exp2_approx(x3);
         st.l[0] += p0 + p2;
@@ -644,9 +657,10 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     const int B = p.batch, Hkv = p.num_kv_heads, Hq = p.num_q_heads;
     const int cta = blockIdx.x;
 
-    // Over chosen blocks the kernel before this one is the one that chose them: it
-    // writes their list alone, and it let this kernel start only after all before
-    // it had completed, so that lengths and q may be read ahead of the wait.
+    // Over chosen blocks the kernel before this one is the one that chose them: of
+    // what this kernel reads it writes their list alone, and it let this kernel
+    // start only after all before it had completed, so that the lengths may be
+    // read ahead of the wait.
     if (!p.per_head) {
         grid_dependency_wait();
         grid_dependents_launch();
@@ -938,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
             const float m = member ? mine_state[G * D + g] : -INFINITY;
             const float l = member ? mine_state[G * D + G + g] : 0.0f;
             top[o] = warp_max(m);
-            w[o] = member ? kern::exp2_approx(m - top[o]) : 0.0f;
+            w[o] = member ? join_weight(m, top[o]) : 0.0f;
             den[o] = warp_sum(w[o] * l);
             num[o] = 0.0f;
         }
@@ -1032,8 +1046,8 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
             for (int o = 0; o < MO; ++o) {
                 const bool in = lane < qn;
                 const float mn = fmaxf(top[o], warp_max(in ? m[o] : -INFINITY));
-                const float a = kern::exp2_approx(top[o] - mn);
-                const float w = in ? kern::exp2_approx(m[o] - mn) : 0.0f;
+                const float a = join_weight(top[o], mn);
+                const float w = in ? join_weight(m[o], mn) : 0.0f;
                 den[o] = fmaf(den[o], a, warp_sum(in ? w * l[o] : 0.0f));
                 num[o] *= a;
                 top[o] = mn;

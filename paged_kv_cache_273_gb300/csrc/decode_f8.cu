@@ -19,9 +19,8 @@ blk::Params block_params(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
     p.seq_lens = seq_lens;
     p.out = out;
     p.counters = static_cast<int *>(workspace);
-    p.partials = reinterpret_cast<float *>(
-        static_cast<unsigned char *>(workspace) +
-        ((size_t)batch * pool->num_kv_heads * sizeof(int) + 255) / 256 * 256);
+    p.partials = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                           block_counter_bytes(pool));
     p.err = pool->d_err;
     p.batch = batch;
     p.num_q_heads = num_q_heads;

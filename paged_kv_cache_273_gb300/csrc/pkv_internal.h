@@ -114,6 +114,23 @@ int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_d
                          const int32_t *slots, int num_tokens, int8_t *bounds, int32_t *exps,
                          pkv_stream_t stream);
 
+// The workspace of decode_blocks_kernel and select_kernel starts with a counter
+// for each KV head of the largest batch, whatever the call's batch: one buffer,
+// zeroed once, then serves calls of any batch, since none writes its scratch
+// where another has counters.  Behind them the partials (softmax states of
+// pieces shared between CTAs).
+inline size_t block_counter_bytes(const pkv_pool *pool)
+{
+    return ((size_t)4096 * pool->num_kv_heads * sizeof(int) + 255) / 256 * 256;
+}
+inline size_t block_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads)
+{
+    const size_t entries = (size_t)(pool->num_sms > 1 ? pool->num_sms : 1) +
+                           (size_t)batch * pool->num_kv_heads;
+    const size_t state = (size_t)(num_q_heads / pool->num_kv_heads) * (pool->head_dim + 2);
+    return block_counter_bytes(pool) + (entries * state * sizeof(float) + 255) / 256 * 256;
+}
+
 // Decode attention over an 8-bit float cache (decode_f8.cu).
 int launch_decode_f8(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num_q_heads,
                      const void *k_cache, const void *v_cache, const void *k_scales,

@@ -474,9 +474,10 @@ __global__ void __launch_bounds__(NT, 2) select_kernel(const SelectArgs a)
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// The regions of the workspace behind the attention's own.
+// The regions of the workspace behind the counters (which the choice and the
+// attention use one after the other, each leaving them zero) and the partials.
 struct Regions {
-    size_t counters, phys, keys, total;
+    size_t phys, keys, total;
 };
 
 Regions regions(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_len, int budget)
@@ -484,8 +485,7 @@ Regions regions(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_le
     const size_t segs = (size_t)batch * pool->num_kv_heads;
     const size_t n = ((size_t)max_seq_len + pool->block_size - 1) / pool->block_size;
     Regions r;
-    r.counters = up256(decode_workspace_bytes(pool, batch, num_q_heads));
-    r.phys = r.counters + up256(segs * sizeof(int));
+    r.phys = block_workspace_bytes(pool, batch, num_q_heads);
     r.keys = r.phys + up256(segs * budget * sizeof(int32_t));
     r.total = r.keys + up256(segs * n * sizeof(uint32_t));
     return r;
@@ -542,7 +542,7 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     a.selected = selected;
     a.phys = reinterpret_cast<int32_t *>(ws + r.phys);
     a.keys = reinterpret_cast<uint32_t *>(ws + r.keys);
-    a.counters = reinterpret_cast<int *>(ws + r.counters);
+    a.counters = reinterpret_cast<int *>(ws);
     a.err = pool->d_err;
     a.batch = batch;
     a.num_kv_heads = H;

@@ -425,6 +425,22 @@ def test_step_and_noalloc_take_f8_pools():
 
 
 @pytest.mark.gpu
+def test_one_workspace_for_calls_of_every_batch():
+    # sized for the largest of them; each call's scratch must leave the others' counters alone
+    c = Cache(300, 2, 16, 128, seed=41, exp=(-9, -6))
+    ws = pkv.alloc_workspace(c.pool, 300, 16)
+    g = np.random.default_rng(1)
+    for B, top in ((1, 4000), (300, 200), (7, 3000), (1, 4800), (150, 700), (3, 4800), (300, 400)):
+        lens = g.integers(0, top + 1, B).tolist()
+        lens[0] = top
+        tables = _batch(c, lens, B)
+        q = _rows(B, (B, 16, 128), "bf16", 1.5)
+        out = _attend(c, q, tables, lens, 0.09, ws=ws)
+        assert not ws[:4 * 2 * 4096].any().item()
+        _check(c, q, tables, lens, 0.09, out, seqs=range(0, B, max(1, B // 5)))
+
+
+@pytest.mark.gpu
 def test_caches_beyond_4_gib():
     # the last blocks of caches of 5 GB: append, bounds, attention, attention over chosen blocks
     NB, H, bs, D, G = 310000, 8, 16, 128, 4

@@ -51,7 +51,8 @@ def test_workspace_grows_with_what_it_holds():
     pool = pkv.kv_block_pool_init(8, 16, 2, 64, pkv.PKV_F16)
     w = pkv.paged_sparse_workspace_bytes
     base = w(pool, 4, 8, 1000, 8)
-    assert base >= pkv.paged_decode_workspace_bytes(pool, 4, 8) + 4 * 2 * (4 + 8 * 4 + 63 * 4)
+    # counters of the largest batch, the chosen ids, the scores of 63 blocks
+    assert base >= 4 * 2 * (4096 + 4 * 8 + 4 * 63)
     assert w(pool, 8, 8, 1000, 8) > base and w(pool, 4, 8, 100000, 8) > base
     assert w(pool, 4, 8, 1000, 64) > base
 
@@ -313,6 +314,43 @@ def test_sparse_with_room_for_all_is_the_dense_call():
                                torch.tensor(lens, dtype=torch.int32, device=DEV), 0.09, dense,
                                pkv.alloc_workspace(s.pool, 5, 16), 1000, s.ks, s.vs)
     assert torch.equal(out, dense)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["f16", "f8"])
+def test_one_workspace_for_calls_of_every_shape(kv):
+    s = Sparse(kv, 200, 2, 8, 64, seed=18)
+    ws = pkv.alloc_sparse_workspace(s.pool, 90, 8, 8 * 700, 40)
+    g = np.random.default_rng(2)
+    for B, top, budget in ((1, 5600, 40), (90, 900, 5), (2, 5600, 3), (40, 2000, 40), (90, 5600, 17)):
+        lens = g.integers(0, top + 1, B).tolist()
+        lens[0] = top
+        tables = _tables(200, lens, 8, B)
+        q = _rows(B, (B, 8, 64), "f16", 1.5)
+        out, sel, _ = s.call(q, tables, lens, budget, 0.125, ws=ws)
+        assert not ws[:4 * 2 * 4096].any().item()
+        s.check(q, tables, lens, budget, 0.125, out, sel, seqs=range(0, B, max(1, B // 6)))
+        if kv == "f8":                                    # the dense call's counters are the same
+            pkv.paged_decode_attention(s.pool, q, s.k, s.v, torch.from_numpy(tables).to(DEV),
+                                       torch.tensor(lens, dtype=torch.int32, device=DEV), 0.125,
+                                       torch.zeros_like(out), ws, top, s.ks, s.vs)
+
+
+@pytest.mark.gpu
+def test_sparse_infinite_keys():
+    # scores of -inf for whole tiles, and for all of a sequence but its last rows, weigh nothing
+    s = Sparse("f16", 40, 1, 16, 64, seed=19)
+    s.k[:30] = 0
+    s.k[:30, :, :, 0] = -math.inf
+    s.hk = s.k.double().cpu().numpy()
+    q = _rows(3, (2, 4, 64), "f16").abs() + 0.1           # q > 0: q . k = -inf there
+    lens = [31 * 16 + 5, 35 * 16]
+    tables = np.stack([np.arange(40), np.arange(40)]).astype(np.int32)
+    out, sel, _ = s.call(q, tables, lens, 40, 0.125)
+    for b, n in enumerate(lens):
+        o, tol = R.attend(q[b].double().cpu().numpy(), s.hk[30:, 0].reshape(-1, 64)[:n - 480],
+                          s.hv[30:, 0].reshape(-1, 64)[:n - 480], 0.125)
+        assert np.abs(out[b].double().cpu().numpy() - o).max() <= tol
 
 
 @pytest.mark.gpu
