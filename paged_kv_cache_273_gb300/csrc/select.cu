@@ -43,8 +43,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int NT = 256;              // threads of a CTA
-constexpr int NW = NT / 32;
+constexpr int RANKED = 256;          // keys left open that are ranked among one another
 constexpr int SMEM_KEYS = 24576;     // score keys that are staged in shared memory, with their ids
 
 struct SelectArgs {
@@ -75,20 +74,23 @@ __device__ __forceinline__ uint32_t sort_key(float x)
 // The `want` largest of n keys (ties: lowest index first), 0 < want < n: their
 // indices, ascending, to sel, their ids to phys.  Keys and ids may be staged, or in
 // the workspace and the block table.
+template <int NT>
 struct Pick {
+    static constexpr int NW = NT / 32;
     int hist[3][256];                    // counts of digit d in d mod 3
-    uint32_t cand[NT];                   // the keys that the digits so far leave open
+    uint32_t cand[RANKED];                   // the keys that the digits so far leave open
     uint32_t lo[NW], hi[NW];
     int gt[NW], eq[NW];
     int ncand, left;
     uint32_t t;
 };
 
-template <bool STAGED>
+template <int NT, bool STAGED>
 __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, int n, int want,
-                                     int32_t *sel, int32_t *phys, Pick &s)
+                                     int32_t *sel, int32_t *phys, Pick<NT> &s)
 {
-    constexpr int BATCH = 8;             // keys a thread loads before it uses them
+    constexpr int NW = NT / 32;
+    constexpr int BATCH = 4;             // keys a thread loads before it uses them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto key = [&](int i) { return STAGED ? keys[i] : __ldcg(keys + i); };
     // f(key) for every key, in no particular order
@@ -117,7 +119,8 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
         s.lo[warp] = lo;
         s.hi[warp] = hi;
     }
-    s.hist[0][tid] = s.hist[1][tid] = 0;
+    if (tid < 256)
+        s.hist[0][tid] = s.hist[1][tid] = 0;
     if (tid == 0)
         s.ncand = 0;
     __syncthreads();
@@ -127,13 +130,13 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
         hi = max(hi, s.hi[w]);
     }
     // t, relative to lo: the want-th largest key, by digits of up to 8 bits; `left`
-    // of the keys that share t's digits so far are still to take.  Once no more
-    // than a thread each are open, their ranks among one another say the rest.
+    // of the keys that share t's digits so far are still to take.  Once few are
+    // open, their ranks among one another say the rest.
     int top = hi > lo ? 32 - __clz(hi - lo) : 0;      // bits not decided yet
     uint32_t t = 0;
     int left = want, open = n;
 #pragma unroll 1
-    for (int d = 0; top > 0 && open > NT; ++d) {
+    for (int d = 0; top > 0 && open > RANKED; ++d) {
         int *hist = s.hist[d % 3];
         const int shift = max(top - 8, 0);
         const uint32_t mask = (1u << (top - shift)) - 1u;
@@ -144,7 +147,8 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
         });
         // the next digit's counts at zero; digit d - 2's, in the same place, were
         // read before the last barrier
-        s.hist[(d + 1) % 3][tid] = 0;
+        if (tid < 256)
+            s.hist[(d + 1) % 3][tid] = 0;
         __syncthreads();
         // every warp finds the digit for itself, bins from the top: lane l
         // holds bins 255 - 8 l .. 248 - 8 l
@@ -256,12 +260,13 @@ __device__ __forceinline__ void pick(const uint32_t *keys, const int32_t *ids, i
     });
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(NT, 2) select_kernel(const SelectArgs a)
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a)
 {
+    constexpr int NW = NT / 32;
     constexpr int NC = D / 32;               // 16-byte chunks a lane reads of a block's bounds
     extern __shared__ uint32_t s_keys[];     // keys, then (from a.stage on) ids
-    __shared__ Pick s_pick;
+    __shared__ Pick<NT> s_pick;
     __shared__ int s_last;
     grid_dependency_wait();
     grid_dependents_launch();
@@ -466,10 +471,10 @@ __global__ void __launch_bounds__(NT, 2) select_kernel(const SelectArgs a)
         }
     }
     if (a.stage)
-        pick<true>(s_keys, reinterpret_cast<const int32_t *>(s_keys + a.stage), n - 1,
-                   a.budget - 1, sel, phys, s_pick);
+        pick<NT, true>(s_keys, reinterpret_cast<const int32_t *>(s_keys + a.stage), n - 1,
+                       a.budget - 1, sel, phys, s_pick);
     else
-        pick<false>(keys, row, n - 1, a.budget - 1, sel, phys, s_pick);
+        pick<NT, false>(keys, row, n - 1, a.budget - 1, sel, phys, s_pick);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -491,26 +496,37 @@ Regions regions(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_le
     return r;
 }
 
-template <int D, int G>
+template <int D, int G, int NT>
 cudaError_t launch_select_t(const SelectArgs &a, unsigned grid, size_t smem, cudaStream_t s)
 {
     if (smem > 40000) {
         const cudaError_t e = cudaFuncSetAttribute(
-            select_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            select_kernel<D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
     }
-    return launch_pdl(select_kernel<D, G>, dim3(grid), dim3(NT), smem, s, a);
+    return launch_pdl(select_kernel<D, G, NT>, dim3(grid), dim3(NT), smem, s, a);
+}
+
+// 16 warps a CTA where every CTA has an SM to itself, else 8 and two CTAs a SM
+// (256 CTAs on 152 SMs: 38 instead of 43 us with the attention behind them).
+template <int D, int G>
+cudaError_t launch_select_g(const SelectArgs &a, int num_sms, unsigned grid, size_t smem,
+                            cudaStream_t s)
+{
+    return (int64_t)grid <= num_sms ? launch_select_t<D, G, 512>(a, grid, smem, s)
+                                    : launch_select_t<D, G, 256>(a, grid, smem, s);
 }
 
 template <int D>
-cudaError_t launch_select(const SelectArgs &a, int G, unsigned grid, size_t smem, cudaStream_t s)
+cudaError_t launch_select(const SelectArgs &a, int G, int num_sms, unsigned grid, size_t smem,
+                          cudaStream_t s)
 {
     switch (G) {
-    case 1: return launch_select_t<D, 1>(a, grid, smem, s);
-    case 2: return launch_select_t<D, 2>(a, grid, smem, s);
-    case 4: return launch_select_t<D, 4>(a, grid, smem, s);
-    default: return launch_select_t<D, 8>(a, grid, smem, s);
+    case 1: return launch_select_g<D, 1>(a, num_sms, grid, smem, s);
+    case 2: return launch_select_g<D, 2>(a, num_sms, grid, smem, s);
+    case 4: return launch_select_g<D, 4>(a, num_sms, grid, smem, s);
+    default: return launch_select_g<D, 8>(a, num_sms, grid, smem, s);
     }
 }
 
@@ -554,11 +570,15 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     a.max_n = (int)((max_seq_len + (int64_t)bs - 1) / bs);
     a.budget = budget;
     a.q_dtype = q_dtype;
-    // a CTA's chunk: whole groups of 32 blocks for its warps, two CTAs a SM (as many as are resident)
+    // a CTA's chunk: all of a (sequence, KV head)'s blocks where there are enough
+    // of those for most SMs (nothing is handed from CTA to CTA then), else in
+    // steps of 8 warps' groups what gives every SM a CTA
     const int64_t segs = (int64_t)batch * H, n = (cap + bs - 1) / bs;
-    const int64_t per = (segs * n + (int64_t)pool->num_sms * 2 - 1) / ((int64_t)pool->num_sms * 2);
-    const int64_t span = 32 * NW;
+    const int64_t per = (segs * n + pool->num_sms - 1) / pool->num_sms;
+    const int64_t span = 256;
     a.chunk = (int)std::max<int64_t>(span, (per + span - 1) / span * span);
+    if (segs * 3 >= (int64_t)pool->num_sms * 2 && n <= SMEM_KEYS)
+        a.chunk = (int)std::max<int64_t>(a.chunk, n);
     a.chunks = (int)std::max<int64_t>(1, (n + a.chunk - 1) / a.chunk);
     a.stage = n <= SMEM_KEYS ? (int)n : 0;
     const size_t smem = (size_t)a.stage * 8;
@@ -570,8 +590,8 @@ int launch_sparse(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int nu
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(segs * a.chunks);
     const int G = num_q_heads / H;
-    const cudaError_t e = pool->head_dim == 64 ? launch_select<64>(a, G, grid, smem, s)
-                                               : launch_select<128>(a, G, grid, smem, s);
+    const cudaError_t e = pool->head_dim == 64 ? launch_select<64>(a, G, pool->num_sms, grid, smem, s)
+                                               : launch_select<128>(a, G, pool->num_sms, grid, smem, s);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess)
         return PKV_ERR_CUDA;
     blk::Params p = block_params(pool, q, q_dtype, num_q_heads, k_cache, v_cache, k_scales,
