@@ -27,7 +27,7 @@ CUDA_SOURCES = ["append.cu", "decode.cu", "decode_f32.cu", "decode_f16.cu", "dec
                 "append_blocks.cu", "select.cu"]
 HOST_SOURCES = ["pool.cpp"]
 HEADERS = ["pkv_internal.h", "device_common.cuh", "decode_kernel.cuh",
-           "decode_blocks.cuh"]
+           "blocks_common.cuh", "decode_blocks.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -17,7 +17,7 @@
 // rows stay in registers between the maximum and the rounding.
 #include <cuda_runtime.h>
 
-#include "device_common.cuh"
+#include "blocks_common.cuh"
 
 namespace pkv {
 namespace {

@@ -35,9 +35,16 @@
 //    that whatever they hold (NaN codes of an earlier owner) is never read.
 #pragma once
 
+#include "blocks_common.cuh"
 #include "decode_kernel.cuh"
 
 namespace pkv {
+namespace kern {
+
+template <> struct KvBits<PKV_F8> { static constexpr int v = 8; };
+
+}  // namespace kern
+
 namespace blk {
 
 using namespace dev;
@@ -525,6 +532,64 @@ __device__ __forceinline__ void join_parts(State<D, G, KV> &st)
     }
 }
 
+// S^T = K q^T of the tile at sK, rows gid and gid + 8 and the lane's quarter of d
+// (the fragments of the kernel for the other caches): e4m3 codes become fp16
+// exactly, word ks of a quarter row being the pairs of k-step ks.
+template <int D, int G, int KV>
+__device__ __forceinline__ void tile_scores(float (&s)[4], const State<D, G, KV> &st,
+                                            const unsigned char *sK, int lane)
+{
+    if constexpr (KV == PKV_F8) {
+        using M = kern::MmaCfg<D, KV>;
+        const int gid = lane >> 2, tig = lane & 3;
+        const uint32_t k0 = gid * M::ROWB + tig * M::KQB, k1 = k0 + 8 * M::ROWB;
+        // two chains, so that a tile's MMAs wait for half as many others
+        float s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < M::KCH; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(sK + kern::swz_off(k0 + c * 16, true));
+            const uint4 y = *reinterpret_cast<const uint4 *>(sK + kern::swz_off(k1 + c * 16, true));
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ks = 4 * c + i;
+                uint32_t a0, a1, a2, a3;
+                f8x4_to_half2(xw[i], a0, a2);
+                f8x4_to_half2(yw[i], a1, a3);
+                kern::mma_16816<false>((i & 1) ? s2 : s, a0, a1, a2, a3, st.qh[ks][0],
+                                       st.qh[ks][1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[i] += s2[i];
+    } else {
+        kern::mma_scores<D, G, KV, false>(s, st, sK, lane, true);
+    }
+}
+
+// The lane's eighth of the V rows of tokens 2 tig, + 1, + 8, + 9 of the tile at sV.
+template <int D, int KV>
+__device__ __forceinline__ void tile_values(uint32_t (&vw)[4][kern::VFrag<D, KV>::VW],
+                                            const unsigned char *sV, int lane)
+{
+    using M = kern::MmaCfg<D, KV>;
+    if constexpr (M::VB >= 16) {
+        kern::load_v_frag<D, KV>(vw, sV, lane, true);
+    } else {
+        const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v0 = (2 * tig + (i & 1) + 8 * (i >> 1)) * M::ROWB + gid * M::VB;
+            const uint2 x = *reinterpret_cast<const uint2 *>(
+                sV + kern::swz_off(v0 & ~15u, true) + (v0 & 15u));
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+        }
+    }
+}
+
 // NS tiles of a piece: scores, online softmax, weighted V (see the head of the
 // file).
 template <int D, int G, int KV, int NS>
@@ -540,8 +605,8 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        kern::mma_scores<D, G, KV, false>(s, st, stage[n], lane, true);
-        kern::load_v_frag<D, KV>(vw[n], stage[n] + C::TILE_BYTES, lane, true);
+        tile_scores<D, G, KV>(s, st, stage[n], lane);
+        tile_values<D, KV>(vw[n], stage[n] + C::TILE_BYTES, lane);
         f[n][0] = f[n][1] = 0.0f;
         if constexpr (C::F8) {
             // the K scales, and the exponents of the V scales, of tokens gid,

@@ -97,7 +97,6 @@ template <> struct KvBits<PKV_F16> { static constexpr int v = 16; };
 template <> struct KvBits<PKV_BF16> { static constexpr int v = 16; };
 template <> struct KvBits<PKV_I8> { static constexpr int v = 8; };
 template <> struct KvBits<PKV_I4> { static constexpr int v = 4; };
-template <> struct KvBits<PKV_F8> { static constexpr int v = 8; };
 
 // Quantized caches carry one fp16 scale per cached row.
 __host__ __device__ constexpr bool quantized(int KV) { return KV == PKV_I8 || KV == PKV_I4; }
@@ -731,7 +730,7 @@ __device__ __forceinline__ int q_elem_index(int ks, int h, int u, int rot)
         constexpr int KCH = MmaCfg<D, KV>::KCH;
         const int chunk = ((ks >> 1) + rot) & (KCH - 1);
         return 8 * chunk + 4 * (ks & 1) + 2 * h + u;
-    } else if constexpr (KV == PKV_I8 || KV == PKV_F8) {
+    } else if constexpr (KV == PKV_I8) {
         return 4 * ks + 2 * h + u;                       // word ks, bytes 2h + u
     } else {
         // 4-bit: word w = ks / 2 holds codes 8w..8w+7; pair k = 2 (ks % 2) + h
@@ -830,27 +829,6 @@ __device__ __forceinline__ void mma_scores(float (&s)[4], const MmaState<D, G, K
                         mma_16816<BF>(s, a0, a1, a2, a3, st.ql[ks][0], st.ql[ks][1]);
                 }
             }
-        } else if constexpr (KV == PKV_F8) {
-            // two chains, so that a tile's MMAs wait for half as many others
-            float s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < M::KCH; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(sK + swz_off(k0 + c * 16, sw));
-                const uint4 y = *reinterpret_cast<const uint4 *>(sK + swz_off(k1 + c * 16, sw));
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ks = 4 * c + i;
-                    uint32_t a0, a1, a2, a3;
-                    f8x4_to_half2(xw[i], a0, a2);
-                    f8x4_to_half2(yw[i], a1, a3);
-                    mma_16816<BF>((i & 1) ? s2 : s, a0, a1, a2, a3, st.qh[ks][0], st.qh[ks][1]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s[i] += s2[i];
         } else {
             static_assert(KV == PKV_I4 && D == 128, "4-bit rows are d = 128");
             const uint4 x = *reinterpret_cast<const uint4 *>(sK + k0);
@@ -899,10 +877,6 @@ __device__ __forceinline__ void load_v_frag(uint32_t (&vw)[4][VFrag<D, KV>::VW],
                     vw[i][4 * c] = x.x; vw[i][4 * c + 1] = x.y;
                     vw[i][4 * c + 2] = x.z; vw[i][4 * c + 3] = x.w;
                 }
-            } else if constexpr (KV == PKV_F8) {
-                const uint2 x =
-                    *reinterpret_cast<const uint2 *>(sV + swz_off(v0 & ~15u, sw) + (v0 & 15u));
-                vw[i][0] = x.x; vw[i][1] = x.y;
             } else {
                 const uint2 x = *reinterpret_cast<const uint2 *>(p);
                 vw[i][0] = x.x; vw[i][1] = x.y;
