@@ -666,7 +666,7 @@ size_t paged_sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_h
  *     sum_d (max(qi_d, 0) * upper_d + min(qi_d, 0) * lower_d)
  *       * 2^(the block's bound exponent),
  * an upper bound of q . k over the block's keys, up to the rounding of q, in
- * units of 2^eq; it is computed exactly (within fp32's exponents).
+ * units of 2^eq; scores are compared exactly.
  *
  *   bounds, bound_exps  as kv_bounds_append keeps them.
  *   selected     device int32 [B][Hkv][max_selected], receives the chosen blocks'

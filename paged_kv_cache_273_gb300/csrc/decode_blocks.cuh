@@ -8,8 +8,9 @@
 //
 // How:
 //  * The work is one list of 16-token tiles, ordered by (sequence, KV head,
-//    tile).  CTA c of P takes the tiles [c T / P, (c + 1) T / P), and its
-//    warps equal parts of those: every warp streams a contiguous run of tiles
+//    tile).  CTA c of P takes the tiles [c T / P, (c + 1) T / P), or, of
+//    sequences about as long as one another, whole (sequence, KV head)s; its
+//    warps take equal parts of those: every warp streams a contiguous run of tiles
 //    through a ring of its own (cp.async, completion counted per thread), so
 //    no warp waits for another and nothing waits on a flag or barrier until
 //    the CTA's end.
@@ -79,7 +80,7 @@ struct Cfg {
     static constexpr bool PAIR = F8 && D == 64;
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
-    // ring stages that fit beside the states and the tile prefix, at most 4,
+    // ring stages that fit beside the states and the tile prefix, at most 6,
     // with 20 KB of the SM's shared memory left if that costs no stage that is
     // needed: room for a CTA of the kernel launched next, whose start then
     // overlaps this one's end (with all of it taken, the choice of blocks
@@ -191,11 +192,11 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+static __device__ __noinline__ int long_quotient(int x, int d) { return x / d; }
+
 // x / d of non-negative ints; a fraction of an integer division's latency where
 // both the quotient's distance to the next whole number, at least 1 / (2 d), and
 // fp32's error in it, at most (x / d) 2^-22, leave no doubt: x < 2^20.
-static __device__ __noinline__ int long_quotient(int x, int d) { return x / d; }
-
 __device__ __forceinline__ int quotient(int x, int d)
 {
     return x < (1 << 20) ? (int)__fdividef((float)x + 0.5f, (float)d) : long_quotient(x, d);

@@ -7,9 +7,10 @@
 // group's query values in steps of one power of two, qi = rint(q 2^-eq) in
 // [-127, 127], the sum is of whole numbers, qi+ . h + qi- . l with the
 // positive and the negative parts of qi (sum_d max(qi l, qi h), as l <= h), below 2^22,
-// and the block's score, its largest over the group's heads times 2^e, is
-// exact in fp32: which blocks are chosen does not depend on the order of any
-// sum.  2^eq is common to the blocks and left out.
+// and the block's score, its largest over the group's heads times 2^(e - 22),
+// is exact in fp32 for every e of a block (-96 to 120): which blocks are chosen
+// does not depend on the order of any sum.  2^(eq + 22) is common to the blocks
+// and left out.
 //
 // Work.  Bounds are read once, 2 D + 4 bytes a (block, KV head).  The scores
 // of 16 blocks and all heads of the group are warp-level MMAs on fp16 (int8
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
             if (j < j_end) {
                 const int ec = min(max(e_now, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
                 const uint32_t k =
-                    ok ? sort_key((lane < 16 ? even : odd) * pow2_f32(ec)) : 0u;
+                    ok ? sort_key((lane < 16 ? even : odd) * pow2_f32(ec - 22)) : 0u;
                 if (parts == 1 && a.stage) {
                     s_keys[j] = k;
                     s_keys[a.stage + j] = raw_now;

@@ -282,6 +282,22 @@ def test_sparse_exponents_far_apart():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lo,hi", [(105, 121), (-96, -80)])
+def test_sparse_exponents_at_the_ends(lo, hi):
+    # whole-number sums up to 2^21 in units of up to 2^120: scores beyond fp32's largest number
+    g = np.random.default_rng(4)
+    s = Sparse("bf16", 64, 2, 16, 128, seed=7, exps=lambda e: g.integers(lo, hi, e.shape))
+    s.hb[:] = np.sort(g.integers(-127, 128, s.hb.shape), 2)
+    s.sync()
+    lens = [16 * 64, 900]
+    tables = np.stack([g.permutation(64) for _ in range(2)]).astype(np.int32)
+    q = _rows(1, (2, 16, 128), "bf16")
+    for budget in (2, 9, 40):
+        out, sel, _ = s.call(q, tables, lens, budget, 0.09)
+        s.check(q, tables, lens, budget, 0.09, out, sel)
+
+
+@pytest.mark.gpu
 def test_sparse_scores_crowded_in_a_few_digits():
     # a few blocks far off, so that the thousands of others share the first digits of the search
     # for the last one chosen; many of them equal
