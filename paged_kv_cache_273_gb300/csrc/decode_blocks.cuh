@@ -80,16 +80,12 @@ struct Cfg {
     static constexpr bool PAIR = F8 && D == 64;
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
-    // ring stages that fit beside the states and the tile prefix, at most 6,
-    // with 20 KB of the SM's shared memory left if that costs no stage that is
-    // needed: room for a CTA of the kernel launched next, whose start then
-    // overlaps this one's end (with all of it taken, the choice of blocks
-    // followed by the attention over them took 57 instead of 50 us on 16
-    // sequences of 2048 blocks).
+    // ring stages that fit beside the states and the tile prefix, at most 5 (six
+    // for e4m3 rows of 64: 36.5 instead of 35.1 us on 64 sequences of up to 2048
+    // tokens, 12 heads)
     static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 6 * 16 + W * 16 + 256;
-    static constexpr int FIT20 = (212448 - FIXED) / (W * STAGE);
-    static constexpr int FIT = FIT20 >= (F8 ? 3 : 2) ? FIT20 : (232448 - FIXED) / (W * STAGE);
-    static constexpr int NST = FIT > 6 ? 6 : FIT;
+    static constexpr int FIT = (232448 - FIXED) / (W * STAGE);
+    static constexpr int NST = FIT > 5 ? 5 : FIT;
     static_assert(NST >= (PAIR ? 3 : 2), "ring");
     static_assert(NST * STAGE >= STATE * 4, "a warp's last state takes its ring's place");
     static_assert(TILE_BYTES % 1024 == 0 || STAGE % 128 == 0, "swizzle period");

@@ -506,6 +506,17 @@ cudaError_t launch_select_t(const SelectArgs &a, unsigned grid, size_t smem, cud
         if (e != cudaSuccess)
             return e;
     }
+    // of the SM's 228 KB for shared memory and L1 no more than the CTAs use as shared
+    // memory: up to 128 KB of bounds are in flight through the L1, and without this
+    // the kernel runs with the division that the one before it had (behind the
+    // attention with all of it as shared memory, 54 instead of 46 us for the choice
+    // of 128 of 2048 blocks of 16 sequences and the attention over them)
+    const size_t used = 512 / NT * (smem + sizeof(Pick<NT>) + 1280);
+    const int percent = (int)std::min<size_t>(100, (used * 100 + 233471) / 233472);
+    const cudaError_t e = cudaFuncSetAttribute(
+        select_kernel<D, G, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
+    if (e != cudaSuccess)
+        return e;
     return launch_pdl(select_kernel<D, G, NT>, dim3(grid), dim3(NT), smem, s, a);
 }
 
