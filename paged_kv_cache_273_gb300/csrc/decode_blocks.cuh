@@ -24,14 +24,21 @@
 //  * Tile math: warp-level MMAs as in the kernel for the other caches; e4m3
 //    codes become fp16 exactly, q becomes fp16 exactly (a bf16 q is brought
 //    to [2^14, 2^15) by a power of two first), products are exact and sums
-//    fp32.  A V scale 2^ev is part of the weight's exponent: with x a row's
-//    score * log2(e), the denominator sums 2^(x - m) and the weighted V sums
-//    w c with w = 2^(x - m + ev - (n - m)) <= 1, c the V codes, where m and n
-//    are whole numbers at or above the largest x and the largest x + ev so
-//    far.  So a weight needs no multiplication by its scale and stays in
-//    fp16's range whatever the scales are, both sums come from the same
-//    rounded x - m, and every rescaling is by a power of two.  Weights are
-//    split into two fp16 or three bf16 parts.
+//    fp32.  With x a row's score * log2(e) and m a whole number at or above the
+//    largest x so far, a row's weight is p = 2^(x - m) <= 1; the denominator
+//    sums p, the numerator p times the row of V, as an MMA for each tile whose
+//    sum is added to the running one in fp32.
+//  * Weights are split into two fp16 or three bf16 parts.  fp16 parts are taken
+//    of 2^15 p: at 1 both parts of a small weight would lie on the one grid of
+//    fp16's subnormal numbers (2^-24), and rows 17 nats below a sequence's
+//    largest would weigh up to half as much again, or nothing.  At 2^15 the grid
+//    leaves 2^-40 of the largest weight.
+//  * A V scale 2^ev stays out of the weights: a tile's sum of p and codes is
+//    multiplied by 2^(ev - r) as it joins the running sum, r the largest exponent
+//    so far, so that blocks may be 2^126 apart.  A tile of two blocks (of 8 rows)
+//    takes the larger of two scales up to 2^4 apart, the other block's weights
+//    brought to it, and else is summed block by block.
+//  * Every rescaling is by a power of two.
 //  * Rows outside the attended range are filled with zeros by the copies, so
 //    that whatever they hold (NaN codes of an earlier owner) is never read.
 #pragma once
@@ -305,17 +312,18 @@ __device__ __forceinline__ void issue_tile(const Params &p, const Tile &d, int j
             cp16_zfill(stage + C::TILE_BYTES + dst_of(i), p.v_cache + off, v);
         }
         if constexpr (C::F8) {
-            bool v;
-            const int64_t head = head_of(lane & (TILE - 1), v);
+            // (of a block with attended rows: all of its rows' entries)
+            const int u = (lane & (TILE - 1)) >> p.bs_log2, id = u == 0 ? id0 : id1;
+            const int64_t head = (int64_t)max(id, 0) * p.num_kv_heads + kvh;
             cp4_zfill(stage + 2 * C::TILE_BYTES + lane * 4,
-                      (lane < TILE ? p.k_scales : p.v_scales) + head, v);
+                      (lane < TILE ? p.k_scales : p.v_scales) + head, id >= 0);
         }
     }
 }
 
 template <int D, int G, int KV>
 struct State : kern::MmaState<D, G, KV, false> {
-    float n[2];          // whole numbers >= x + ev of heads 2 tig, 2 tig + 1 (m: >= x)
+    int r;               // largest exponent of a V scale so far: acc's unit is 2^(r - 15)
 };
 
 // The lane's quarter of q's row for its head column (head gid mod G: the
@@ -409,9 +417,19 @@ __device__ __forceinline__ float warp_sum(float x)
 }
 
 // Parts a weight is split into, each of the MMA's type: two of fp16 leave
-// 2^-22 of it, three of bf16 2^-27 (two would leave 2^-18).
+// 2^-22 of it and 2^-25 whatever it is, three of bf16 2^-27 (two would leave
+// 2^-18).  The largest weight is 2^weight_top_log2: 2^15 for fp16, whose largest
+// number is 65504.
 template <int KV>
 __host__ __device__ constexpr int weight_parts() { return KV == PKV_BF16 ? 3 : 2; }
+template <int KV>
+__host__ __device__ constexpr int weight_top_log2() { return KV == PKV_BF16 ? 0 : 15; }
+
+// 2^d for d <= 0, 0 where that is not a normal number.
+__device__ __forceinline__ float pow2_down(int d)
+{
+    return d < -126 ? 0.0f : pow2_f32(d);
+}
 
 // The B fragments of a tile's weights.  The MMA's 8 head columns take 8 / G
 // parts of the weights at a time: column c holds part c / G of head c mod G (the
@@ -467,20 +485,21 @@ __device__ __forceinline__ void split_weights(uint32_t (&bf)[weight_mmas<KV, G>(
         }
 }
 
-// O^T += V^T P^T of NS tiles.  Their sum starts at zero and is added to the
-// running one in fp32: an MMA truncates what it adds to its accumulator, and
-// over a long run of tiles that would show (3e-6 of the result at 230 tiles a
-// warp).
+// O^T += V^T P^T of NS tiles, tile n's in units of g[n].  A tile's sum starts at
+// zero and is added to the running one in fp32: an MMA truncates what it adds to
+// its accumulator, and over a long run of tiles that would show (3e-6 of the
+// result at 230 tiles a warp).
 template <int D, int G, int KV, int NS>
 __device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
                                         const uint32_t (&vw)[NS][4][kern::VFrag<D, KV>::VW],
-                                        const uint32_t (&bf)[NS][weight_mmas<KV, G>()][2])
+                                        const uint32_t (&bf)[NS][weight_mmas<KV, G>()][2],
+                                        const float (&g)[NS])
 {
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
+            float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t a0, a1, a2, a3;
             if constexpr (KV == PKV_F8) {
                 const int w = j >> 1;
@@ -496,11 +515,10 @@ __device__ __forceinline__ void weigh_v(State<D, G, KV> &st,
 #pragma unroll
             for (int m = 0; m < weight_mmas<KV, G>(); ++m)
                 kern::mma_16816<kern::MmaBf16<KV>::v>(t, a0, a1, a2, a3, bf[n][m][0], bf[n][m][1]);
-        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            st.acc[j][u] += t[u];
-    }
+            for (int u = 0; u < 4; ++u)
+                st.acc[j][u] = KV == PKV_F8 ? fmaf(t[u], g[n], st.acc[j][u]) : st.acc[j][u] + t[u];
+        }
 }
 
 // At a piece's end: the sums of a head's parts, in the head's own columns.
@@ -587,35 +605,49 @@ __device__ __forceinline__ void tile_values(uint32_t (&vw)[4][kern::VFrag<D, KV>
     }
 }
 
+// (x, y) * f, packed.
+__device__ __forceinline__ void scale2(float &x, float &y, float f)
+{
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(f));
+}
+
 // NS tiles of a piece: scores, online softmax, weighted V (see the head of the
-// file).
-template <int D, int G, int KV, int NS>
+// file).  ONE: a tile's rows are of one block.
+template <int D, int G, int KV, int NS, bool ONE>
 __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)[2],
                                       const unsigned char *const (&stage)[NS],
-                                      const int (&bits)[NS], bool one_block, int lane)
+                                      const int (&bits)[NS], int lane)
 {
     using C = Cfg<D, G, KV>;
     const int gid = lane >> 2;
     uint32_t vw[NS][4][kern::VFrag<D, KV>::VW];
-    float x[NS][4], f[NS][2];          // (token gid | gid + 8, heads 2 tig, 2 tig + 1); V exponents
-    float mx0 = -INFINITY, mx1 = -INFINITY, my0 = -INFINITY, my1 = -INFINITY;
+    float x[NS][4];                    // (token gid | gid + 8, heads 2 tig, 2 tig + 1)
+    int ev[NS][2], top = BLOCK_MIN_EXP;   // exponents of the V scales of rows 0..7, 8..15
+    float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         tile_scores<D, G, KV>(s, st, stage[n], lane);
         tile_values<D, KV>(vw[n], stage[n] + C::TILE_BYTES, lane);
-        f[n][0] = f[n][1] = 0.0f;
         if constexpr (C::F8) {
-            // the K scales, and the exponents of the V scales, of tokens gid,
-            // gid + 8 (of one block, unless blocks are smaller than a tile)
+            // the scales of rows 0..7 and 8..15 (of one block, unless blocks are
+            // smaller than a tile)
             const float *sc = reinterpret_cast<const float *>(stage[n] + 2 * C::TILE_BYTES);
-            const float k0 = sc[gid];
+            const float k0 = sc[0];
             float k1 = k0;
-            f[n][0] = f[n][1] = exponent_f32(sc[TILE + gid]);
-            if (!one_block) {
-                k1 = sc[gid + 8];
-                f[n][1] = exponent_f32(sc[TILE + gid + 8]);
+            ev[n][0] = ev[n][1] = block_exponent(sc[TILE]);
+            if constexpr (!ONE) {
+                k1 = sc[8];
+                // (a block without an attended row has no say)
+                if (rows_of(bits[n]) > 8)
+                    ev[n][1] = block_exponent(sc[TILE + 8]);
+                if (skip_of(bits[n]) >= 8)
+                    ev[n][0] = ev[n][1];
             }
+            top = max(top, max(ev[n][0], ev[n][1]));
             s[0] *= k0;
             s[1] *= k0;
             s[2] *= k1;
@@ -634,23 +666,15 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
         }
         mx0 = fmaxf(mx0, fmaxf(x[n][0], x[n][2]));
         mx1 = fmaxf(mx1, fmaxf(x[n][1], x[n][3]));
-        if constexpr (C::F8) {
-            my0 = fmaxf(my0, fmaxf(x[n][0] + f[n][0], x[n][2] + f[n][1]));
-            my1 = fmaxf(my1, fmaxf(x[n][1] + f[n][0], x[n][3] + f[n][1]));
-        }
     }
     bool above = mx0 > st.m[0] || mx1 > st.m[1];
     if constexpr (C::F8)
-        above |= my0 > st.n[0] || my1 > st.n[1];
+        above |= top > st.r;
     if (__any_sync(FULL_MASK, above)) {
 #pragma unroll
         for (int mask = 4; mask < 32; mask <<= 1) {
             mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, mask));
             mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, mask));
-            if constexpr (C::F8) {
-                my0 = fmaxf(my0, __shfl_xor_sync(FULL_MASK, my0, mask));
-                my1 = fmaxf(my1, __shfl_xor_sync(FULL_MASK, my1, mask));
-            }
         }
         const float t0 = fmaxf(st.m[0], ceilf(mx0)), t1 = fmaxf(st.m[1], ceilf(mx1));
         // (a head whose scores are all -inf so far has nothing to rescale)
@@ -662,11 +686,11 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
         st.l[1] *= c1;
         float a0 = c0, a1 = c1;
         if constexpr (C::F8) {
-            const float n0 = fmaxf(st.n[0], ceilf(my0)), n1 = fmaxf(st.n[1], ceilf(my1));
-            a0 = kern::exp2_approx(st.n[0] - n0);
-            a1 = kern::exp2_approx(st.n[1] - n1);
-            st.n[0] = n0;
-            st.n[1] = n1;
+            const int r = max(st.r, top);
+            const float u = pow2_down(st.r - r);
+            a0 *= u;
+            a1 *= u;
+            st.r = r;
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -680,25 +704,58 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
     // for scores of -inf while there has been no other)
     const float m0 = !C::F8 && st.m[0] == -INFINITY ? 0.0f : st.m[0];
     const float m1 = !C::F8 && st.m[1] == -INFINITY ? 0.0f : st.m[1];
-    uint32_t bf[NS][weight_mmas<KV, G>()][2];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        const float x0 = x[n][0] - m0, x1 = x[n][1] - m1;
-        const float x2 = x[n][2] - m0, x3 = x[n][3] - m1;
-        float p0 = kern::exp2_approx(x0), p1 = kern::exp2_approx(x1);
-        float p2 = kern::exp2_approx(x2), p3 = kern::exp2_approx(x3);
-        st.l[0] += p0 + p2;
-        st.l[1] += p1 + p3;
-        if constexpr (C::F8) {
-            const float d0 = st.n[0] - st.m[0], d1 = st.n[1] - st.m[1];
-            p0 = kern::exp2_approx(x0 + (f[n][0] - d0));
-            p1 = kern::exp2_approx(x1 + (f[n][0] - d1));
-            p2 = kern::exp2_approx(x2 + (f[n][1] - d0));
-            p3 = kern::exp2_approx(x3 + (f[n][1] - d1));
-        }
-        split_weights<G, KV>(bf[n], p0, p1, p2, p3, lane);
+        x[n][0] = kern::exp2_approx(x[n][0] - m0);
+        x[n][1] = kern::exp2_approx(x[n][1] - m1);
+        x[n][2] = kern::exp2_approx(x[n][2] - m0);
+        x[n][3] = kern::exp2_approx(x[n][3] - m1);
+        st.l[0] += x[n][0] + x[n][2];
+        st.l[1] += x[n][1] + x[n][3];
     }
-    weigh_v<D, G, KV, NS>(st, vw, bf);
+    constexpr float TOP = (float)(1 << weight_top_log2<KV>());
+    uint32_t bf[NS][weight_mmas<KV, G>()][2];
+    float g[NS];
+    if constexpr (!C::F8 || ONE) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            if constexpr (weight_top_log2<KV>() != 0) {
+                scale2(x[n][0], x[n][1], TOP);
+                scale2(x[n][2], x[n][3], TOP);
+            }
+            if constexpr (C::F8)
+                g[n] = pow2_down(ev[n][0] - st.r);
+            split_weights<G, KV>(bf[n], x[n][0], x[n][1], x[n][2], x[n][3], lane);
+        }
+        weigh_v<D, G, KV, NS>(st, vw, bf, g);
+    } else {
+        // two blocks a tile: together where their scales are close, else one by one
+        bool again = false;
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const int far = max(ev[n][0], ev[n][1]);
+                int e = far;
+                float f0, f1;              // of rows 0..7 and 8..15
+                if (far - min(ev[n][0], ev[n][1]) > 4) {
+                    e = pass ? ev[n][1] : ev[n][0];
+                    f0 = pass ? 0.0f : TOP;
+                    f1 = pass ? TOP : 0.0f;
+                    again = true;
+                } else {
+                    f0 = pass ? 0.0f : TOP * pow2_f32(ev[n][0] - far);
+                    f1 = pass ? 0.0f : TOP * pow2_f32(ev[n][1] - far);
+                }
+                g[n] = pow2_down(e - st.r);
+                split_weights<G, KV>(bf[n], x[n][0] * f0, x[n][1] * f0, x[n][2] * f1,
+                                     x[n][3] * f1, lane);
+            }
+            weigh_v<D, G, KV, NS>(st, vw, bf, g);
+            if (!again || pass == 1)
+                break;
+        }
+    }
 }
 
 template <int D, int G, int KV>
@@ -876,7 +933,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 use_q<D, G, KV>(st, qscale, qraw, p, lane);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    st.m[r] = st.n[r] = -INFINITY;
+                    st.m[r] = -INFINITY;
                     st.l[r] = 0.0f;
                 }
 #pragma unroll
@@ -884,6 +941,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         st.acc[j][u] = 0.0f;
+                st.r = BLOCK_MIN_EXP;
                 fresh = false;
             }
             issue();
@@ -895,19 +953,26 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 fetch_q<D, G>(qraw, p, next.y, next.z, lane);
             }
             const unsigned char *s0 = ring + (k % NST) * C::STAGE;
-            const bool one_block = p.block_size >= TILE;
+            // (16-bit caches: nothing of the tile math goes by blocks)
+            const bool one = !C::F8 || p.block_size >= TILE;
             if (two) {
                 if constexpr (C::PAIR) {
                     const unsigned char *const st2[2] = {s0, ring + ((k + 1) % NST) * C::STAGE};
                     const int b2[2] = {it.x, bits1};
-                    tiles<D, G, KV, 2>(st, qscale, st2, b2, one_block, lane);
+                    if (one)
+                        tiles<D, G, KV, 2, true>(st, qscale, st2, b2, lane);
+                    else
+                        tiles<D, G, KV, 2, false>(st, qscale, st2, b2, lane);
                     __syncwarp();      // the first tile's stage may be filled again
                     issue();
                 }
             } else {
                 const unsigned char *const st1[1] = {s0};
                 const int b1[1] = {it.x};
-                tiles<D, G, KV, 1>(st, qscale, st1, b1, one_block, lane);
+                if (one)
+                    tiles<D, G, KV, 1, true>(st, qscale, st1, b1, lane);
+                else if constexpr (C::F8)
+                    tiles<D, G, KV, 1, false>(st, qscale, st1, b1, lane);
             }
             if (ends || k + step == n) {
                 // ---- the piece's end, or the run's
@@ -935,15 +1000,13 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 for (int r = 0; r < 2; ++r) {
                     const int h = 2 * tig + r;
                     if (h < G) {
-                        // (8-bit float: from units of 2^(n - m) codes to values)
-                        float f = C::F8 ? pow2_f32(min(max((int)(st.n[r] - st.m[r]), -126), 127))
-                                        : 1.0f;
-                        if (out_now)
-                            f = f / st.l[r];
+                        // from acc's unit to values
+                        const float f = pow2_f32((C::F8 ? st.r : 0) - weight_top_log2<KV>());
+                        const float inv = out_now ? 1.0f / st.l[r] : 1.0f;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
                             *reinterpret_cast<float2 *>(dst + h * D + gid * (D / 8) + 2 * j) =
-                                make_float2(st.acc[j][r] * f, st.acc[j][r + 2] * f);
+                                make_float2(st.acc[j][r] * inv * f, st.acc[j][r + 2] * inv * f);
                         if (!out_now && gid == 0) {
                             dst[G * D + h] = st.m[r];
                             dst[G * D + G + h] = st.l[r];
