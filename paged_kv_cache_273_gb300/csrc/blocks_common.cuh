@@ -49,15 +49,6 @@ __device__ __forceinline__ int block_exponent(float scale)
     return min(max(e, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
 }
 
-// The same as a float: the exponent's bits as the low mantissa bits of 2^23,
-// less 2^23 + 127.
-__device__ __forceinline__ float exponent_f32(float scale)
-{
-    const float e = __uint_as_float(((__float_as_uint(scale) >> 23) & 255u) | 0x4B000000u) -
-                    8388735.0f;
-    return fminf(fmaxf(e, (float)BLOCK_MIN_EXP), (float)BLOCK_MAX_EXP);
-}
-
 // The least e in the range of block exponents with amax <= 127 * 2^e (127 =
 // 1.984375 * 2^6; amax >= 0): int8 steps for values up to amax.
 __device__ __forceinline__ int int8_exponent(float amax)

@@ -343,16 +343,26 @@ __device__ __forceinline__ void fetch_q(uint32_t (&w)[D / 8], const Params &p, i
     }
 }
 
-// Raw q -> B fragments of the score MMAs, and the factors that turn an MMA sum
-// over the lane's two heads into a log2-domain score.
+// What turns an MMA sum of the lane's two heads into a log2-domain score:
+// * first, * the K scale, * second, in this order.  second (8-bit float caches) is
+// the part of a bf16 q's power of two beyond 2^-60 or 2^60, 1 for most: a first
+// product is then in range whatever q is, and the next one leaves it only where
+// the score does.
+template <int KV>
+struct QScale {
+    float first[2];
+    float second[2];
+};
+
+// Raw q -> B fragments of the score MMAs, and those factors.
 template <int D, int G, int KV>
-__device__ __forceinline__ void use_q(State<D, G, KV> &st, float (&qscale)[2],
+__device__ __forceinline__ void use_q(State<D, G, KV> &st, QScale<KV> &qscale,
                                       uint32_t (&w)[D / 8], const Params &p, int lane)
 {
     constexpr bool F8 = KV == PKV_F8;
     constexpr int NQ = D / 32;                       // 16-byte chunks of the lane's quarter row
     const int tig = lane & 3;
-    float unscale = p.scale_log2;
+    float unscale = p.scale_log2, rest = 1.0f;
     if (F8 && p.q_dtype == PKV_BF16) {
         // fp16 has bf16's 8 significant bits but not its exponents: bring the
         // head's largest magnitude to [2^14, 2^15); values down to 2^-28 of it
@@ -370,7 +380,9 @@ __device__ __forceinline__ void use_q(State<D, G, KV> &st, float (&qscale)[2],
             const __half2 h = __floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        unscale = p.scale_log2 * pow2_f32(max(e, -112) - 14);
+        const int near = min(max(e - 14, -60), 60);
+        unscale = p.scale_log2 * pow2_f32(near);
+        rest = pow2_f32(e - 14 - near);
     }
     // word 2 ks + h of the fragment order
     const int rot = kern::MmaCfg<D, KV>::ROTATE ? (tig >> 1) * 2 : 0;
@@ -390,8 +402,12 @@ __device__ __forceinline__ void use_q(State<D, G, KV> &st, float (&qscale)[2],
             }
         }
     // the heads of columns 2 tig, 2 tig + 1 (lane 4 n holds column n's head)
-    qscale[0] = __shfl_sync(FULL_MASK, unscale, 8 * tig);
-    qscale[1] = __shfl_sync(FULL_MASK, unscale, 8 * tig + 4);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        qscale.first[r] = __shfl_sync(FULL_MASK, unscale, 8 * tig + 4 * r);
+        if constexpr (F8)
+            qscale.second[r] = __shfl_sync(FULL_MASK, rest, 8 * tig + 4 * r);
+    }
 }
 
 __device__ __forceinline__ float warp_max(float x)
@@ -401,11 +417,15 @@ __device__ __forceinline__ float warp_max(float x)
     return y;
 }
 
-// 2^(m - top), the weight of a state in a join; 0 where neither has seen a score
-// above -inf.
+// The reference of a state that has seen no score above -inf, the least fp32
+// number rather than -inf: such scores (products beyond fp32, infinite keys) then
+// weigh 2^(-inf - m) = 0, not 2^(-inf + inf).
+constexpr float NO_SCORE = -3.402823466e38f;
+
+// 2^(m - top), the weight of a state in a join.
 __device__ __forceinline__ float join_weight(float m, float top)
 {
-    return top == -INFINITY ? 0.0f : kern::exp2_approx(m - top);
+    return kern::exp2_approx(m - top);
 }
 
 __device__ __forceinline__ float warp_sum(float x)
@@ -605,19 +625,19 @@ __device__ __forceinline__ void tile_values(uint32_t (&vw)[4][kern::VFrag<D, KV>
     }
 }
 
-// (x, y) * f, packed.
-__device__ __forceinline__ void scale2(float &x, float &y, float f)
+// x * f, y * g, packed.
+__device__ __forceinline__ void scale2(float &x, float &y, float f, float g)
 {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
         "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(x), "+f"(y)
-        : "f"(f));
+        : "f"(f), "f"(g));
 }
 
 // NS tiles of a piece: scores, online softmax, weighted V (see the head of the
 // file).  ONE: a tile's rows are of one block.
 template <int D, int G, int KV, int NS, bool ONE>
-__device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)[2],
+__device__ __forceinline__ void tiles(State<D, G, KV> &st, const QScale<KV> &qscale,
                                       const unsigned char *const (&stage)[NS],
                                       const int (&bits)[NS], int lane)
 {
@@ -648,15 +668,19 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
                     ev[n][0] = ev[n][1];
             }
             top = max(top, max(ev[n][0], ev[n][1]));
-            s[0] *= k0;
-            s[1] *= k0;
-            s[2] *= k1;
-            s[3] *= k1;
+            scale2(s[0], s[1], qscale.first[0], qscale.first[1]);
+            scale2(s[2], s[3], qscale.first[0], qscale.first[1]);
+            scale2(s[0], s[1], k0, k0);
+            scale2(s[2], s[3], k1, k1);
+            scale2(s[0], s[1], qscale.second[0], qscale.second[1]);
+            scale2(s[2], s[3], qscale.second[0], qscale.second[1]);
+        } else {
+            scale2(s[0], s[1], qscale.first[0], qscale.first[1]);
+            scale2(s[2], s[3], qscale.first[0], qscale.first[1]);
         }
-        x[n][0] = s[0] * qscale[0];
-        x[n][1] = s[1] * qscale[1];
-        x[n][2] = s[2] * qscale[0];
-        x[n][3] = s[3] * qscale[1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            x[n][u] = s[u];
         if (!is_full(bits[n])) {
             const int rows = rows_of(bits[n]), skip = skip_of(bits[n]);
             if (gid >= rows || gid < skip)
@@ -677,9 +701,8 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
             mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, mask));
         }
         const float t0 = fmaxf(st.m[0], ceilf(mx0)), t1 = fmaxf(st.m[1], ceilf(mx1));
-        // (a head whose scores are all -inf so far has nothing to rescale)
-        const float c0 = !C::F8 && t0 == -INFINITY ? 1.0f : kern::exp2_approx(st.m[0] - t0);
-        const float c1 = !C::F8 && t1 == -INFINITY ? 1.0f : kern::exp2_approx(st.m[1] - t1);
+        const float c0 = kern::exp2_approx(st.m[0] - t0);
+        const float c1 = kern::exp2_approx(st.m[1] - t1);
         st.m[0] = t0;
         st.m[1] = t1;
         st.l[0] *= c0;
@@ -700,16 +723,12 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
             st.acc[j][3] *= a1;
         }
     }
-    // (keys of 16-bit caches may hold infinities: no weight, rather than inf - inf,
-    // for scores of -inf while there has been no other)
-    const float m0 = !C::F8 && st.m[0] == -INFINITY ? 0.0f : st.m[0];
-    const float m1 = !C::F8 && st.m[1] == -INFINITY ? 0.0f : st.m[1];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        x[n][0] = kern::exp2_approx(x[n][0] - m0);
-        x[n][1] = kern::exp2_approx(x[n][1] - m1);
-        x[n][2] = kern::exp2_approx(x[n][2] - m0);
-        x[n][3] = kern::exp2_approx(x[n][3] - m1);
+        x[n][0] = kern::exp2_approx(x[n][0] - st.m[0]);
+        x[n][1] = kern::exp2_approx(x[n][1] - st.m[1]);
+        x[n][2] = kern::exp2_approx(x[n][2] - st.m[0]);
+        x[n][3] = kern::exp2_approx(x[n][3] - st.m[1]);
         st.l[0] += x[n][0] + x[n][2];
         st.l[1] += x[n][1] + x[n][3];
     }
@@ -720,8 +739,8 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const float (&qscale)
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             if constexpr (weight_top_log2<KV>() != 0) {
-                scale2(x[n][0], x[n][1], TOP);
-                scale2(x[n][2], x[n][3], TOP);
+                scale2(x[n][0], x[n][1], TOP, TOP);
+                scale2(x[n][2], x[n][3], TOP, TOP);
             }
             if constexpr (C::F8)
                 g[n] = pow2_down(ev[n][0] - st.r);
@@ -911,7 +930,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
             issue();
 
         State<D, G, KV> st;
-        float qscale[2];
+        QScale<KV> qscale;
         bool fresh = true;
         bool whole = true;                 // the piece began in this run
         const int gid = lane >> 2, tig = lane & 3;
@@ -933,7 +952,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                 use_q<D, G, KV>(st, qscale, qraw, p, lane);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    st.m[r] = -INFINITY;
+                    st.m[r] = NO_SCORE;
                     st.l[r] = 0.0f;
                 }
 #pragma unroll

@@ -1,6 +1,7 @@
 """Decode attention over 8-bit float caches and over chosen blocks where a few rows or blocks
-outweigh the rest: rows of large scores and no value, blocks of far larger scales; against
-float64, each element held to its own weighted sum of magnitudes."""
+outweigh the rest: rows of large scores and no value, blocks of far larger scales, scores at
+the ends of fp32's range; against float64, each element held to its own weighted sum of
+magnitudes."""
 import math
 
 import numpy as np
@@ -150,3 +151,55 @@ def test_scales_of_every_distance(D, bs):
     q = _rows(5, (len(lens), H * G, D), "f16")
     out = _attend(c, q, tables.astype(np.int32), lens, 0.09)
     check(c, q, tables, lens, 0.09, out, floor=floor_of(bs))
+
+
+# ---------------------------------------------------------------------- the ends of fp32's range
+@pytest.mark.parametrize("lens", [[100, 16, 1], [2000, 40, 900]])
+@pytest.mark.parametrize("kexp,amp,scale", [
+    (100, 2.0 ** -98, 0.09), (115, 2.0 ** -100, 2.0 ** -11), (112, 2.0 ** -110, 0.09),
+    (118, 2.0 ** -117, 0.09), (-60, 2.0 ** 60, 0.09), (-85, 2.0 ** 85, 0.09),
+    (30, 2.0 ** 90, 2.0 ** -125)])
+def test_key_scales_of_any_size(kexp, amp, scale, lens):
+    # scores of ordinary size from keys and queries that are not
+    c = Cache(130, 2, 16, 128, seed=4)
+    c.hks[:] = np.exp2(np.random.default_rng(1).integers(kexp - 9, kexp - 6, c.hks.shape))
+    c.upload()
+    tables = _batch(c, lens, 5, extra=0)
+    q = _rows(3, (3, 8, 128), "bf16", amp)
+    out = _attend(c, q, tables, lens, scale)
+    check(c, q, tables, lens, scale, out)
+
+
+def test_zero_scores_of_the_largest_scales():
+    # q . k is 0 where q's one channel meets codes of 0, whatever the scales are
+    c = Cache(20, 1, 16, 64, seed=4)
+    c.hk[..., 0] = 0
+    c.hks[:] = 2.0 ** 119
+    c.upload()
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 2.0 ** 120
+    tables = _batch(c, [200, 17], 5, extra=0)
+    out = _attend(c, q, tables, [200, 17], 0.125)
+    check(c, q, tables, [200, 17], 0.125, out)
+
+
+def test_scores_below_fp32s_range_weigh_nothing():
+    # whole tiles at the front, then one in the middle, score -inf in fp32
+    c = Cache(200, 1, 16, 64, seed=4, exp=(-9, -6))
+    c.hk[:, :, :, 0] = R.e4m3_encode(np.zeros(1))[0]
+    far = np.r_[0:12, 30:33]
+    c.hk[far, :, :, 0] = R.e4m3_encode(np.array([-448.0]))[0]
+    c.hk[far, :, :, 1:] = 0
+    c.hks[far] = 2.0 ** 119
+    c.upload()
+    lens = [190 * 16, 13 * 16, 12 * 16 + 1]
+    tables = np.stack([np.arange(200)] * 3).astype(np.int32)
+    q = _rows(3, (3, 4, 64), "bf16")
+    q[..., 0] = 64.0
+    out = _attend(c, q, tables, lens, 1.0)
+    got, qh = out.double().cpu().numpy(), q.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        k, v = c.rows(tables[b, :-(-n // 16)], 0, n, "k"), c.rows(tables[b, :-(-n // 16)], 0, n, "v")
+        at = ~np.isin(np.arange(n) // 16, far)
+        hold(got[b], qh[b], k[at], v[at], 1.0)
+    assert pkv.pkv_check_error(c.pool) == pkv.PKV_OK
