@@ -20,7 +20,9 @@
 //    neighbours; their states go to shared memory, the CTA joins the states
 //    of its warps at its end, and a piece shared with other CTAs is left in
 //    the workspace and joined, in CTA order, by the last of them to finish
-//    (the result does not depend on timing).
+//    (the result does not depend on timing).  A state that is handed on holds
+//    2^-24 of its weighted sum, which is in range for any V over 2^24 rows, where
+//    the sum itself is not; what that takes from the small end is below 2^-125.
 //  * Tile math: warp-level MMAs as in the kernel for the other caches; e4m3
 //    codes become fp16 exactly, q becomes fp16 exactly (a bf16 q is brought
 //    to [2^14, 2^15) by a power of two first), products are exact and sums
@@ -444,6 +446,9 @@ template <int KV>
 __host__ __device__ constexpr int weight_parts() { return KV == PKV_BF16 ? 3 : 2; }
 template <int KV>
 __host__ __device__ constexpr int weight_top_log2() { return KV == PKV_BF16 ? 0 : 15; }
+
+// What a state's weighted sum is kept by once it leaves the registers.
+constexpr float STATE_UNIT = 16777216.0f;
 
 // 2^d for d <= 0, 0 where that is not a normal number.
 __device__ __forceinline__ float pow2_down(int d)
@@ -1021,7 +1026,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
                     if (h < G) {
                         // from acc's unit to values
                         const float f = pow2_f32((C::F8 ? st.r : 0) - weight_top_log2<KV>());
-                        const float inv = out_now ? 1.0f / st.l[r] : 1.0f;
+                        const float inv = out_now ? 1.0f / st.l[r] : 1.0f / STATE_UNIT;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j)
                             *reinterpret_cast<float2 *>(dst + h * D + gid * (D / 8) + 2 * j) =
@@ -1130,7 +1135,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         for (int o = 0; o < MO; ++o) {
             const int i = o * NT + tid, g = i / D;
             if (i < G * D) {
-                dst[i] = mine ? num[o] / den[o] : num[o];
+                dst[i] = mine ? num[o] / den[o] * STATE_UNIT : num[o];
                 if (!mine && i % D == 0) {
                     dst[G * D + g] = top[o];
                     dst[G * D + G + g] = den[o];
@@ -1204,7 +1209,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         for (int o = 0; o < MO; ++o)
             if (tid + o * NT < G * D)
                 p.out[(int64_t)seg * G * D + o * NT + tid] =
-                    num[o] / den[o];
+                    num[o] / den[o] * STATE_UNIT;
     }
 }
 

@@ -1,6 +1,6 @@
 """Decode attention over 8-bit float caches and over chosen blocks where a few rows or blocks
-outweigh the rest: rows of large scores and no value, blocks of far larger scales, scores at
-the ends of fp32's range; against float64, each element held to its own weighted sum of
+outweigh the rest: rows of large scores and no value, blocks of far larger scales, scores and
+sums at the ends of fp32's range; against float64, each element held to its own weighted sum of
 magnitudes."""
 import math
 
@@ -203,3 +203,16 @@ def test_scores_below_fp32s_range_weigh_nothing():
         at = ~np.isin(np.arange(n) // 16, far)
         hold(got[b], qh[b], k[at], v[at], 1.0)
     assert pkv.pkv_check_error(c.pool) == pkv.PKV_OK
+
+
+@pytest.mark.parametrize("lens", [[30], [3000], [4800, 900, 17]])
+def test_values_near_fp32s_largest(lens):
+    # their mean is in range, their weighted sum is not
+    c = Cache(300, 1, 16, 128, seed=4, exp=(-9, -6))
+    c.hvs[:] = 2.0 ** 119
+    c.hv[:] = np.where(c.hv & 128, c.hv, 126 - c.hv % 20)
+    c.upload()
+    tables = _batch(c, lens, 5, extra=0)
+    q = _rows(3, (len(lens), 4, 128), "f16")
+    out = _attend(c, q, tables, lens, 0.09)
+    check(c, q, tables, lens, 0.09, out)
