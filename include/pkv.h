@@ -185,8 +185,9 @@ int kv_reserve_slots(pkv_pool *pool, int batch, const int32_t *seq_lens, const i
  * Sequences are handled in order, so when every holder of a shared block
  * appends in one step, all but the last one to be handled get copies and
  * that last one writes in place.  At most `batch` pairs; *num_copies
- * receives their number.  The caller must run kv_block_copy on the pairs
- * before the kv_append of this step.  Slots and new blocks are then handled
+ * receives their number.  The caller must run kv_block_copy on the pairs, and
+ * kv_bounds_copy where it keeps key bounds, before the kv_append and the
+ * kv_bounds_append of this step.  Slots and new blocks are then handled
  * as in kv_reserve_slots.
  * All-or-nothing: PKV_ERR_NO_BLOCKS if the pool cannot cover the new blocks
  * and the copies; PKV_ERR_INVALID for a table row that would overflow or a
@@ -256,8 +257,8 @@ int kv_append(const pkv_pool *pool, const void *k_new, const void *v_new, pkv_dt
 /*
  * kv_block_copy — the copy half of copy-on-write ([VIS] "PagedAttention: the
  * cache in blocks"): for i < n, every cached K and V row of block src[i] (all
- * KV heads; and the fp16 scales for int8 pools) is copied bit for bit to
- * block dst[i].
+ * KV heads; and the scales of int8, int4 and F8 pools) is copied bit for bit
+ * to block dst[i].  Key bounds are copied by kv_bounds_copy.
  *
  *   src, dst   device int32 [n] block ids (as kv_reserve_slots_cow writes
  *              them).  The dst blocks must be distinct and none may be a src
@@ -628,13 +629,32 @@ int kv_device_release(const pkv_pool *pool, int32_t *free_ids, int free_capacity
  *   lower[d] = floor(min x_d * 2^-E), upper[d] = ceil(max x_d * 2^-E),
  * joined with the block's bounds of its earlier rows, rounded down (up) to the
  * new E.  The bounds of a block do not depend on how its rows were split over
- * calls.  A slot out of range sets PKV_ERR_BAD_INDEX and its token is skipped.
+ * calls.  A run that goes on in a block joins the bounds that the block holds, so
+ * a block that a sequence takes over partly filled needs its bounds as well as its
+ * rows (kv_bounds_copy).  A slot out of range sets PKV_ERR_BAD_INDEX and its token
+ * is skipped.
  * num_tokens == 0 is a no-op.  PKV_ERR_INVALID also if the pool's device is not
  * the current one.
  */
 int kv_bounds_append(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype,
                      const int32_t *slot_mapping, int num_tokens, int8_t *bounds,
                      int32_t *bound_exps, pkv_stream_t stream);
+
+/*
+ * kv_bounds_copy — kv_block_copy for the key bounds: block dst[i] receives the
+ * bounds and exponents of block src[i], all KV heads, for i < n.  Run with the
+ * pairs of kv_block_copy: bounds belong to physical blocks, and appends to the copy
+ * go on from them.
+ *
+ *   src, dst             as for kv_block_copy.
+ *   bounds, bound_exps   as kv_bounds_append keeps them.
+ *
+ * An id outside [0, NB) sets PKV_ERR_BAD_INDEX in the error word and that pair is
+ * skipped.  n == 0 is a no-op.  PKV_ERR_INVALID also if the pool's device is not
+ * the current one.
+ */
+int kv_bounds_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                   int8_t *bounds, int32_t *bound_exps, pkv_stream_t stream);
 
 /*
  * paged_sparse_workspace_bytes — bytes of the workspace of

@@ -379,6 +379,32 @@ __global__ void __launch_bounds__(256) append_bounds_kernel(
     });
 }
 
+// One thread a 16-byte chunk of a block's bounds, or a head's exponent: a copied
+// block is a few KB, the launch is what it costs.
+__global__ void __launch_bounds__(256) bounds_copy_kernel(
+    const int32_t *src, const int32_t *dst, int64_t items, int chunks, int num_kv_heads,
+    int num_blocks, uint4 *bounds, int32_t *exps, unsigned int *err)
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int per = chunks + num_kv_heads;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; c < items; c += stride) {
+        const int64_t i = c / per;
+        const int r = (int)(c - i * per);
+        const int32_t s = src[i], d = dst[i];
+        if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) {
+            if (r == 0)
+                atomicOr(err, PKV_EBIT_BLOCK);
+        } else if (r < chunks) {
+            bounds[(int64_t)d * chunks + r] = bounds[(int64_t)s * chunks + r];
+        } else {
+            const int h = r - chunks;
+            exps[(int64_t)d * num_kv_heads + h] = exps[(int64_t)s * num_kv_heads + h];
+        }
+    }
+}
+
 // Tokens a warp looks for runs in: one while that keeps every SM's warps few
 // (a decode step: every token is a run of its own), else 32, so that a bulk
 // write's warps find a run or two each and few find none (131k rows of 8 heads:
@@ -444,6 +470,18 @@ int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_d
         else PKV_B8(float, 64);
     }
 #undef PKV_B8
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int launch_bounds_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                       int8_t *bounds, int32_t *exps, pkv_stream_t stream)
+{
+    const int H = pool->num_kv_heads, chunks = H * 2 * pool->head_dim / 16;
+    const int64_t items = (int64_t)n * (chunks + H);
+    const int64_t grid = (items + 255) / 256, most = (int64_t)pool->num_sms * 8;
+    launch_pdl(bounds_copy_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0,
+               reinterpret_cast<cudaStream_t>(stream), src, dst, items, chunks, H,
+               pool->num_blocks, reinterpret_cast<uint4 *>(bounds), exps, pool->d_err);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

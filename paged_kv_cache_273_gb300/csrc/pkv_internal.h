@@ -113,6 +113,8 @@ int launch_append_f8(const pkv_pool *pool, const void *k_new, const void *v_new,
 int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype,
                          const int32_t *slots, int num_tokens, int8_t *bounds, int32_t *exps,
                          pkv_stream_t stream);
+int launch_bounds_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                       int8_t *bounds, int32_t *exps, pkv_stream_t stream);
 
 // The workspace of decode_blocks_kernel and select_kernel starts with a counter
 // for each KV head of the largest batch, whatever the call's batch: one buffer,

@@ -898,6 +898,23 @@ int kv_bounds_append(const pkv_pool *pool, const void *k_new, pkv_dtype in_dtype
                                      bound_exps, stream);
 }
 
+int kv_bounds_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                   int8_t *bounds, int32_t *bound_exps, pkv_stream_t stream)
+{
+    Range range("pkv.kv_bounds_copy");
+    if (!pool || n < 0)
+        return PKV_ERR_INVALID;
+    if (n == 0)
+        return PKV_OK;
+    if (!src || !dst || !bounds || !bound_exps || !aligned4(src) || !aligned4(dst) ||
+        !pkv::aligned16(bounds) || !aligned4(bound_exps))
+        return PKV_ERR_INVALID;
+    const int dc = device_check(pool);
+    if (dc != PKV_OK)
+        return dc;
+    return pkv::launch_bounds_copy(pool, src, dst, n, bounds, bound_exps, stream);
+}
+
 size_t paged_sparse_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
                                     int max_seq_len, int max_selected)
 {

@@ -49,7 +49,7 @@ SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "
            "paged_decode_attention_window", "paged_prefill_attention", "kv_prefix_groups",
            "paged_decode_cascade_workspace_bytes", "paged_decode_attention_cascade",
            "paged_decode_attention_noalloc", "paged_decode_step", "kv_device_reserve",
-           "kv_device_release", "kv_bounds_append", "paged_sparse_workspace_bytes",
+           "kv_device_release", "kv_bounds_append", "kv_bounds_copy", "paged_sparse_workspace_bytes",
            "paged_decode_attention_sparse", "pkv_selftest_wait_timeout", "pkv_check_error")
 
 
@@ -146,6 +146,8 @@ def load() -> ctypes.CDLL:
         lib.kv_device_release.restype = I
         lib.kv_bounds_append.argtypes = [P, P, I, P, I, P, P, P]
         lib.kv_bounds_append.restype = I
+        lib.kv_bounds_copy.argtypes = [P, P, P, I, P, P, P]
+        lib.kv_bounds_copy.restype = I
         lib.paged_sparse_workspace_bytes.argtypes = [P, I, I, I, I]
         lib.paged_sparse_workspace_bytes.restype = SZ
         lib.paged_decode_attention_sparse.argtypes = [P, P, I, I, P, P, P, P, P, P, P, I, P, I, I,
@@ -368,7 +370,8 @@ def kv_append(pool: Pool, k_new, v_new, slot_mapping, k_cache, v_cache, k_scales
 
 def kv_block_copy(pool: Pool, src, dst, k_cache, v_cache, k_scales=None, v_scales=None,
                   stream=None) -> None:
-    """Copy blocks src[i] -> dst[i] (device int32 tensors) in the caches."""
+    """Copy blocks src[i] -> dst[i] (device int32 tensors) in the caches (key bounds:
+    kv_bounds_copy)."""
     if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.numel() != dst.numel():
         raise ValueError("src and dst must be int32 tensors of equal length")
     _check_scales(pool, k_scales, v_scales)
@@ -691,7 +694,8 @@ def alloc_bounds(pool: Pool, device="cuda"):
 
 
 def kv_bounds_append(pool: Pool, k_new, slot_mapping, bounds, bound_exps, stream=None) -> None:
-    """Join the new keys to their blocks' bounds (see include/pkv.h)."""
+    """Join the new keys to their blocks' bounds (see include/pkv.h).  Blocks copied on write
+    need kv_bounds_copy first."""
     if k_new.dtype not in PKV_DTYPE:
         raise ValueError("unsupported k_new dtype %s" % k_new.dtype)
     T, head = k_new.shape[0], (pool.num_blocks, pool.num_kv_heads)
@@ -702,6 +706,18 @@ def kv_bounds_append(pool: Pool, k_new, slot_mapping, bounds, bound_exps, stream
     _check(load().kv_bounds_append(pool.handle, _dptr(k_new), PKV_DTYPE[k_new.dtype],
                                    _dptr(slot_mapping), T, _dptr(bounds), _dptr(bound_exps),
                                    _stream(stream)), "kv_bounds_append")
+
+
+def kv_bounds_copy(pool: Pool, src, dst, bounds, bound_exps, stream=None) -> None:
+    """Copy the bounds of blocks src[i] to blocks dst[i] (device int32 tensors): what
+    kv_block_copy does for the rows, with the same pairs."""
+    head = (pool.num_blocks, pool.num_kv_heads)
+    _vector("src", src)
+    _shaped("dst", dst, _I32, (src.shape[0],))
+    _shaped("bounds", bounds, _I8, head + (2, pool.head_dim))
+    _shaped("bound_exps", bound_exps, _I32, head)
+    _check(load().kv_bounds_copy(pool.handle, _dptr(src), _dptr(dst), src.shape[0], _dptr(bounds),
+                                 _dptr(bound_exps), _stream(stream)), "kv_bounds_copy")
 
 
 def paged_sparse_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_seq_len: int,
