@@ -579,7 +579,8 @@ int paged_decode_attention_noalloc(const pkv_pool *pool, const void *q, pkv_dtyp
  * call then changes no table, copies the lengths and the free count, and fills
  * slot_mapping with -1 and q_start with 0.  An id outside the pool, on the stack
  * or in a table row, is recorded (PKV_ERR_BAD_INDEX) and its tokens' slots are
- * -1.  Apart from the pairs named here the arrays must not overlap.  batch <= 4096; batch == 0
+ * -1 (a table row takes -1 for one off the stack, and kv_device_release refuses the
+ * row): the tables and the stack are then to be set up again.  Apart from the pairs named here the arrays must not overlap.  batch <= 4096; batch == 0
  * is a no-op.  One kernel.  PKV_ERR_INVALID also if the pool's device is not the
  * current one.
  */
@@ -602,10 +603,12 @@ int kv_device_reserve(const pkv_pool *pool, const int32_t *free_ids, int free_ca
  *   free_in, free_out, seq_lens, seq_lens_out, block_tables, limits  as for
  *                  kv_device_reserve (block_tables is read only here).
  *
- * All or nothing: a length out of range or a stack that would outgrow
- * free_capacity gives PKV_ERR_BAD_INDEX at the next pkv_check_error, and the
- * call only copies the lengths and the count.  A block that two rows hold, or
- * one that is on the stack already, is not noticed.  One kernel.
+ * All or nothing: a length out of range, a stack that would outgrow
+ * free_capacity, or an id outside the pool among the blocks to release gives
+ * PKV_ERR_BAD_INDEX at the next pkv_check_error, and the call only copies the
+ * lengths and the count (entries of free_ids above the count may have been
+ * written).  A block that two rows hold, or one that is on the stack already, is
+ * not noticed.  One kernel.
  */
 int kv_device_release(const pkv_pool *pool, int32_t *free_ids, int free_capacity,
                       const int32_t *free_in, int32_t *free_out, const int32_t *seq_lens,

@@ -85,22 +85,27 @@ __device__ __forceinline__ int find(const int *start, int n, int x)
 }
 
 // True in every thread of the last CTA to get here (all of whose CTAs' reads
-// and writes are then done); the ticket is left at zero.
-__device__ __forceinline__ bool last_cta(int32_t *ticket)
+// and writes are then done); the ticket is left at zero.  bad: in the last CTA,
+// whether any thread of any CTA came with it set (each CTA with one counts
+// 2^16 on the ticket; there are at most 3 a SM).
+__device__ __forceinline__ bool last_cta(int32_t *ticket, bool &bad)
 {
-    __shared__ int last;
-    __syncthreads();
+    __shared__ int last, any;
+    bad = __syncthreads_or(bad) != 0;
     if (gridDim.x == 1)
         return true;
     if (threadIdx.x == 0) {
         __threadfence();
-        last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+        const int old = atomicAdd(ticket, 1 + (bad ? 1 << 16 : 0));
+        last = (old & 0xffff) == (int)gridDim.x - 1;
+        any = bad || (old >> 16) != 0;
         if (last) {
             __threadfence();
             *ticket = 0;
         }
     }
     __syncthreads();
+    bad = any != 0;
     return last != 0;
 }
 
@@ -227,7 +232,8 @@ __global__ void __launch_bounds__(NT) reserve_kernel(TableArgs a, const int32_t 
         for (int b = first; b <= B; b += stride)
             q_start[b] = ok ? s_tok[b] : 0;
 
-    if (last_cta(a.free_out + 1)) {
+    bool none = false;
+    if (last_cta(a.free_out + 1, none)) {
         for (int b = tid; b < B; b += NT)
             a.lens_out[b] = a.lens[b] + (ok ? s_tok[b + 1] - s_tok[b] : 0);
         if (tid == 0)
@@ -275,18 +281,21 @@ __global__ void __launch_bounds__(NT) release_kernel(TableArgs a, int32_t *free_
     }
     __syncthreads();
     const int R = ok ? (int)total : 0;
+    bool bad_id = false;
     for (int k = blockIdx.x * NT + tid; k < R; k += gridDim.x * NT) {
         const int b = find(s_blk, B, k);
         const int id = __ldg(tables + (int64_t)b * a.max_blocks + (k - s_blk[b]));
-        if (id < 0 || id >= a.num_blocks)
+        if (id < 0 || id >= a.num_blocks) {
             atomicOr(a.err, PKV_EBIT_BLOCK);
-        free_ids[count + k] = id;
+            bad_id = true;
+        }
+        free_ids[count + k] = id;          // (counted only below, if all are good)
     }
-    if (last_cta(a.free_out + 1)) {
+    if (last_cta(a.free_out + 1, bad_id)) {
         for (int b = tid; b < B; b += NT)
-            a.lens_out[b] = ok && done[b] != 0 ? 0 : a.lens[b];
+            a.lens_out[b] = ok && !bad_id && done[b] != 0 ? 0 : a.lens[b];
         if (tid == 0)
-            a.free_out[0] = count + R;
+            a.free_out[0] = count + (bad_id ? 0 : R);
     }
 }
 

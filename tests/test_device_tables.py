@@ -295,3 +295,35 @@ def test_captured_steps_replay():
         got = slots.cpu().tolist()
         assert got == want + [-1] * (16 - len(want)), i
         s.same()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,maxb", [(3, 5), (200, 300)])     # one CTA, several
+def test_release_of_ids_outside_the_pool_is_refused(B, maxb):
+    bs = 4
+    s = Step(B, maxb, bs, B * maxb)
+    s.check_reserve(s.rng.integers(1, (maxb - 1) * bs + 1, B))
+    done = (s.rng.random(B) < 0.7).astype(np.int32)
+    done[:2], done[2] = 1, 0
+    s.check_reserve(np.array([3, 1] + [0] * (B - 2)))        # rows 0 and 1 hold a block
+    good = s.dtables.clone()
+    for row, at, bad in ((0, 0, -1), (1, -1, B * maxb), (0, 0, -2 ** 31), (B - 1, 0, 2 ** 31 - 1)):
+        n = -(-int(s.lens[row]) // bs)
+        s.dtables[row, at % n] = bad
+        before = s.dlens.clone()
+        free, state = s.free_ids.clone(), s.state.clone()
+        pkv.kv_device_release(s.pool, s.free_ids, s.state, s.dlens,
+                              torch.as_tensor(np.maximum(done, np.arange(B) == row),
+                                              dtype=torch.int32, device=DEV), s.dtables)
+        assert pkv.pkv_check_error(s.pool) == pkv.PKV_ERR_BAD_INDEX
+        assert torch.equal(s.state, state) and torch.equal(s.dlens, before)
+        top = int(state[0])
+        assert torch.equal(s.free_ids[:top], free[:top])
+        s.dtables.copy_(good)
+    # an id that is not released is not looked at, nor one behind a row's blocks
+    s.dtables[2, 0] = -1
+    n = -(-int(s.lens[0]) // bs)
+    if n < maxb:
+        s.dtables[0, n] = -1
+    s.tables = s.dtables.cpu().numpy()
+    s.check_release(done)
