@@ -39,6 +39,11 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
             return nullptr;
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }();
+    // A driver call: it wants the device's context to be current, which a host thread
+    // has only from its first runtime call of certain kinds on.
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)
+        return nullptr;
     return fn;
 }
 
