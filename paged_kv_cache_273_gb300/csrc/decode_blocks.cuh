@@ -1219,8 +1219,12 @@ int launch_k(const pkv_pool *pool, const Params &base, cudaStream_t stream, int6
     const int smem = Smem<D, G, KV>::total(prm.batch);
     if (smem > pool->max_smem_optin)
         return PKV_ERR_UNSUPPORTED;
+    // The limit belongs to the kernel, not to the launch: the largest batch's, the same
+    // from every call, so that a call from another host thread between this one's
+    // setting and its launch changes nothing.
     if (cudaFuncSetAttribute(decode_blocks_kernel<D, G, KV, ONE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D, G, KV>::total(MAX_BATCH)) != cudaSuccess)
         return PKV_ERR_CUDA;
     // a CTA for each piece, or one for the least its warps take
     int64_t P = max_tiles / (C::W * MIN_TILES);

@@ -500,21 +500,24 @@ Regions regions(const pkv_pool *pool, int batch, int num_q_heads, int max_seq_le
 template <int D, int G, int NT>
 cudaError_t launch_select_t(const SelectArgs &a, unsigned grid, size_t smem, cudaStream_t s)
 {
-    if (smem > 40000) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            select_kernel<D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    // The limit belongs to the kernel, not to the launch: the most that any call asks for,
+    // so that a call from another host thread between this one's setting and its launch
+    // changes nothing.
+    cudaError_t e = cudaFuncSetAttribute(select_kernel<D, G, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SMEM_KEYS * 8);
+    if (e != cudaSuccess)
+        return e;
     // of the SM's 228 KB for shared memory and L1 no more than the CTAs use as shared
     // memory: up to 128 KB of bounds are in flight through the L1, and without this
     // the kernel runs with the division that the one before it had (behind the
     // attention with all of it as shared memory, 54 instead of 46 us for the choice
-    // of 128 of 2048 blocks of 16 sequences and the attention over them)
+    // of 128 of 2048 blocks of 16 sequences and the attention over them).  A preference:
+    // another thread's call in between costs time, not the launch.
     const size_t used = 512 / NT * (smem + sizeof(Pick<NT>) + 1280);
     const int percent = (int)std::min<size_t>(100, (used * 100 + 233471) / 233472);
-    const cudaError_t e = cudaFuncSetAttribute(
-        select_kernel<D, G, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
+    e = cudaFuncSetAttribute(select_kernel<D, G, NT>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout, percent);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(select_kernel<D, G, NT>, dim3(grid), dim3(NT), smem, s, a);
