@@ -2254,9 +2254,12 @@ int launch_t(const pkv_pool *pool, const Params &base, int batch, int max_seq_le
 
     // The dynamic shared-memory limit is an attribute of the kernel in the
     // current device's context (a context that a device reset replaces), so
-    // it is set on every call rather than remembered by the process.
+    // it is set on every call rather than remembered by the process, and to the
+    // device's limit whatever this call's batch needs: a call from another host
+    // thread between this setting and the launch then changes nothing.
     if (cudaFuncSetAttribute(paged_decode_kernel<D, G, KV, QS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, lay.total) != cudaSuccess)
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             pool->max_smem_optin) != cudaSuccess)
         return PKV_ERR_CUDA;
     const int64_t max_tiles =
         (int64_t)batch * pool->num_kv_heads * ((max_seq_len + C::TT - 1) / C::TT);

@@ -63,7 +63,7 @@ def _pool(kv, bs, nb=64, H=1, D=64):
     return pool, k, v, ks, vs
 
 
-@pytest.mark.parametrize("kv", [pkv.PKV_F8])
+@pytest.mark.parametrize("kv", [pkv.PKV_F8, pkv.PKV_F16, pkv.PKV_BF16])
 def test_decode_of_different_batches(kv):
     pool, k, v, ks, vs = _pool(kv, 16)
     qt = torch.float16 if kv == pkv.PKV_F8 else pkv.TORCH_DTYPE[kv]
