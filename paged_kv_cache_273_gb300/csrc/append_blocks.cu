@@ -146,10 +146,10 @@ __device__ __forceinline__ void for_runs(const int32_t *slots, int64_t t0, int C
 {
     const int lane = threadIdx.x & 31;
     const int64_t t = t0 + lane;
-    const int s = lane < C && t < T ? __ldg(slots + t) : -1;
+    const int s = lane < C && t < T ? slots[t] : -1;
     int before = __shfl_up_sync(FULL_MASK, s, 1);
     if (lane == 0)
-        before = t0 > 0 ? __ldg(slots + t0 - 1) : -1;
+        before = t0 > 0 ? slots[t0 - 1] : -1;
     if (report && s >= 0 && (int64_t)s >= num_slots)
         atomicOr(err, PKV_EBIT_SLOT);
     const bool starts = s >= 0 && (int64_t)s < num_slots &&
@@ -163,7 +163,7 @@ __device__ __forceinline__ void for_runs(const int32_t *slots, int64_t t0, int C
         int n = 1;                                   // rows of the run
         for (;;) {
             const int64_t tn = t0 + i + n + lane;
-            const bool more = off + n + lane < bs && tn < T && __ldg(slots + tn) == slot + n + lane;
+            const bool more = off + n + lane < bs && tn < T && slots[tn] == slot + n + lane;
             const unsigned gap = ~__ballot_sync(FULL_MASK, more);
             if (gap) {
                 n += __ffs(gap) - 1;
@@ -178,10 +178,9 @@ __device__ __forceinline__ void for_runs(const int32_t *slots, int64_t t0, int C
 // One warp per (chunk of C tokens, K or V, head).
 template <typename T, int D>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) append_f8_kernel(
-    const T *__restrict__ k_new, const T *__restrict__ v_new, const int32_t *__restrict__ slots,
-    int64_t num_tokens, int C, int num_kv_heads, int block_size, int64_t num_slots,
-    uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache, float *__restrict__ k_scales,
-    float *__restrict__ v_scales, unsigned int *__restrict__ err)
+    const T *k_new, const T *v_new, const int32_t *slots, int64_t num_tokens, int C,
+    int num_kv_heads, int block_size, int64_t num_slots, uint8_t *k_cache, uint8_t *v_cache,
+    float *k_scales, float *v_scales, unsigned int *err)
 {
     using A = Rows<T, D>;
     using X = Row16<T>;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) append_f8_kernel(
 #pragma unroll
             for (int i = 0; i < A::NR; ++i) {
                 const int k = k0 + i * A::RPI + r0;
-                x[i].w = k < n ? __ldg(in + k * step) : make_uint4(0u, 0u, 0u, 0u);
+                x[i].w = k < n ? in[k * step] : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int i = 0; i < A::NR; ++i)
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) append_f8_kernel(
                 for (int i = 0; i < A::NR; ++i) {
                     const int k = k0 + i * A::RPI + r0;
                     if (k < n)
-                        x[i].w = __ldg(in + k * step);
+                        x[i].w = in[k * step];
                 }
             }
 #pragma unroll
@@ -282,9 +281,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) append_f8_kernel(
 // minima rounded down, then the maxima rounded up, in units of 2^exps.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) append_bounds_kernel(
-    const T *__restrict__ k_new, const int32_t *__restrict__ slots, int64_t num_tokens, int C,
-    int num_kv_heads, int block_size, int64_t num_slots, int8_t *__restrict__ bounds,
-    int32_t *__restrict__ exps, unsigned int *__restrict__ err)
+    const T *k_new, const int32_t *slots, int64_t num_tokens, int C, int num_kv_heads,
+    int block_size, int64_t num_slots, int8_t *bounds, int32_t *exps, unsigned int *err)
 {
     using A = Rows<T, D>;
     using X = Row16<T>;

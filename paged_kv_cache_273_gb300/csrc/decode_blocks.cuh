@@ -166,7 +166,7 @@ __device__ __forceinline__ int first_row(const Params &p, int L)
 // A sequence's attended length, 0 for one out of range.
 __device__ __forceinline__ int seq_len(const Params &p, int b)
 {
-    const int L = __ldg(p.seq_lens + b);
+    const int L = p.seq_lens[b];
     return L < 0 || L > p.len_cap ? 0 : attended_len(p, L);
 }
 
@@ -245,7 +245,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *tstart, int 
         t.id[u] = -1;
         if (u < n && (n == 1 || (r0 < rows_of(t.bits) &&
                                  r0 + p.block_size > skip_of(t.bits)))) {
-            const int id = __ldg(row + ((t0 >> p.bs_log2) + u));
+            const int id = row[(t0 >> p.bs_log2) + u];
             if (id < 0 || id >= p.num_blocks)
                 atomicOr(p.err, PKV_EBIT_BLOCK);
             else
@@ -340,7 +340,7 @@ __device__ __forceinline__ void fetch_q(uint32_t (&w)[D / 8], const Params &p, i
         ((int64_t)b * p.num_q_heads + kvh * G + gid % G) * D + tig * (D / 4));
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-        const uint4 x = __ldg(src + c);
+        const uint4 x = src[c];
         w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
     }
 }
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
         int n = 0, most = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const int raw = __ldg(p.seq_lens + b);
+            const int raw = p.seq_lens[b];
             if ((raw < 0 || raw > p.len_cap) && cta == 0)
                 atomicOr(p.err, PKV_EBIT_SEQLEN);
             const int L = raw < 0 || raw > p.len_cap ? 0 : attended_len(p, raw);

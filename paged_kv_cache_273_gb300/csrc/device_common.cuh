@@ -130,6 +130,9 @@ __device__ __forceinline__ bool count_wait_bounded(volatile int *c, int target,
 // grid_dependents_launch() lets the next such kernel start early (it still
 // waits for this one to finish before touching memory).  Both are no-ops for
 // a kernel launched without the attribute.
+// What the previous kernel may write is read by plain loads, and not through
+// `const ... __restrict__`: ld.global.nc wants data that nothing writes while the
+// kernel is on the GPU, and the wait comes after its start.
 __device__ __forceinline__ void grid_dependency_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

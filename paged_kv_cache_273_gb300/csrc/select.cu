@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seg = blockIdx.x / a.chunks, part = blockIdx.x - seg * a.chunks;
     const int H = a.num_kv_heads, b = seg / H, kvh = seg - b * H;
-    int L = __ldg(a.seq_lens + b);
+    int L = a.seq_lens[b];
     if (L < 0 || L > a.len_cap)
         L = 0;                               // (the attention records it)
     const int n = (L + a.block_size - 1) >> a.bs_log2;
@@ -291,13 +291,13 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
     if (n <= a.budget) {
         for (int i = tid; i < n; i += NT) {
             sel[i] = i;
-            phys[i] = __ldg(row + i);
+            phys[i] = row[i];
         }
         return;
     }
     if (part == 0 && tid == 0) {             // the newest block, always
         sel[nsel - 1] = n - 1;
-        phys[nsel - 1] = __ldg(row + n - 1);
+        phys[nsel - 1] = row[n - 1];
     }
     if (a.budget == 1)
         return;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
         for (int c = 0; c < NC / 2; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint4 x = __ldg(qsrc + 8 * c + h);
+                const uint4 x = qsrc[8 * c + h];
                 raw[c][4 * h] = x.x; raw[c][4 * h + 1] = x.y;
                 raw[c][4 * h + 2] = x.z; raw[c][4 * h + 3] = x.w;
             }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
     // the block ids of the lane's block of a group, its exponent, and the
     // bounds of rows gid, gid + 8 of a 16-block tile (the lane's chunks)
     auto load_id = [&](int j0) {
-        return j0 + lane < j_end ? __ldg(row + j0 + lane) : 0;
+        return j0 + lane < j_end ? row[j0 + lane] : 0;
     };
     auto valid_id = [&](int id) {
         if (id >= 0 && id < a.num_blocks)
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
                 a.bounds + ((int64_t)id_r * H + kvh) * 2 * D) + tig;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                x[r][c] = __ldg(src + 4 * c);
+                x[r][c] = src[4 * c];
         }
     };
     // a tile's scores: lane l gets that of row l mod 16
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
         // a tile's bounds are on their way while the one before is scored
         int raw = load_id(j0), raw_next = load_id(j0 + STEP);
         int id = valid_id(raw);
-        int e = __ldg(a.exps + (int64_t)id * H + kvh);
+        int e = a.exps[(int64_t)id * H + kvh];
         uint4 x0[2][NC], x1[2][NC];
         load_tile(x0, id, 0);
 #pragma unroll 1
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
                 raw = raw_next;
                 id = valid_id(raw);
                 raw_next = load_id(j0 + STEP);
-                e = __ldg(a.exps + (int64_t)id * H + kvh);
+                e = a.exps[(int64_t)id * H + kvh];
                 load_tile(x0, id, 0);
             }
             const float odd = score_tile(x1);
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_kernel(const SelectArgs a
 #pragma unroll 4
             for (int i = tid; i < n - 1; i += NT) {
                 s_keys[i] = __ldcg(keys + i);
-                s_keys[a.stage + i] = __ldg(row + i);
+                s_keys[a.stage + i] = row[i];
             }
             __syncthreads();
         }

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(NT) reserve_kernel(TableArgs a, const int32_t 
 
     // a new block's id, or -1 (recorded) for one outside the pool
     auto fresh = [&](int k) {
-        const int id = __ldg(free_ids + (count - 1 - k));
+        const int id = free_ids[count - 1 - k];
         if (id < 0 || id >= a.num_blocks) {
             atomicOr(a.err, PKV_EBIT_BLOCK);
             return -1;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(NT) release_kernel(TableArgs a, int32_t *free_
     bool bad_id = false;
     for (int k = blockIdx.x * NT + tid; k < R; k += gridDim.x * NT) {
         const int b = find(s_blk, B, k);
-        const int id = __ldg(tables + (int64_t)b * a.max_blocks + (k - s_blk[b]));
+        const int id = tables[(int64_t)b * a.max_blocks + (k - s_blk[b])];
         if (id < 0 || id >= a.num_blocks) {
             atomicOr(a.err, PKV_EBIT_BLOCK);
             bad_id = true;
