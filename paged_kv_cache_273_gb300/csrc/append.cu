@@ -25,21 +25,21 @@ using namespace dev;
 // One thread per 16-byte chunk of a (token, head) row, K and V in the same
 // pass.  chunks_per_row = D * eb / 16.
 __global__ void __launch_bounds__(256) append_copy_kernel(
-    const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-    const int32_t *__restrict__ slot_mapping, int64_t total_chunks, int chunks_per_row,
-    int num_kv_heads, int block_size, int64_t num_slots, uint4 *__restrict__ k_cache,
-    uint4 *__restrict__ v_cache, unsigned int *__restrict__ err)
+    const uint4 *k_new, const uint4 *v_new, const int32_t *slot_mapping, int64_t total_chunks,
+    int chunks_per_row, int num_kv_heads, int block_size, int64_t num_slots,
+    uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache, unsigned int *__restrict__ err)
 {
     grid_dependency_wait();
     grid_dependents_launch();
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     for (int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; c < total_chunks;
          c += stride) {
+        const uint4 k = k_new[c], v = v_new[c];           // on their way beside the slot
         const int64_t row = c / chunks_per_row;          // (token, head)
         const int chunk = (int)(c - row * chunks_per_row);
         const int64_t t = row / num_kv_heads;
         const int h = (int)(row - t * num_kv_heads);
-        const int32_t slot = __ldg(slot_mapping + t);
+        const int32_t slot = slot_mapping[t];
         if (slot < 0)
             continue;                                     // padding token
         if ((int64_t)slot >= num_slots) {
@@ -49,30 +49,30 @@ __global__ void __launch_bounds__(256) append_copy_kernel(
         const int64_t blk = slot / block_size;
         const int64_t off = slot - blk * block_size;
         const int64_t dst = ((blk * num_kv_heads + h) * block_size + off) * chunks_per_row + chunk;
-        k_cache[dst] = __ldg(k_new + c);
-        v_cache[dst] = __ldg(v_new + c);
+        k_cache[dst] = k;
+        v_cache[dst] = v;
     }
 }
 
 template <typename T>
 __device__ __forceinline__ float load_as_float(const T *p);
 template <>
-__device__ __forceinline__ float load_as_float<float>(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_as_float<float>(const float *p) { return *p; }
 template <>
-__device__ __forceinline__ float load_as_float<__half>(const __half *p) { return __half2float(__ldg(p)); }
+__device__ __forceinline__ float load_as_float<__half>(const __half *p) { return __half2float(*p); }
 template <>
 __device__ __forceinline__ float load_as_float<__nv_bfloat16>(const __nv_bfloat16 *p)
 {
-    return __bfloat162float(__ldg(p));
+    return __bfloat162float(*p);
 }
 
 // One warp per (token, head, K|V) row.  D = 32 * E.
 template <typename T, int E>
 __global__ void __launch_bounds__(256) append_q8_kernel(
-    const T *__restrict__ k_new, const T *__restrict__ v_new,
-    const int32_t *__restrict__ slot_mapping, int64_t num_rows /* T*Hkv */, int num_kv_heads,
-    int block_size, int64_t num_slots, int8_t *__restrict__ k_cache, int8_t *__restrict__ v_cache,
-    __half *__restrict__ k_scales, __half *__restrict__ v_scales, unsigned int *__restrict__ err)
+    const T *k_new, const T *v_new, const int32_t *slot_mapping, int64_t num_rows /* T*Hkv */,
+    int num_kv_heads, int block_size, int64_t num_slots, int8_t *__restrict__ k_cache,
+    int8_t *__restrict__ v_cache, __half *__restrict__ k_scales, __half *__restrict__ v_scales,
+    unsigned int *__restrict__ err)
 {
     constexpr int D = 32 * E;
     grid_dependency_wait();
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) append_q8_kernel(
         const int64_t row = is_v ? w - num_rows : w;
         const int64_t t = row / num_kv_heads;
         const int h = (int)(row - t * num_kv_heads);
-        const int32_t slot = __ldg(slot_mapping + t);
+        const int32_t slot = slot_mapping[t];
         if (slot < 0)
             continue;
         if ((int64_t)slot >= num_slots) {
@@ -140,9 +140,8 @@ __global__ void __launch_bounds__(256) append_q8_kernel(
 // each lane packs its 4 codes into 2 bytes.
 template <typename T>
 __global__ void __launch_bounds__(256) append_q4_kernel(
-    const T *__restrict__ k_new, const T *__restrict__ v_new,
-    const int32_t *__restrict__ slot_mapping, int64_t num_rows /* T*Hkv */, int num_kv_heads,
-    int block_size, int64_t num_slots, uint8_t *__restrict__ k_cache,
+    const T *k_new, const T *v_new, const int32_t *slot_mapping, int64_t num_rows /* T*Hkv */,
+    int num_kv_heads, int block_size, int64_t num_slots, uint8_t *__restrict__ k_cache,
     uint8_t *__restrict__ v_cache, __half *__restrict__ k_scales, __half *__restrict__ v_scales,
     unsigned int *__restrict__ err)
 {
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(256) append_q4_kernel(
         const int64_t row = is_v ? w - num_rows : w;
         const int64_t t = row / num_kv_heads;
         const int h = (int)(row - t * num_kv_heads);
-        const int32_t slot = __ldg(slot_mapping + t);
+        const int32_t slot = slot_mapping[t];
         if (slot < 0)
             continue;
         if ((int64_t)slot >= num_slots) {
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(256) append_q4_kernel(
 // thread per 16-byte chunk; a block-head tile row is a multiple of 16 bytes.
 // int8 scales ([NB][Hkv][bs] fp16) follow as 2-byte elements.
 __global__ void __launch_bounds__(256) block_copy_kernel(
-    const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n,
+    const int32_t *src, const int32_t *dst, int n,
     int64_t chunks_per_block, int64_t scales_per_block, int num_blocks,
     uint4 *__restrict__ k_cache, uint4 *__restrict__ v_cache, __half *__restrict__ k_scales,
     __half *__restrict__ v_scales, unsigned int *__restrict__ err)
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(256) block_copy_kernel(
          c += stride) {
         const int i = (int)(c / per_pair);
         int64_t r = c - (int64_t)i * per_pair;
-        const int32_t s = __ldg(src + i), d = __ldg(dst + i);
+        const int32_t s = src[i], d = dst[i];
         if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) {
             if (r == 0)
                 atomicOr(err, PKV_EBIT_BLOCK);
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(256) block_copy_kernel(
 constexpr int SC = 4;
 
 template <bool LOAD_FIRST>
-__global__ void __launch_bounds__(256) stage_copy_kernel(const uint4 *__restrict__ src,
+__global__ void __launch_bounds__(256) stage_copy_kernel(const uint4 *src,
                                                          uint4 *__restrict__ dst, int64_t n)
 {
     grid_dependents_launch();

@@ -1218,7 +1218,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NTHREADS, 1) paged_decode_kerne
 
     // Sequence lengths (validated) and the exclusive prefix of tiles.
     for (int b = tid; b < B; b += NTHREADS) {
-        int L = __ldg(p.seq_lens + b);
+        int L = p.seq_lens[b];
         if (L < 0 || L > p.len_cap) {
             if (blockIdx.x == 0)
                 atomicOr(p.err, PKV_EBIT_SEQLEN);
@@ -1228,7 +1228,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NTHREADS, 1) paged_decode_kerne
         int lo = (p.window > 0 && L > p.window) ? L - p.window : 0;
         if (p.seq_prefix) {
             // the rows after the shared prefix (none if the prefix is all)
-            lo = __ldg(p.seq_prefix + b);
+            lo = p.seq_prefix[b];
             if (lo < 0 || lo > L) {
                 if (blockIdx.x == 0)
                     atomicOr(p.err, PKV_EBIT_SEQLEN);
@@ -1423,7 +1423,7 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NTHREADS, 1) paged_decode_kerne
                         if (r < nr) {
                             const int rr = r < r_lo ? r_lo : (r < d.nblk ? r : d.nblk - 1);
                             const int tok = C::TT * d.ti + rr * rt;
-                            const int blk = __ldg(row + (tok >> p.bs_log2));
+                            const int blk = row[tok >> p.bs_log2];
                             d.id[r] = (blk >= 0 && blk < p.num_blocks)
                                           ? (blk * Hkv + d.kvh) * (bs / rt) + (tok & (bs - 1)) / rt
                                           : -1;
@@ -1432,10 +1432,10 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NTHREADS, 1) paged_decode_kerne
                 } else {
                     const int first = (TILE * d.ti) >> p.bs_log2;
                     d.nblk = bs >= TILE ? 1 : (nvalid + bs - 1) >> p.bs_log2;   // 1..4 (bs >= 4)
-                    d.id[0] = __ldg(row + first);
-                    if (d.nblk > 1) d.id[1] = __ldg(row + first + 1);
-                    if (d.nblk > 2) d.id[2] = __ldg(row + first + 2);
-                    if (d.nblk > 3) d.id[3] = __ldg(row + first + 3);
+                    d.id[0] = row[first];
+                    if (d.nblk > 1) d.id[1] = row[first + 1];
+                    if (d.nblk > 2) d.id[2] = row[first + 2];
+                    if (d.nblk > 3) d.id[3] = row[first + 3];
                 }
             }
             return d;

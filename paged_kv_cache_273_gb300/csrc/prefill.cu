@@ -331,11 +331,11 @@ __device__ __forceinline__ Item make_prefix_item(const PrefillParams &p, int i)
     it.kvh = rem / p.nkc;
     it.c = rem - it.kvh * p.nkc;
     it.h = it.kvh * p.group_q;
-    it.q0 = __ldg(p.grp_start + it.g);
-    const int members = __ldg(p.grp_start + it.g + 1) - it.q0;
-    const int P = __ldg(p.grp_len + it.g);
-    it.b = members > 0 ? __ldg(p.grp_seqs + it.q0) : 0;
-    const int L = members > 0 ? __ldg(p.seq_lens + it.b) : 0;
+    it.q0 = p.grp_start[it.g];
+    const int members = p.grp_start[it.g + 1] - it.q0;
+    const int P = p.grp_len[it.g];
+    it.b = members > 0 ? p.grp_seqs[it.q0] : 0;
+    const int L = members > 0 ? p.seq_lens[it.b] : 0;
     it.kt0 = it.c * p.kc_tiles;
     const int rows_total = members * p.group_q;
     const bool rows = it.qt * QT < rows_total && P > 0 && it.kt0 * TBK < P;
@@ -365,9 +365,9 @@ __device__ __forceinline__ Item make_item(const PrefillParams &p, int i)
     it.qt = p.nqt - 1 - qt_rev;
     it.b = rem % p.batch;
     it.h = rem / p.batch;
-    it.q0 = __ldg(p.q_start + it.b);
-    const int n = __ldg(p.q_start + it.b + 1) - it.q0;
-    const int L = __ldg(p.seq_lens + it.b);
+    it.q0 = p.q_start[it.b];
+    const int n = p.q_start[it.b + 1] - it.q0;
+    const int L = p.seq_lens[it.b];
     const bool rows = it.qt * QT < n;
     it.bad_len = rows && (L < n || L > p.max_blocks_per_seq * p.block_size);
     it.live = rows && !it.bad_len;
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(TNT, 1) paged_prefill_tc_kernel(const __grid_c
                         return p.out + ((row0 + x) * p.num_q_heads + it.h) * D;
                     const int mr = it.qt * QT + hh * TBQ + quad * 32 + x;   // member row
                     const int mem = mr / p.group_q;
-                    const int seq = __ldg(p.grp_seqs + it.q0 + mem);
+                    const int seq = p.grp_seqs[it.q0 + mem];
                     return p.part + (((int64_t)it.c * p.batch + seq) * p.num_q_heads +
                                      it.kvh * p.group_q + (mr - mem * p.group_q)) * (D + 4);
                 };
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(TNT, 1) paged_prefill_tc_kernel(const __grid_c
                     // member row: member mr / G's q head kvh G + mr % G
                     const int mr = it.qt * QT + (ok ? r : 0);
                     const int mem = mr / p.group_q;
-                    const int seq = __ldg(p.grp_seqs + it.q0 + mem);
+                    const int seq = p.grp_seqs[it.q0 + mem];
                     src = qg + ((int64_t)seq * p.num_q_heads + it.h + (mr - mem * p.group_q)) * D;
                 } else {
                     src = qg + ((int64_t)(it.q0 + it.qt * QT + (ok ? r : 0)) * p.num_q_heads +
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(TNT, 1) paged_prefill_tc_kernel(const __grid_c
                 const int pos0 = (it.kt0 + kt) * TBK + lane * R;
                 const bool inbox = lane < nbox;
                 const bool live = inbox && pos0 <= it.last_pos;
-                const int32_t blk = live ? __ldg(table + (pos0 >> p.bs_log2)) : 0;
+                const int32_t blk = live ? table[pos0 >> p.bs_log2] : 0;
                 if (g >= NSLOT && !wait(empty, (uint32_t)(((g / NSLOT) & 1) ^ 1)))
                     goto producer_done;
                 int z = oob;
@@ -1005,7 +1005,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const int32_t *seq_pr
         const int64_t row = u / (D / 4);
         const int d = (int)(u - row * (D / 4)) * 4;
         const int b = (int)(row / num_q_heads);
-        const int P = __ldg(seq_prefix + b);
+        const int P = seq_prefix[b];
         if (P <= 0)
             continue;
         const int nkc = ((P + TBK - 1) / TBK + kc_tiles - 1) / kc_tiles;
