@@ -20,7 +20,10 @@
  *                      Each (block, KV head) tile of bs*D elements is contiguous.
  *   k_scales, v_scales [NB][Hkv][bs]     fp16, int8 and int4 pools (one scale
  *                      per cached token per KV head); [NB][Hkv] fp32, F8 pools
- *                      (one power of two per block and KV head); NULL otherwise.
+ *                      (one power of two per block and KV head, 2^-96 to 2^120 as
+ *                      kv_append writes them; the attention reads a V scale's
+ *                      exponent alone, of a block never written it reads zeros if
+ *                      the cache was zeroed); NULL otherwise.
  *   q                  [B][Hq][D]        q_dtype.
  *   out                [B][Hq][D]        fp32.
  *   block_tables       [B][max_blocks_per_seq] int32: entry j of row b is the
@@ -539,7 +542,8 @@ int paged_decode_step(const pkv_pool *pool, const void *host_in, void *dev_in, s
  *  - Returns PKV_ERR_UNSUPPORTED when the batch needs more scratch than the
  *    array holds (paged_decode_workspace_bytes() > 4 MiB: on 152 SMs, more
  *    than about 1,800 sequence x KV-head pairs at G = 4, d = 128, or about
- *    850 at G = 8).
+ *    850 at G = 8; F8 pools, whose counters take 16 KiB a KV head whatever the
+ *    batch: about 1,800 and 820 at 8 KV heads).
  */
 int paged_decode_attention_noalloc(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
                                    int num_q_heads, const void *k_cache, const void *v_cache,

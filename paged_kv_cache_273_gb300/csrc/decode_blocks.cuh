@@ -79,19 +79,19 @@ struct Cfg {
     static constexpr int SC_BYTES = F8 ? 2 * TILE * 4 : 0;   // each row's K scale, then V scale
     static constexpr int STAGE = 2 * TILE_BYTES + SC_BYTES;
     // warps: a multiple of the SM's four partitions, as many as the registers
-    // allow (8-bit rows of 128, 16 x 4096 tokens, 32 / 8 heads: 29 us with 12
-    // warps, 30 to 35 us with 9 to 11 or 13 to 15)
+    // allow (8-bit rows of 128, 16 x 4096 tokens, 32 / 8 heads: 28.0 us with 12
+    // warps, 29.0 with 11, 32.3 with 13)
     static constexpr int W = F8 ? (D == 64 ? 16 : 12) : 8;
     // two tiles of a piece computed together: where the registers allow it
-    // beside as many warps (rows of 64: 34.6 instead of 35.5 us on 64
+    // beside as many warps (rows of 64: 33.8 instead of 34.5 us on 64
     // sequences of up to 2048 tokens, 12 heads; rows of 128 in pairs, with 8
-    // warps for the registers, 31 instead of 29 us on the shape above)
+    // warps for the registers, 30.0 instead of 28.0 us on the shape above)
     static constexpr bool PAIR = F8 && D == 64;
     static constexpr int NT = W * 32;
     static constexpr int STATE = G * (D + 2);       // floats of one softmax state
-    // ring stages that fit beside the states and the tile prefix, at most 5 (six
-    // for e4m3 rows of 64: 36.5 instead of 35.1 us on 64 sequences of up to 2048
-    // tokens, 12 heads)
+    // ring stages that fit beside the states and the tile prefix, at most 5 (e4m3
+    // rows of 64, 64 sequences of up to 2048 tokens, 12 heads: 33.8 us with 5, 34.1
+    // with 6, 34.6 with 4)
     static constexpr int FIXED = W * STATE * 4 + (MAX_BATCH + 1) * 4 + W * 6 * 16 + W * 16 + 256;
     static constexpr int FIT = (232448 - FIXED) / (W * STAGE);
     static constexpr int NST = FIT > 5 ? 5 : FIT;
@@ -785,7 +785,7 @@ __device__ __forceinline__ void tiles(State<D, G, KV> &st, const QScale<KV> &qsc
 // ONE: a tile's rows are of one block (16-bit caches: nothing of the math asks).
 // A kernel of its own for 8-bit float blocks of 8 rows: its tile math beside the
 // other's in one kernel costs registers (64 sequences of up to 4096 tokens, 32 / 8
-// heads of 64, blocks of 16: 46.7 instead of 39.8 us).
+// heads of 64, blocks of 16: 46.7 instead of 40.5 us).
 template <int D, int G, int KV, bool ONE>
 __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     decode_blocks_kernel(const __grid_constant__ Params p)
@@ -867,8 +867,10 @@ __global__ void __launch_bounds__(Cfg<D, G, KV>::NT, 1)
     // ---- this CTA's tiles [c0, c1), and how many CTAs have any (P).  Where the
     // sequences are about as long as one another, a CTA takes `each` whole
     // pieces, so that none is joined across CTAs: if that leaves at most a
-    // fifth of the CTAs idle (fewer SMs still draw the memory's full rate), or
-    // if the pieces are so short that joining costs more than it spreads.
+    // fifth of the CTAs idle (joining costs more than they would take over: 16 x
+    // 4096 e4m3 tokens of 8 KV heads on 128 of 152 SMs 28.0 us, shared out over
+    // all 30.0; 128 chosen blocks of 16 bf16 sequences 45.1 and 49.4), or if the
+    // pieces are so short that joining costs more than it spreads.
     // Else every CTA takes an equal part of the list, but no fewer than
     // MIN_TILES tiles a warp.
     int most = scan[W];
