@@ -26,23 +26,33 @@ namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// A driver function by name, null if there is none.
+void *driver_entry(const char *name, unsigned version)
+{
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion(name, &f, version, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return f;
+}
+
 }  // namespace
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    // A driver call: it wants the device's context to be current, which a host thread
-    // has only from its first runtime call of certain kinds on.
+    static const auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
+        driver_entry("cuTensorMapEncodeTiled", 12000));
+    static const auto current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(
+        driver_entry("cuCtxGetCurrent", 4000));
+    // A driver call: it wants a context to be current, which a host thread has only
+    // from its first runtime call of certain kinds on.  One that is current stays.
+    CUcontext ctx = nullptr;
+    if (!current || current(&ctx) != CUDA_SUCCESS)
+        return nullptr;
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)
+    if (!ctx && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
         return nullptr;
     return fn;
 }

@@ -1239,8 +1239,8 @@ int launch_k(const pkv_pool *pool, const Params &base, cudaStream_t stream, int6
     const int64_t pieces = (int64_t)prm.batch * prm.num_kv_heads;
     prm.pieces_each = (int)((pieces + P - 1) / P);
     prm.whole_ctas = (int)((pieces + prm.pieces_each - 1) / prm.pieces_each);
-    if (launch_pdl(decode_blocks_kernel<D, G, KV, ONE>, dim3((unsigned)P), dim3(C::NT), (size_t)smem,
-                   stream, prm) != cudaSuccess)
+    if (launch_pdl(decode_blocks_kernel<D, G, KV, ONE>, dim3((unsigned)P), dim3(C::NT),
+                   (size_t)smem, stream, prm) != cudaSuccess)
         return PKV_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
