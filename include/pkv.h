@@ -716,6 +716,117 @@ int paged_decode_attention_sparse(const pkv_pool *pool, const void *q, pkv_dtype
                                   void *workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /*
+ * pkv_rope — a rotation of positions, as kv_rope_rotate and kv_rope_append take it.
+ * The pages give no positions; this is the rotary scheme that models with this cache
+ * use: pair i of a head's first rot_dim channels, (a, b), at position p becomes
+ *   magnitude * (a cos - b sin, b cos + a sin),   angle = p * theta_i,
+ * and the channels from rot_dim on stay as they are.
+ *   freqs      device uint64 [rot_dim / 2], theta_i as a fraction of a turn in units
+ *              of 2^-64 (kv_rope_frequencies fills a host array; the caller copies it
+ *              to the device once), 16-byte aligned.  Angles are exact modulo a turn
+ *              at every position.
+ *   rot_dim    a multiple of 16, 16..head_dim.
+ *   layout     PKV_ROPE_HALF: pair i is channels (i, i + rot_dim / 2);
+ *              PKV_ROPE_INTERLEAVED: channels (2 i, 2 i + 1).
+ *   magnitude  a factor on the rotated values, 1 unless the scaling asks for another.
+ */
+typedef enum { PKV_ROPE_HALF = 0, PKV_ROPE_INTERLEAVED = 1 } pkv_rope_layout;
+typedef enum {
+    PKV_ROPE_PLAIN = 0,
+    PKV_ROPE_LINEAR = 1,
+    PKV_ROPE_PARTS = 2,
+    PKV_ROPE_WAVELENGTH = 3
+} pkv_rope_scaling;
+typedef struct {
+    const uint64_t *freqs;
+    int rot_dim;
+    int layout;
+    float magnitude;
+} pkv_rope;
+
+/*
+ * kv_rope_frequencies — host: the frequencies and the magnitude of a pkv_rope.
+ * With f_i = base^(-2 i / rot_dim) radians a position, i < rot_dim / 2, and N =
+ * trained_len, theta_i is
+ *   PLAIN       f_i (factor, trained_len, low and high are not looked at);
+ *   LINEAR      f_i / factor (positions interpolated);
+ *   PARTS       f_i / factor * s + f_i * (1 - s), s = clamp((i - first) /
+ *               max(last - first, 0.001), 0, 1), with first = max(0, floor(at(high))),
+ *               last = min(rot_dim - 1, ceil(at(low))) and at(t) = the i whose pair
+ *               makes t turns over N positions, rot_dim ln(N / (2 pi t)) / (2 ln base):
+ *               pairs of more than `high` turns keep their frequency, those of fewer
+ *               than `low` are interpolated; magnitude 0.1 ln(factor) + 1 for factor > 1;
+ *   WAVELENGTH  f_i / factor * (1 - s) + f_i * s, s = clamp((N f_i / (2 pi) - low) /
+ *               (high - low), 0, 1).
+ * magnitude is 1 but for PARTS.  PKV_ERR_INVALID for a null pointer, base < 1 (PARTS:
+ * <= 1), factor <= 0, and for PARTS and WAVELENGTH trained_len < 1, low <= 0 or high <=
+ * low, or a value that is not finite; PKV_ERR_UNSUPPORTED for a rot_dim that is not one
+ * of 16, 32, .. 128.
+ */
+int kv_rope_frequencies(int rot_dim, double base, pkv_rope_scaling scaling, double factor,
+                        int trained_len, double low, double high, uint64_t *freqs,
+                        float *magnitude);
+
+/*
+ * kv_rope_rotate — rotate the heads of num_tokens tokens to their positions.
+ *
+ *   x          device rows of num_heads heads of head_dim (64 or 128) values, dtype
+ *              F32, F16 or BF16; token t's first value is x_stride * t values behind
+ *              x.  q's and K's heads of one projection's output lie side by side: one
+ *              call rotates both.
+ *   positions  device int32 [num_tokens], any value (a negative one turns back).
+ *   transposed != 0: the transposed rotation, magnitude * (a cos + b sin,
+ *              b cos - a sin): what takes the gradient of the rotated rows to the
+ *              gradient of the rows (and, for magnitude 1, a rotated row back).
+ *   out        device rows like x, out_stride apart; may be x itself with the same
+ *              stride (in place), and must not overlap it otherwise.
+ *
+ * Products and sums in fp32, each value rounded once to dtype.  Values between
+ * the heads' end and the next token's first value are left as they are.  Strides are
+ * multiples of 16 bytes and at least num_heads * head_dim; pointers 16-byte
+ * aligned (PKV_ERR_INVALID otherwise).  num_tokens == 0 or num_heads == 0 is a no-op.
+ * Launched on the current device, where every pointer must be.  One kernel.
+ */
+int kv_rope_rotate(const pkv_rope *rope, const void *x, int64_t x_stride, pkv_dtype dtype,
+                   int num_heads, int head_dim, const int32_t *positions, int num_tokens,
+                   int transposed, void *out, int64_t out_stride, pkv_stream_t stream);
+
+/*
+ * kv_rope_append — kv_rope_rotate of q and K and kv_append of K and V in one kernel:
+ * from a projection's output to the attention's q and the cache ([NOTES] "What
+ * happens at each decoding step", step 4; [GUIDE] "How the cache turns the loop cheap").
+ *
+ *   q, k, v    device rows of num_q_heads, Hkv and Hkv heads of the pool's head_dim,
+ *              element type in_dtype, token t's first value q_stride * t (k_stride,
+ *              v_stride) values behind: slices of one projection's output are
+ *              passed as they are.  num_q_heads == 0: K and V only (q and q_out are
+ *              not looked at).
+ *   positions  device int32 [T], the angle's position (apart from the slot, so drafted
+ *              tokens of a tree may share one).
+ *   slot_mapping  device int32 [T].  A token with a slot < 0 is skipped altogether:
+ *              its row of q_out stays as it was.
+ *   q_out      device rows of in_dtype, q_out_stride apart ([T][Hq][D] with
+ *              q_out_stride = Hq * D is what the attention takes); may be q itself with
+ *              the same stride, and overlaps nothing else.
+ *   k_cache, v_cache, k_scales, v_scales  as for kv_append.
+ *
+ * Pools: F32, F16 and BF16 (in_dtype the pool's: K rounded once, V bit for bit) and F8
+ * (in_dtype F32, F16 or BF16; scales, codes and runs as for kv_append, of K's rotated
+ * fp32 values, which are rounded once, to their codes).  Pools with a scale a row (I8,
+ * I4) are PKV_ERR_UNSUPPORTED: kv_rope_rotate, then kv_append.  The same two calls serve
+ * where kv_bounds_append wants the rotated keys.  A slot out of range sets
+ * PKV_ERR_BAD_INDEX and its token is skipped.  Strides and pointers as for kv_rope_rotate.
+ * num_tokens == 0 is a no-op.  PKV_ERR_INVALID also if the pool's device is not the
+ * current one.  One kernel.
+ */
+int kv_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q, int64_t q_stride,
+                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   pkv_dtype in_dtype, int num_q_heads, const int32_t *positions,
+                   const int32_t *slot_mapping, int num_tokens, void *q_out,
+                   int64_t q_out_stride, void *k_cache, void *v_cache, void *k_scales,
+                   void *v_scales, pkv_stream_t stream);
+
+/*
  * pkv_selftest_wait_timeout — a check of the failure path of the library's
  * bounded device waits (not part of the method).  Launches one kernel whose
  * single waiting thread waits, the way every mbarrier wait in this library

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 CUDA_SOURCES = ["append.cu", "decode.cu", "decode_f32.cu", "decode_f16.cu", "decode_bf16.cu",
                 "decode_i8.cu", "decode_i4.cu", "decode_f8.cu", "decode_blocks_16.cu",
                 "decode_noalloc.cu", "prefill.cu", "selftest.cu", "tables.cu",
-                "append_blocks.cu", "select.cu"]
+                "append_blocks.cu", "select.cu", "rope.cu"]
 HOST_SOURCES = ["pool.cpp"]
 HEADERS = ["pkv_internal.h", "device_common.cuh", "decode_kernel.cuh",
            "blocks_common.cuh", "decode_blocks.cuh"]

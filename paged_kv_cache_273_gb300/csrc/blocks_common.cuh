@@ -58,5 +58,81 @@ __device__ __forceinline__ int int8_exponent(float amax)
     return min(max(e, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
 }
 
+// The least e >= BLOCK_MIN_EXP with amax <= 448 * 2^e, the largest e4m3 value
+// being 448 = 1.75 * 2^8 (amax finite, >= 0).
+__device__ __forceinline__ int code_exponent(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, BLOCK_MIN_EXP), BLOCK_MAX_EXP);
+}
+
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, m));
+    return x;
+}
+
+// For every run that starts at a token of [t0, t0 + C) (C <= 32), in order:
+// f(first token, block, first offset in the block, rows).  All lanes call f
+// together.  `report`: record slots beyond the cache.
+template <typename F>
+__device__ __forceinline__ void for_runs(const int32_t *slots, int64_t t0, int C, int64_t T,
+                                         int bs, int64_t num_slots, bool report,
+                                         unsigned int *err, F f)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t t = t0 + lane;
+    const int s = lane < C && t < T ? slots[t] : -1;
+    int before = __shfl_up_sync(FULL_MASK, s, 1);
+    if (lane == 0)
+        before = t0 > 0 ? slots[t0 - 1] : -1;
+    if (report && s >= 0 && (int64_t)s >= num_slots)
+        atomicOr(err, PKV_EBIT_SLOT);
+    const bool starts = s >= 0 && (int64_t)s < num_slots &&
+                        (before != s - 1 || (s & (bs - 1)) == 0);
+    unsigned todo = __ballot_sync(FULL_MASK, starts);
+    while (todo) {
+        const int i = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int slot = __shfl_sync(FULL_MASK, s, i);
+        const int off = slot & (bs - 1);
+        int n = 1;                                   // rows of the run
+        for (;;) {
+            const int64_t tn = t0 + i + n + lane;
+            const bool more = off + n + lane < bs && tn < T && slots[tn] == slot + n + lane;
+            const unsigned gap = ~__ballot_sync(FULL_MASK, more);
+            if (gap) {
+                n += __ffs(gap) - 1;
+                break;
+            }
+            n += 32;
+        }
+        f(t0 + i, slot / bs, off, n);
+    }
+}
+
+// A block's first n 16-byte pieces of e4m3 codes by 2^down (<= 0), a piece a lane of
+// the warp: the rows that it holds when its exponent grows.
+__device__ __forceinline__ void rescale_rows(uint8_t *rows, int n, int down)
+{
+    const float f = pow2_f32(max(down, -126));
+    uint4 *p = reinterpret_cast<uint4 *>(rows);
+    for (int i = threadIdx.x & 31; i < n; i += 32) {
+        const uint4 old = p[i];
+        uint32_t v[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float y[4];
+            f8_unpack(v[u] & 0xffffu, y[0], y[1]);
+            f8_unpack(v[u] >> 16, y[2], y[3]);
+            v[u] = f8_pack(y[0] * f, y[1] * f) | f8_pack(y[2] * f, y[3] * f) << 16;
+        }
+        p[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
 }  // namespace dev
 }  // namespace pkv

@@ -116,6 +116,18 @@ int launch_append_bounds(const pkv_pool *pool, const void *k_new, pkv_dtype in_d
 int launch_bounds_copy(const pkv_pool *pool, const int32_t *src, const int32_t *dst, int n,
                        int8_t *bounds, int32_t *exps, pkv_stream_t stream);
 
+// Rotary positions (rope.cu).
+int launch_rope_rotate(const pkv_rope *rope, const void *x, int64_t x_stride, pkv_dtype dtype,
+                       int num_heads, int head_dim, const int32_t *positions, int num_tokens,
+                       bool transposed, void *out, int64_t out_stride, int num_sms,
+                       pkv_stream_t stream);
+int launch_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q,
+                       int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, pkv_dtype in_dtype, int num_q_heads,
+                       const int32_t *positions, const int32_t *slots, int num_tokens,
+                       void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                       void *k_scales, void *v_scales, pkv_stream_t stream);
+
 // The workspace of decode_blocks_kernel and select_kernel starts with a counter
 // for each KV head of the largest batch, whatever the call's batch: one buffer,
 // zeroed once, then serves calls of any batch, since none writes its scratch

@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 #include <unordered_map>
 
@@ -956,6 +957,137 @@ int paged_decode_attention_sparse(const pkv_pool *pool, const void *q, pkv_dtype
                               bounds, bound_exps, block_tables, max_blocks_per_seq, seq_lens,
                               batch, max_seq_len, max_selected, scale, out, selected, workspace,
                               stream);
+}
+
+int kv_rope_frequencies(int rot_dim, double base, pkv_rope_scaling scaling, double factor,
+                        int trained_len, double low, double high, uint64_t *freqs,
+                        float *magnitude)
+{
+    if (!freqs || !magnitude || !std::isfinite(base) || base < 1.0)
+        return PKV_ERR_INVALID;
+    if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0)
+        return PKV_ERR_UNSUPPORTED;
+    const bool by_part = scaling == PKV_ROPE_PARTS, by_wave = scaling == PKV_ROPE_WAVELENGTH;
+    if (scaling != PKV_ROPE_PLAIN && scaling != PKV_ROPE_LINEAR && !by_part && !by_wave)
+        return PKV_ERR_INVALID;
+    if (scaling == PKV_ROPE_PLAIN)
+        factor = 1.0;
+    if (!std::isfinite(factor) || factor <= 0.0)
+        return PKV_ERR_INVALID;
+    if ((by_part || by_wave) && (trained_len < 1 || !std::isfinite(low) || !std::isfinite(high) ||
+                                 low <= 0.0 || high <= low || (by_part && base <= 1.0)))
+        return PKV_ERR_INVALID;
+    const double tau = 6.283185307179586476925;
+    double first = 0.0, last = 0.0;
+    if (by_part) {
+        auto at = [&](double turns) {
+            return rot_dim * std::log(trained_len / (turns * tau)) / (2.0 * std::log(base));
+        };
+        first = std::max(0.0, std::floor(at(high)));
+        last = std::min((double)(rot_dim - 1), std::ceil(at(low)));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double theta = f / factor;
+        if (by_part) {
+            const double s = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
+            theta = f / factor * s + f * (1.0 - s);
+        } else if (by_wave) {
+            const double s = std::min(1.0, std::max(0.0, (trained_len * f / tau - low) / (high - low)));
+            theta = f / factor * (1.0 - s) + f * s;
+        }
+        // a fraction of a turn in units of 2^-64 (whole turns make no difference at
+        // whole positions)
+        const double turn = theta / tau, part = std::ldexp(turn - std::floor(turn), 64);
+        freqs[i] = part < 0x1p52 ? (uint64_t)(part + 0.5) : (uint64_t)part;
+    }
+    *magnitude = by_part && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return PKV_OK;
+}
+
+namespace {
+
+// A rotation's own fields, for heads of head_dim.
+int rope_check(const pkv_rope *rope, int head_dim)
+{
+    if (!rope || !rope->freqs || !pkv::aligned16(rope->freqs) ||
+        (rope->layout != PKV_ROPE_HALF && rope->layout != PKV_ROPE_INTERLEAVED) ||
+        !std::isfinite(rope->magnitude))
+        return PKV_ERR_INVALID;
+    if (rope->rot_dim < 16 || rope->rot_dim > head_dim || rope->rot_dim % 16 != 0)
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// Rows of `heads` heads, `stride` values apart, that 16-byte accesses reach.
+bool rows_ok(const void *p, int64_t stride, int heads, int head_dim, pkv_dtype dtype)
+{
+    return p && pkv::aligned16(p) && stride >= (int64_t)heads * head_dim &&
+           stride < ((int64_t)1 << 40) && stride * pkv::dtype_bytes(dtype) % 16 == 0;
+}
+
+bool plain_dtype(pkv_dtype t) { return t == PKV_F32 || t == PKV_F16 || t == PKV_BF16; }
+
+}  // namespace
+
+int kv_rope_rotate(const pkv_rope *rope, const void *x, int64_t x_stride, pkv_dtype dtype,
+                   int num_heads, int head_dim, const int32_t *positions, int num_tokens,
+                   int transposed, void *out, int64_t out_stride, pkv_stream_t stream)
+{
+    Range range("pkv.kv_rope_rotate");
+    if (num_tokens < 0 || num_heads < 0 || num_heads > 65535)
+        return PKV_ERR_INVALID;
+    if (!plain_dtype(dtype) || (head_dim != 64 && head_dim != 128))
+        return PKV_ERR_UNSUPPORTED;
+    const int rc = rope_check(rope, head_dim);
+    if (rc != PKV_OK || num_tokens == 0 || num_heads == 0)
+        return rc;
+    if (!rows_ok(x, x_stride, num_heads, head_dim, dtype) ||
+        !rows_ok(out, out_stride, num_heads, head_dim, dtype) || !positions ||
+        !aligned4(positions) || (out == x && out_stride != x_stride))
+        return PKV_ERR_INVALID;
+    int dev = -1, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();                // a missing device is not sticky for the caller
+        return PKV_ERR_CUDA;
+    }
+    return pkv::launch_rope_rotate(rope, x, x_stride, dtype, num_heads, head_dim, positions,
+                                   num_tokens, transposed != 0, out, out_stride, sms, stream);
+}
+
+int kv_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q, int64_t q_stride,
+                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   pkv_dtype in_dtype, int num_q_heads, const int32_t *positions,
+                   const int32_t *slot_mapping, int num_tokens, void *q_out,
+                   int64_t q_out_stride, void *k_cache, void *v_cache, void *k_scales,
+                   void *v_scales, pkv_stream_t stream)
+{
+    Range range("pkv.kv_rope_append");
+    if (!pool || num_tokens < 0 || num_q_heads < 0 || num_q_heads > 65535)
+        return PKV_ERR_INVALID;
+    if (pool->kv_dtype == PKV_I8 || pool->kv_dtype == PKV_I4)
+        return PKV_ERR_UNSUPPORTED;
+    int rc = rope_check(rope, pool->head_dim);
+    if (rc == PKV_OK)
+        rc = append_check(pool, k, v, in_dtype, slot_mapping, num_tokens, k_cache, v_cache,
+                          k_scales, v_scales);
+    if (rc != PKV_OK || num_tokens == 0)
+        return rc;
+    const int D = pool->head_dim, H = pool->num_kv_heads;
+    if (!rows_ok(k, k_stride, H, D, in_dtype) || !rows_ok(v, v_stride, H, D, in_dtype) ||
+        !positions || !aligned4(positions))
+        return PKV_ERR_INVALID;
+    if (num_q_heads > 0 && (!rows_ok(q, q_stride, num_q_heads, D, in_dtype) ||
+                            !rows_ok(q_out, q_out_stride, num_q_heads, D, in_dtype) ||
+                            (q_out == q && q_out_stride != q_stride)))
+        return PKV_ERR_INVALID;
+    rc = device_check(pool);
+    if (rc != PKV_OK)
+        return rc;
+    return pkv::launch_rope_append(pool, rope, q, q_stride, k, k_stride, v, v_stride, in_dtype,
+                                   num_q_heads, positions, slot_mapping, num_tokens, q_out,
+                                   q_out_stride, k_cache, v_cache, k_scales, v_scales, stream);
 }
 
 int pkv_selftest_wait_timeout(const pkv_pool *pool, pkv_stream_t stream)

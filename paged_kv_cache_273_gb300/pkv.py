@@ -50,7 +50,8 @@ SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "
            "paged_decode_cascade_workspace_bytes", "paged_decode_attention_cascade",
            "paged_decode_attention_noalloc", "paged_decode_step", "kv_device_reserve",
            "kv_device_release", "kv_bounds_append", "kv_bounds_copy", "paged_sparse_workspace_bytes",
-           "paged_decode_attention_sparse", "pkv_selftest_wait_timeout", "pkv_check_error")
+           "paged_decode_attention_sparse", "kv_rope_frequencies", "kv_rope_rotate",
+           "kv_rope_append", "pkv_selftest_wait_timeout", "pkv_check_error")
 
 
 class StepLayout(ctypes.Structure):
@@ -58,6 +59,12 @@ class StepLayout(ctypes.Structure):
     buffer."""
     _fields_ = [("k_new", ctypes.c_size_t), ("v_new", ctypes.c_size_t), ("q", ctypes.c_size_t),
                 ("slot_mapping", ctypes.c_size_t), ("seq_lens", ctypes.c_size_t)]
+
+
+class Rope(ctypes.Structure):
+    """pkv_rope: a rotation of positions (see RopePlan)."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
 
 
 class PkvError(RuntimeError):
@@ -153,6 +160,15 @@ def load() -> ctypes.CDLL:
         lib.paged_decode_attention_sparse.argtypes = [P, P, I, I, P, P, P, P, P, P, P, I, P, I, I,
                                                       I, F, P, P, P, SZ, P]
         lib.paged_decode_attention_sparse.restype = I
+        I64, DB, RP = ctypes.c_int64, ctypes.c_double, ctypes.POINTER(Rope)
+        lib.kv_rope_frequencies.argtypes = [I, DB, I, DB, I, DB, DB,
+                                            ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(F)]
+        lib.kv_rope_frequencies.restype = I
+        lib.kv_rope_rotate.argtypes = [RP, P, I64, I, I, I, P, I, I, P, I64, P]
+        lib.kv_rope_rotate.restype = I
+        lib.kv_rope_append.argtypes = [P, RP, P, I64, P, I64, P, I64, I, I, P, P, I, P, I64, P, P,
+                                       P, P, P]
+        lib.kv_rope_append.restype = I
         lib.pkv_selftest_wait_timeout.argtypes = [P, P]
         lib.pkv_selftest_wait_timeout.restype = I
         lib.pkv_check_error.argtypes = [P, P]
@@ -761,6 +777,129 @@ def paged_decode_attention_sparse(pool: Pool, q, k_cache, v_cache, bounds, bound
         float(scale), _dptr(out), _dptr(selected), _dptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)),
         "paged_decode_attention_sparse")
+
+
+# ------------------------------------------------------------- rotary positions
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "parts": 2, "wavelength": 3}
+
+
+def kv_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
+                        factor: float = 1.0, trained_len: int = 0, low: float = 0.0,
+                        high: float = 0.0):
+    """The pairs' frequencies (uint64 numpy array, turns a position in units of 2^-64) and the
+    magnitude of a rotation (see include/pkv.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    freqs = np.zeros(max(1, rot_dim // 2), np.uint64)
+    mag = ctypes.c_float(0.0)
+    _check(load().kv_rope_frequencies(rot_dim, base, ROPE_SCALINGS[scaling], factor, trained_len,
+                                      low, high,
+                                      freqs.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)),
+                                      ctypes.byref(mag)), "kv_rope_frequencies")
+    return freqs, mag.value
+
+
+class RopePlan:
+    """A rotation of positions, its frequencies on the device: made once, for any number of
+    kv_rope_rotate and kv_rope_append calls."""
+
+    def __init__(self, freqs, magnitude: float, layout: str = "half", device="cuda"):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError("layout must be one of %s" % ", ".join(ROPE_LAYOUTS))
+        self.freqs = torch.from_numpy(freqs.view(np.int64).copy()).to(device)
+        self.rot_dim, self.layout, self.magnitude = 2 * freqs.size, layout, magnitude
+        self.struct = Rope(self.freqs.data_ptr(), self.rot_dim, ROPE_LAYOUTS[layout], magnitude)
+
+
+def rope_plan(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "plain",
+              factor: float = 1.0, trained_len: int = 0, low: float = 0.0, high: float = 0.0,
+              device="cuda") -> RopePlan:
+    """The rotation of a head's first rot_dim channels by base^(-2 i / rot_dim) radians a
+    position, scaled for long contexts (see kv_rope_frequencies in include/pkv.h)."""
+    freqs, mag = kv_rope_frequencies(rot_dim, base, scaling, factor, trained_len, low, high)
+    return RopePlan(freqs, mag, layout, device)
+
+
+def _head_rows(name: str, t, dtype, heads, head_dim):
+    """The pointer and token stride of rows [T, heads, head_dim] whose heads lie side by side:
+    a contiguous tensor, or a slice of one projection's output."""
+    _shaped(name, t, dtype, (None, heads, head_dim))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    T, H, D = t.shape
+    if T == 0 or H == 0:
+        return 0, H * D
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s: a token's heads must lie side by side" % name)
+    return t.data_ptr(), t.stride(0) if T > 1 else max(t.stride(0), H * D)
+
+
+def _on_current(*tensors) -> None:
+    """Kernels run on the current device: raise for a tensor on another."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError("expected tensors on the current device (cuda:%d)" % cur)
+
+
+def kv_rope_rotate(rope: RopePlan, x, positions, out=None, transposed: bool = False,
+                   stream=None):
+    """Rotate the heads x [T, heads, D] to their positions (see include/pkv.h), into `out`
+    (default: a new tensor; x itself: in place), which is returned.  x and out may be slices
+    of wider rows.  transposed: the rotation's gradient."""
+    if x.dim() != 3 or x.dtype not in PKV_DTYPE:
+        raise ValueError("x must be [T, heads, D] of float32, float16 or bfloat16")
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    xp, xs = _head_rows("x", x, x.dtype, H, D)
+    op, os_ = _head_rows("out", out, x.dtype, H, D)
+    _shaped("out", out, x.dtype, (T, H, D))
+    _shaped("positions", positions, _I32, (T,))
+    _on_current(x, out, positions, rope.freqs)
+    _check(load().kv_rope_rotate(ctypes.byref(rope.struct), xp, xs, PKV_DTYPE[x.dtype], H, D,
+                                 _dptr(positions), T, int(transposed), op, os_,
+                                 _stream(stream)), "kv_rope_rotate")
+    return out
+
+
+def kv_rope_append(pool: Pool, rope: RopePlan, q, k, v, positions, slot_mapping, q_out, k_cache,
+                   v_cache, k_scales=None, v_scales=None, stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out and K [T, Hkv, D] into the cache, V beside it, in one
+    kernel (see include/pkv.h).  q, k and v may be slices of one projection's output; q None:
+    K and V only."""
+    if k.dtype not in PKV_DTYPE:
+        raise ValueError("unsupported k dtype %s" % k.dtype)
+    H, D, T = pool.num_kv_heads, pool.head_dim, k.shape[0]
+    kp, ks = _head_rows("k", k, k.dtype, H, D)
+    vp, vs = _head_rows("v", v, k.dtype, H, D)
+    _shaped("v", v, k.dtype, (T, H, D))
+    _shaped("positions", positions, _I32, (T,))
+    _shaped("slot_mapping", slot_mapping, _I32, (T,))
+    qp = qs = op = os_ = Hq = 0
+    if q is not None:
+        _shaped("q", q, k.dtype, (T, None, D))
+        Hq = q.shape[1]
+        qp, qs = _head_rows("q", q, k.dtype, Hq, D)
+        _shaped("q_out", q_out, k.dtype, (T, Hq, D))
+        op, os_ = _head_rows("q_out", q_out, k.dtype, Hq, D)
+        _on_current(q, q_out)
+    _on_current(k, v, positions, slot_mapping, rope.freqs)
+    _cache_of(pool, k_cache, v_cache)
+    _check_scales(pool, k_scales, v_scales)
+    _check(load().kv_rope_append(pool.handle, ctypes.byref(rope.struct), qp, qs, kp, ks, vp, vs,
+                                 PKV_DTYPE[k.dtype], Hq, _dptr(positions), _dptr(slot_mapping), T,
+                                 op, os_, _dptr(k_cache), _dptr(v_cache), _dptr(k_scales),
+                                 _dptr(v_scales), _stream(stream)), "kv_rope_append")
+
+
+def _cache_of(pool: Pool, *caches) -> None:
+    """Raise unless these are caches of the pool's shape and type."""
+    shape = (pool.num_blocks, pool.num_kv_heads, pool.block_size, pool.head_dim)
+    for c in caches:
+        if c.shape != shape or c.dtype is not TORCH_DTYPE[pool.kv_dtype]:
+            _shaped("a cache", c, TORCH_DTYPE[pool.kv_dtype], shape)
 
 
 def pkv_selftest_wait_timeout(pool: Pool, stream=None) -> None:
