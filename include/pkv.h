@@ -827,6 +827,69 @@ int kv_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q, in
                    void *v_scales, pkv_stream_t stream);
 
 /*
+ * paged_chunk_workspace_bytes — bytes of the workspace of paged_chunk_attention for
+ * calls of up to max_q_len new tokens a sequence: where each CTA's share of the work
+ * starts, and two softmax states a CTA (it depends on the GPU's SMs, not on
+ * the batch).  Nothing in it needs to be zeroed, and a larger one serves smaller calls.
+ * 0 on bad arguments.
+ */
+size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
+                                   int max_q_len);
+
+/*
+ * paged_chunk_attention — attention of each sequence's new tokens over its cached rows,
+ * for steps that bring several tokens a sequence: pieces of prompts, whole prompts,
+ * drafted tokens to be checked, and single tokens among them ([VIS] "Prefill and decode feel
+ * different"; the math is [NOTES] "Concept").  Sequence b has n_b = q_start[b+1] -
+ * q_start[b] new tokens, the last n_b of its seq_lens[b] cached rows (written before, by
+ * kv_append or kv_rope_append); new token i sits at position p = seq_lens[b] - n_b + i and,
+ * for each query head h (KV head h / G),
+ *   out[q_start[b] + i][h] = softmax(scale * q[q_start[b] + i][h] . K^T) . V
+ * over the cached positions j <= p, with window > 0 those of j > p - window, and with
+ * `visible` those of j < seq_lens[b] - n_b and the new tokens whose bit is set.  A token
+ * that sees nothing gets zeros.  Beside paged_prefill_attention: 8-bit caches, windows
+ * and trees of drafts, output of q's type, and the keys of few tokens split over the GPU.
+ *
+ *   q          device [num_tokens][Hq][D]; q_dtype the pool's for F16 and BF16 pools, F16
+ *              or BF16 for F8 pools.
+ *   num_q_heads  a multiple of Hkv with G in {1, 2, 4, 8}.
+ *   q_start    device int32 [batch + 1], non-decreasing, q_start[0] >= 0 and
+ *              q_start[batch] <= num_tokens; rows of `out` behind the last sequence's (and
+ *              before the first's) are left as they were.
+ *   seq_lens   device int32 [batch], seq_lens[b] >= n_b.
+ *   max_q_len  >= every n_b (sizes the items of work; host value, no device read).
+ *   window     0: none.
+ *   visible    device uint64 [num_tokens] or NULL: bit j of token i's word: i sees new token
+ *              j of its sequence (itself only with its own bit).  Sequences then have at
+ *              most 64 new tokens, and window is 0.
+ *   scale      > 0 and finite.
+ *   out        device [num_tokens][Hq][D] of q_dtype.
+ *   workspace  device scratch of at least paged_chunk_workspace_bytes(); not shared by
+ *              calls that run concurrently.
+ *
+ * Scores and sums in fp32; the weights enter the second product rounded to q's type (over
+ * F8 caches to bf16, and for fp16 q in two parts), which moves an output by about as much as its own
+ * rounding does.  An F16 or BF16 row of V that is not finite makes the outputs of its own
+ * sequence's earlier tokens in the same call unspecified (those of the same 32 to 256 tokens),
+ * an F8 cache's values are finite.  Pools: F16, BF16, F8 (others
+ * PKV_ERR_UNSUPPORTED).  Lengths out of range (n_b > max_q_len or n_b > 64 with `visible`
+ * among them) set PKV_ERR_BAD_INDEX and that sequence's rows of `out` are left as they
+ * were; a block id outside the pool sets it too and its rows are read as zeros.  Table
+ * entries of blocks before every token's window are not looked at.  batch == 0, num_tokens == 0
+ * or max_q_len == 0 is a no-op; batch <= 65535.  Two kernels.  The result does not depend on timing.
+ * PKV_ERR_INVALID also if the pool's device is not the current one; PKV_ERR_CUDA if a
+ * tensor map cannot be encoded.
+ */
+int paged_chunk_attention(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
+                          int num_q_heads, int num_tokens, const void *k_cache,
+                          const void *v_cache, const void *k_scales, const void *v_scales,
+                          const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *q_start, const int32_t *seq_lens, int batch,
+                          int max_q_len, int window, const uint64_t *visible, float scale,
+                          void *out, void *workspace, size_t workspace_bytes,
+                          pkv_stream_t stream);
+
+/*
  * pkv_selftest_wait_timeout — a check of the failure path of the library's
  * bounded device waits (not part of the method).  Launches one kernel whose
  * single waiting thread waits, the way every mbarrier wait in this library

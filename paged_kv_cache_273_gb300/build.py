@@ -24,10 +24,10 @@ LIB = os.path.join(PKG, "libpkv.so")
 CUDA_SOURCES = ["append.cu", "decode.cu", "decode_f32.cu", "decode_f16.cu", "decode_bf16.cu",
                 "decode_i8.cu", "decode_i4.cu", "decode_f8.cu", "decode_blocks_16.cu",
                 "decode_noalloc.cu", "prefill.cu", "selftest.cu", "tables.cu",
-                "append_blocks.cu", "select.cu", "rope.cu"]
+                "append_blocks.cu", "select.cu", "rope.cu", "chunk.cu"]
 HOST_SOURCES = ["pool.cpp"]
 HEADERS = ["pkv_internal.h", "device_common.cuh", "decode_kernel.cuh",
-           "blocks_common.cuh", "decode_blocks.cuh"]
+           "blocks_common.cuh", "decode_blocks.cuh", "tc_common.cuh", "chunk_schedule.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

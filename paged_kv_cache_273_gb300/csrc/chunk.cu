@@ -1,0 +1,1208 @@
+// paged_chunk_attention: attention of each sequence's new tokens over its cached rows
+// (the new ones among them): a piece of a prompt, a whole one, or a few drafted tokens.
+//
+// softmax(scale q K^T) V of "KV cache: the engine behind fast LLM inference",
+// "Concept", in tiles of 128 keys with a running maximum and sum ("Flash attention:
+// don't build the giant matrix" in the guide), on the fifth-generation tensor cores.
+//
+// A (token, query head) pair is a row; the G query heads of a KV head are packed, so
+// one read of K and V serves them all, and n tokens make n G rows.  An item is up to 256
+// (or 128) rows of one (sequence, KV head); chunk_schedule.h cuts all items' key tiles
+// into one share a CTA, so that one long sequence fills the GPU as well as a large batch
+// does.  An item that is cut leaves one state (weighted sum, maximum, sum) a
+// piece, which chunk_join_kernel joins in the order of the keys: the result does not depend on
+// timing.
+//
+// Within a CTA two softmax groups of 128 threads, a thread a row, alternate on the
+// tensor cores.  Of an item of more than 128 rows each group has its own rows, and both read
+// each K and V tile; of a smaller one both have the same rows, and every other
+// key tile each: their two states are joined at the piece's end, through tensor memory.
+//
+// Bound: few new tokens read K and V once for n G rows, so memory is the floor (n G below
+// about 290 rows of 16-bit keys, half that of e4m3); long pieces are bound by the tensor cores
+// and the exponentials.
+#include <algorithm>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "blocks_common.cuh"
+#include "chunk_schedule.h"
+#include "tc_common.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace dev;
+using chunk::Place;
+using chunk::Rules;
+using chunk::Seq;
+using chunk::TILE;
+
+struct ChunkParams {
+    CUtensorMap tm_q;             // q [T][Hq][D]: boxes of 64 columns x G heads x 128 / G tokens
+    CUtensorMap tm_k, tm_v;       // 16-bit caches: boxes of 64 columns x box_rows
+    const void *q, *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    const int32_t *tables, *q_start, *seq_lens;
+    const uint64_t *visible;
+    void *out;
+    int32_t *places;              // [0]: shares; from [8] on: 8 words a share, where it starts
+    float *part;                  // 2 states a CTA: that of its first piece, and of its last
+    unsigned int *err;
+    int batch, num_tokens, max_q_len, num_q_heads, num_kv_heads, lg_g;
+    int block_size, bs_log2, max_blocks, num_blocks;
+    int box_rows;                 // min(block_size, 128): rows of a tile from one block
+    float scale_log2;
+    Rules rules;
+};
+
+// Warps: 0-7 the softmax groups; then, of a 16-bit cache, one that brings K, one V,
+// one q, and one that issues the MMAs; of an 8-bit cache, four that convert tiles, the MMA
+// warp, one that brings tiles, and two that bring q where that is converted too.
+template <int D, bool F8, bool BF, int NQ>
+struct Cfg {
+    static constexpr int ROWS = NQ * TILE_M;
+    static constexpr int Q_BYTES = TILE_M * D * 2;                       // one half
+    static constexpr int KV_BYTES = TILE * D * 2;
+    static constexpr int RAW_BYTES = TILE * D;
+    // ring slots: what shared memory holds
+    static constexpr int NS = D == 64 ? 4 : (!F8 && NQ == 1 ? 3 : 2);
+    static constexpr int NR = !F8 ? 0 : (NQ == 1 ? 2 : 1) * (D == 64 ? 2 : 1);
+    // tiles' scales: K's are read until the tile's softmax, when NS + 1 tiles more may be
+    // converted and NR brought
+    static constexpr int RING = D == 64 ? 16 : 8;
+    static_assert(RING >= NS + NR + 2, "scales in use");
+    static constexpr int OFF_K = NQ * Q_BYTES;
+    static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
+    static constexpr int OFF_RK = OFF_V + NS * KV_BYTES;
+    static constexpr int OFF_RV = OFF_RK + NR * RAW_BYTES;
+    static constexpr int OFF_ML = OFF_RV + NR * RAW_BYTES;               // the second group's states
+    static constexpr int OFF_SC = OFF_ML + TILE_M * 8;                   // [RING][16] K, then V scales
+    static constexpr int OFF_LIVE = OFF_SC + (F8 ? RING * 16 * 8 : 0);   // [RING]
+    static constexpr int OFF_QE = OFF_LIVE + (F8 ? RING * 4 : 0);        // q's exponents, two items
+    static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * ROWS : 0);
+    static constexpr int NBARS = 4 * NS + 4 * NR + 8 + 5;
+    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;                 // tensor memory's address, flags, places
+    static constexpr int SMEM_BYTES = OFF_MISC + 256;
+    static constexpr int W_MMA = F8 ? 12 : 11;
+    static constexpr bool QCONV = F8 && BF;
+    static constexpr int NT = 32 * (F8 ? (BF ? 16 : 14) : 12);
+    static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
+    // P in one 16-bit part, rounded as the output is; over an 8-bit cache P is bf16, for
+    // its range, and in two parts where the output is fp16
+    static constexpr bool PBF = F8 || BF;
+    static constexpr bool SPLIT = F8 && !BF;
+    static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+// The share's walk over its items' pieces; every role walks it alike.
+struct Piece {
+    int b, h;
+    int tok;               // first token, as a row of q
+    int rows;
+    int first, last;       // positions of the first token and of the last key in sight
+    int sight;             // first key in sight of any row
+    int base;              // cached rows before the new tokens (L - n)
+    int len;               // L
+    int t0, t1;            // key tiles
+    int kind;              // 0: the whole item; 1: not from its start; 2: from its start, not to its end
+};
+
+struct Walk {
+    Place at, end;
+    Seq q;
+    int q0;
+
+    // Sequence b's lengths; false if it has no work.
+    __device__ __forceinline__ static bool lengths(const ChunkParams &p, int b, Seq &q, int &q0,
+                                                   bool &bad)
+    {
+        q0 = p.q_start[b];
+        const int64_t n = (int64_t)p.q_start[b + 1] - q0;
+        const int L = p.seq_lens[b];
+        bad = n < 0 || (n > 0 && (q0 < 0 || n > p.max_q_len || q0 + n > p.num_tokens || L < n ||
+                                  (int64_t)L > (int64_t)p.max_blocks * p.block_size ||
+                                  (p.rules.tree && n > 64)));
+        q.n = bad ? 0 : (int)n;
+        q.L = L;
+        return q.n > 0;
+    }
+
+    __device__ __forceinline__ void start(const ChunkParams &p, const Place *places)
+    {
+        at = places[0];
+        end = places[1];
+        bool bad;
+        if (at.b < p.batch)
+            lengths(p, at.b, q, q0, bad);
+    }
+
+    __device__ __forceinline__ bool next(const ChunkParams &p, Piece &c)
+    {
+        const bool last_item = at.b == end.b && at.h == end.h && at.rt == end.rt;
+        if (at.b >= p.batch || (last_item && at.tile >= end.tile))
+            return false;
+        int lo, hi;
+        chunk::tiles(p.rules, q, at.rt, lo, hi);
+        chunk::span(p.rules, q, at.rt, c.first, c.last);
+        c.b = at.b;
+        c.h = at.h;
+        c.tok = q0 + at.rt * p.rules.tpr;
+        c.rows = min(p.rules.tpr, q.n - at.rt * p.rules.tpr) << p.lg_g;
+        c.sight = p.rules.window > 0 ? max(0, c.first - p.rules.window + 1) : 0;
+        c.base = q.L - q.n;
+        c.len = q.L;
+        c.t0 = at.tile;
+        c.t1 = last_item ? end.tile : hi;
+        c.kind = c.t0 > lo ? 1 : c.t1 < hi ? 2 : 0;
+        if (last_item) {
+            at.tile = end.tile;
+            return true;
+        }
+        if (++at.rt == chunk::row_tiles(p.rules, q)) {
+            at.rt = 0;
+            if (++at.h == p.num_kv_heads) {
+                at.h = 0;
+                bool bad;
+                do
+                    ++at.b;
+                while (at.b < p.batch && !lengths(p, at.b, q, q0, bad));
+                if (at.b >= p.batch)
+                    return true;
+            }
+        }
+        chunk::tiles(p.rules, q, at.rt, lo, hi);
+        at.tile = lo;
+        return true;
+    }
+};
+
+// What a group does of a piece: its rows, and its s-th key tile.
+__device__ __forceinline__ bool shared_rows(const Piece &c) { return c.rows <= TILE_M; }
+__device__ __forceinline__ int group_tiles(const ChunkParams &p, const Piece &c, int g)
+{
+    const int nt = c.t1 - c.t0;
+    if (shared_rows(c))
+        return (nt + 1 - g) / 2;
+    if (g == 1 || p.rules.tree)
+        return nt;
+    // the first half's last token sees fewer keys
+    const int last = c.first + (TILE_M >> p.lg_g) - 1;
+    return min(nt, max(0, last / TILE + 1 - c.t0));
+}
+__device__ __forceinline__ int tile_at(const Piece &c, int g, int s)
+{
+    return shared_rows(c) ? 2 * s + g : s;            // behind t0
+}
+
+// Where this share starts and ends: the sequences' costs are summed over the CTA, and the
+// threads whose sequences hold the two positions place them.
+template <int NT>
+__device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, int64_t *sums)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.batch + NT - 1) / NT;
+    const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        Seq q;
+        int q0;
+        bool bad;
+        if (Walk::lengths(p, b, q, q0, bad))
+            mine += p.num_kv_heads * chunk::cost_of(p.rules, q);
+        if (bad && blockIdx.x == 0)
+            atomicOr(p.err, PKV_EBIT_SEQLEN);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(FULL_MASK, upto, m);
+        if (lane >= m)
+            upto += o;
+    }
+    if (lane == 31)
+        sums[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, U = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp)
+            before += sums[w];
+        U += sums[w];
+    }
+    const int n = chunk::shares(U, gridDim.x), c = blockIdx.x;
+    if (c == 0 && tid == 0)
+        p.places[0] = U > 0 ? n : 0;
+    if (U == 0 || c >= n)
+        return false;
+    if (tid == 0 && c + 1 == n) {
+        Place e{};
+        e.b = p.batch;
+        places[1] = e;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        int64_t x = chunk::share_start(U, n, c + k) - (before + upto - mine);
+        if (x < 0 || x >= mine)
+            continue;
+        for (int b = b0; b < b1; ++b) {
+            Seq q;
+            int q0;
+            bool bad;
+            if (!Walk::lengths(p, b, q, q0, bad))
+                continue;
+            const int64_t cost = p.num_kv_heads * chunk::cost_of(p.rules, q);
+            if (x < cost) {
+                places[k] = chunk::place_in(p.rules, q, b, x);
+                break;
+            }
+            x -= cost;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int32_t *o = p.places + 8 + 8 * c;
+        o[0] = places[0].b;
+        o[1] = places[0].h;
+        o[2] = places[0].rt;
+        o[3] = places[0].split;
+    }
+    return true;
+}
+
+// 16 e4m3 codes -> 16 fp16 values (exact), as two 16-byte chunks.
+__device__ __forceinline__ void codes_to_half(const uint4 &w, uint4 &lo, uint4 &hi)
+{
+    f8x4_to_half2(w.x, lo.x, lo.y);
+    f8x4_to_half2(w.y, lo.z, lo.w);
+    f8x4_to_half2(w.z, hi.x, hi.y);
+    f8x4_to_half2(w.w, hi.z, hi.w);
+}
+
+// The same times a power of two, as bf16 (exact: four significant bits).
+__device__ __forceinline__ uint32_t scaled_bf16(uint32_t h2, float f)
+{
+    const float2 x = half2_to_float2(h2);
+    return pack2<__nv_bfloat16>(x.x * f, x.y * f);
+}
+__device__ __forceinline__ uint4 scaled_bf16(const uint4 &h, float f)
+{
+    return make_uint4(scaled_bf16(h.x, f), scaled_bf16(h.y, f), scaled_bf16(h.z, f),
+                      scaled_bf16(h.w, f));
+}
+
+// V of an 8-bit cache enters P V times 2^-16 (its largest values are beyond bf16's
+// otherwise; its smallest stay normal), and the quotient is multiplied back.
+constexpr int V_SHIFT = 16;
+
+// fp16 weights are taken times 2^7: the running maximum moves when a score is 2^8 above it, so
+// they stay below 2^15, and weights down to 2^-21 of the largest keep all their bits.
+constexpr float P_SHIFT = 7.0f;
+
+template <int D, bool F8, bool BF, int NQ>
+__global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
+    chunk_kernel(const __grid_constant__ ChunkParams p)
+{
+    using C = Cfg<D, F8, BF, NQ>;
+    constexpr int NS = C::NS, NR = C::NR;
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    float *k_sc = reinterpret_cast<float *>(smem + C::OFF_SC), *v_sc = k_sc + C::RING * 16;
+    uint32_t *live_of = reinterpret_cast<uint32_t *>(smem + C::OFF_LIVE);
+    signed char *q_exp = reinterpret_cast<signed char *>(smem + C::OFF_QE);
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
+    uint64_t *s_full = v_empty + NS, *p_full = s_full + 2, *o_done = p_full + 2, *o_free = o_done + 2;
+    uint64_t *q_full = o_free + 2, *q_empty = q_full + 1, *ml_full = q_empty + 1, *ml_free = ml_full + 1;
+    uint64_t *drain = ml_free + 1;
+    uint64_t *kr_full = drain + 1, *kr_empty = kr_full + NR, *vr_full = kr_empty + NR, *vr_empty = vr_full + NR;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    Place *places = reinterpret_cast<Place *>(smem + C::OFF_MISC + 16);
+    int64_t *sums = reinterpret_cast<int64_t *>(smem + C::OFF_MISC + 64);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (!find_share<C::NT>(p, places, sums))
+        return;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&k_full[i], F8 ? 128 : 2);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], F8 ? 128 : 2);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&kr_full[i], 1);
+            mbar_init(&kr_empty[i], 128);
+            mbar_init(&vr_full[i], 1);
+            mbar_init(&vr_empty[i], 128);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&s_full[g], 1);
+            mbar_init(&p_full[g], TILE_M);
+            mbar_init(&o_done[g], 1);
+            mbar_init(&o_free[g], TILE_M);
+        }
+        mbar_init(q_full, C::QCONV ? 64 : 1);
+        mbar_init(q_empty, 1);
+        mbar_init(ml_full, TILE_M);
+        mbar_init(ml_free, TILE_M);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == C::W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(tmem_slot)),
+                     "n"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // A wait that runs out raises the error bit once and makes every role stop.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_wait_bounded(bar, parity & 1, abort_flag))
+            return true;
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            atomicOr(p.err, PKV_EBIT_TIMEOUT);
+        }
+        return false;
+    };
+    Walk walk;
+    Piece c;
+    walk.start(p, places);
+
+    if (warp < 8) {
+        // ================= softmax: group g, one thread a row
+        const int g = warp >> 2, quad = warp & 3;
+        const int r = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t t_s = tmem + g * C::GROUP_COLS + lane_base, t_o = t_s + TILE;
+        uint32_t sc = 0, oc = 0, mc = 0;           // phases of s_full, o_done, ml
+        uint32_t done1 = 0;                        // group 0: of the second group's o_done
+        int gt = 0;                                // the CTA's tiles so far
+        for (uint32_t item = 0; walk.next(p, c); ++item) {
+            const bool both = shared_rows(c);
+            const int row = both ? r : g * TILE_M + r;
+            const bool warp_live = (both ? quad * 32 : g * TILE_M + quad * 32) < c.rows;
+            const int pos = c.first + (row >> p.lg_g);
+            // keys in sight: up to `lim`, from `from`, and of the new ones those of `bits`
+            const bool valid = row < c.rows;
+            const int lim = !valid ? -1 : p.visible ? c.len - 1 : pos;
+            const int from = p.rules.window > 0 ? pos - p.rules.window + 1 : 0;
+            uint64_t bits = ~(uint64_t)0;
+            if (p.visible && valid)
+                bits = p.visible[c.tok + (row >> p.lg_g)];
+            const int nt = group_tiles(p, c, g);
+            float m_run = -INFINITY, l_run = 0.0f, rs = p.scale_log2;
+            for (int s = 0; s < nt; ++s) {
+                const int tb = (c.t0 + tile_at(c, g, s)) * TILE;       // the tile's first key
+                if (!__all_sync(FULL_MASK, wait(&s_full[g], sc)))
+                    goto softmax_done;
+                ++sc;
+                tc_fence_after();
+                if (warp_live) {
+                    if (C::QCONV && s == 0)
+                        rs = p.scale_log2 * pow2_f32(q_exp[(item & 1) * C::ROWS + row]);
+                    // a tile's factor for eight keys: an 8-bit cache's scale, the row's
+                    // own and the softmax's
+                    const float4 *fac = reinterpret_cast<const float4 *>(
+                        k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 16);
+                    const bool masked = __any_sync(
+                        FULL_MASK, tb + TILE - 1 > lim || tb < from ||
+                                       (p.visible && tb + TILE > c.base));
+                    auto in_sight = [&](int c0) -> uint32_t {
+                        const int k0 = tb + c0, u = lim - k0, d = from - k0;
+                        uint32_t w = u >= 31 ? 0xffffffffu : u < 0 ? 0u : (2u << u) - 1u;
+                        if (d > 0)
+                            w = d < 32 ? w & (0xffffffffu << d) : 0u;
+                        if (p.visible) {
+                            const int e = k0 - c.base;
+                            if (e >= 0)
+                                w &= e < 64 ? (uint32_t)(bits >> e) : 0u;
+                            else if (e > -32)
+                                w &= (uint32_t)(bits << -e) | ((1u << -e) - 1u);
+                        }
+                        return w;
+                    };
+                    // pass 1: the row's maximum, in the base-2 logarithm's units
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < TILE; c0 += 32) {
+                        float v[32];
+                        tmem_ld32(t_s + c0, v);
+                        if (masked) {
+                            const uint32_t w = in_sight(c0);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = (w >> j) & 1 ? v[j] : -INFINITY;
+                        }
+                        if constexpr (F8) {
+                            const float4 f = fac[c0 / 32];
+                            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float *x = v + 8 * k;
+                                const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
+                                                      fmaxf(x[6], x[7]));
+                                mx = fmaxf(mx, a * (ff[k] * rs));
+                            }
+                        } else {
+                            float t[11];
+#pragma unroll
+                            for (int j = 0; j < 10; ++j)
+                                t[j] = max3f(v[3 * j], v[3 * j + 1], v[3 * j + 2]);
+                            t[10] = fmaxf(v[30], v[31]);
+                            mx = max3f(mx, max3f(t[0], t[1], t[2]), max3f(t[3], t[4], t[5]));
+                            mx = max3f(mx, max3f(t[6], t[7], t[8]), fmaxf(t[9], t[10]));
+                        }
+                    }
+                    if (!F8)
+                        mx *= rs;                  // scale > 0: the maximum commutes
+                    // The running maximum moves only when a score exceeds it by more than
+                    // 2^8 (or is the first in sight): below that the weights stay <= 2^8, and
+                    // the quotient by the sum of the same weights is unchanged.
+                    const bool move = mx > m_run + 8.0f;
+                    const float m_new = move ? mx : m_run;
+                    const float corr = !move ? 1.0f : m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_new);
+                    m_run = m_new;
+                    // O is idle here: the P V of the previous tile finished before this S
+                    // did, the next one waits for p_full
+                    if (s > 0 && __any_sync(FULL_MASK, move)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            float o[32];
+                            tmem_ld32(t_o + c0, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] *= corr;
+                            tmem_st32(t_o + c0, o);
+                        }
+                    }
+                    // pass 2: weights, their sum, and P (keys 32c..32c+31 as 16-bit pairs in
+                    // columns 32c..32c+15, low parts in the next 16: S columns already read)
+                    const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_new == -INFINITY ? 0.0f : m_new);
+                    float sum = 0.0f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < TILE; c0 += 32) {
+                        float v[32];
+                        tmem_ld32(t_s + c0, v);
+                        if (masked) {
+                            const uint32_t w = in_sight(c0);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = (w >> j) & 1 ? v[j] : -INFINITY;
+                        }
+                        if constexpr (F8) {
+                            const float4 f = fac[c0 / 32];
+                            const float ff[4] = {f.x * rs, f.y * rs, f.z * rs, f.w * rs};
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2)
+                                fma2_bc(v[j], v[j + 1], ff[j / 8], off);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2)
+                                fma2_bc(v[j], v[j + 1], rs, off);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = ex2_approx(v[j]);
+                        using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack2<PT>(v[2 * j], v[2 * j + 1]);
+                        tmem_st16(t_s + c0, w);
+                        if constexpr (C::SPLIT) {
+                            uint32_t wl[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float2 h = unpack2<PT>(w[j]);
+                                float r0 = v[2 * j], r1 = v[2 * j + 1];
+                                add2(r0, r1, -h.x, -h.y);
+                                wl[j] = pack2<PT>(r0, r1);
+                            }
+                            tmem_st16(t_s + c0 + 16, wl);
+                        }
+#pragma unroll
+                        for (int k = 16; k > 1; k >>= 1)       // tree sum over pairs
+#pragma unroll
+                            for (int j = 0; j < k; j += 2)
+                                add2(v[j], v[j + 1], v[j + k], v[j + k + 1]);
+                        sum += v[0] + v[1];
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    l_run = l_run * corr + sum;
+                }
+                tc_fence_before();
+                mbar_arrive(&p_full[g]);
+            }
+            gt += c.t1 - c.t0;
+            // ---- the piece's end
+            const int nt1 = both ? group_tiles(p, c, 1) : 0;
+            if (g == 1 && both) {
+                // hand the state over: the first group reads it and this group's O
+                if (nt1 > 0) {
+                    ++oc;                          // (the first group waits for it)
+                    if (mc > 0 && !__all_sync(FULL_MASK, wait(ml_free, mc - 1)))
+                        goto softmax_done;
+                    ml[r] = make_float2(m_run, l_run);
+                    mbar_arrive(ml_full);
+                    ++mc;
+                }
+                continue;
+            }
+            if (nt > 0) {
+                if (!__all_sync(FULL_MASK, wait(&o_done[g], oc)))
+                    goto softmax_done;
+                ++oc;
+            }
+            float a0 = 1.0f, a1 = 0.0f;
+            const uint32_t of1 = done1;
+            if (g == 0 && group_tiles(p, c, 1) > 0)
+                ++done1;
+            if (nt1 > 0) {
+                if (!__all_sync(FULL_MASK, wait(&o_done[1], of1) && wait(ml_full, mc)))
+                    goto softmax_done;
+                ++mc;
+                const float2 o = ml[r];
+                mbar_arrive(ml_free);
+                const float m = fmaxf(m_run, o.x);
+                a0 = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m);
+                a1 = o.x == -INFINITY ? 0.0f : ex2_approx(o.x - m);
+                m_run = m;
+                l_run = l_run * a0 + o.y * a1;
+            }
+            tc_fence_after();
+            if (warp_live) {
+                const float vs = F8 ? (float)(1 << V_SHIFT) : 1.0f;
+                if (c.kind == 0) {
+                    const float inv = l_run == 0.0f ? 0.0f : vs / l_run;
+                    a0 *= inv;
+                    a1 *= inv;
+                }
+                T *out = static_cast<T *>(p.out) +
+                         ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
+                          (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D;
+                float *part = p.part + ((int64_t)blockIdx.x * 2 + (c.kind == 2)) * C::ROWS * (D + 2) +
+                              (int64_t)row * D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float o[32];
+                    if (nt > 0) {
+                        tmem_ld32(t_o + c0, o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] *= a0;
+                    }
+                    if (nt1 > 0) {
+                        float o1[32];
+                        tmem_ld32(t_o + C::GROUP_COLS + c0, o1);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = fmaf(o1[j], a1, o[j]);
+                    }
+                    if (!valid || (c.kind && nt == 0)) {
+                        // (padding rows, and a half that sees none of the piece's keys: its
+                        // sum of 0 says so)
+                    } else if (c.kind == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(out + c0 + 8 * j) = make_uint4(
+                                pack2<T>(o[8 * j], o[8 * j + 1]), pack2<T>(o[8 * j + 2], o[8 * j + 3]),
+                                pack2<T>(o[8 * j + 4], o[8 * j + 5]), pack2<T>(o[8 * j + 6], o[8 * j + 7]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(part + c0 + 4 * j) =
+                                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+                if (c.kind && valid)
+                    *reinterpret_cast<float2 *>(part - (int64_t)row * D + C::ROWS * D + 2 * row) =
+                        make_float2(m_run, l_run);
+            }
+            tc_fence_before();
+            if (nt > 0)
+                mbar_arrive(&o_free[g]);
+            if (nt1 > 0)
+                mbar_arrive(&o_free[1]);
+        }
+    softmax_done:;
+    } else if (!F8 && warp < 10) {
+        // ================= K (warp 8) or V (warp 9) tiles of a 16-bit cache
+        const bool is_k = warp == 8;
+        unsigned char *ring = is_k ? sK : sV;
+        uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+        const CUtensorMap *tm = is_k ? &p.tm_k : &p.tm_v;
+        const T *cache = static_cast<const T *>(is_k ? p.k_cache : p.v_cache);
+        const int R = p.box_rows, nbox = TILE / R;
+        const int oob = p.num_blocks * p.num_kv_heads;     // a block past the end: zeros
+        constexpr int DCH = D / 8;
+        uint32_t gt = 0;
+        bool ok = true;
+        while (ok && walk.next(p, c)) {
+            const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
+            // lane j: rows [j R, j R + R) of a tile, from one block; ids a tile ahead
+            auto block_of = [&](int t) -> int32_t {
+                const int pos0 = t * TILE + lane * R;
+                return lane < nbox && t < c.t1 && pos0 <= c.last && pos0 + R > c.sight
+                           ? table[pos0 >> p.bs_log2] : -2;
+            };
+            int32_t ahead = block_of(c.t0);
+            for (int t = c.t0; t < c.t1; ++t, ++gt) {
+                const int slot = gt % NS;
+                const int pos0 = t * TILE + lane * R;
+                const int32_t blk = ahead;
+                ahead = block_of(t + 1);
+                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&empty[slot], gt / NS + 1))))
+                    break;
+                const bool inbox = lane < nbox;
+                int z = oob;
+                if (inbox && blk != -2) {
+                    if (blk < 0 || blk >= p.num_blocks)
+                        atomicOr(p.err, PKV_EBIT_BLOCK);
+                    else
+                        z = blk * p.num_kv_heads + c.h;
+                }
+                const int y = pos0 & (p.block_size - 1);
+                unsigned char *dst = ring + slot * C::KV_BYTES;
+                // By tensor copies, a 64-column panel each, where the box starts on a
+                // 1024-byte boundary and holds no row past the last in sight (those are
+                // zeros: P is 0 there, but 0 times a stale NaN is not); by 16-byte
+                // copies otherwise.
+                const bool by_tma = inbox && R >= 8 && (z == oob || pos0 + R - 1 <= c.last);
+                const unsigned tma_boxes = __popc(__ballot_sync(FULL_MASK, by_tma));
+                const unsigned cp_boxes = __ballot_sync(FULL_MASK, inbox && !by_tma);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[slot], tma_boxes * (uint32_t)R * 2u * D);
+                __syncwarp();
+                if (by_tma) {
+#pragma unroll
+                    for (int pn = 0; pn < D / 64; ++pn)
+                        tma_load_3d(dst + pn * (TILE * 128) + lane * R * 128, tm, pn * 64, y, z,
+                                    &full[slot]);
+                }
+                if (cp_boxes) {
+                    for (unsigned m = cp_boxes; m; m &= m - 1) {
+                        const int bx = __ffs(m) - 1;
+                        const int zb = __shfl_sync(FULL_MASK, z, bx);
+                        const int yb = __shfl_sync(FULL_MASK, y, bx);
+                        for (int idx = lane; idx < R * DCH; idx += 32) {
+                            const int rr = bx * R + idx / DCH, ch = idx % DCH;
+                            const bool in = zb != oob && t * TILE + rr <= c.last;
+                            const int64_t row = in ? (int64_t)zb * p.block_size + yb + idx / DCH : 0;
+                            cp_async16(dst + (ch >> 3) * (TILE * 128) + rr * 128 +
+                                           (((ch & 7) ^ (rr & 7)) << 4),
+                                       cache + row * D + ch * 8, in);
+                        }
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&full[slot]);
+            }
+        }
+    } else if (F8 && warp < 12) {
+        // ================= convert tiles of an 8-bit cache: K's codes to fp16, V's values
+        // to bf16; this warp's 32 rows
+        const int w0 = (warp - 8) * 32;
+        constexpr int LPR = D / 16, RPI = 32 / LPR;            // lanes a row of codes, rows at once
+        const int rr = lane / LPR, j = lane % LPR;
+        uint32_t gt = 0;
+        bool ok = true;
+        while (ok && walk.next(p, c)) {
+            for (int t = c.t0; t < c.t1 && ok; ++t, ++gt) {
+                const int slot = gt % NS, rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint64_t *rf = kv ? vr_full : kr_full, *re = kv ? vr_empty : kr_empty;
+                    uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
+                    if (!(ok = __all_sync(FULL_MASK, wait(&rf[rs], gt / (NR ? NR : 1)) &&
+                                                         (gt < NS || wait(&empty[slot], gt / NS + 1)))))
+                        break;
+                    const unsigned char *raw = smem + (kv ? C::OFF_RV : C::OFF_RK) + rs * C::RAW_BYTES;
+                    unsigned char *dst = (kv ? sV : sK) + slot * C::KV_BYTES;
+                    const uint32_t live = live_of[ring];
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += RPI) {
+                        const int row = w0 + i + rr;
+                        const bool in = ((live >> (row >> 3)) & 1) && t * TILE + row <= c.last;
+                        uint4 w = *reinterpret_cast<const uint4 *>(raw + row * D + j * 16);
+                        if (!in)
+                            w = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 lo, hi;
+                        codes_to_half(w, lo, hi);
+                        if (kv) {
+                            const float f = v_sc[ring * 16 + (row >> 3)];
+                            lo = scaled_bf16(lo, f);
+                            hi = scaled_bf16(hi, f);
+                        }
+                        // chunks 2j and 2j + 1 of the row; the second panel's lanes write their odd one
+                        // first, so that eight lanes' stores fall on all banks
+                        const int c0 = 2 * j, odd = (c0 >> 3) & 1;
+                        unsigned char *base = dst + (c0 >> 3) * (TILE * 128) + row * 128;
+                        const int k0 = (c0 & 7) + odd, k1 = (c0 & 7) + 1 - odd;
+                        *reinterpret_cast<uint4 *>(base + ((k0 ^ (row & 7)) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4 *>(base + ((k1 ^ (row & 7)) << 4)) = odd ? lo : hi;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&full[slot]);
+                    mbar_arrive(&re[rs]);
+                }
+            }
+        }
+    } else if (F8 && warp == 13) {
+        // ================= bring codes and scales of an 8-bit cache
+        const int R = p.box_rows, nbox = TILE / R, H = p.num_kv_heads;
+        int lg_r = 0;
+        while ((1 << lg_r) < R)
+            ++lg_r;
+        const unsigned char *kc = static_cast<const unsigned char *>(p.k_cache);
+        const unsigned char *vc = static_cast<const unsigned char *>(p.v_cache);
+        uint32_t gt = 0, item = 0;
+        bool ok = true;
+        while (ok && walk.next(p, c)) {
+            const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
+            auto block_of = [&](int t) -> int32_t {
+                const int pos0 = t * TILE + lane * R;
+                return lane < nbox && t < c.t1 && pos0 <= c.last && pos0 + R > c.sight
+                           ? table[pos0 >> p.bs_log2] : -2;
+            };
+            // a block's scales: of a block that is not there, anything finite
+            auto scale_of = [&](int32_t blk, const float *s) -> float {
+                return blk >= 0 && blk < p.num_blocks ? s[(int64_t)blk * H + c.h] : 1.0f;
+            };
+            // ids two tiles ahead, scales one: each is a trip to memory after the other
+            int32_t blk1 = block_of(c.t0), blk2 = block_of(c.t0 + 1);
+            float ks1 = scale_of(blk1, p.k_scales), vs1 = scale_of(blk1, p.v_scales);
+            if (!C::QCONV) {
+                if (item > 0 && !(ok = __all_sync(FULL_MASK, wait(q_empty, item - 1))))
+                    break;
+                const int halves = shared_rows(c) ? 1 : 2;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, halves * (uint32_t)C::Q_BYTES);
+                    for (int hh = 0; hh < halves; ++hh)
+                        for (int pn = 0; pn < D / 64; ++pn)
+                            tma_load_3d(sQ + hh * C::Q_BYTES + pn * (TILE_M * 128), &p.tm_q, pn * 64,
+                                        c.h << p.lg_g, c.tok + hh * (TILE_M >> p.lg_g), q_full);
+                }
+                __syncwarp();
+            }
+            ++item;
+            for (int t = c.t0; t < c.t1; ++t, ++gt) {
+                const int rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
+                const uint32_t turn = gt / (NR ? NR : 1);
+                const int32_t blk = blk1;
+                const float ks = ks1, vs = vs1;
+                blk1 = blk2;
+                ks1 = scale_of(blk1, p.k_scales);
+                vs1 = scale_of(blk1, p.v_scales);
+                blk2 = block_of(t + 2);
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                if (blk != -2 && !good)
+                    atomicOr(p.err, PKV_EBIT_BLOCK);
+                const unsigned boxes = __ballot_sync(FULL_MASK, good);
+                const int pos0 = t * TILE + lane * R;
+                const int64_t src = good ? (((int64_t)blk * H + c.h) * p.block_size +
+                                            (pos0 & (p.block_size - 1))) * D : 0;
+                // entry i of the tile's scales: keys 8 i .. 8 i + 7
+                const int bx = (8 * (lane & 15)) >> lg_r;
+                const float ke = __shfl_sync(FULL_MASK, ks, bx), ve = __shfl_sync(FULL_MASK, vs, bx);
+                const uint32_t live = __ballot_sync(FULL_MASK, lane < 16 && ((boxes >> bx) & 1));
+                if (!(ok = __all_sync(FULL_MASK, (int)gt < NR || wait(&kr_empty[rs], turn + 1))))
+                    break;
+                if (lane < 16) {
+                    k_sc[ring * 16 + lane] = pow2_f32(block_exponent(ke));
+                    v_sc[ring * 16 + lane] = pow2_f32(block_exponent(ve) - V_SHIFT);
+                }
+                if (lane == 0)
+                    live_of[ring] = live;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&kr_full[rs], __popc(boxes) * (uint32_t)(R * D));
+                __syncwarp();
+                if (good)
+                    bulk_g2s(smem + C::OFF_RK + rs * C::RAW_BYTES + lane * R * D, kc + src, R * D,
+                             &kr_full[rs]);
+                if (!(ok = __all_sync(FULL_MASK, (int)gt < NR || wait(&vr_empty[rs], turn + 1))))
+                    break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&vr_full[rs], __popc(boxes) * (uint32_t)(R * D));
+                __syncwarp();
+                if (good)
+                    bulk_g2s(smem + C::OFF_RV + rs * C::RAW_BYTES + lane * R * D, vc + src, R * D,
+                             &vr_full[rs]);
+            }
+        }
+    } else if (!F8 && warp == 10) {
+        // ================= q, once the previous item's last S has read its own
+        for (uint32_t item = 0; walk.next(p, c); ++item) {
+            if (item > 0 && !__all_sync(FULL_MASK, wait(q_empty, item - 1)))
+                break;
+            const int halves = shared_rows(c) ? 1 : 2;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, halves * (uint32_t)C::Q_BYTES);
+                for (int hh = 0; hh < halves; ++hh)
+                    for (int pn = 0; pn < D / 64; ++pn)
+                        tma_load_3d(sQ + hh * C::Q_BYTES + pn * (TILE_M * 128), &p.tm_q, pn * 64,
+                                    c.h << p.lg_g, c.tok + hh * (TILE_M >> p.lg_g), q_full);
+            }
+            __syncwarp();
+        }
+    } else if (C::QCONV && warp >= 14) {
+        // ================= bf16 q over an 8-bit cache: fp16 times a power of two a row
+        // (K's codes are fp16; what a row's small values lose is below 2^-38 of its largest)
+        constexpr int LPR = D / 8, RPI = 32 / LPR;              // lanes a row, rows at once
+        const int rr = lane / LPR, ch = lane % LPR;
+        for (uint32_t item = 0; walk.next(p, c); ++item) {
+            if (item > 0 && !__all_sync(FULL_MASK, wait(q_empty, item - 1)))
+                break;
+            const int rows = shared_rows(c) ? TILE_M : 2 * TILE_M, half = rows / 2;
+            const int r0 = (warp - 14) * half;
+            constexpr int U = 4;
+#pragma unroll 1
+            for (int i0 = 0; i0 < half; i0 += U * RPI) {
+                uint4 w[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int row = r0 + i0 + u * RPI + rr;
+                    const T *src = static_cast<const T *>(p.q) +
+                                   ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
+                                    (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + ch * 8;
+                    w[u] = row < c.rows ? *reinterpret_cast<const uint4 *>(src)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int row = r0 + i0 + u * RPI + rr;
+                    uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                    uint32_t top = 0;                          // magnitudes order as their bits
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        top = max(top, max(v[k] << 16 & 0x7fffffffu, v[k] & 0x7fff0000u));
+#pragma unroll
+                    for (int m = 1; m < LPR; m <<= 1)
+                        top = max(top, __shfl_xor_sync(FULL_MASK, top, m));
+                    // the largest in [2^14, 2^15)
+                    const int e = max((int)(top >> 23) - 127 - 14, -126);
+                    const float f = pow2_f32(-e);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = pack2<__half>(bf16lo(v[k]) * f, bf16hi(v[k]) * f);
+                    *reinterpret_cast<uint4 *>(sQ + (row >> 7) * C::Q_BYTES + (ch >> 3) * (TILE_M * 128) +
+                                               (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(v[0], v[1], v[2], v[3]);
+                    if (ch == 0)
+                        q_exp[(item & 1) * C::ROWS + row] = (signed char)e;
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(q_full);
+        }
+    } else if (warp == C::W_MMA && lane == 0) {
+        // ================= MMA issue (one thread)
+        // S = Q K^T, both K-major, and O += P V, P in tensor memory, V MN-major; all of them
+        // 128-byte swizzled panels of 64 channels: a row every 128 bytes, eight rows 1024
+        // bytes, the next panel 128 rows on.  A step of 16 along the contraction is 32 bytes
+        // into S's rows, 16 rows of V.
+        const uint32_t idesc_s = umma_idesc(BF && !F8 ? 1u : 0u, 0u, TILE);
+        const uint32_t idesc_o = umma_idesc(C::PBF ? 1u : 0u, 1u, D);
+        const uint32_t sQa = smem_addr(sQ), sKa = smem_addr(sK), sVa = smem_addr(sV);
+        uint32_t gt = 0, pc[2] = {0, 0}, ofc[2] = {0, 0};
+        bool o_used[2] = {false, false};
+        bool ok = true;
+        for (uint32_t item = 0; ok && walk.next(p, c); ++item) {
+            const bool both = shared_rows(c);
+            const int nt[2] = {group_tiles(p, c, 0), group_tiles(p, c, 1)};
+            int s_left = nt[0] + nt[1];
+            auto issue_s = [&](int g, int s) -> bool {
+                const uint32_t k = gt + tile_at(c, g, s);
+                if (!wait(&k_full[k % NS], k / NS))
+                    return false;
+                tc_fence_after();
+                const uint32_t kb = sKa + k % NS * C::KV_BYTES, qb = sQa + (both ? 0 : g) * C::Q_BYTES;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    umma_f16(tmem + g * C::GROUP_COLS,
+                             umma_desc_sw128(qb + (ks / 4) * (TILE_M * 128) + (ks % 4) * 32, 16, 1024),
+                             umma_desc_sw128(kb + (ks / 4) * (TILE * 128) + (ks % 4) * 32, 16, 1024),
+                             idesc_s, ks > 0 ? 1u : 0u);
+                if (both || g == 1)                // the tile's last reader
+                    umma_commit(&k_empty[k % NS]);
+                umma_commit(&s_full[g]);
+                if (--s_left == 0)
+                    umma_commit(q_empty);
+                return true;
+            };
+            auto issue_pv = [&](int g, int s) -> bool {
+                const uint32_t k = gt + tile_at(c, g, s);
+                if (!wait(&p_full[g], pc[g]) || !wait(&v_full[k % NS], k / NS))
+                    return false;
+                ++pc[g];
+                if (s == 0 && o_used[g]) {         // the softmax threads have read O out
+                    if (!wait(&o_free[g], ofc[g]))
+                        return false;
+                    ++ofc[g];
+                }
+                tc_fence_after();
+                const uint32_t vb = sVa + k % NS * C::KV_BYTES, base = tmem + g * C::GROUP_COLS;
+#pragma unroll
+                for (int ks = 0; ks < TILE / 16; ++ks) {
+                    const uint32_t pa = base + 32 * (ks >> 1) + 8 * (ks & 1);
+                    const uint64_t vd = umma_desc_sw128(vb + ks * 2048, TILE * 128, 1024);
+                    umma_f16_ta(base + TILE, pa, vd, idesc_o, s > 0 || ks > 0 ? 1u : 0u);
+                    if (C::SPLIT)
+                        umma_f16_ta(base + TILE, pa + 16, vd, idesc_o, 1u);
+                }
+                if (both || g == 1)
+                    umma_commit(&v_empty[k % NS]);
+                return true;
+            };
+            if (!(ok = wait(q_full, item)))
+                break;
+            for (int g = 0; g < 2 && ok; ++g)
+                if (nt[g] > 0)
+                    ok = issue_s(g, 0);
+            const int steps = max(nt[0], nt[1]);
+            for (int s = 0; s < steps && ok; ++s)
+                for (int g = 0; g < 2 && ok; ++g) {
+                    if (s >= nt[g])
+                        continue;
+                    if (!(ok = issue_pv(g, s)))
+                        break;
+                    if (s + 1 < nt[g]) {
+                        ok = issue_s(g, s + 1);
+                    } else {
+                        umma_commit(&o_done[g]);
+                        o_used[g] = true;
+                    }
+                }
+            gt += c.t1 - c.t0;
+        }
+        // every issued MMA has finished before tensor memory is released
+        umma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0u) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // copies in flight land before the shared memory is another CTA's
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) {
+        }
+    }
+    if (warp == C::W_MMA) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+    }
+}
+
+// Items that were cut: the states of an item's pieces joined, a warp a row, in the order of
+// the keys.  The CTA of share c (blockIdx.x + 1) handles the item that the cut before c
+// is the first within; the others have nothing to do.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
+                                                         int item_rows, float v_scale)
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int n = p.places[0], c = blockIdx.x + 1;
+    if (c >= n)
+        return;
+    const int32_t *at = p.places + 8 + 8 * c;
+    const int b = at[0], h = at[1], rt = at[2];
+    auto within = [&](int k) {                             // the cut before share k is in this item
+        const int32_t *o = p.places + 8 + 8 * k;
+        return o[0] == b && o[1] == h && o[2] == rt && o[3] != 0;
+    };
+    if (!at[3] || within(c - 1))
+        return;
+    Seq q;
+    int q0;
+    bool bad;
+    if (!Walk::lengths(p, b, q, q0, bad))
+        return;
+    int last = c;                                          // the last share with a piece of it
+    while (last + 1 < n && within(last + 1))
+        ++last;
+    const int pieces = last - c + 2;
+    const int rows = min(p.rules.tpr, q.n - rt * p.rules.tpr) << p.lg_g;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t state = (int64_t)item_rows * (D + 2);
+    // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
+    auto piece = [&](int i) -> const float * {
+        return p.part + (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * state;
+    };
+    for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+        float m = -INFINITY;
+        for (int i = lane; i < pieces; i += 32) {
+            const float2 s = *reinterpret_cast<const float2 *>(piece(i) + item_rows * D + 2 * row);
+            if (s.y != 0.0f)
+                m = fmaxf(m, s.x);
+        }
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, k));
+        constexpr int W = D / 32;
+        float acc[W] = {}, l = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < pieces; ++i) {
+            const float *s = piece(i);
+            const float2 ml = *reinterpret_cast<const float2 *>(s + item_rows * D + 2 * row);
+            if (ml.y == 0.0f)                              // none of its keys in sight
+                continue;
+            const float w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+            l = fmaf(w, ml.y, l);
+            const float *o = s + (int64_t)row * D + lane * W;
+            if constexpr (W == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(o);
+                acc[0] = fmaf(w, x.x, acc[0]);
+                acc[1] = fmaf(w, x.y, acc[1]);
+                acc[2] = fmaf(w, x.z, acc[2]);
+                acc[3] = fmaf(w, x.w, acc[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(o);
+                acc[0] = fmaf(w, x.x, acc[0]);
+                acc[1] = fmaf(w, x.y, acc[1]);
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : v_scale / l;
+        T *out = static_cast<T *>(p.out) +
+                 ((int64_t)(q0 + rt * p.rules.tpr + (row >> p.lg_g)) * p.num_q_heads +
+                  (h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + lane * W;
+        if constexpr (W == 4)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv),
+                                                         pack2<T>(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(out) = pack2<T>(acc[0] * inv, acc[1] * inv);
+    }
+}
+
+// q [T][Hq][D] as the tensor {D, Hq, T}, boxes of 64 x G x 128 / G: a half's rows.
+bool encode_q_map(CUtensorMap *m, const pkv_pool *pool, const void *q, int num_q_heads,
+                  int num_tokens, int G, bool bf)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint64_t D = pool->head_dim;
+    const cuuint64_t dims[3] = {D, (cuuint64_t)num_q_heads, (cuuint64_t)num_tokens};
+    const cuuint64_t strides[2] = {D * 2, D * 2 * (cuuint64_t)num_q_heads};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(TILE_M / G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void *>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F8, bool BF, int NQ>
+int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
+{
+    using C = Cfg<D, F8, BF, NQ>;
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    // set per call (for the current device, from any host thread)
+    if (cudaFuncSetAttribute(chunk_kernel<D, F8, BF, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM_BYTES) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    const int sms = pool->num_sms;
+    if (sms < 1)
+        return PKV_ERR_CUDA;
+    if (launch_pdl(chunk_kernel<D, F8, BF, NQ>, dim3((unsigned)sms), dim3(C::NT),
+                   (size_t)C::SMEM_BYTES, s, p) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    if (sms > 1 && launch_pdl(chunk_join_kernel<D, T>, dim3((unsigned)(sms - 1), C::ROWS / 32), dim3(256),
+                              0, s, p, (int)C::ROWS, F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// Rows of an item: 128 where every sequence's rows fit (its keys are then read by both
+// softmax groups in turn), else 256.
+int item_rows(int max_q_len, int G) { return (int64_t)max_q_len * G <= TILE_M ? TILE_M : 2 * TILE_M; }
+
+size_t places_bytes(const pkv_pool *pool)
+{
+    return ((size_t)(8 + 8 * std::max(1, pool->num_sms)) * 4 + 255) / 256 * 256;
+}
+
+}  // namespace
+
+size_t chunk_workspace_bytes(const pkv_pool *pool, int num_q_heads, int max_q_len)
+{
+    const int G = num_q_heads / pool->num_kv_heads;
+    return places_bytes(pool) + (size_t)2 * std::max(1, pool->num_sms) * item_rows(max_q_len, G) *
+                                    (pool->head_dim + 2) * sizeof(float);
+}
+
+int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num_q_heads,
+                 int num_tokens, const void *k_cache, const void *v_cache, const void *k_scales,
+                 const void *v_scales, const int32_t *tables, int max_blocks,
+                 const int32_t *q_start, const int32_t *seq_lens, int batch, int max_q_len,
+                 int window, const uint64_t *visible, float scale, void *out, void *workspace,
+                 pkv_stream_t stream)
+{
+    ChunkParams p{};
+    const int G = num_q_heads / pool->num_kv_heads;
+    const bool f8 = pool->kv_dtype == PKV_F8, bf = q_dtype == PKV_BF16;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = static_cast<const float *>(k_scales);
+    p.v_scales = static_cast<const float *>(v_scales);
+    p.tables = tables;
+    p.q_start = q_start;
+    p.seq_lens = seq_lens;
+    p.visible = visible;
+    p.out = out;
+    p.places = static_cast<int32_t *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + places_bytes(pool));
+    p.err = pool->d_err;
+    p.batch = batch;
+    p.num_tokens = num_tokens;
+    p.max_q_len = max_q_len;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = pool->num_kv_heads;
+    p.lg_g = log2_of(G);
+    p.block_size = pool->block_size;
+    p.bs_log2 = log2_of(pool->block_size);
+    p.max_blocks = max_blocks;
+    p.num_blocks = pool->num_blocks;
+    p.box_rows = std::min(pool->block_size, TILE);
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    const int rows = item_rows(max_q_len, G);
+    p.rules.tpr = rows / G;
+    p.rules.window = window;
+    p.rules.tree = visible != nullptr;
+    if (!encode_q_map(&p.tm_q, pool, q, num_q_heads, num_tokens, G, bf))
+        return PKV_ERR_CUDA;
+    if (!f8 && (!encode_cache_map(&p.tm_k, pool, k_cache, p.box_rows) ||
+                !encode_cache_map(&p.tm_v, pool, v_cache, p.box_rows)))
+        return PKV_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+#define PKV_CHUNK(D, F)                                                                          \
+    (bf ? (rows == TILE_M ? launch_chunk_t<D, F, true, 1>(pool, p, s)                            \
+                          : launch_chunk_t<D, F, true, 2>(pool, p, s))                           \
+        : (rows == TILE_M ? launch_chunk_t<D, F, false, 1>(pool, p, s)                           \
+                          : launch_chunk_t<D, F, false, 2>(pool, p, s)))
+    if (pool->head_dim == 128)
+        return f8 ? PKV_CHUNK(128, true) : PKV_CHUNK(128, false);
+    return f8 ? PKV_CHUNK(64, true) : PKV_CHUNK(64, false);
+#undef PKV_CHUNK
+}
+
+}  // namespace pkv

@@ -1,0 +1,142 @@
+// How paged_chunk_attention's work is cut into one share a CTA.
+//
+// An item is a row tile of one (sequence, KV head): up to `rows` (token, query head)
+// rows, tpr = rows / G tokens of all G query heads of the KV head.  It covers the key
+// tiles (of 128) from the first that its first token sees to the last that its last
+// one does.  Items are numbered by sequence, KV head, row tile; an item costs its tiles
+// and ITEM_COST more for its q, its first tile's latency and its output.  The costs end
+// to end are a line that is cut into equal shares; a cut within an item falls between two of its
+// tiles.  Where a position of the line falls is worked out in closed form, so a CTA
+// finds its share without looking at other CTAs' items.  Host and device.
+#pragma once
+
+#include <cstdint>
+
+#if defined(__CUDACC__)
+#define PKV_HD __host__ __device__ __forceinline__
+#else
+#define PKV_HD inline
+#endif
+
+namespace pkv {
+namespace chunk {
+
+constexpr int TILE = 128;             // keys of a tile
+constexpr int ITEM_COST = 2;
+
+struct Rules {
+    int tpr;                          // tokens of a row tile: a power of two, 16..256
+    int window;                       // 0: none
+    bool tree;                        // every new token may see any other
+};
+
+// sum over s < x of floor((a + s w) / 128), w a power of two, a >= 0.
+PKV_HD int64_t floor_sum(int64_t x, int64_t a, int w)
+{
+    if (w >= TILE)
+        return x * (a / TILE) + (int64_t)(w / TILE) * (x * (x - 1) / 2);
+    const int k = TILE / w;
+    // floor((a + s w) / 128) = floor((floor(a / w) + s) / k); H(y) sums floor(i / k), i < y
+    const int64_t a0 = a / w, y0 = a0, y1 = a0 + x;
+    const int64_t q0 = y0 / k, q1 = y1 / k;
+    const int64_t h0 = k * (q0 * (q0 - 1) / 2) + (y0 - q0 * k) * q0;
+    const int64_t h1 = k * (q1 * (q1 - 1) / 2) + (y1 - q1 * k) * q1;
+    return h1 - h0;
+}
+
+// One sequence: n new tokens, the last of L cached rows (0 < n <= L).
+struct Seq {
+    int n, L;
+};
+
+PKV_HD int row_tiles(const Rules &r, const Seq &q) { return (q.n - 1) / r.tpr + 1; }
+
+// Positions of a row tile's first token and of the last key that a row of it may see.
+PKV_HD void span(const Rules &r, const Seq &q, int rt, int &first, int &last)
+{
+    const int end = q.n - rt * r.tpr < r.tpr ? q.n : (rt + 1) * r.tpr;
+    first = q.L - q.n + rt * r.tpr;
+    last = (r.tree ? q.L : q.L - q.n + end) - 1;
+}
+
+// Its key tiles [lo, hi).
+PKV_HD void tiles(const Rules &r, const Seq &q, int rt, int &lo, int &hi)
+{
+    int first, last;
+    span(r, q, rt, first, last);
+    lo = r.window > 0 && first - r.window + 1 > 0 ? (first - r.window + 1) / TILE : 0;
+    hi = last / TILE + 1;
+}
+
+// Cost of the row tiles before rt, all of them whole ones (of one KV head).
+PKV_HD int64_t cost_before(const Rules &r, const Seq &q, int64_t rt)
+{
+    const int64_t A = q.L - q.n;
+    if (r.tree)
+        return rt * ((q.L - 1) / TILE + 1 + ITEM_COST);
+    int64_t c = floor_sum(rt, A + r.tpr - 1, r.tpr) + rt * (1 + ITEM_COST);
+    if (r.window > 0) {
+        const int64_t first = A - r.window + 1;
+        const int64_t s0 = first < 0 ? (-first + r.tpr - 1) / r.tpr : 0;   // tiles from key 0
+        if (rt > s0)
+            c -= floor_sum(rt - s0, first + s0 * r.tpr, r.tpr);
+    }
+    return c;
+}
+
+PKV_HD int64_t cost_of(const Rules &r, const Seq &q)
+{
+    const int R = row_tiles(r, q);
+    int lo, hi;
+    tiles(r, q, R - 1, lo, hi);
+    return cost_before(r, q, R - 1) + (hi - lo) + ITEM_COST;
+}
+
+// A place between two tiles: of sequence b, KV head h, row tile rt, before key tile
+// `tile`; `split`: within the item, not at its start.
+struct Place {
+    int b, h, rt, tile, split;
+};
+
+// Position x (0 <= x < Hkv * cost_of) of sequence b's stretch of the line.
+PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x)
+{
+    const int64_t c = cost_of(r, q);
+    Place p;
+    p.b = b;
+    p.h = (int)(x / c);
+    x -= p.h * c;
+    int a = 0, e = row_tiles(r, q) - 1;               // the last row tile that starts by x
+    while (a < e) {
+        const int m = (a + e + 1) / 2;
+        if (cost_before(r, q, m) <= x)
+            a = m;
+        else
+            e = m - 1;
+    }
+    p.rt = a;
+    x -= cost_before(r, q, a);
+    int lo, hi;
+    tiles(r, q, a, lo, hi);
+    p.tile = x > ITEM_COST ? lo + (int)(x - ITEM_COST) : lo;
+    p.split = p.tile > lo;
+    return p;
+}
+
+// Shares for a line of length U on `ctas` CTAs: none of them shorter than MIN_SHARE
+// (a share of a tile or two costs more in its start and in the joining of its state
+// than it saves).
+constexpr int MIN_SHARE = 4;
+PKV_HD int shares(int64_t U, int ctas)
+{
+    const int64_t n = U / MIN_SHARE;
+    return n < 1 ? 1 : n < ctas ? (int)n : ctas;
+}
+PKV_HD int64_t share_start(int64_t U, int n, int c)
+{
+    // U c / n without a product beyond 64 bits
+    return U / n * c + U % n * c / n;
+}
+
+}  // namespace chunk
+}  // namespace pkv

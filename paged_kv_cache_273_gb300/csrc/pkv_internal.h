@@ -128,6 +128,15 @@ int launch_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q
                        void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
                        void *k_scales, void *v_scales, pkv_stream_t stream);
 
+// Attention of chunks of new tokens (chunk.cu).
+size_t chunk_workspace_bytes(const pkv_pool *pool, int num_q_heads, int max_q_len);
+int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num_q_heads,
+                 int num_tokens, const void *k_cache, const void *v_cache, const void *k_scales,
+                 const void *v_scales, const int32_t *tables, int max_blocks,
+                 const int32_t *q_start, const int32_t *seq_lens, int batch, int max_q_len,
+                 int window, const uint64_t *visible, float scale, void *out, void *workspace,
+                 pkv_stream_t stream);
+
 // The workspace of decode_blocks_kernel and select_kernel starts with a counter
 // for each KV head of the largest batch, whatever the call's batch: one buffer,
 // zeroed once, then serves calls of any batch, since none writes its scratch
@@ -219,6 +228,11 @@ int launch_prefix_merge(const pkv_pool *pool, const int32_t *seq_prefix, float *
 // The driver's tensor-map encoder (cuTensorMapEncodeTiled), looked up once
 // through the runtime; null if unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// A cache [NB][Hkv][bs][D] of 16-bit elements as the tensor that the tcgen05 kernels
+// read: {D, bs, NB * Hkv}, boxes of 64 x rows x 1, 128-byte swizzle (prefill.cu).
+// False if the encoder is unavailable or refuses.
+bool encode_cache_map(CUtensorMap *m, const pkv_pool *pool, const void *base, int rows);
 
 // A cache [NB][Hkv][bs][row_bytes] (row_bytes 128 or 256) as the tensor the
 // decode kernel's swizzled tile copies read: bytes in 128-byte segments,

@@ -1090,6 +1090,61 @@ int kv_rope_append(const pkv_pool *pool, const pkv_rope *rope, const void *q, in
                                    q_out_stride, k_cache, v_cache, k_scales, v_scales, stream);
 }
 
+size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_heads,
+                                   int max_q_len)
+{
+    if (!pool || batch < 0 || num_q_heads < 1 || num_q_heads % pool->num_kv_heads != 0 ||
+        max_q_len < 0)
+        return 0;
+    return pkv::chunk_workspace_bytes(pool, num_q_heads, max_q_len);
+}
+
+int paged_chunk_attention(const pkv_pool *pool, const void *q, pkv_dtype q_dtype,
+                          int num_q_heads, int num_tokens, const void *k_cache,
+                          const void *v_cache, const void *k_scales, const void *v_scales,
+                          const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *q_start, const int32_t *seq_lens, int batch,
+                          int max_q_len, int window, const uint64_t *visible, float scale,
+                          void *out, void *workspace, size_t workspace_bytes,
+                          pkv_stream_t stream)
+{
+    Range range("pkv.paged_chunk_attention");
+    if (!pool || batch < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || max_q_len < 0 ||
+        window < 0 || num_q_heads < 1 || num_q_heads % pool->num_kv_heads != 0)
+        return PKV_ERR_INVALID;
+    const int G = num_q_heads / pool->num_kv_heads;
+    if (G != 1 && G != 2 && G != 4 && G != 8)
+        return PKV_ERR_UNSUPPORTED;
+    const bool f8 = pool->kv_dtype == PKV_F8;
+    if (!f8 && pool->kv_dtype != PKV_F16 && pool->kv_dtype != PKV_BF16)
+        return PKV_ERR_UNSUPPORTED;
+    if (f8 ? q_dtype != PKV_F16 && q_dtype != PKV_BF16 : q_dtype != pool->kv_dtype)
+        return PKV_ERR_INVALID;
+    if (batch > 65535 || num_q_heads > 65535)
+        return PKV_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale) || scale <= 0.0f || (visible && window > 0))
+        return PKV_ERR_INVALID;
+    if (batch == 0 || num_tokens == 0 || max_q_len == 0)
+        return PKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !q_start || !seq_lens || !out ||
+        !workspace || (f8 && (!k_scales || !v_scales)))
+        return PKV_ERR_INVALID;
+    if (!pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache) ||
+        !pkv::aligned16(out) || !pkv::aligned16(workspace) || !aligned4(block_tables) ||
+        !aligned4(q_start) || !aligned4(seq_lens) || (f8 && (!aligned4(k_scales) || !aligned4(v_scales))) ||
+        (reinterpret_cast<uintptr_t>(visible) & 7u))
+        return PKV_ERR_INVALID;
+    const int rc = device_check(pool);
+    if (rc != PKV_OK)
+        return rc;
+    if (workspace_bytes < pkv::chunk_workspace_bytes(pool, num_q_heads, max_q_len))
+        return PKV_ERR_INVALID;
+    return pkv::launch_chunk(pool, q, q_dtype, num_q_heads, num_tokens, k_cache, v_cache,
+                             k_scales, v_scales, block_tables, max_blocks_per_seq, q_start,
+                             seq_lens, batch, max_q_len, window, visible, scale, out, workspace,
+                             stream);
+}
+
 int pkv_selftest_wait_timeout(const pkv_pool *pool, pkv_stream_t stream)
 {
     if (!pool)

@@ -51,7 +51,7 @@ SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "
            "paged_decode_attention_noalloc", "paged_decode_step", "kv_device_reserve",
            "kv_device_release", "kv_bounds_append", "kv_bounds_copy", "paged_sparse_workspace_bytes",
            "paged_decode_attention_sparse", "kv_rope_frequencies", "kv_rope_rotate",
-           "kv_rope_append", "pkv_selftest_wait_timeout", "pkv_check_error")
+           "kv_rope_append", "paged_chunk_workspace_bytes", "paged_chunk_attention", "pkv_selftest_wait_timeout", "pkv_check_error")
 
 
 class StepLayout(ctypes.Structure):
@@ -169,6 +169,11 @@ def load() -> ctypes.CDLL:
         lib.kv_rope_append.argtypes = [P, RP, P, I64, P, I64, P, I64, I, I, P, P, I, P, I64, P, P,
                                        P, P, P]
         lib.kv_rope_append.restype = I
+        lib.paged_chunk_workspace_bytes.argtypes = [P, I, I, I]
+        lib.paged_chunk_workspace_bytes.restype = SZ
+        lib.paged_chunk_attention.argtypes = [P, P, I, I, I, P, P, P, P, P, I, P, P, I, I, I, P, F,
+                                              P, P, SZ, P]
+        lib.paged_chunk_attention.restype = I
         lib.pkv_selftest_wait_timeout.argtypes = [P, P]
         lib.pkv_selftest_wait_timeout.restype = I
         lib.pkv_check_error.argtypes = [P, P]
@@ -900,6 +905,48 @@ def _cache_of(pool: Pool, *caches) -> None:
     for c in caches:
         if c.shape != shape or c.dtype is not TORCH_DTYPE[pool.kv_dtype]:
             _shaped("a cache", c, TORCH_DTYPE[pool.kv_dtype], shape)
+
+
+# ------------------------------------------------------------- chunks of new tokens
+def paged_chunk_workspace_bytes(pool: Pool, batch: int, num_q_heads: int, max_q_len: int) -> int:
+    return int(load().paged_chunk_workspace_bytes(pool.handle, batch, num_q_heads, max_q_len))
+
+
+def alloc_chunk_workspace(pool: Pool, batch: int, num_q_heads: int, max_q_len: int,
+                          device="cuda") -> torch.Tensor:
+    """A workspace for paged_chunk_attention calls of up to max_q_len new tokens a sequence."""
+    n = paged_chunk_workspace_bytes(pool, batch, num_q_heads, max_q_len)
+    if n == 0:
+        raise PkvError(PKV_ERR_INVALID, "paged_chunk_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_chunk_attention(pool: Pool, q, k_cache, v_cache, block_tables, q_start, seq_lens,
+                          scale: float, out, workspace, max_q_len: int, k_scales=None,
+                          v_scales=None, window: int = 0, visible=None, stream=None) -> None:
+    """Attention of each sequence's new tokens, q [num_tokens, Hq, D] with sequence b's at rows
+    q_start[b] .. q_start[b + 1], over its cached rows (see include/pkv.h): causal, in a sliding
+    `window`, or (`visible`, int64 [num_tokens]) with the drafted tokens' own masks.  out is
+    of q's shape and type."""
+    if q.dtype not in PKV_DTYPE:
+        raise ValueError("unsupported q dtype %s" % q.dtype)
+    T, B = q.shape[0], seq_lens.numel()
+    _shaped("q", q, q.dtype, (T, None, pool.head_dim))
+    _shaped("out", out, q.dtype, tuple(q.shape))
+    _shaped("seq_lens", seq_lens, _I32, (B,))
+    _shaped("q_start", q_start, _I32, (B + 1,))
+    _rows("block_tables", block_tables, B)
+    _cache_of(pool, k_cache, v_cache)
+    _check_scales(pool, k_scales, v_scales)
+    if visible is not None:
+        _shaped("visible", visible, torch.int64, (T,))
+    _on_current(q, out, k_cache, workspace, visible)
+    _check(load().paged_chunk_attention(
+        pool.handle, _dptr(q), PKV_DTYPE[q.dtype], q.shape[1], T, _dptr(k_cache), _dptr(v_cache),
+        _dptr(k_scales), _dptr(v_scales), _dptr(block_tables), block_tables.shape[1],
+        _dptr(q_start), _dptr(seq_lens), B, int(max_q_len), int(window), _dptr(visible),
+        float(scale), _dptr(out), _dptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "paged_chunk_attention")
 
 
 def pkv_selftest_wait_timeout(pool: Pool, stream=None) -> None:
