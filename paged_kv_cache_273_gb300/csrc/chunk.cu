@@ -88,7 +88,12 @@ struct Cfg {
     static constexpr int SMEM_BYTES = OFF_MISC + 256;
     static constexpr int W_MMA = F8 ? 12 : 11;
     static constexpr bool QCONV = F8 && BF;
-    static constexpr int NT = 32 * (F8 ? (BF ? 16 : 14) : 12);
+    static constexpr int NT = 32 * (F8 ? 16 : 12);
+    // registers of a thread of each warpgroup: the softmax groups hold a row of 128 scores; a
+    // block is launched with 168 (128) each, and the shares add up to that
+    static constexpr int REGS = F8 ? 128 : 168;
+    static constexpr int R_SOFT = F8 ? 184 : 208, R_2 = F8 ? 80 : 88, R_3 = F8 ? 64 : 0;
+    static_assert(2 * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
     static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
     // P in one 16-bit part, rounded as the output is; over an 8-bit cache P is bf16, for
     // its range, and in two parts where the output is fp16
@@ -380,6 +385,12 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     Piece c;
     walk.start(p, places);
 
+    if (warp < 8)
+        more_registers<C::R_SOFT>();
+    else if (warp < 12)
+        fewer_registers<C::R_2>();
+    else
+        fewer_registers<F8 ? C::R_3 : 24>();
     if (warp < 8) {
         // ================= softmax: group g, one thread a row
         const int g = warp >> 2, quad = warp & 3;
@@ -433,40 +444,42 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         return w;
                     };
-                    // pass 1: the row's maximum, in the base-2 logarithm's units
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < TILE; c0 += 32) {
-                        float v[32];
-                        tmem_ld32(t_s + c0, v);
-                        if (masked) {
+                    float v[TILE];
+                    tmem_ld64(t_s, v);
+                    tmem_ld64(t_s + 64, v + 64);
+                    if (masked) {
+#pragma unroll
+                        for (int c0 = 0; c0 < TILE; c0 += 32) {
                             const uint32_t w = in_sight(c0);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                v[j] = (w >> j) & 1 ? v[j] : -INFINITY;
-                        }
-                        if constexpr (F8) {
-                            const float4 f = fac[c0 / 32];
-                            const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float *x = v + 8 * k;
-                                const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
-                                                      fmaxf(x[6], x[7]));
-                                mx = fmaxf(mx, a * (ff[k] * rs));
-                            }
-                        } else {
-                            float t[11];
-#pragma unroll
-                            for (int j = 0; j < 10; ++j)
-                                t[j] = max3f(v[3 * j], v[3 * j + 1], v[3 * j + 2]);
-                            t[10] = fmaxf(v[30], v[31]);
-                            mx = max3f(mx, max3f(t[0], t[1], t[2]), max3f(t[3], t[4], t[5]));
-                            mx = max3f(mx, max3f(t[6], t[7], t[8]), fmaxf(t[9], t[10]));
+                                v[c0 + j] = (w >> j) & 1 ? v[c0 + j] : -INFINITY;
                         }
                     }
-                    if (!F8)
-                        mx *= rs;                  // scale > 0: the maximum commutes
+                    // the row's maximum, in the base-2 logarithm's units
+                    float mx = -INFINITY;
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; ++k) {
+                            const float4 f = fac[k];
+                            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float *x = v + 32 * k + 8 * e;
+                                mx = fmaxf(mx, max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
+                                                     fmaxf(x[6], x[7])) * (ff[e] * rs));
+                            }
+                        }
+                    } else {
+                        float t[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                        for (int j = 4; j < TILE; j += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                t[k] = j + 4 + k < TILE ? max3f(t[k], v[j + k], v[j + 4 + k])
+                                                        : fmaxf(t[k], v[j + k]);
+                        mx = max3f(fmaxf(t[0], t[1]), t[2], t[3]) * rs;   // scale > 0: the maximum commutes
+                    }
                     // The running maximum moves only when a score exceeds it by more than
                     // 2^8 (or is the first in sight): below that the weights stay <= 2^8, and
                     // the quotient by the sum of the same weights is unchanged.
@@ -487,60 +500,52 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                             tmem_st32(t_o + c0, o);
                         }
                     }
-                    // pass 2: weights, their sum, and P (keys 32c..32c+31 as 16-bit pairs in
-                    // columns 32c..32c+15, low parts in the next 16: S columns already read)
+                    // weights, their sum, and P over the S columns: 16-bit pairs of keys in
+                    // columns 0..63, their low parts (where there are two) in 64..127
                     const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_new == -INFINITY ? 0.0f : m_new);
-                    float sum = 0.0f;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < TILE; c0 += 32) {
-                        float v[32];
-                        tmem_ld32(t_s + c0, v);
-                        if (masked) {
-                            const uint32_t w = in_sight(c0);
+                    float sum[4] = {};
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = (w >> j) & 1 ? v[j] : -INFINITY;
-                        }
+                    for (int c0 = 0; c0 < TILE; c0 += 32) {
+                        float *x = v + c0;
                         if constexpr (F8) {
                             const float4 f = fac[c0 / 32];
                             const float ff[4] = {f.x * rs, f.y * rs, f.z * rs, f.w * rs};
 #pragma unroll
                             for (int j = 0; j < 32; j += 2)
-                                fma2_bc(v[j], v[j + 1], ff[j / 8], off);
+                                fma2_bc(x[j], x[j + 1], ff[j / 8], off);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 32; j += 2)
-                                fma2_bc(v[j], v[j + 1], rs, off);
+                                fma2_bc(x[j], x[j + 1], rs, off);
                         }
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            v[j] = ex2_approx(v[j]);
+                            x[j] = ex2_approx(x[j]);
                         using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            w[j] = pack2<PT>(v[2 * j], v[2 * j + 1]);
-                        tmem_st16(t_s + c0, w);
+                            w[j] = pack2<PT>(x[2 * j], x[2 * j + 1]);
+                        tmem_st16(t_s + c0 / 2, w);
                         if constexpr (C::SPLIT) {
                             uint32_t wl[16];
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
                                 const float2 h = unpack2<PT>(w[j]);
-                                float r0 = v[2 * j], r1 = v[2 * j + 1];
+                                float r0 = x[2 * j], r1 = x[2 * j + 1];
                                 add2(r0, r1, -h.x, -h.y);
                                 wl[j] = pack2<PT>(r0, r1);
                             }
-                            tmem_st16(t_s + c0 + 16, wl);
+                            tmem_st16(t_s + TILE / 2 + c0 / 2, wl);
                         }
 #pragma unroll
-                        for (int k = 16; k > 1; k >>= 1)       // tree sum over pairs
-#pragma unroll
-                            for (int j = 0; j < k; j += 2)
-                                add2(v[j], v[j + 1], v[j + k], v[j + k + 1]);
-                        sum += v[0] + v[1];
+                        for (int j = 0; j < 32; j += 4) {
+                            add2(sum[0], sum[1], x[j], x[j + 1]);
+                            add2(sum[2], sum[3], x[j + 2], x[j + 3]);
+                        }
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    l_run = l_run * corr + sum;
+                    l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                 }
                 tc_fence_before();
                 mbar_arrive(&p_full[g]);
@@ -911,91 +916,102 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(q_full);
         }
-    } else if (warp == C::W_MMA && lane == 0) {
-        // ================= MMA issue (one thread)
+    } else if (warp == C::W_MMA) {
+        // ================= MMA issue: the warp walks as one, an elected lane issues
         // S = Q K^T, both K-major, and O += P V, P in tensor memory, V MN-major; all of them
         // 128-byte swizzled panels of 64 channels: a row every 128 bytes, eight rows 1024
         // bytes, the next panel 128 rows on.  A step of 16 along the contraction is 32 bytes
         // into S's rows, 16 rows of V.
+        constexpr uint32_t PANEL = TILE * 128;
         const uint32_t idesc_s = umma_idesc(BF && !F8 ? 1u : 0u, 0u, TILE);
         const uint32_t idesc_o = umma_idesc(C::PBF ? 1u : 0u, 1u, D);
-        const uint32_t sQa = smem_addr(sQ), sKa = smem_addr(sK), sVa = smem_addr(sV);
+        const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0), el = elect_lane();
+        const uint64_t dq = umma_desc_sw128(smem_addr(sQ), 16, 1024);
+        const uint64_t dk = umma_desc_sw128(smem_addr(sK), 16, 1024);
+        const uint64_t dv = umma_desc_sw128(smem_addr(sV), PANEL, 1024);
+        const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
+        const uint32_t s_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
         uint32_t gt = 0, pc[2] = {0, 0}, ofc[2] = {0, 0};
         bool o_used[2] = {false, false};
         bool ok = true;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(FULL_MASK, wait(bar, parity));
+        };
         for (uint32_t item = 0; ok && walk.next(p, c); ++item) {
             const bool both = shared_rows(c);
             const int nt[2] = {group_tiles(p, c, 0), group_tiles(p, c, 1)};
             int s_left = nt[0] + nt[1];
             auto issue_s = [&](int g, int s) -> bool {
-                const uint32_t k = gt + tile_at(c, g, s);
-                if (!wait(&k_full[k % NS], k / NS))
+                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
+                if (!wait_all(&k_full[slot], k / NS))
                     return false;
                 tc_fence_after();
-                const uint32_t kb = sKa + k % NS * C::KV_BYTES, qb = sQa + (both ? 0 : g) * C::Q_BYTES;
+                const uint32_t kb = k_lo + slot * (C::KV_BYTES / 16);
+                const uint32_t qb = q_lo + (both ? 0 : g) * (C::Q_BYTES / 16);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    umma_f16(tmem + g * C::GROUP_COLS,
-                             umma_desc_sw128(qb + (ks / 4) * (TILE_M * 128) + (ks % 4) * 32, 16, 1024),
-                             umma_desc_sw128(kb + (ks / 4) * (TILE * 128) + (ks % 4) * 32, 16, 1024),
-                             idesc_s, ks > 0 ? 1u : 0u);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t step = (ks / 4) * (PANEL / 16) + (ks % 4) * 2;
+                    umma_f16_elected(el, tm + g * C::GROUP_COLS, qb + step, s_hi, kb + step, s_hi,
+                                     idesc_s, ks > 0 ? 1u : 0u);
+                }
                 if (both || g == 1)                // the tile's last reader
-                    umma_commit(&k_empty[k % NS]);
-                umma_commit(&s_full[g]);
+                    umma_commit_elected(el, &k_empty[slot]);
+                umma_commit_elected(el, &s_full[g]);
                 if (--s_left == 0)
-                    umma_commit(q_empty);
+                    umma_commit_elected(el, q_empty);
                 return true;
             };
             auto issue_pv = [&](int g, int s) -> bool {
-                const uint32_t k = gt + tile_at(c, g, s);
-                if (!wait(&p_full[g], pc[g]) || !wait(&v_full[k % NS], k / NS))
+                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
+                if (!wait_all(&v_full[slot], k / NS) || !wait_all(&p_full[g], pc[g]))
                     return false;
                 ++pc[g];
                 if (s == 0 && o_used[g]) {         // the softmax threads have read O out
-                    if (!wait(&o_free[g], ofc[g]))
+                    if (!wait_all(&o_free[g], ofc[g]))
                         return false;
                     ++ofc[g];
                 }
                 tc_fence_after();
-                const uint32_t vb = sVa + k % NS * C::KV_BYTES, base = tmem + g * C::GROUP_COLS;
+                const uint32_t vb = v_lo + slot * (C::KV_BYTES / 16), base = tm + g * C::GROUP_COLS;
 #pragma unroll
                 for (int ks = 0; ks < TILE / 16; ++ks) {
-                    const uint32_t pa = base + 32 * (ks >> 1) + 8 * (ks & 1);
-                    const uint64_t vd = umma_desc_sw128(vb + ks * 2048, TILE * 128, 1024);
-                    umma_f16_ta(base + TILE, pa, vd, idesc_o, s > 0 || ks > 0 ? 1u : 0u);
+                    umma_f16_ta_elected(el, base + TILE, base + 8 * ks, vb + ks * (2048 / 16), v_hi,
+                                        idesc_o, s > 0 || ks > 0 ? 1u : 0u);
                     if (C::SPLIT)
-                        umma_f16_ta(base + TILE, pa + 16, vd, idesc_o, 1u);
+                        umma_f16_ta_elected(el, base + TILE, base + TILE / 2 + 8 * ks,
+                                            vb + ks * (2048 / 16), v_hi, idesc_o, 1u);
                 }
                 if (both || g == 1)
-                    umma_commit(&v_empty[k % NS]);
+                    umma_commit_elected(el, &v_empty[slot]);
                 return true;
             };
-            if (!(ok = wait(q_full, item)))
+            if (!(ok = wait_all(q_full, item)))
                 break;
-            for (int g = 0; g < 2 && ok; ++g)
-                if (nt[g] > 0)
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if (ok && nt[g] > 0)
                     ok = issue_s(g, 0);
             const int steps = max(nt[0], nt[1]);
             for (int s = 0; s < steps && ok; ++s)
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (s >= nt[g])
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!ok || s >= nt[g] || !(ok = issue_pv(g, s)))
                         continue;
-                    if (!(ok = issue_pv(g, s)))
-                        break;
                     if (s + 1 < nt[g]) {
                         ok = issue_s(g, s + 1);
                     } else {
-                        umma_commit(&o_done[g]);
+                        umma_commit_elected(el, &o_done[g]);
                         o_used[g] = true;
                     }
                 }
             gt += c.t1 - c.t0;
         }
         // every issued MMA has finished before tensor memory is released
-        umma_commit(drain);
+        umma_commit_elected(el, drain);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0u) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
         }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
