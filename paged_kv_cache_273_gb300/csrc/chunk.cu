@@ -42,7 +42,7 @@ using chunk::TILE;
 
 struct ChunkParams {
     CUtensorMap tm_q;             // q [T][Hq][D]: boxes of 64 columns x G heads x 128 / G tokens
-    CUtensorMap tm_k, tm_v;       // 16-bit caches: boxes of 64 columns x box_rows
+    CUtensorMap tm_k, tm_v;       // 16-bit caches: boxes of box_rows whole rows
     const void *q, *k_cache, *v_cache;
     const float *k_scales, *v_scales;
     const int32_t *tables, *q_start, *seq_lens;
@@ -58,11 +58,14 @@ struct ChunkParams {
     Rules rules;
 };
 
-// Warps: 0-7 the softmax groups; then, of a 16-bit cache, one that brings K, one V,
-// one q, and one that issues the MMAs; of an 8-bit cache, four that convert tiles, the MMA
-// warp, one that brings tiles, and two that bring q where that is converted too.
+// Warps: the softmax groups; then, of a 16-bit cache, one that brings K, one V, one that
+// hands out the pieces and brings their q, and one that issues the MMAs; of an 8-bit cache,
+// four that convert tiles, the MMA warp, one that brings tiles, and the one for pieces and q.
 template <int D, bool F8, bool BF, int NQ>
 struct Cfg {
+    // threads a row of a softmax group: two halve the time from S to P, which the tensor cores
+    // wait for; over an 8-bit cache the registers are wanted for the conversion
+    static constexpr int HT = 1;
     static constexpr int ROWS = NQ * TILE_M;
     static constexpr int Q_BYTES = TILE_M * D * 2;                       // one half
     static constexpr int KV_BYTES = TILE * D * 2;
@@ -78,23 +81,32 @@ struct Cfg {
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
     static constexpr int OFF_RK = OFF_V + NS * KV_BYTES;
     static constexpr int OFF_RV = OFF_RK + NR * RAW_BYTES;
-    static constexpr int OFF_ML = OFF_RV + NR * RAW_BYTES;               // the second group's states
-    static constexpr int OFF_SC = OFF_ML + TILE_M * 8;                   // [RING][16] K, then V scales
+    static constexpr int OFF_ML = OFF_RV + NR * RAW_BYTES;               // what threads of a row exchange
+    static constexpr int XM1 = HT == 2 ? 2 * TILE_M : 0;                 // the second group's slots
+    static constexpr int OFF_SC = OFF_ML + (XM1 + 2 * TILE_M) * 4;       // [RING][16] K, then V scales
     static constexpr int OFF_LIVE = OFF_SC + (F8 ? RING * 16 * 8 : 0);   // [RING]
-    static constexpr int OFF_QE = OFF_LIVE + (F8 ? RING * 4 : 0);        // q's exponents, two items
-    static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * ROWS : 0);
-    static constexpr int NBARS = 4 * NS + 4 * NR + 8 + 5;
-    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;                 // tensor memory's address, flags, places
-    static constexpr int SMEM_BYTES = OFF_MISC + 256;
-    static constexpr int W_MMA = F8 ? 12 : 11;
+    static constexpr int OFF_QE = OFF_LIVE + (F8 ? RING * 4 : 0);        // q's exponents, two pieces
+    static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * TILE_M : 0);
+    static constexpr int PIECES = 4;                                     // handed out and not done
+    static constexpr int NBARS = 4 * NS + 4 * NR + 8 + 6 + 2 * PIECES + (HT == 2 ? 8 : 0);
+    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;                 // tensor memory's address, flag, pieces
+    static constexpr int SMEM_BYTES = OFF_MISC + 224;
+    static constexpr int W0 = 8 * HT;                                    // the first warp behind the groups
+    static constexpr int W_MMA = F8 ? W0 + 4 : W0 + 3, W_FEED = F8 ? W0 + 6 : W0 + 2;
+    static constexpr int CONSUMERS = W0 + (F8 ? 6 : 3);                  // warps that a piece is for
     static constexpr bool QCONV = F8 && BF;
-    static constexpr int NT = 32 * (F8 ? 16 : 12);
-    // registers of a thread of each warpgroup: the softmax groups hold a row of 128 scores; a
-    // block is launched with 168 (128) each, and the shares add up to that
+    static constexpr int NT = 32 * (F8 ? W0 + 8 : W0 + 4);
+    // registers of a thread: at launch, and from then on in the softmax groups, the four
+    // warps behind them, and the last four (the shares add up to what was there at launch)
     static constexpr int REGS = F8 ? 128 : 168;
-    static constexpr int R_SOFT = F8 ? 184 : 208, R_2 = F8 ? 80 : 88, R_3 = F8 ? 64 : 0;
-    static_assert(2 * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
+    static constexpr int R_SOFT = F8 ? 184 : 216, R_2 = F8 ? 80 : 72, R_3 = F8 ? 64 : 0;
+    static_assert(2 * HT * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
     static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
+    // a K or V tile: eight rows of 64 columns are 1024 bytes (128-byte swizzled); a group of
+    // eight rows holds its panels one after the other, so that one tensor copy brings
+    // a block's whole rows (two of 64 columns each cost the warp that issues them
+    // twice as long, more than a tile's time on the tensor cores)
+    static constexpr int GROUP8 = 1024 * (D / 64);
     // P in one 16-bit part, rounded as the output is; over an 8-bit cache P is bf16, for
     // its range, and in two parts where the output is fp16
     static constexpr bool PBF = F8 || BF;
@@ -102,7 +114,15 @@ struct Cfg {
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-// The share's walk over its items' pieces; every role walks it alike.
+// Byte offset of 16-byte chunk ch of row r in a K or V tile.
+template <int D>
+__device__ __forceinline__ uint32_t tile_off(int r, int ch)
+{
+    return (uint32_t)((r >> 3) * (1024 * (D / 64)) + (ch >> 3) * 1024 + (r & 7) * 128 +
+                      (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// The share's walk over its items' pieces.
 struct Piece {
     int b, h;
     int tok;               // first token, as a row of q
@@ -112,7 +132,8 @@ struct Piece {
     int base;              // cached rows before the new tokens (L - n)
     int len;               // L
     int t0, t1;            // key tiles
-    int kind;              // 0: the whole item; 1: not from its start; 2: from its start, not to its end
+    int kind;              // 0: the whole item; 1: not from its start; 2: from its start, not to its end;
+                           // -1: no more pieces
 };
 
 struct Walk {
@@ -276,6 +297,17 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
     return true;
 }
 
+// One block's rows (or 128 of them) of one KV head, from its group `y` of eight on.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int y, int z,
+                                            uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // 16 e4m3 codes -> 16 fp16 values (exact), as two 16-byte chunks.
 __device__ __forceinline__ void codes_to_half(const uint4 &w, uint4 &lo, uint4 &hi)
 {
@@ -305,16 +337,72 @@ constexpr int V_SHIFT = 16;
 // they stay below 2^15, and weights down to 2^-21 of the largest keep all their bits.
 constexpr float P_SHIFT = 7.0f;
 
+__device__ __forceinline__ float ld_shared(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, float x)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+
+// Row r of a half of q (bf16, as the tensor copy left it) -> fp16 times 2^-e in place, the
+// row's largest magnitude in [2^14, 2^15); returns e.
+template <int D>
+__device__ __forceinline__ int halve_row(unsigned char *q, int r)
+{
+    auto at = [&](int ch) {
+        return reinterpret_cast<uint4 *>(q + (ch >> 3) * (TILE_M * 128) + r * 128 +
+                                         (((ch & 7) ^ (r & 7)) << 4));
+    };
+    uint32_t top = 0;                              // magnitudes order as their bits
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 w = *at(ch);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            top = max(top, max(v[k] << 16 & 0x7fffffffu, v[k] & 0x7fff0000u));
+    }
+    const int e = max((int)(top >> 23) - 127 - 14, -126);
+    const float f = pow2_f32(-e);
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 w = *at(ch);
+        uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[k] = pack2<__half>(bf16lo(v[k]) * f, bf16hi(v[k]) * f);
+        *at(ch) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    return e;
+}
+
+// The part of a wait that is not over at once; a call, for the instruction cache's sake.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                     unsigned int *err)
+{
+    if (mbar_wait_bounded(bar, parity, abort_flag))
+        return true;
+    if (!*abort_flag) {
+        *abort_flag = 1;
+        atomicOr(err, PKV_EBIT_TIMEOUT);
+    }
+    return false;
+}
+
 template <int D, bool F8, bool BF, int NQ>
 __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     chunk_kernel(const __grid_constant__ ChunkParams p)
 {
     using C = Cfg<D, F8, BF, NQ>;
-    constexpr int NS = C::NS, NR = C::NR;
+    constexpr int NS = C::NS, NR = C::NR, W0 = C::W0;
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    float *xm = reinterpret_cast<float *>(smem + C::OFF_ML);
     float *k_sc = reinterpret_cast<float *>(smem + C::OFF_SC), *v_sc = k_sc + C::RING * 16;
     uint32_t *live_of = reinterpret_cast<uint32_t *>(smem + C::OFF_LIVE);
     signed char *q_exp = reinterpret_cast<signed char *>(smem + C::OFF_QE);
@@ -322,12 +410,14 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
     uint64_t *s_full = v_empty + NS, *p_full = s_full + 2, *o_done = p_full + 2, *o_free = o_done + 2;
     uint64_t *q_full = o_free + 2, *q_empty = q_full + 1, *ml_full = q_empty + 1, *ml_free = ml_full + 1;
-    uint64_t *drain = ml_free + 1;
-    uint64_t *kr_full = drain + 1, *kr_empty = kr_full + NR, *vr_full = kr_empty + NR, *vr_empty = vr_full + NR;
+    uint64_t *drain = ml_free + 1, *pair = drain + 1;
+    uint64_t *pc_full = pair + (C::HT == 2 ? 8 : 0), *pc_empty = pc_full + C::PIECES, *q_raw = pc_empty + C::PIECES;
+    uint64_t *kr_full = q_raw + 1, *kr_empty = kr_full + NR, *vr_full = kr_empty + NR, *vr_empty = vr_full + NR;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Place *places = reinterpret_cast<Place *>(smem + C::OFF_MISC + 16);
     int64_t *sums = reinterpret_cast<int64_t *>(smem + C::OFF_MISC + 64);
+    Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_MISC + 16);    // (over the two above)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
@@ -349,14 +439,21 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&s_full[g], 1);
-            mbar_init(&p_full[g], TILE_M);
+            mbar_init(&p_full[g], 4 * C::HT);      // (a lane a warp arrives)
             mbar_init(&o_done[g], 1);
-            mbar_init(&o_free[g], TILE_M);
+            mbar_init(&o_free[g], 4 * C::HT);
         }
-        mbar_init(q_full, C::QCONV ? 64 : 1);
+        for (int i = 0; C::HT == 2 && i < 8; ++i)
+            mbar_init(&pair[i], 2);
+        mbar_init(q_full, C::QCONV ? 8 : 1);
+        mbar_init(q_raw, 1);
+        for (int i = 0; i < C::PIECES; ++i) {
+            mbar_init(&pc_full[i], 1);
+            mbar_init(&pc_empty[i], C::CONSUMERS);
+        }
         mbar_init(q_empty, 1);
-        mbar_init(ml_full, TILE_M);
-        mbar_init(ml_free, TILE_M);
+        mbar_init(ml_full, 4 * C::HT);
+        mbar_init(ml_free, 4 * C::HT);
         mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_fence_init();
@@ -373,70 +470,117 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     const uint32_t tmem = *tmem_slot;
     // A wait that runs out raises the error bit once and makes every role stop.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (mbar_wait_bounded(bar, parity & 1, abort_flag))
-            return true;
-        if (!*abort_flag) {
-            *abort_flag = 1;
-            atomicOr(p.err, PKV_EBIT_TIMEOUT);
-        }
-        return false;
+        return mbar_try_wait(bar, parity & 1) || wait_on(bar, parity & 1, abort_flag, p.err);
     };
-    Walk walk;
     Piece c;
-    walk.start(p, places);
+    // The item-th piece, and when this warp is done with it.
+    auto take = [&](uint32_t item) -> bool {
+        if (!__all_sync(FULL_MASK, wait(&pc_full[item % C::PIECES], item / C::PIECES)))
+            return false;
+        c = pieces[item % C::PIECES];
+        return c.kind >= 0;
+    };
+    auto done = [&](uint32_t item) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&pc_empty[item % C::PIECES]);
+    };
 
-    if (warp < 8)
+    if (warp < W0)
         more_registers<C::R_SOFT>();
-    else if (warp < 12)
+    else if (warp < W0 + 4)
         fewer_registers<C::R_2>();
     else
         fewer_registers<F8 ? C::R_3 : 24>();
-    if (warp < 8) {
-        // ================= softmax: group g, one thread a row
-        const int g = warp >> 2, quad = warp & 3;
+    if (warp < W0) {
+        // ================= softmax: group g, HT threads a row, each its share of a tile's
+        // keys and of the output's columns
+        constexpr int HT = C::HT, CW = TILE / HT, OW = D / HT;
+        const int g = warp / (4 * HT), hf = warp / 4 % HT, quad = warp & 3;
         const int r = quad * 32 + lane;
-        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t t_s = tmem + g * C::GROUP_COLS + lane_base, t_o = t_s + TILE;
-        uint32_t sc = 0, oc = 0, mc = 0;           // phases of s_full, o_done, ml
-        uint32_t done1 = 0;                        // group 0: of the second group's o_done
+        const uint32_t t_row = tmem + g * C::GROUP_COLS + ((uint32_t)(quad * 32) << 16);
+        const uint32_t t_s = t_row + hf * CW, t_p = t_row + hf * (CW / 2);
+        const uint32_t t_o = t_row + TILE + hf * OW;
+        const uint32_t mine = smem_addr(xm + g * C::XM1 + hf * TILE_M + r);
+        const uint32_t other = HT == 2 ? mine ^ (TILE_M * 4) : mine;
+        // the parities of the phases that come next, of s_full, o_done, ml_full, the row's pair
+        // and (group 0) the second group's o_done; and (group 1) whether its slots of xm
+        // are being read
+        uint32_t ph = 0;
+        constexpr uint32_t P_S = 1, P_O = 2, P_ML = 4, P_X = 8, P_O1 = 16, LENT = 32;
         int gt = 0;                                // the CTA's tiles so far
-        for (uint32_t item = 0; walk.next(p, c); ++item) {
+        auto phase = [&](uint64_t *bar, uint32_t bit) -> bool {
+            const bool ok = __all_sync(FULL_MASK, wait(bar, (ph & bit) ? 1u : 0u));
+            ph ^= bit;
+            return ok;
+        };
+        // what both threads of a row say, to each other
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(pair + g * 4 + quad);
+            return phase(pair + g * 4 + quad, P_X);
+        };
+        auto read_back = [&]() -> bool {           // the first group has read what was lent
+            if (!(ph & LENT))
+                return true;
+            ph ^= LENT;
+            return __all_sync(FULL_MASK, wait(ml_free, (ph & P_ML) ? 0u : 1u));
+        };
+        for (uint32_t item = 0; take(item); ++item) {
             const bool both = shared_rows(c);
             const int row = both ? r : g * TILE_M + r;
             const bool warp_live = (both ? quad * 32 : g * TILE_M + quad * 32) < c.rows;
             const int pos = c.first + (row >> p.lg_g);
-            // keys in sight: up to `lim`, from `from`, and of the new ones those of `bits`
+            // keys in sight: up to `lim`, from `from`, and of the new ones those of the row's bits
             const bool valid = row < c.rows;
             const int lim = !valid ? -1 : p.visible ? c.len - 1 : pos;
             const int from = p.rules.window > 0 ? pos - p.rules.window + 1 : 0;
-            uint64_t bits = ~(uint64_t)0;
-            if (p.visible && valid)
-                bits = p.visible[c.tok + (row >> p.lg_g)];
+            const uint64_t *bits_at = p.visible + (p.visible && valid ? c.tok + (row >> p.lg_g) : 0);
             const int nt = group_tiles(p, c, g);
             float m_run = -INFINITY, l_run = 0.0f, rs = p.scale_log2;
+            if constexpr (C::QCONV) {
+                // bf16 q over an 8-bit cache becomes fp16 times a power of two a row (K's
+                // codes are fp16; what a row's small values lose is below 2^-38 of its
+                // largest), in place
+                // (a group whose rows the other converts waits all the same: its arrival
+                // counts once an item)
+                if (!__all_sync(FULL_MASK, wait(q_raw, item)))
+                    goto softmax_done;
+                if (!both || g == 0) {
+                    const int e = halve_row<D>(sQ + (both ? 0 : g) * C::Q_BYTES, r);
+                    rs *= pow2_f32(e);
+                    if (both)
+                        q_exp[(item & 1) * TILE_M + r] = (signed char)e;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full);
+            }
             for (int s = 0; s < nt; ++s) {
                 const int tb = (c.t0 + tile_at(c, g, s)) * TILE;       // the tile's first key
-                if (!__all_sync(FULL_MASK, wait(&s_full[g], sc)))
+                if (!phase(&s_full[g], P_S))
                     goto softmax_done;
-                ++sc;
                 tc_fence_after();
                 if (warp_live) {
-                    if (C::QCONV && s == 0)
-                        rs = p.scale_log2 * pow2_f32(q_exp[(item & 1) * C::ROWS + row]);
+                    if (C::QCONV && both && g == 1 && s == 0)
+                        rs *= pow2_f32(q_exp[(item & 1) * TILE_M + r]);
                     // a tile's factor for eight keys: an 8-bit cache's scale, the row's
                     // own and the softmax's
-                    const float4 *fac = reinterpret_cast<const float4 *>(
-                        k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 16);
+                    const float *fac = k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 16 + hf * (CW / 8);
                     const bool masked = __any_sync(
                         FULL_MASK, tb + TILE - 1 > lim || tb < from ||
                                        (p.visible && tb + TILE > c.base));
+                    // keys in sight among the 32 from this thread's c0 on
                     auto in_sight = [&](int c0) -> uint32_t {
-                        const int k0 = tb + c0, u = lim - k0, d = from - k0;
+                        const int k0 = tb + hf * CW + c0, u = lim - k0, d = from - k0;
                         uint32_t w = u >= 31 ? 0xffffffffu : u < 0 ? 0u : (2u << u) - 1u;
                         if (d > 0)
                             w = d < 32 ? w & (0xffffffffu << d) : 0u;
                         if (p.visible) {
                             const int e = k0 - c.base;
+                            const uint64_t bits = *bits_at;
                             if (e >= 0)
                                 w &= e < 64 ? (uint32_t)(bits >> e) : 0u;
                             else if (e > -32)
@@ -444,41 +588,56 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         return w;
                     };
-                    float v[TILE];
-                    tmem_ld64(t_s, v);
-                    tmem_ld64(t_s + 64, v + 64);
-                    if (masked) {
+                    // half of the scores, then their maximum under way while the others come
+                    constexpr int HW = CW / 2;
+                    float v[CW], mx = -INFINITY;
+                    auto highest = [&](int h0) {
+                        if (masked) {
 #pragma unroll
-                        for (int c0 = 0; c0 < TILE; c0 += 32) {
-                            const uint32_t w = in_sight(c0);
+                            for (int c0 = h0; c0 < h0 + HW; c0 += 32) {
+                                const uint32_t w = in_sight(c0);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[c0 + j] = (w >> j) & 1 ? v[c0 + j] : -INFINITY;
-                        }
-                    }
-                    // the row's maximum, in the base-2 logarithm's units
-                    float mx = -INFINITY;
-                    if constexpr (F8) {
-#pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k) {
-                            const float4 f = fac[k];
-                            const float ff[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float *x = v + 32 * k + 8 * e;
-                                mx = fmaxf(mx, max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
-                                                     fmaxf(x[6], x[7])) * (ff[e] * rs));
+                                for (int j = 0; j < 32; ++j)
+                                    v[c0 + j] = (w >> j) & 1 ? v[c0 + j] : -INFINITY;
                             }
                         }
-                    } else {
-                        float t[4] = {v[0], v[1], v[2], v[3]};
+                        if constexpr (F8) {
 #pragma unroll
-                        for (int j = 4; j < TILE; j += 8)
+                            for (int k = h0 / 8; k < (h0 + HW) / 8; ++k) {
+                                const float *x = v + 8 * k;
+                                mx = fmaxf(mx, max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
+                                                     fmaxf(x[6], x[7])) * (fac[k] * rs));
+                            }
+                        } else {
+                            const float *x = v + h0;
+                            float t[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                t[k] = j + 4 + k < TILE ? max3f(t[k], v[j + k], v[j + 4 + k])
-                                                        : fmaxf(t[k], v[j + k]);
-                        mx = max3f(fmaxf(t[0], t[1]), t[2], t[3]) * rs;   // scale > 0: the maximum commutes
+                            for (int j = 4; j < HW; j += 8)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    t[k] = j + 4 < HW ? max3f(t[k], x[j + k], x[j + 4 + k])
+                                                      : fmaxf(t[k], x[j + k]);
+                            mx = fmaxf(mx, max3f(fmaxf(t[0], t[1]), t[2], t[3]));
+                        }
+                    };
+                    tmem_ld_begin<HW>(t_s, v);
+                    tmem_ld_end<HW>(v);
+                    tmem_ld_begin<HW>(t_s + HW, v + HW);
+                    highest(0);
+                    tmem_ld_end<HW>(v + HW);
+                    highest(HW);
+                    if (!F8)
+                        mx *= rs;                  // scale > 0: the maximum commutes
+                    if constexpr (HT == 2) {
+                        // the row's maximum; and from here on both have read their scores, over
+                        // which the weights go.  (The slots' last reader was done before
+                        // this S was multiplied, but at an item's end.)
+                        if (!read_back())
+                            goto softmax_done;
+                        st_shared(mine, mx);
+                        if (!meet())
+                            goto softmax_done;
+                        mx = fmaxf(mx, ld_shared(other));
                     }
                     // The running maximum moves only when a score exceeds it by more than
                     // 2^8 (or is the first in sight): below that the weights stay <= 2^8, and
@@ -490,101 +649,122 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                     // O is idle here: the P V of the previous tile finished before this S
                     // did, the next one waits for p_full
                     if (s > 0 && __any_sync(FULL_MASK, move)) {
+                        // (rare: few registers rather than few loads)
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            float o[32];
-                            tmem_ld32(t_o + c0, o);
+                        for (int c0 = 0; c0 < OW; c0 += 8) {
+                            float o[8];
+                            uint32_t w[8];
+                            tmem_ld_begin<8>(t_o + c0, o);
+                            tmem_ld_end<8>(o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                o[j] *= corr;
-                            tmem_st32(t_o + c0, o);
+                            for (int j = 0; j < 8; ++j)
+                                w[j] = __float_as_uint(o[j] * corr);
+                            tmem_st8(t_o + c0, w);
                         }
                     }
                     // weights, their sum, and P over the S columns: 16-bit pairs of keys in
-                    // columns 0..63, their low parts (where there are two) in 64..127
+                    // columns 0..63, their low parts (where there are two) in 64..127.
+                    // Eight keys a step: the exponents of one eight, the exponentials of the
+                    // one before, the rounding and summing of the one before that, so that the
+                    // three units that they run on work at once.
                     const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_new == -INFINITY ? 0.0f : m_new);
                     float sum[4] = {};
+                    using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
+                    constexpr int E = CW / 8;
+                    uint32_t w[8], wl[8];
 #pragma unroll
-                    for (int c0 = 0; c0 < TILE; c0 += 32) {
-                        float *x = v + c0;
-                        if constexpr (F8) {
-                            const float4 f = fac[c0 / 32];
-                            const float ff[4] = {f.x * rs, f.y * rs, f.z * rs, f.w * rs};
+                    for (int i = 0; i < E + 2; ++i) {
+                        if (i < E) {
+                            const float f = F8 ? fac[i] * rs : rs;
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2)
-                                fma2_bc(x[j], x[j + 1], ff[j / 8], off);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2)
-                                fma2_bc(x[j], x[j + 1], rs, off);
+                            for (int j = 8 * i; j < 8 * i + 8; j += 2)
+                                fma2_bc(v[j], v[j + 1], f, off);
                         }
+                        if (i >= 1 && i <= E)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[j] = ex2_approx(x[j]);
-                        using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
-                        uint32_t w[16];
+                            for (int j = 8 * i - 8; j < 8 * i; ++j)
+                                v[j] = ex2_approx(v[j]);
+                        if (i >= 2) {
+                            const float *x = v + 8 * i - 16;
+                            const int at = (i - 2) % 2 * 4;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = pack2<PT>(x[2 * j], x[2 * j + 1]);
-                        tmem_st16(t_s + c0 / 2, w);
-                        if constexpr (C::SPLIT) {
-                            uint32_t wl[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float2 h = unpack2<PT>(w[j]);
-                                float r0 = x[2 * j], r1 = x[2 * j + 1];
-                                add2(r0, r1, -h.x, -h.y);
-                                wl[j] = pack2<PT>(r0, r1);
+                            for (int j = 0; j < 4; ++j) {
+                                w[at + j] = pack2<PT>(x[2 * j], x[2 * j + 1]);
+                                if constexpr (C::SPLIT) {
+                                    const float2 h = unpack2<PT>(w[at + j]);
+                                    float r0 = x[2 * j], r1 = x[2 * j + 1];
+                                    add2(r0, r1, -h.x, -h.y);
+                                    wl[at + j] = pack2<PT>(r0, r1);
+                                }
                             }
-                            tmem_st16(t_s + TILE / 2 + c0 / 2, wl);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            add2(sum[0], sum[1], x[j], x[j + 1]);
-                            add2(sum[2], sum[3], x[j + 2], x[j + 3]);
+                            add2(sum[0], sum[1], x[0], x[1]);
+                            add2(sum[2], sum[3], x[2], x[3]);
+                            add2(sum[0], sum[1], x[4], x[5]);
+                            add2(sum[2], sum[3], x[6], x[7]);
+                            if ((i - 2) % 2 == 1) {
+                                const uint32_t col = t_p + (i - 2) / 2 * 8;
+                                tmem_st8(col, w);
+                                if constexpr (C::SPLIT)
+                                    tmem_st8(col + TILE / 2, wl);
+                            }
                         }
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    tc_fence_before();
                 }
-                tc_fence_before();
-                mbar_arrive(&p_full[g]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[g]);
             }
             gt += c.t1 - c.t0;
             // ---- the piece's end
+            c = pieces[item % C::PIECES];          // (read again: not kept through the tiles)
             const int nt1 = both ? group_tiles(p, c, 1) : 0;
+            if (nt > 0 && !phase(&o_done[g], P_O))
+                goto softmax_done;
+            if (HT == 2 && warp_live && nt > 0) {  // (nothing reads the maxima any more: O is done)
+                if (!read_back())
+                    goto softmax_done;
+                st_shared(mine, l_run);
+                if (!meet())
+                    goto softmax_done;
+                l_run += ld_shared(other);
+                if (!meet())                       // both have read
+                    goto softmax_done;
+            }
             if (g == 1 && both) {
                 // hand the state over: the first group reads it and this group's O
-                if (nt1 > 0) {
-                    ++oc;                          // (the first group waits for it)
-                    if (mc > 0 && !__all_sync(FULL_MASK, wait(ml_free, mc - 1)))
+                if (nt > 0) {
+                    if (!read_back())
                         goto softmax_done;
-                    ml[r] = make_float2(m_run, l_run);
-                    mbar_arrive(ml_full);
-                    ++mc;
+                    if (hf == 0)
+                        xm[C::XM1 + r] = l_run;
+                    if (hf == HT - 1)
+                        xm[C::XM1 + TILE_M + r] = m_run;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(ml_full);
+                    ph ^= P_ML | LENT;
                 }
+                done(item);
                 continue;
             }
-            if (nt > 0) {
-                if (!__all_sync(FULL_MASK, wait(&o_done[g], oc)))
-                    goto softmax_done;
-                ++oc;
-            }
             float a0 = 1.0f, a1 = 0.0f;
-            const uint32_t of1 = done1;
-            if (g == 0 && group_tiles(p, c, 1) > 0)
-                ++done1;
+            if (g == 0 && !both)
+                ph ^= P_O1;                        // (the second group waits for its own)
             if (nt1 > 0) {
-                if (!__all_sync(FULL_MASK, wait(&o_done[1], of1) && wait(ml_full, mc)))
+                if (!phase(&o_done[1], P_O1) || !phase(ml_full, P_ML))
                     goto softmax_done;
-                ++mc;
-                const float2 o = ml[r];
-                mbar_arrive(ml_free);
-                const float m = fmaxf(m_run, o.x);
+                const float l1 = xm[C::XM1 + r], n1 = xm[C::XM1 + TILE_M + r];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(ml_free);
+                const float m = fmaxf(m_run, n1);
                 a0 = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m);
-                a1 = o.x == -INFINITY ? 0.0f : ex2_approx(o.x - m);
+                a1 = n1 == -INFINITY ? 0.0f : ex2_approx(n1 - m);
                 m_run = m;
-                l_run = l_run * a0 + o.y * a1;
+                l_run = l_run * a0 + l1 * a1;
             }
             tc_fence_after();
             if (warp_live) {
@@ -596,11 +776,11 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 }
                 T *out = static_cast<T *>(p.out) +
                          ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
-                          (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D;
-                float *part = p.part + ((int64_t)blockIdx.x * 2 + (c.kind == 2)) * C::ROWS * (D + 2) +
-                              (int64_t)row * D;
+                          (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + hf * OW;
+                float *states = p.part + ((int64_t)blockIdx.x * 2 + (c.kind == 2)) * C::ROWS * (D + 2);
+                float *part = states + (int64_t)row * D + hf * OW;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < OW; c0 += 32) {
                     float o[32];
                     if (nt > 0) {
                         tmem_ld32(t_o + c0, o);
@@ -631,20 +811,23 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                                 make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                 }
-                if (c.kind && valid)
-                    *reinterpret_cast<float2 *>(part - (int64_t)row * D + C::ROWS * D + 2 * row) =
-                        make_float2(m_run, l_run);
+                if (c.kind && valid && hf == 0)
+                    *reinterpret_cast<float2 *>(states + C::ROWS * D + 2 * row) = make_float2(m_run, l_run);
             }
             tc_fence_before();
-            if (nt > 0)
-                mbar_arrive(&o_free[g]);
-            if (nt1 > 0)
-                mbar_arrive(&o_free[1]);
+            __syncwarp();
+            if (lane == 0) {
+                if (nt > 0)
+                    mbar_arrive(&o_free[g]);
+                if (nt1 > 0)
+                    mbar_arrive(&o_free[1]);
+            }
+            done(item);
         }
     softmax_done:;
-    } else if (!F8 && warp < 10) {
-        // ================= K (warp 8) or V (warp 9) tiles of a 16-bit cache
-        const bool is_k = warp == 8;
+    } else if (!F8 && warp < W0 + 2) {
+        // ================= K or V tiles of a 16-bit cache
+        const bool is_k = warp == W0;
         unsigned char *ring = is_k ? sK : sV;
         uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
         const CUtensorMap *tm = is_k ? &p.tm_k : &p.tm_v;
@@ -654,7 +837,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         constexpr int DCH = D / 8;
         uint32_t gt = 0;
         bool ok = true;
-        while (ok && walk.next(p, c)) {
+        for (uint32_t item = 0; ok && take(item); ++item) {
             const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
             // lane j: rows [j R, j R + R) of a tile, from one block; ids a tile ahead
             auto block_of = [&](int t) -> int32_t {
@@ -680,22 +863,17 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 }
                 const int y = pos0 & (p.block_size - 1);
                 unsigned char *dst = ring + slot * C::KV_BYTES;
-                // By tensor copies, a 64-column panel each, where the box starts on a
-                // 1024-byte boundary and holds no row past the last in sight (those are
-                // zeros: P is 0 there, but 0 times a stale NaN is not); by 16-byte
-                // copies otherwise.
+                // By a tensor copy where the box is of whole groups of eight rows and
+                // holds no row past the last in sight (those are zeros: P is 0 there, but 0
+                // times a stale NaN is not); by 16-byte copies otherwise.
                 const bool by_tma = inbox && R >= 8 && (z == oob || pos0 + R - 1 <= c.last);
                 const unsigned tma_boxes = __popc(__ballot_sync(FULL_MASK, by_tma));
                 const unsigned cp_boxes = __ballot_sync(FULL_MASK, inbox && !by_tma);
                 if (lane == 0)
                     mbar_arrive_expect_tx(&full[slot], tma_boxes * (uint32_t)R * 2u * D);
                 __syncwarp();
-                if (by_tma) {
-#pragma unroll
-                    for (int pn = 0; pn < D / 64; ++pn)
-                        tma_load_3d(dst + pn * (TILE * 128) + lane * R * 128, tm, pn * 64, y, z,
-                                    &full[slot]);
-                }
+                if (by_tma)
+                    tma_load_5d(dst + lane * R * 2 * D, tm, y >> 3, z, &full[slot]);
                 if (cp_boxes) {
                     for (unsigned m = cp_boxes; m; m &= m - 1) {
                         const int bx = __ffs(m) - 1;
@@ -705,9 +883,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                             const int rr = bx * R + idx / DCH, ch = idx % DCH;
                             const bool in = zb != oob && t * TILE + rr <= c.last;
                             const int64_t row = in ? (int64_t)zb * p.block_size + yb + idx / DCH : 0;
-                            cp_async16(dst + (ch >> 3) * (TILE * 128) + rr * 128 +
-                                           (((ch & 7) ^ (rr & 7)) << 4),
-                                       cache + row * D + ch * 8, in);
+                            cp_async16(dst + tile_off<D>(rr, ch), cache + row * D + ch * 8, in);
                         }
                     }
                     cp_async_commit();
@@ -718,16 +894,17 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 if (lane == 0)
                     mbar_arrive(&full[slot]);
             }
+            done(item);
         }
-    } else if (F8 && warp < 12) {
+    } else if (F8 && warp < W0 + 4) {
         // ================= convert tiles of an 8-bit cache: K's codes to fp16, V's values
         // to bf16; this warp's 32 rows
-        const int w0 = (warp - 8) * 32;
+        const int w0 = (warp - W0) * 32;
         constexpr int LPR = D / 16, RPI = 32 / LPR;            // lanes a row of codes, rows at once
         const int rr = lane / LPR, j = lane % LPR;
         uint32_t gt = 0;
         bool ok = true;
-        while (ok && walk.next(p, c)) {
+        for (uint32_t item = 0; ok && take(item); ++item) {
             for (int t = c.t0; t < c.t1 && ok; ++t, ++gt) {
                 const int slot = gt % NS, rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
 #pragma unroll 1
@@ -756,19 +933,18 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         // chunks 2j and 2j + 1 of the row; the second panel's lanes write their odd one
                         // first, so that eight lanes' stores fall on all banks
-                        const int c0 = 2 * j, odd = (c0 >> 3) & 1;
-                        unsigned char *base = dst + (c0 >> 3) * (TILE * 128) + row * 128;
-                        const int k0 = (c0 & 7) + odd, k1 = (c0 & 7) + 1 - odd;
-                        *reinterpret_cast<uint4 *>(base + ((k0 ^ (row & 7)) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4 *>(base + ((k1 ^ (row & 7)) << 4)) = odd ? lo : hi;
+                        const int odd = j >> 2;
+                        *reinterpret_cast<uint4 *>(dst + tile_off<D>(row, 2 * j + odd)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4 *>(dst + tile_off<D>(row, 2 * j + 1 - odd)) = odd ? lo : hi;
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(&full[slot]);
                     mbar_arrive(&re[rs]);
                 }
             }
+            done(item);
         }
-    } else if (F8 && warp == 13) {
+    } else if (F8 && warp == W0 + 5) {
         // ================= bring codes and scales of an 8-bit cache
         const int R = p.box_rows, nbox = TILE / R, H = p.num_kv_heads;
         int lg_r = 0;
@@ -776,9 +952,9 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             ++lg_r;
         const unsigned char *kc = static_cast<const unsigned char *>(p.k_cache);
         const unsigned char *vc = static_cast<const unsigned char *>(p.v_cache);
-        uint32_t gt = 0, item = 0;
+        uint32_t gt = 0;
         bool ok = true;
-        while (ok && walk.next(p, c)) {
+        for (uint32_t item = 0; ok && take(item); ++item) {
             const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
             auto block_of = [&](int t) -> int32_t {
                 const int pos0 = t * TILE + lane * R;
@@ -792,20 +968,6 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             // ids two tiles ahead, scales one: each is a trip to memory after the other
             int32_t blk1 = block_of(c.t0), blk2 = block_of(c.t0 + 1);
             float ks1 = scale_of(blk1, p.k_scales), vs1 = scale_of(blk1, p.v_scales);
-            if (!C::QCONV) {
-                if (item > 0 && !(ok = __all_sync(FULL_MASK, wait(q_empty, item - 1))))
-                    break;
-                const int halves = shared_rows(c) ? 1 : 2;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, halves * (uint32_t)C::Q_BYTES);
-                    for (int hh = 0; hh < halves; ++hh)
-                        for (int pn = 0; pn < D / 64; ++pn)
-                            tma_load_3d(sQ + hh * C::Q_BYTES + pn * (TILE_M * 128), &p.tm_q, pn * 64,
-                                        c.h << p.lg_g, c.tok + hh * (TILE_M >> p.lg_g), q_full);
-                }
-                __syncwarp();
-            }
-            ++item;
             for (int t = c.t0; t < c.t1; ++t, ++gt) {
                 const int rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
                 const uint32_t turn = gt / (NR ? NR : 1);
@@ -850,161 +1012,144 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                     bulk_g2s(smem + C::OFF_RV + rs * C::RAW_BYTES + lane * R * D, vc + src, R * D,
                              &vr_full[rs]);
             }
+            done(item);
         }
-    } else if (!F8 && warp == 10) {
-        // ================= q, once the previous item's last S has read its own
-        for (uint32_t item = 0; walk.next(p, c); ++item) {
-            if (item > 0 && !__all_sync(FULL_MASK, wait(q_empty, item - 1)))
-                break;
-            const int halves = shared_rows(c) ? 1 : 2;
+    } else if (warp == C::W_FEED) {
+        // ================= hand out the share's pieces, one ahead of the one whose q is
+        // brought (once the last S before has read its own)
+        Walk walk;
+        walk.start(p, places);
+        __syncwarp();                              // (places lie where the pieces go)
+        auto hand_out = [&](uint32_t item, bool more) -> bool {
+            const uint32_t slot = item % C::PIECES;
+            if (item >= C::PIECES &&
+                !__all_sync(FULL_MASK, wait(&pc_empty[slot], item / C::PIECES + 1)))
+                return false;
+            if (!more)
+                c.kind = -1;
             if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, halves * (uint32_t)C::Q_BYTES);
+                pieces[slot] = c;
+                mbar_arrive(&pc_full[slot]);
+            }
+            return true;
+        };
+        bool more = walk.next(p, c), ok = hand_out(0, more);
+        for (uint32_t item = 0; ok && more; ++item) {
+            const int halves = shared_rows(c) ? 1 : 2, y = c.h << p.lg_g, z = c.tok;
+            more = walk.next(p, c);
+            if (!(ok = hand_out(item + 1, more)))
+                break;
+            if (item > 0 && !(ok = __all_sync(FULL_MASK, wait(q_empty, item - 1))))
+                break;
+            if (lane == 0) {
+                uint64_t *bar = C::QCONV ? q_raw : q_full;
+                mbar_arrive_expect_tx(bar, halves * (uint32_t)C::Q_BYTES);
                 for (int hh = 0; hh < halves; ++hh)
                     for (int pn = 0; pn < D / 64; ++pn)
-                        tma_load_3d(sQ + hh * C::Q_BYTES + pn * (TILE_M * 128), &p.tm_q, pn * 64,
-                                    c.h << p.lg_g, c.tok + hh * (TILE_M >> p.lg_g), q_full);
+                        tma_load_3d(sQ + hh * C::Q_BYTES + pn * (TILE_M * 128), &p.tm_q, pn * 64, y,
+                                    z + hh * (TILE_M >> p.lg_g), bar);
             }
             __syncwarp();
-        }
-    } else if (C::QCONV && warp >= 14) {
-        // ================= bf16 q over an 8-bit cache: fp16 times a power of two a row
-        // (K's codes are fp16; what a row's small values lose is below 2^-38 of its largest)
-        constexpr int LPR = D / 8, RPI = 32 / LPR;              // lanes a row, rows at once
-        const int rr = lane / LPR, ch = lane % LPR;
-        for (uint32_t item = 0; walk.next(p, c); ++item) {
-            if (item > 0 && !__all_sync(FULL_MASK, wait(q_empty, item - 1)))
-                break;
-            const int rows = shared_rows(c) ? TILE_M : 2 * TILE_M, half = rows / 2;
-            const int r0 = (warp - 14) * half;
-            constexpr int U = 4;
-#pragma unroll 1
-            for (int i0 = 0; i0 < half; i0 += U * RPI) {
-                uint4 w[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int row = r0 + i0 + u * RPI + rr;
-                    const T *src = static_cast<const T *>(p.q) +
-                                   ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
-                                    (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + ch * 8;
-                    w[u] = row < c.rows ? *reinterpret_cast<const uint4 *>(src)
-                                        : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int row = r0 + i0 + u * RPI + rr;
-                    uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-                    uint32_t top = 0;                          // magnitudes order as their bits
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top = max(top, max(v[k] << 16 & 0x7fffffffu, v[k] & 0x7fff0000u));
-#pragma unroll
-                    for (int m = 1; m < LPR; m <<= 1)
-                        top = max(top, __shfl_xor_sync(FULL_MASK, top, m));
-                    // the largest in [2^14, 2^15)
-                    const int e = max((int)(top >> 23) - 127 - 14, -126);
-                    const float f = pow2_f32(-e);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = pack2<__half>(bf16lo(v[k]) * f, bf16hi(v[k]) * f);
-                    *reinterpret_cast<uint4 *>(sQ + (row >> 7) * C::Q_BYTES + (ch >> 3) * (TILE_M * 128) +
-                                               (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
-                    if (ch == 0)
-                        q_exp[(item & 1) * C::ROWS + row] = (signed char)e;
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(q_full);
         }
     } else if (warp == C::W_MMA) {
         // ================= MMA issue: the warp walks as one, an elected lane issues
         // S = Q K^T, both K-major, and O += P V, P in tensor memory, V MN-major; all of them
         // 128-byte swizzled panels of 64 channels: a row every 128 bytes, eight rows 1024
-        // bytes, the next panel 128 rows on.  A step of 16 along the contraction is 32 bytes
-        // into S's rows, 16 rows of V.
-        constexpr uint32_t PANEL = TILE * 128;
+        // bytes.  q's next panel is 128 rows on; K's and V's lies beside the first, and the next
+        // eight rows behind both.  A step of 16 along the contraction is 32 bytes into S's
+        // rows, 16 rows of V.
+        constexpr uint32_t Q_PANEL = TILE_M * 128;
         const uint32_t idesc_s = umma_idesc(BF && !F8 ? 1u : 0u, 0u, TILE);
         const uint32_t idesc_o = umma_idesc(C::PBF ? 1u : 0u, 1u, D);
         const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0), el = elect_lane();
         const uint64_t dq = umma_desc_sw128(smem_addr(sQ), 16, 1024);
-        const uint64_t dk = umma_desc_sw128(smem_addr(sK), 16, 1024);
-        const uint64_t dv = umma_desc_sw128(smem_addr(sV), PANEL, 1024);
+        const uint64_t dk = umma_desc_sw128(smem_addr(sK), 16, C::GROUP8);
+        const uint64_t dv = umma_desc_sw128(smem_addr(sV), 1024, C::GROUP8);
         const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
-        const uint32_t s_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+        const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
         uint32_t gt = 0, pc[2] = {0, 0}, ofc[2] = {0, 0};
         bool o_used[2] = {false, false};
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(FULL_MASK, wait(bar, parity));
         };
-        for (uint32_t item = 0; ok && walk.next(p, c); ++item) {
+        for (uint32_t item = 0; ok && take(item); ++item) {
             const bool both = shared_rows(c);
             const int nt[2] = {group_tiles(p, c, 0), group_tiles(p, c, 1)};
             int s_left = nt[0] + nt[1];
-            auto issue_s = [&](int g, int s) -> bool {
-                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
-                if (!wait_all(&k_full[slot], k / NS))
-                    return false;
-                tc_fence_after();
+            auto k_here = [&](int g, int s) -> bool {
+                const uint32_t k = gt + tile_at(c, g, s);
+                return wait_all(&k_full[k % NS], k / NS);
+            };
+            auto issue_s = [&](int g, int s) {
+                const uint32_t slot = (gt + tile_at(c, g, s)) % NS;
                 const uint32_t kb = k_lo + slot * (C::KV_BYTES / 16);
                 const uint32_t qb = q_lo + (both ? 0 : g) * (C::Q_BYTES / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t step = (ks / 4) * (PANEL / 16) + (ks % 4) * 2;
-                    umma_f16_elected(el, tm + g * C::GROUP_COLS, qb + step, s_hi, kb + step, s_hi,
-                                     idesc_s, ks > 0 ? 1u : 0u);
+                    umma_f16_elected(el, tm + g * C::GROUP_COLS,
+                                     qb + (ks / 4) * (Q_PANEL / 16) + (ks % 4) * 2, q_hi,
+                                     kb + (ks / 4) * (1024 / 16) + (ks % 4) * 2, k_hi, idesc_s,
+                                     ks > 0 ? 1u : 0u);
                 }
+                umma_commit_elected(el, &s_full[g]);
                 if (both || g == 1)                // the tile's last reader
                     umma_commit_elected(el, &k_empty[slot]);
-                umma_commit_elected(el, &s_full[g]);
                 if (--s_left == 0)
                     umma_commit_elected(el, q_empty);
-                return true;
             };
+            // O += P V of tile s, and S of tile s + 1 (whose K is waited for first: once P
+            // is there, nothing but the MMAs is left to do)
             auto issue_pv = [&](int g, int s) -> bool {
                 const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
-                if (!wait_all(&v_full[slot], k / NS) || !wait_all(&p_full[g], pc[g]))
+                const bool more = s + 1 < nt[g];
+                if (!wait_all(&v_full[slot], k / NS) || (more && !k_here(g, s + 1)))
                     return false;
-                ++pc[g];
                 if (s == 0 && o_used[g]) {         // the softmax threads have read O out
                     if (!wait_all(&o_free[g], ofc[g]))
                         return false;
                     ++ofc[g];
                 }
-                tc_fence_after();
                 const uint32_t vb = v_lo + slot * (C::KV_BYTES / 16), base = tm + g * C::GROUP_COLS;
+                if (!wait_all(&p_full[g], pc[g]))
+                    return false;
+                tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < TILE / 16; ++ks) {
-                    umma_f16_ta_elected(el, base + TILE, base + 8 * ks, vb + ks * (2048 / 16), v_hi,
+                    umma_f16_ta_elected(el, base + TILE, base + 8 * ks, vb + ks * (C::GROUP8 / 8), v_hi,
                                         idesc_o, s > 0 || ks > 0 ? 1u : 0u);
                     if (C::SPLIT)
                         umma_f16_ta_elected(el, base + TILE, base + TILE / 2 + 8 * ks,
-                                            vb + ks * (2048 / 16), v_hi, idesc_o, 1u);
+                                            vb + ks * (C::GROUP8 / 8), v_hi, idesc_o, 1u);
                 }
+                ++pc[g];
                 if (both || g == 1)
                     umma_commit_elected(el, &v_empty[slot]);
+                if (more)
+                    issue_s(g, s + 1);
                 return true;
             };
             if (!(ok = wait_all(q_full, item)))
                 break;
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-                if (ok && nt[g] > 0)
-                    ok = issue_s(g, 0);
+                if (ok && nt[g] > 0 && (ok = k_here(g, 0))) {
+                    tc_fence_after();
+                    issue_s(g, 0);
+                }
             const int steps = max(nt[0], nt[1]);
             for (int s = 0; s < steps && ok; ++s)
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (!ok || s >= nt[g] || !(ok = issue_pv(g, s)))
                         continue;
-                    if (s + 1 < nt[g]) {
-                        ok = issue_s(g, s + 1);
-                    } else {
+                    if (s + 1 == nt[g]) {
                         umma_commit_elected(el, &o_done[g]);
                         o_used[g] = true;
                     }
                 }
             gt += c.t1 - c.t0;
+            done(item);
         }
         // every issued MMA has finished before tensor memory is released
         umma_commit_elected(el, drain);
@@ -1126,6 +1271,27 @@ bool encode_q_map(CUtensorMap *m, const pkv_pool *pool, const void *q, int num_q
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A cache [NB][Hkv][bs][D] of 16-bit elements as the tensor {64, 8, D / 64, bs / 8, NB * Hkv}:
+// columns of a panel, rows of a group of eight, panels, groups, (block, KV head)s; boxes of
+// up to 128 rows.  (Blocks of 4 rows have no group and no map.)
+bool encode_tile_map(CUtensorMap *m, const pkv_pool *pool, const void *base, bool bf)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint64_t D = pool->head_dim, groups = pool->block_size / 8;
+    const cuuint64_t dims[5] = {64, 8, D / 64, groups,
+                                (cuuint64_t)pool->num_blocks * pool->num_kv_heads};
+    const cuuint64_t strides[4] = {D * 2, 128, D * 16, (cuuint64_t)pool->block_size * D * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64),
+                               (cuuint32_t)std::min<cuuint64_t>(groups, TILE / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool F8, bool BF, int NQ>
 int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
 {
@@ -1206,8 +1372,8 @@ int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num
     p.rules.tree = visible != nullptr;
     if (!encode_q_map(&p.tm_q, pool, q, num_q_heads, num_tokens, G, bf))
         return PKV_ERR_CUDA;
-    if (!f8 && (!encode_cache_map(&p.tm_k, pool, k_cache, p.box_rows) ||
-                !encode_cache_map(&p.tm_v, pool, v_cache, p.box_rows)))
+    if (!f8 && pool->block_size >= 8 && (!encode_tile_map(&p.tm_k, pool, k_cache, bf) ||
+                                         !encode_tile_map(&p.tm_v, pool, v_cache, bf)))
         return PKV_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 #define PKV_CHUNK(D, F)                                                                          \

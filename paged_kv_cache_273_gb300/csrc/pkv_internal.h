@@ -229,11 +229,6 @@ int launch_prefix_merge(const pkv_pool *pool, const int32_t *seq_prefix, float *
 // through the runtime; null if unavailable.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
-// A cache [NB][Hkv][bs][D] of 16-bit elements as the tensor that the tcgen05 kernels
-// read: {D, bs, NB * Hkv}, boxes of 64 x rows x 1, 128-byte swizzle (prefill.cu).
-// False if the encoder is unavailable or refuses.
-bool encode_cache_map(CUtensorMap *m, const pkv_pool *pool, const void *base, int rows);
-
 // A cache [NB][Hkv][bs][row_bytes] (row_bytes 128 or 256) as the tensor the
 // decode kernel's swizzled tile copies read: bytes in 128-byte segments,
 // {128, bs, NB * Hkv} or {128, 2, bs, NB * Hkv}, boxes of 16 rows, 128-byte

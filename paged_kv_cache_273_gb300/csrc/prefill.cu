@@ -726,8 +726,6 @@ int launch_prefill_t(const pkv_pool *pool, const PrefillParams &prm, int max_q_l
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-}  // namespace
-
 // A cache [num_blocks][num_kv_heads][block_size][D] of 16-bit elements as the
 // 3-D tensor {D, block_size, num_blocks * num_kv_heads}, boxes of 64 x rows x 1.
 bool encode_cache_map(CUtensorMap *m, const pkv_pool *pool, const void *base, int rows)
@@ -747,6 +745,8 @@ bool encode_cache_map(CUtensorMap *m, const pkv_pool *pool, const void *base, in
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+}  // namespace
 
 int launch_prefill(const pkv_pool *pool, const void *q, int num_q_heads, const void *k_cache,
                    const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
