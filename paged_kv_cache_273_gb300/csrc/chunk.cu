@@ -60,7 +60,7 @@ struct ChunkParams {
 
 // Warps: the softmax groups; then, of a 16-bit cache, one that brings K, one V, one that
 // hands out the pieces and brings their q, and one that issues the MMAs; of an 8-bit cache,
-// four that convert tiles, the MMA warp, one that brings tiles, and the one for pieces and q.
+// four that bring and convert tiles, the MMA warp, and the one for pieces and q.
 template <int D, bool F8, bool BF, int NQ>
 struct Cfg {
     // threads a row of a softmax group: two halve the time from S to P, which the tensor cores
@@ -69,37 +69,31 @@ struct Cfg {
     static constexpr int ROWS = NQ * TILE_M;
     static constexpr int Q_BYTES = TILE_M * D * 2;                       // one half
     static constexpr int KV_BYTES = TILE * D * 2;
-    static constexpr int RAW_BYTES = TILE * D;
     // ring slots: what shared memory holds
-    static constexpr int NS = D == 64 ? 4 : (!F8 && NQ == 1 ? 3 : 2);
-    static constexpr int NR = !F8 ? 0 : (NQ == 1 ? 2 : 1) * (D == 64 ? 2 : 1);
-    // tiles' scales: K's are read until the tile's softmax, when NS + 1 tiles more may be
-    // converted and NR brought
-    static constexpr int RING = D == 64 ? 16 : 8;
-    static_assert(RING >= NS + NR + 2, "scales in use");
+    static constexpr int NS = D == 64 ? 4 : NQ == 1 ? 3 : 2;
+    // tiles' scales of K: read until the tile's softmax, when NS + 1 tiles more may be there
+    static constexpr int RING = 8;
+    static_assert(RING >= NS + 2, "scales in use");
     static constexpr int OFF_K = NQ * Q_BYTES;
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
-    static constexpr int OFF_RK = OFF_V + NS * KV_BYTES;
-    static constexpr int OFF_RV = OFF_RK + NR * RAW_BYTES;
-    static constexpr int OFF_ML = OFF_RV + NR * RAW_BYTES;               // what threads of a row exchange
+    static constexpr int OFF_ML = OFF_V + NS * KV_BYTES;                 // what threads of a row exchange
     static constexpr int XM1 = HT == 2 ? 2 * TILE_M : 0;                 // the second group's slots
-    static constexpr int OFF_SC = OFF_ML + (XM1 + 2 * TILE_M) * 4;       // [RING][16] K, then V scales
-    static constexpr int OFF_LIVE = OFF_SC + (F8 ? RING * 16 * 8 : 0);   // [RING]
-    static constexpr int OFF_QE = OFF_LIVE + (F8 ? RING * 4 : 0);        // q's exponents, two pieces
+    static constexpr int OFF_SC = OFF_ML + (XM1 + 2 * TILE_M) * 4;       // [RING][16] scales of K
+    static constexpr int OFF_QE = OFF_SC + (F8 ? RING * 16 * 4 : 0);     // q's exponents, two pieces
     static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * TILE_M : 0);
     static constexpr int PIECES = 4;                                     // handed out and not done
-    static constexpr int NBARS = 4 * NS + 4 * NR + 8 + 6 + 2 * PIECES + (HT == 2 ? 8 : 0);
+    static constexpr int NBARS = 4 * NS + 8 + 6 + 2 * PIECES + (HT == 2 ? 8 : 0);
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;                 // tensor memory's address, flag, pieces
     static constexpr int SMEM_BYTES = OFF_MISC + 224;
     static constexpr int W0 = 8 * HT;                                    // the first warp behind the groups
-    static constexpr int W_MMA = F8 ? W0 + 4 : W0 + 3, W_FEED = F8 ? W0 + 6 : W0 + 2;
-    static constexpr int CONSUMERS = W0 + (F8 ? 6 : 3);                  // warps that a piece is for
+    static constexpr int W_MMA = F8 ? W0 + 4 : W0 + 3, W_FEED = F8 ? W0 + 5 : W0 + 2;
+    static constexpr int CONSUMERS = W0 + (F8 ? 5 : 3);                  // warps that a piece is for
     static constexpr bool QCONV = F8 && BF;
     static constexpr int NT = 32 * (F8 ? W0 + 8 : W0 + 4);
     // registers of a thread: at launch, and from then on in the softmax groups, the four
     // warps behind them, and the last four (the shares add up to what was there at launch)
     static constexpr int REGS = F8 ? 128 : 168;
-    static constexpr int R_SOFT = F8 ? 184 : 216, R_2 = F8 ? 80 : 72, R_3 = F8 ? 64 : 0;
+    static constexpr int R_SOFT = F8 ? 152 : 216, R_2 = F8 ? 128 : 72, R_3 = F8 ? 80 : 0;
     static_assert(2 * HT * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
     static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
     // a K or V tile: eight rows of 64 columns are 1024 bytes (128-byte swizzled); a group of
@@ -175,8 +169,8 @@ struct Walk {
         chunk::span(p.rules, q, at.rt, c.first, c.last);
         c.b = at.b;
         c.h = at.h;
-        c.tok = q0 + at.rt * p.rules.tpr;
-        c.rows = min(p.rules.tpr, q.n - at.rt * p.rules.tpr) << p.lg_g;
+        c.tok = q0 + (at.rt << p.rules.lg_tpr);
+        c.rows = min(1 << p.rules.lg_tpr, q.n - (at.rt << p.rules.lg_tpr)) << p.lg_g;
         c.sight = p.rules.window > 0 ? max(0, c.first - p.rules.window + 1) : 0;
         c.base = q.L - q.n;
         c.len = q.L;
@@ -231,68 +225,74 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.batch + NT - 1) / NT;
     const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        Seq q;
-        int q0;
-        bool bad;
-        if (Walk::lengths(p, b, q, q0, bad))
-            mine += p.num_kv_heads * chunk::cost_of(p.rules, q);
-        if (bad && blockIdx.x == 0)
-            atomicOr(p.err, PKV_EBIT_SEQLEN);
-    }
-    int64_t upto = mine;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const int64_t o = __shfl_up_sync(FULL_MASK, upto, m);
-        if (lane >= m)
-            upto += o;
-    }
-    if (lane == 31)
-        sums[warp] = upto;
-    __syncthreads();
-    int64_t before = 0, U = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp)
-            before += sums[w];
-        U += sums[w];
-    }
-    const int n = chunk::shares(U, gridDim.x), c = blockIdx.x;
-    if (c == 0 && tid == 0)
-        p.places[0] = U > 0 ? n : 0;
-    if (U == 0 || c >= n)
-        return false;
-    if (tid == 0 && c + 1 == n) {
-        Place e{};
-        e.b = p.batch;
-        places[1] = e;
-    }
+    const int c = blockIdx.x;
+    int64_t mine = 0, before = 0, U = 0;
+    int n = 0;
+    // first the sum, then the two places (one body, for the instruction cache's sake)
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        int64_t x = chunk::share_start(U, n, c + k) - (before + upto - mine);
-        if (x < 0 || x >= mine)
+    for (int k = -1; k < 2; ++k) {
+        int64_t x = k < 0 ? -1 : chunk::share_start(U, n, c + k) - before;
+        if (k >= 0 && (x < 0 || x >= mine))
             continue;
+        int64_t sum = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             Seq q;
             int q0;
             bool bad;
-            if (!Walk::lengths(p, b, q, q0, bad))
-                continue;
-            const int64_t cost = p.num_kv_heads * chunk::cost_of(p.rules, q);
-            if (x < cost) {
-                places[k] = chunk::place_in(p.rules, q, b, x);
-                break;
+            if (Walk::lengths(p, b, q, q0, bad)) {
+                const int64_t one = chunk::cost_of(p.rules, q), cost = p.num_kv_heads * one;
+                if (k >= 0 && x < sum + cost) {
+                    places[k] = chunk::place_in(p.rules, q, b, x - sum, one);
+                    break;
+                }
+                sum += cost;
             }
-            x -= cost;
+            if (bad && k < 0 && c == 0)
+                atomicOr(p.err, PKV_EBIT_SEQLEN);
+        }
+        if (k >= 0)
+            continue;
+        mine = sum;
+        int64_t upto = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t o = __shfl_up_sync(FULL_MASK, upto, m);
+            if (lane >= m)
+                upto += o;
+        }
+        if (lane == 31)
+            sums[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp)
+                before += sums[w];
+            U += sums[w];
+        }
+        before += upto - mine;
+        n = chunk::shares(U, gridDim.x);
+        if (c == 0 && tid == 0)
+            p.places[0] = U > 0 ? n : 0;
+        if (U == 0 || c >= n)
+            return false;
+        if (tid == 0 && c + 1 == n) {
+            Place e{};
+            e.b = p.batch;
+            places[1] = e;
         }
     }
     __syncthreads();
     if (tid == 0) {
-        int32_t *o = p.places + 8 + 8 * c;
-        o[0] = places[0].b;
-        o[1] = places[0].h;
-        o[2] = places[0].rt;
-        o[3] = places[0].split;
+        // for the joining: the item, whether the share starts within it, its first token and
+        // its rows
+        const Place &a = places[0];
+        Seq q;
+        int q0;
+        bool bad;
+        Walk::lengths(p, a.b, q, q0, bad);
+        int4 *o = reinterpret_cast<int4 *>(p.places + 8 + 8 * c);
+        o[0] = make_int4(a.b, a.h, a.rt, a.split);
+        o[1] = make_int4(q0 + (a.rt << p.rules.lg_tpr), min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, 0, 0);
     }
     return true;
 }
@@ -321,12 +321,28 @@ __device__ __forceinline__ void codes_to_half(const uint4 &w, uint4 &lo, uint4 &
 __device__ __forceinline__ uint32_t scaled_bf16(uint32_t h2, float f)
 {
     const float2 x = half2_to_float2(h2);
-    return pack2<__nv_bfloat16>(x.x * f, x.y * f);
+    float a = x.x, b = x.y;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f));
+    return pack2<__nv_bfloat16>(a, b);
 }
 __device__ __forceinline__ uint4 scaled_bf16(const uint4 &h, float f)
 {
     return make_uint4(scaled_bf16(h.x, f), scaled_bf16(h.y, f), scaled_bf16(h.z, f),
                       scaled_bf16(h.w, f));
+}
+
+// Chunks 2j and 2j + 1 of a row: the second panel's lanes write their odd one first, so that
+// eight lanes' stores fall on all banks.
+template <int D>
+__device__ __forceinline__ void put_chunks(unsigned char *tile, int row, int j, const uint4 &lo,
+                                           const uint4 &hi)
+{
+    const int odd = j >> 2;
+    *reinterpret_cast<uint4 *>(tile + tile_off<D>(row, 2 * j + odd)) = odd ? hi : lo;
+    *reinterpret_cast<uint4 *>(tile + tile_off<D>(row, 2 * j + 1 - odd)) = odd ? lo : hi;
 }
 
 // V of an 8-bit cache enters P V times 2^-16 (its largest values are beyond bf16's
@@ -336,6 +352,8 @@ constexpr int V_SHIFT = 16;
 // fp16 weights are taken times 2^7: the running maximum moves when a score is 2^8 above it, so
 // they stay below 2^15, and weights down to 2^-21 of the largest keep all their bits.
 constexpr float P_SHIFT = 7.0f;
+
+constexpr uint32_t WAIT_TRIES = 1u << 22;
 
 __device__ __forceinline__ float ld_shared(uint32_t addr)
 {
@@ -380,17 +398,18 @@ __device__ __forceinline__ int halve_row(unsigned char *q, int r)
     return e;
 }
 
-// The part of a wait that is not over at once; a call, for the instruction cache's sake.
+// Wait for a phase, with a limit in tries (each lets the warp sleep for a while: some
+// seconds in all), or until another role has given up.  Kept short: it is inlined at every wait.
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                     unsigned int *err)
+                                        unsigned int *err)
 {
-    if (mbar_wait_bounded(bar, parity, abort_flag))
-        return true;
-    if (!*abort_flag) {
-        *abort_flag = 1;
-        atomicOr(err, PKV_EBIT_TIMEOUT);
-    }
-    return false;
+    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries)
+        if ((tries & 1023) == 0 && (*abort_flag || tries >= WAIT_TRIES)) {
+            *abort_flag = 1;
+            atomicOr(err, PKV_EBIT_TIMEOUT);
+            return false;
+        }
+    return true;
 }
 
 template <int D, bool F8, bool BF, int NQ>
@@ -398,13 +417,12 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     chunk_kernel(const __grid_constant__ ChunkParams p)
 {
     using C = Cfg<D, F8, BF, NQ>;
-    constexpr int NS = C::NS, NR = C::NR, W0 = C::W0;
+    constexpr int NS = C::NS, W0 = C::W0;
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
     float *xm = reinterpret_cast<float *>(smem + C::OFF_ML);
-    float *k_sc = reinterpret_cast<float *>(smem + C::OFF_SC), *v_sc = k_sc + C::RING * 16;
-    uint32_t *live_of = reinterpret_cast<uint32_t *>(smem + C::OFF_LIVE);
+    float *k_sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     signed char *q_exp = reinterpret_cast<signed char *>(smem + C::OFF_QE);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
@@ -412,7 +430,6 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     uint64_t *q_full = o_free + 2, *q_empty = q_full + 1, *ml_full = q_empty + 1, *ml_free = ml_full + 1;
     uint64_t *drain = ml_free + 1, *pair = drain + 1;
     uint64_t *pc_full = pair + (C::HT == 2 ? 8 : 0), *pc_empty = pc_full + C::PIECES, *q_raw = pc_empty + C::PIECES;
-    uint64_t *kr_full = q_raw + 1, *kr_empty = kr_full + NR, *vr_full = kr_empty + NR, *vr_empty = vr_full + NR;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Place *places = reinterpret_cast<Place *>(smem + C::OFF_MISC + 16);
@@ -426,16 +443,10 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         return;
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&k_full[i], F8 ? 128 : 2);
+            mbar_init(&k_full[i], F8 ? 4 : 2);
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], F8 ? 128 : 2);
+            mbar_init(&v_full[i], F8 ? 4 : 2);
             mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < NR; ++i) {
-            mbar_init(&kr_full[i], 1);
-            mbar_init(&kr_empty[i], 128);
-            mbar_init(&vr_full[i], 1);
-            mbar_init(&vr_empty[i], 128);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&s_full[g], 1);
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     const uint32_t tmem = *tmem_slot;
     // A wait that runs out raises the error bit once and makes every role stop.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return mbar_try_wait(bar, parity & 1) || wait_on(bar, parity & 1, abort_flag, p.err);
+        return wait_on(bar, parity & 1, abort_flag, p.err);
     };
     Piece c;
     // The item-th piece, and when this warp is done with it.
@@ -499,7 +510,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         const int g = warp / (4 * HT), hf = warp / 4 % HT, quad = warp & 3;
         const int r = quad * 32 + lane;
         const uint32_t t_row = tmem + g * C::GROUP_COLS + ((uint32_t)(quad * 32) << 16);
-        const uint32_t t_s = t_row + hf * CW, t_p = t_row + hf * (CW / 2);
+        const uint32_t t_s = t_row + hf * CW;
         const uint32_t t_o = t_row + TILE + hf * OW;
         const uint32_t mine = smem_addr(xm + g * C::XM1 + hf * TILE_M + r);
         const uint32_t other = HT == 2 ? mine ^ (TILE_M * 4) : mine;
@@ -588,28 +599,31 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         return w;
                     };
-                    // half of the scores, then their maximum under way while the others come
-                    constexpr int HW = CW / 2;
-                    float v[CW], mx = -INFINITY;
-                    auto highest = [&](int h0) {
+                    // Half of the scores, then their maximum under way while the others come;
+                    // over an 8-bit cache (whose conversion wants registers too) one half
+                    // after the other, the second one read again for its weights.
+                    constexpr int HW = CW / 2, KEEP = F8 ? HW : CW;
+                    float v[KEEP], mx = -INFINITY;
+                    auto hide = [&](float *x, int h0) {
                         if (masked) {
 #pragma unroll
-                            for (int c0 = h0; c0 < h0 + HW; c0 += 32) {
-                                const uint32_t w = in_sight(c0);
+                            for (int c0 = 0; c0 < HW; c0 += 32) {
+                                const uint32_t w = in_sight(h0 + c0);
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
-                                    v[c0 + j] = (w >> j) & 1 ? v[c0 + j] : -INFINITY;
+                                    x[c0 + j] = (w >> j) & 1 ? x[c0 + j] : -INFINITY;
                             }
                         }
+                    };
+                    auto highest = [&](const float *x, int h0) {
                         if constexpr (F8) {
 #pragma unroll
-                            for (int k = h0 / 8; k < (h0 + HW) / 8; ++k) {
-                                const float *x = v + 8 * k;
-                                mx = fmaxf(mx, max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
-                                                     fmaxf(x[6], x[7])) * (fac[k] * rs));
-                            }
+                            for (int k = 0; k < HW / 8; ++k)
+                                mx = fmaxf(mx, max3f(max3f(x[8 * k], x[8 * k + 1], x[8 * k + 2]),
+                                                     max3f(x[8 * k + 3], x[8 * k + 4], x[8 * k + 5]),
+                                                     fmaxf(x[8 * k + 6], x[8 * k + 7])) *
+                                                   (fac[h0 / 8 + k] * rs));
                         } else {
-                            const float *x = v + h0;
                             float t[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                             for (int j = 4; j < HW; j += 8)
@@ -620,14 +634,26 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                             mx = fmaxf(mx, max3f(fmaxf(t[0], t[1]), t[2], t[3]));
                         }
                     };
-                    tmem_ld_begin<HW>(t_s, v);
-                    tmem_ld_end<HW>(v);
-                    tmem_ld_begin<HW>(t_s + HW, v + HW);
-                    highest(0);
-                    tmem_ld_end<HW>(v + HW);
-                    highest(HW);
-                    if (!F8)
+                    if constexpr (F8) {
+                        tmem_ld_begin<HW>(t_s + HW, v);
+                        tmem_ld_end<HW>(v);
+                        hide(v, HW);
+                        highest(v, HW);
+                        tmem_ld_begin<HW>(t_s, v);
+                        tmem_ld_end<HW>(v);
+                        hide(v, 0);
+                        highest(v, 0);
+                    } else {
+                        tmem_ld_begin<HW>(t_s, v);
+                        tmem_ld_end<HW>(v);
+                        tmem_ld_begin<HW>(t_s + HW, v + KEEP - HW);
+                        hide(v, 0);
+                        highest(v, 0);
+                        tmem_ld_end<HW>(v + KEEP - HW);
+                        hide(v + KEEP - HW, HW);
+                        highest(v + KEEP - HW, HW);
                         mx *= rs;                  // scale > 0: the maximum commutes
+                    }
                     if constexpr (HT == 2) {
                         // the row's maximum; and from here on both have read their scores, over
                         // which the weights go.  (The slots' last reader was done before
@@ -662,52 +688,63 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                             tmem_st8(t_o + c0, w);
                         }
                     }
-                    // weights, their sum, and P over the S columns: 16-bit pairs of keys in
-                    // columns 0..63, their low parts (where there are two) in 64..127.
-                    // Eight keys a step: the exponents of one eight, the exponentials of the
-                    // one before, the rounding and summing of the one before that, so that the
-                    // three units that they run on work at once.
+                    // weights, their sum, and P over the S columns: of each 64 keys the 16-bit
+                    // pairs in 32 columns, their low parts (where there are two) in the next
+                    // 32.  Eight keys a step: the exponents of one eight, the exponentials of
+                    // the one before, the rounding and summing of the one before that, so
+                    // that the three units that they run on work at once.
                     const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_new == -INFINITY ? 0.0f : m_new);
                     float sum[4] = {};
                     using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
-                    constexpr int E = CW / 8;
-                    uint32_t w[8], wl[8];
+                    auto weigh = [&](float *x, int h0, uint32_t t_p) {   // 64 keys
+                        constexpr int E = 64 / 8;
+                        uint32_t w[8], wl[8];
 #pragma unroll
-                    for (int i = 0; i < E + 2; ++i) {
-                        if (i < E) {
-                            const float f = F8 ? fac[i] * rs : rs;
+                        for (int i = 0; i < E + 2; ++i) {
+                            if (i < E) {
+                                const float f = F8 ? fac[h0 / 8 + i] * rs : rs;
 #pragma unroll
-                            for (int j = 8 * i; j < 8 * i + 8; j += 2)
-                                fma2_bc(v[j], v[j + 1], f, off);
-                        }
-                        if (i >= 1 && i <= E)
+                                for (int j = 8 * i; j < 8 * i + 8; j += 2)
+                                    fma2_bc(x[j], x[j + 1], f, off);
+                            }
+                            if (i >= 1 && i <= E)
 #pragma unroll
-                            for (int j = 8 * i - 8; j < 8 * i; ++j)
-                                v[j] = ex2_approx(v[j]);
-                        if (i >= 2) {
-                            const float *x = v + 8 * i - 16;
-                            const int at = (i - 2) % 2 * 4;
+                                for (int j = 8 * i - 8; j < 8 * i; ++j)
+                                    x[j] = ex2_approx(x[j]);
+                            if (i >= 2) {
+                                const float *y = x + 8 * i - 16;
+                                const int at = (i - 2) % 2 * 4;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                w[at + j] = pack2<PT>(x[2 * j], x[2 * j + 1]);
-                                if constexpr (C::SPLIT) {
-                                    const float2 h = unpack2<PT>(w[at + j]);
-                                    float r0 = x[2 * j], r1 = x[2 * j + 1];
-                                    add2(r0, r1, -h.x, -h.y);
-                                    wl[at + j] = pack2<PT>(r0, r1);
+                                for (int j = 0; j < 4; ++j) {
+                                    w[at + j] = pack2<PT>(y[2 * j], y[2 * j + 1]);
+                                    if constexpr (C::SPLIT) {
+                                        const float2 h = unpack2<PT>(w[at + j]);
+                                        float r0 = y[2 * j], r1 = y[2 * j + 1];
+                                        add2(r0, r1, -h.x, -h.y);
+                                        wl[at + j] = pack2<PT>(r0, r1);
+                                    }
+                                }
+                                add2(sum[0], sum[1], y[0], y[1]);
+                                add2(sum[2], sum[3], y[2], y[3]);
+                                add2(sum[0], sum[1], y[4], y[5]);
+                                add2(sum[2], sum[3], y[6], y[7]);
+                                if ((i - 2) % 2 == 1) {
+                                    const uint32_t col = t_p + (i - 2) / 2 * 8;
+                                    tmem_st8(col, w);
+                                    if constexpr (C::SPLIT)
+                                        tmem_st8(col + 32, wl);
                                 }
                             }
-                            add2(sum[0], sum[1], x[0], x[1]);
-                            add2(sum[2], sum[3], x[2], x[3]);
-                            add2(sum[0], sum[1], x[4], x[5]);
-                            add2(sum[2], sum[3], x[6], x[7]);
-                            if ((i - 2) % 2 == 1) {
-                                const uint32_t col = t_p + (i - 2) / 2 * 8;
-                                tmem_st8(col, w);
-                                if constexpr (C::SPLIT)
-                                    tmem_st8(col + TILE / 2, wl);
-                            }
                         }
+                    };
+                    weigh(v, 0, t_s);
+                    if constexpr (F8) {
+                        tmem_ld_begin<HW>(t_s + HW, v);
+                        tmem_ld_end<HW>(v);
+                        hide(v, HW);
+                        weigh(v, HW, t_s + HW);
+                    } else if constexpr (HT == 1) {
+                        weigh(v + KEEP - HW, HW, t_s + HW);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -897,120 +934,121 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             done(item);
         }
     } else if (F8 && warp < W0 + 4) {
-        // ================= convert tiles of an 8-bit cache: K's codes to fp16, V's values
-        // to bf16; this warp's 32 rows
-        const int w0 = (warp - W0) * 32;
-        constexpr int LPR = D / 16, RPI = 32 / LPR;            // lanes a row of codes, rows at once
+        // ================= bring and convert tiles of an 8-bit cache: K's codes to fp16, V's
+        // values to bf16; this warp's 32 rows.  The codes come through registers, a tile ahead
+        // (through shared memory they would take as much of its bandwidth again as the
+        // converted tiles' writing does, and room for a slot of each).
+        const int w0 = (warp - W0) * 32, H = p.num_kv_heads;
+        constexpr int LPR = D / 16, RPI = 32 / LPR, NI = 32 / RPI;  // lanes a row, rows at once
         const int rr = lane / LPR, j = lane % LPR;
-        uint32_t gt = 0;
-        bool ok = true;
-        for (uint32_t item = 0; ok && take(item); ++item) {
-            for (int t = c.t0; t < c.t1 && ok; ++t, ++gt) {
-                const int slot = gt % NS, rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
-                    uint64_t *rf = kv ? vr_full : kr_full, *re = kv ? vr_empty : kr_empty;
-                    uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
-                    if (!(ok = __all_sync(FULL_MASK, wait(&rf[rs], gt / (NR ? NR : 1)) &&
-                                                         (gt < NS || wait(&empty[slot], gt / NS + 1)))))
-                        break;
-                    const unsigned char *raw = smem + (kv ? C::OFF_RV : C::OFF_RK) + rs * C::RAW_BYTES;
-                    unsigned char *dst = (kv ? sV : sK) + slot * C::KV_BYTES;
-                    const uint32_t live = live_of[ring];
-#pragma unroll 4
-                    for (int i = 0; i < 32; i += RPI) {
-                        const int row = w0 + i + rr;
-                        const bool in = ((live >> (row >> 3)) & 1) && t * TILE + row <= c.last;
-                        uint4 w = *reinterpret_cast<const uint4 *>(raw + row * D + j * 16);
-                        if (!in)
-                            w = make_uint4(0u, 0u, 0u, 0u);
-                        uint4 lo, hi;
-                        codes_to_half(w, lo, hi);
-                        if (kv) {
-                            const float f = v_sc[ring * 16 + (row >> 3)];
-                            lo = scaled_bf16(lo, f);
-                            hi = scaled_bf16(hi, f);
-                        }
-                        // chunks 2j and 2j + 1 of the row; the second panel's lanes write their odd one
-                        // first, so that eight lanes' stores fall on all banks
-                        const int odd = j >> 2;
-                        *reinterpret_cast<uint4 *>(dst + tile_off<D>(row, 2 * j + odd)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4 *>(dst + tile_off<D>(row, 2 * j + 1 - odd)) = odd ? lo : hi;
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(&full[slot]);
-                    mbar_arrive(&re[rs]);
-                }
-            }
-            done(item);
-        }
-    } else if (F8 && warp == W0 + 5) {
-        // ================= bring codes and scales of an 8-bit cache
-        const int R = p.box_rows, nbox = TILE / R, H = p.num_kv_heads;
-        int lg_r = 0;
-        while ((1 << lg_r) < R)
-            ++lg_r;
         const unsigned char *kc = static_cast<const unsigned char *>(p.k_cache);
         const unsigned char *vc = static_cast<const unsigned char *>(p.v_cache);
         uint32_t gt = 0;
         bool ok = true;
         for (uint32_t item = 0; ok && take(item); ++item) {
             const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
+            // lane q < 4: the block of rows w0 + 8 q .. w0 + 8 q + 7 of a tile (-2: none in sight)
             auto block_of = [&](int t) -> int32_t {
-                const int pos0 = t * TILE + lane * R;
-                return lane < nbox && t < c.t1 && pos0 <= c.last && pos0 + R > c.sight
+                const int pos0 = t * TILE + w0 + 8 * (lane & 3);
+                const int first = pos0 & ~(p.block_size - 1);
+                return t < c.t1 && pos0 <= c.last && first + p.block_size > c.sight
                            ? table[pos0 >> p.bs_log2] : -2;
             };
-            // a block's scales: of a block that is not there, anything finite
-            auto scale_of = [&](int32_t blk, const float *s) -> float {
-                return blk >= 0 && blk < p.num_blocks ? s[(int64_t)blk * H + c.h] : 1.0f;
-            };
-            // ids two tiles ahead, scales one: each is a trip to memory after the other
-            int32_t blk1 = block_of(c.t0), blk2 = block_of(c.t0 + 1);
-            float ks1 = scale_of(blk1, p.k_scales), vs1 = scale_of(blk1, p.v_scales);
-            for (int t = c.t0; t < c.t1; ++t, ++gt) {
-                const int rs = gt % (NR ? NR : 1), ring = gt & (C::RING - 1);
-                const uint32_t turn = gt / (NR ? NR : 1);
-                const int32_t blk = blk1;
-                const float ks = ks1, vs = vs1;
-                blk1 = blk2;
-                ks1 = scale_of(blk1, p.k_scales);
-                vs1 = scale_of(blk1, p.v_scales);
-                blk2 = block_of(t + 2);
-                const bool good = blk >= 0 && blk < p.num_blocks;
-                if (blk != -2 && !good)
-                    atomicOr(p.err, PKV_EBIT_BLOCK);
-                const unsigned boxes = __ballot_sync(FULL_MASK, good);
-                const int pos0 = t * TILE + lane * R;
-                const int64_t src = good ? (((int64_t)blk * H + c.h) * p.block_size +
-                                            (pos0 & (p.block_size - 1))) * D : 0;
-                // entry i of the tile's scales: keys 8 i .. 8 i + 7
-                const int bx = (8 * (lane & 15)) >> lg_r;
-                const float ke = __shfl_sync(FULL_MASK, ks, bx), ve = __shfl_sync(FULL_MASK, vs, bx);
-                const uint32_t live = __ballot_sync(FULL_MASK, lane < 16 && ((boxes >> bx) & 1));
-                if (!(ok = __all_sync(FULL_MASK, (int)gt < NR || wait(&kr_empty[rs], turn + 1))))
-                    break;
-                if (lane < 16) {
-                    k_sc[ring * 16 + lane] = pow2_f32(block_exponent(ke));
-                    v_sc[ring * 16 + lane] = pow2_f32(block_exponent(ve) - V_SHIFT);
+            auto good = [&](int32_t blk) { return blk >= 0 && blk < p.num_blocks; };
+            // Where a tile's rows are (a row's 16 bytes of this lane, by groups of eight rows),
+            // and which of them count: the others, of no block or behind the last key, come
+            // from block 0 and become zeros (a load under a condition would be waited for
+            // where the condition ends).
+            int64_t at[4];
+            auto find = [&](int t, int32_t ids) -> uint32_t {
+                uint32_t count = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int32_t blk = __shfl_sync(FULL_MASK, ids, q);
+                    const int pos = t * TILE + w0 + 8 * q + rr;
+                    const bool in = good(blk);
+                    at[q] = (((int64_t)(in ? blk : 0) * H + c.h) * p.block_size +
+                             (pos & (p.block_size - 1))) * D + j * 16;
+                    // (the rows of group q: pos, and with four lanes' rows at once pos + 4)
+#pragma unroll
+                    for (int u = 0; u < NI / 4; ++u)
+                        count |= in && pos + 4 * u <= c.last ? 1u << (q * (NI / 4) + u) : 0u;
                 }
-                if (lane == 0)
-                    live_of[ring] = live;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&kr_full[rs], __popc(boxes) * (uint32_t)(R * D));
-                __syncwarp();
-                if (good)
-                    bulk_g2s(smem + C::OFF_RK + rs * C::RAW_BYTES + lane * R * D, kc + src, R * D,
-                             &kr_full[rs]);
-                if (!(ok = __all_sync(FULL_MASK, (int)gt < NR || wait(&vr_empty[rs], turn + 1))))
+                return count;
+            };
+            uint4 kd[NI], vd[NI];
+            auto bring = [&](uint4 (&d)[NI], const unsigned char *cache) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    d[i] = *reinterpret_cast<const uint4 *>(cache + at[i / (NI / 4)] +
+                                                            i % (NI / 4) * 4 * D);
+            };
+            auto clear = [&](uint4 (&d)[NI], uint32_t count) {
+                if (__all_sync(FULL_MASK, count == (1u << NI) - 1u))
+                    return;
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (!((count >> i) & 1))
+                        d[i] = make_uint4(0u, 0u, 0u, 0u);
+            };
+            int32_t ids = block_of(c.t0), ids1 = block_of(c.t0 + 1);
+            float ks = 1.0f, vs = 1.0f;            // lane q's blocks' scales
+            auto scales = [&](int32_t blk) {
+                const int64_t sc = (int64_t)(good(blk) ? blk : 0) * H + c.h;
+                ks = p.k_scales[sc];
+                vs = p.v_scales[sc];
+                if (blk != -2 && !good(blk))
+                    atomicOr(p.err, PKV_EBIT_BLOCK);
+            };
+            uint32_t count1 = find(c.t0, ids);
+            scales(ids);
+            bring(kd, kc);
+            bring(vd, vc);
+#pragma unroll 1
+            for (int t = c.t0; t < c.t1; ++t, ++gt) {
+                const int slot = gt % NS;
+                const uint32_t count = count1;
+                const float kf = pow2_f32(block_exponent(ks));
+                const float vf = pow2_f32(block_exponent(vs) - V_SHIFT);
+                ids = ids1;
+                ids1 = block_of(t + 2);
+                scales(ids);
+                count1 = find(t + 1, ids);
+                // K
+                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&k_empty[slot], gt / NS + 1))))
                     break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&vr_full[rs], __popc(boxes) * (uint32_t)(R * D));
+                if (lane < 4)
+                    k_sc[(gt & (C::RING - 1)) * 16 + (w0 >> 3) + lane] = kf;
+                unsigned char *dst = sK + slot * C::KV_BYTES;
+                clear(kd, count);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    uint4 lo, hi;
+                    codes_to_half(kd[i], lo, hi);
+                    put_chunks<D>(dst, w0 + i * RPI + rr, j, lo, hi);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (good)
-                    bulk_g2s(smem + C::OFF_RV + rs * C::RAW_BYTES + lane * R * D, vc + src, R * D,
-                             &vr_full[rs]);
+                if (lane == 0)
+                    mbar_arrive(&k_full[slot]);
+                bring(kd, kc);
+                // V
+                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&v_empty[slot], gt / NS + 1))))
+                    break;
+                dst = sV + slot * C::KV_BYTES;
+                clear(vd, count);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const float f = __shfl_sync(FULL_MASK, vf, (i * RPI) >> 3);
+                    uint4 lo, hi;
+                    codes_to_half(vd[i], lo, hi);
+                    put_chunks<D>(dst, w0 + i * RPI + rr, j, scaled_bf16(lo, f), scaled_bf16(hi, f));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&v_full[slot]);
+                bring(vd, vc);
             }
             done(item);
         }
@@ -1067,87 +1105,82 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         const uint64_t dv = umma_desc_sw128(smem_addr(sV), 1024, C::GROUP8);
         const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
         const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
-        uint32_t gt = 0, pc[2] = {0, 0}, ofc[2] = {0, 0};
-        bool o_used[2] = {false, false};
+        // per group, a bit each: the parity of p_full's and o_free's next phase, and whether O
+        // holds an earlier piece's
+        uint32_t gt = 0, p_par = 0, of_par = 0, used = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(FULL_MASK, wait(bar, parity));
         };
         for (uint32_t item = 0; ok && take(item); ++item) {
             const bool both = shared_rows(c);
-            const int nt[2] = {group_tiles(p, c, 0), group_tiles(p, c, 1)};
-            int s_left = nt[0] + nt[1];
-            auto k_here = [&](int g, int s) -> bool {
-                const uint32_t k = gt + tile_at(c, g, s);
-                return wait_all(&k_full[k % NS], k / NS);
-            };
-            auto issue_s = [&](int g, int s) {
-                const uint32_t slot = (gt + tile_at(c, g, s)) % NS;
-                const uint32_t kb = k_lo + slot * (C::KV_BYTES / 16);
-                const uint32_t qb = q_lo + (both ? 0 : g) * (C::Q_BYTES / 16);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    umma_f16_elected(el, tm + g * C::GROUP_COLS,
-                                     qb + (ks / 4) * (Q_PANEL / 16) + (ks % 4) * 2, q_hi,
-                                     kb + (ks / 4) * (1024 / 16) + (ks % 4) * 2, k_hi, idesc_s,
-                                     ks > 0 ? 1u : 0u);
-                }
-                umma_commit_elected(el, &s_full[g]);
-                if (both || g == 1)                // the tile's last reader
-                    umma_commit_elected(el, &k_empty[slot]);
-                if (--s_left == 0)
-                    umma_commit_elected(el, q_empty);
-            };
-            // O += P V of tile s, and S of tile s + 1 (whose K is waited for first: once P
-            // is there, nothing but the MMAs is left to do)
-            auto issue_pv = [&](int g, int s) -> bool {
-                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
-                const bool more = s + 1 < nt[g];
-                if (!wait_all(&v_full[slot], k / NS) || (more && !k_here(g, s + 1)))
-                    return false;
-                if (s == 0 && o_used[g]) {         // the softmax threads have read O out
-                    if (!wait_all(&o_free[g], ofc[g]))
-                        return false;
-                    ++ofc[g];
-                }
-                const uint32_t vb = v_lo + slot * (C::KV_BYTES / 16), base = tm + g * C::GROUP_COLS;
-                if (!wait_all(&p_full[g], pc[g]))
-                    return false;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < TILE / 16; ++ks) {
-                    umma_f16_ta_elected(el, base + TILE, base + 8 * ks, vb + ks * (C::GROUP8 / 8), v_hi,
-                                        idesc_o, s > 0 || ks > 0 ? 1u : 0u);
-                    if (C::SPLIT)
-                        umma_f16_ta_elected(el, base + TILE, base + TILE / 2 + 8 * ks,
-                                            vb + ks * (C::GROUP8 / 8), v_hi, idesc_o, 1u);
-                }
-                ++pc[g];
-                if (both || g == 1)
-                    umma_commit_elected(el, &v_empty[slot]);
-                if (more)
-                    issue_s(g, s + 1);
-                return true;
-            };
+            const int nt0 = group_tiles(p, c, 0), nt1 = group_tiles(p, c, 1);
+            int s_left = nt0 + nt1;
             if (!(ok = wait_all(q_full, item)))
                 break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                if (ok && nt[g] > 0 && (ok = k_here(g, 0))) {
-                    tc_fence_after();
-                    issue_s(g, 0);
+            // Step s of a group: O += P V of its tile s, and S of its tile s + 1, whose K is
+            // waited for first: once P is there, nothing but the MMAs is left to do.  One
+            // copy of the code for both groups and the first S: the instruction cache is
+            // what roles that run long straight code at the same time contend for.
+#pragma unroll 1
+            for (int i = -2; i < 2 * max(nt0, nt1) && ok; ++i) {
+                const int g = i & 1, s = i >> 1, nt = g ? nt1 : nt0;
+                if (s >= nt)
+                    continue;
+                const bool more = s + 1 < nt;
+                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
+                const uint32_t k1 = gt + tile_at(c, g, s + 1), slot1 = k1 % NS;
+                if ((s >= 0 && !wait_all(&v_full[slot], k / NS)) ||
+                    (more && !wait_all(&k_full[slot1], k1 / NS))) {
+                    ok = false;
+                    break;
                 }
-            const int steps = max(nt[0], nt[1]);
-            for (int s = 0; s < steps && ok; ++s)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (!ok || s >= nt[g] || !(ok = issue_pv(g, s)))
-                        continue;
-                    if (s + 1 == nt[g]) {
-                        umma_commit_elected(el, &o_done[g]);
-                        o_used[g] = true;
+                const uint32_t base = tm + g * C::GROUP_COLS;
+                if (s >= 0) {
+                    if (s == 0) {
+                        // the softmax threads have read an earlier piece's O out
+                        if ((used >> g) & 1) {
+                            if (!(ok = wait_all(&o_free[g], (of_par >> g) & 1)))
+                                break;
+                            of_par ^= 1u << g;
+                        }
+                        used |= 1u << g;
                     }
+                    if (!(ok = wait_all(&p_full[g], (p_par >> g) & 1)))
+                        break;
+                    p_par ^= 1u << g;
+                    tc_fence_after();
+                    const uint32_t vb = v_lo + slot * (C::KV_BYTES / 16);
+#pragma unroll
+                    for (int ks = 0; ks < TILE / 16; ++ks) {
+                        const uint32_t pa = base + ks / 4 * 64 + ks % 4 * 8;
+                        umma_f16_ta_elected(el, base + TILE, pa, vb + ks * (C::GROUP8 / 8), v_hi,
+                                            idesc_o, s > 0 || ks > 0 ? 1u : 0u);
+                        if (C::SPLIT)
+                            umma_f16_ta_elected(el, base + TILE, pa + 32, vb + ks * (C::GROUP8 / 8),
+                                                v_hi, idesc_o, 1u);
+                    }
+                    if (both || g == 1)            // the tile's last reader
+                        umma_commit_elected(el, &v_empty[slot]);
+                    if (!more)
+                        umma_commit_elected(el, &o_done[g]);
                 }
+                if (more) {
+                    tc_fence_after();
+                    const uint32_t kb = k_lo + slot1 * (C::KV_BYTES / 16);
+                    const uint32_t qb = q_lo + (both ? 0 : g) * (C::Q_BYTES / 16);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_f16_elected(el, base, qb + (ks / 4) * (Q_PANEL / 16) + (ks % 4) * 2, q_hi,
+                                         kb + (ks / 4) * (1024 / 16) + (ks % 4) * 2, k_hi, idesc_s,
+                                         ks > 0 ? 1u : 0u);
+                    umma_commit_elected(el, &s_full[g]);
+                    if (both || g == 1)
+                        umma_commit_elected(el, &k_empty[slot1]);
+                    if (--s_left == 0)
+                        umma_commit_elected(el, q_empty);
+                }
+            }
             gt += c.t1 - c.t0;
             done(item);
         }
@@ -1173,42 +1206,49 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
 }
 
 // Items that were cut: the states of an item's pieces joined, a warp a row, in the order of
-// the keys.  The CTA of share c (blockIdx.x + 1) handles the item that the cut before c
-// is the first within; the others have nothing to do.
+// the keys.  A warp takes (share c, row) pairs; the row of the item that share c starts within
+// is joined where c is the first such share.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
-                                                         int item_rows, float v_scale)
+                                                         int item_rows, int per, float v_scale)
 {
     grid_dependency_wait();
     grid_dependents_launch();
-    const int n = p.places[0], c = blockIdx.x + 1;
-    if (c >= n)
-        return;
-    const int32_t *at = p.places + 8 + 8 * c;
-    const int b = at[0], h = at[1], rt = at[2];
-    auto within = [&](int k) {                             // the cut before share k is in this item
-        const int32_t *o = p.places + 8 + 8 * k;
-        return o[0] == b && o[1] == h && o[2] == rt && o[3] != 0;
-    };
-    if (!at[3] || within(c - 1))
-        return;
-    Seq q;
-    int q0;
-    bool bad;
-    if (!Walk::lengths(p, b, q, q0, bad))
-        return;
-    int last = c;                                          // the last share with a piece of it
-    while (last + 1 < n && within(last + 1))
-        ++last;
-    const int pieces = last - c + 2;
-    const int rows = min(p.rules.tpr, q.n - rt * p.rules.tpr) << p.lg_g;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = p.places[0], lane = threadIdx.x & 31;
+    const int warps = gridDim.x * 8;
     const int64_t state = (int64_t)item_rows * (D + 2);
-    // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
-    auto piece = [&](int i) -> const float * {
-        return p.part + (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i)) * state;
-    };
-    for (int row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+    const int4 *place = reinterpret_cast<const int4 *>(p.places + 8);      // two a share
+    constexpr int W = D / 32;
+    for (int k = blockIdx.x * 8 + (threadIdx.x >> 5); k < (n - 1) * per; k += warps) {
+        const int c = k / per + 1, row = k - (c - 1) * per;
+        const int4 at = place[2 * c], more = place[2 * c + 1];             // b, h, row tile, split; token, rows
+        // lanes look at the shares from c - 1 on: those that start within the item
+        int pieces = 1;
+        bool first = true;
+        for (int s0 = c - 1; s0 < n; s0 += 32) {
+            const int s = s0 + lane;
+            bool in = false;
+            if (s < n) {
+                const int4 o = place[2 * s];
+                in = o.x == at.x && o.y == at.y && o.z == at.z && o.w != 0;
+            }
+            unsigned here = __ballot_sync(FULL_MASK, in);
+            if (s0 == c - 1) {
+                first = !(here & 1);
+                here |= 1;                                                 // (as if: counted in `pieces`)
+            }
+            const int run = here == FULL_MASK ? 32 : __ffs(~here) - 1;
+            pieces += run - (s0 == c - 1 ? 1 : 0);
+            if (run < 32)
+                break;
+        }
+        if (!at.w || !first || row >= more.y)
+            continue;
+        // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
+        const float *start = p.part + (2 * (int64_t)(c - 1) + 1) * state;
+        auto piece = [&](int i) -> const float * {
+            return i == 0 ? start : start + (2 * (int64_t)i - 1) * state;
+        };
         float m = -INFINITY;
         for (int i = lane; i < pieces; i += 32) {
             const float2 s = *reinterpret_cast<const float2 *>(piece(i) + item_rows * D + 2 * row);
@@ -1216,35 +1256,32 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
                 m = fmaxf(m, s.x);
         }
 #pragma unroll
-        for (int k = 16; k >= 1; k >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, k));
-        constexpr int W = D / 32;
+        for (int d = 16; d >= 1; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, d));
         float acc[W] = {}, l = 0.0f;
 #pragma unroll 4
         for (int i = 0; i < pieces; ++i) {
             const float *s = piece(i);
             const float2 ml = *reinterpret_cast<const float2 *>(s + item_rows * D + 2 * row);
-            if (ml.y == 0.0f)                              // none of its keys in sight
-                continue;
-            const float w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
-            l = fmaf(w, ml.y, l);
-            const float *o = s + (int64_t)row * D + lane * W;
+            float x[W];
             if constexpr (W == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(o);
-                acc[0] = fmaf(w, x.x, acc[0]);
-                acc[1] = fmaf(w, x.y, acc[1]);
-                acc[2] = fmaf(w, x.z, acc[2]);
-                acc[3] = fmaf(w, x.w, acc[3]);
+                const float4 o = *reinterpret_cast<const float4 *>(s + (int64_t)row * D + lane * W);
+                x[0] = o.x; x[1] = o.y; x[2] = o.z; x[3] = o.w;
             } else {
-                const float2 x = *reinterpret_cast<const float2 *>(o);
-                acc[0] = fmaf(w, x.x, acc[0]);
-                acc[1] = fmaf(w, x.y, acc[1]);
+                const float2 o = *reinterpret_cast<const float2 *>(s + (int64_t)row * D + lane * W);
+                x[0] = o.x; x[1] = o.y;
             }
+            // (a piece that has none of the row's keys in sight wrote no sum)
+            const float w = ml.y == 0.0f || ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+            l = fmaf(w, ml.y, l);
+#pragma unroll
+            for (int d = 0; d < W; ++d)
+                acc[d] = ml.y == 0.0f ? acc[d] : fmaf(w, x[d], acc[d]);
         }
         const float inv = l == 0.0f ? 0.0f : v_scale / l;
         T *out = static_cast<T *>(p.out) +
-                 ((int64_t)(q0 + rt * p.rules.tpr + (row >> p.lg_g)) * p.num_q_heads +
-                  (h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + lane * W;
+                 ((int64_t)(more.x + (row >> p.lg_g)) * p.num_q_heads + (at.y << p.lg_g) +
+                  (row & ((1 << p.lg_g) - 1))) * D + lane * W;
         if constexpr (W == 4)
             *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv),
                                                          pack2<T>(acc[2] * inv, acc[3] * inv));
@@ -1307,8 +1344,9 @@ int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
     if (launch_pdl(chunk_kernel<D, F8, BF, NQ>, dim3((unsigned)sms), dim3(C::NT),
                    (size_t)C::SMEM_BYTES, s, p) != cudaSuccess)
         return PKV_ERR_CUDA;
-    if (sms > 1 && launch_pdl(chunk_join_kernel<D, T>, dim3((unsigned)(sms - 1), C::ROWS / 32), dim3(256),
-                              0, s, p, (int)C::ROWS, F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
+    if (sms > 1 && launch_pdl(chunk_join_kernel<D, T>, dim3((unsigned)(4 * sms)), dim3(256),
+                              0, s, p, (int)C::ROWS,
+                              (int)std::min<int64_t>(C::ROWS, (int64_t)p.max_q_len << p.lg_g), F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
         return PKV_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1367,7 +1405,7 @@ int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num
     p.box_rows = std::min(pool->block_size, TILE);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int rows = item_rows(max_q_len, G);
-    p.rules.tpr = rows / G;
+    p.rules.lg_tpr = log2_of(rows / G);
     p.rules.window = window;
     p.rules.tree = visible != nullptr;
     if (!encode_q_map(&p.tm_q, pool, q, num_q_heads, num_tokens, G, bf))

@@ -21,26 +21,27 @@
 namespace pkv {
 namespace chunk {
 
-constexpr int TILE = 128;             // keys of a tile
+constexpr int TILE = 128, LG_TILE = 7;   // keys of a tile
 constexpr int ITEM_COST = 2;
 
 struct Rules {
-    int tpr;                          // tokens of a row tile: a power of two, 16..256
+    int lg_tpr;                       // tokens of a row tile: tpr = 2^lg_tpr, 16..256
     int window;                       // 0: none
     bool tree;                        // every new token may see any other
 };
 
-// sum over s < x of floor((a + s w) / 128), w a power of two, a >= 0.
-PKV_HD int64_t floor_sum(int64_t x, int64_t a, int w)
+// sum over s < x of floor((a + s w) / 128), w = 2^lg_w, a >= 0.  (Shifts: a division of 64-bit
+// integers is a hundred instructions.)
+PKV_HD int64_t floor_sum(int64_t x, int64_t a, int lg_w)
 {
-    if (w >= TILE)
-        return x * (a / TILE) + (int64_t)(w / TILE) * (x * (x - 1) / 2);
-    const int k = TILE / w;
-    // floor((a + s w) / 128) = floor((floor(a / w) + s) / k); H(y) sums floor(i / k), i < y
-    const int64_t a0 = a / w, y0 = a0, y1 = a0 + x;
-    const int64_t q0 = y0 / k, q1 = y1 / k;
-    const int64_t h0 = k * (q0 * (q0 - 1) / 2) + (y0 - q0 * k) * q0;
-    const int64_t h1 = k * (q1 * (q1 - 1) / 2) + (y1 - q1 * k) * q1;
+    if (lg_w >= LG_TILE)
+        return x * (a >> LG_TILE) + ((x * (x - 1) / 2) << (lg_w - LG_TILE));
+    const int lg_k = LG_TILE - lg_w;
+    // floor((a + s w) / 128) = floor((floor(a / w) + s) / k), k = 128 / w; H(y) sums floor(i / k)
+    // over i < y: k q (q - 1) / 2 + (y - q k) q with q = floor(y / k)
+    const int64_t y0 = a >> lg_w, y1 = y0 + x, q0 = y0 >> lg_k, q1 = y1 >> lg_k;
+    const int64_t h0 = ((q0 * (q0 - 1) / 2) << lg_k) + (y0 - (q0 << lg_k)) * q0;
+    const int64_t h1 = ((q1 * (q1 - 1) / 2) << lg_k) + (y1 - (q1 << lg_k)) * q1;
     return h1 - h0;
 }
 
@@ -49,13 +50,13 @@ struct Seq {
     int n, L;
 };
 
-PKV_HD int row_tiles(const Rules &r, const Seq &q) { return (q.n - 1) / r.tpr + 1; }
+PKV_HD int row_tiles(const Rules &r, const Seq &q) { return ((q.n - 1) >> r.lg_tpr) + 1; }
 
 // Positions of a row tile's first token and of the last key that a row of it may see.
 PKV_HD void span(const Rules &r, const Seq &q, int rt, int &first, int &last)
 {
-    const int end = q.n - rt * r.tpr < r.tpr ? q.n : (rt + 1) * r.tpr;
-    first = q.L - q.n + rt * r.tpr;
+    const int at = rt << r.lg_tpr, tpr = 1 << r.lg_tpr, end = q.n - at < tpr ? q.n : at + tpr;
+    first = q.L - q.n + at;
     last = (r.tree ? q.L : q.L - q.n + end) - 1;
 }
 
@@ -64,22 +65,22 @@ PKV_HD void tiles(const Rules &r, const Seq &q, int rt, int &lo, int &hi)
 {
     int first, last;
     span(r, q, rt, first, last);
-    lo = r.window > 0 && first - r.window + 1 > 0 ? (first - r.window + 1) / TILE : 0;
-    hi = last / TILE + 1;
+    lo = r.window > 0 && first - r.window + 1 > 0 ? (first - r.window + 1) >> LG_TILE : 0;
+    hi = (last >> LG_TILE) + 1;
 }
 
 // Cost of the row tiles before rt, all of them whole ones (of one KV head).
 PKV_HD int64_t cost_before(const Rules &r, const Seq &q, int64_t rt)
 {
-    const int64_t A = q.L - q.n;
+    const int64_t A = q.L - q.n, tpr = 1 << r.lg_tpr;
     if (r.tree)
-        return rt * ((q.L - 1) / TILE + 1 + ITEM_COST);
-    int64_t c = floor_sum(rt, A + r.tpr - 1, r.tpr) + rt * (1 + ITEM_COST);
+        return rt * (((q.L - 1) >> LG_TILE) + 1 + ITEM_COST);
+    int64_t c = floor_sum(rt, A + tpr - 1, r.lg_tpr) + rt * (1 + ITEM_COST);
     if (r.window > 0) {
         const int64_t first = A - r.window + 1;
-        const int64_t s0 = first < 0 ? (-first + r.tpr - 1) / r.tpr : 0;   // tiles from key 0
+        const int64_t s0 = first < 0 ? (-first + tpr - 1) >> r.lg_tpr : 0;   // tiles from key 0
         if (rt > s0)
-            c -= floor_sum(rt - s0, first + s0 * r.tpr, r.tpr);
+            c -= floor_sum(rt - s0, first + (s0 << r.lg_tpr), r.lg_tpr);
     }
     return c;
 }
@@ -98,24 +99,27 @@ struct Place {
     int b, h, rt, tile, split;
 };
 
-// Position x (0 <= x < Hkv * cost_of) of sequence b's stretch of the line.
-PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x)
+// Position x (0 <= x < Hkv * c, c the sequence's cost_of) of sequence b's stretch of the line.
+PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x, int64_t c)
 {
-    const int64_t c = cost_of(r, q);
     Place p;
     p.b = b;
     p.h = (int)(x / c);
     x -= p.h * c;
     int a = 0, e = row_tiles(r, q) - 1;               // the last row tile that starts by x
+    int64_t before = 0;                               // and the cost before it
     while (a < e) {
         const int m = (a + e + 1) / 2;
-        if (cost_before(r, q, m) <= x)
+        const int64_t cm = cost_before(r, q, m);
+        if (cm <= x) {
             a = m;
-        else
+            before = cm;
+        } else {
             e = m - 1;
+        }
     }
     p.rt = a;
-    x -= cost_before(r, q, a);
+    x -= before;
     int lo, hi;
     tiles(r, q, a, lo, hi);
     p.tile = x > ITEM_COST ? lo + (int)(x - ITEM_COST) : lo;
