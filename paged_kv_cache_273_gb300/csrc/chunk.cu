@@ -48,7 +48,9 @@ struct ChunkParams {
     const int32_t *tables, *q_start, *seq_lens;
     const uint64_t *visible;
     void *out;
-    int32_t *places;              // [0]: shares; from [8] on: 8 words a share, where it starts
+    int32_t *places;              // [0]: shares; from [8] on a share's pieces to join; from
+                                  // [items_at] on their item: token, rows, KV head
+    int items_at;
     float *part;                  // 2 states a CTA: that of its first piece, and of its last
     unsigned int *err;
     int batch, num_tokens, max_q_len, num_q_heads, num_kv_heads, lg_g;
@@ -283,16 +285,29 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
     }
     __syncthreads();
     if (tid == 0) {
-        // for the joining: the item, whether the share starts within it, its first token and
-        // its rows
+        // for the joining: the item that this share starts within, if it is the first to do so,
+        // its pieces, its first token and its rows
         const Place &a = places[0];
-        Seq q;
-        int q0;
-        bool bad;
-        Walk::lengths(p, a.b, q, q0, bad);
-        int4 *o = reinterpret_cast<int4 *>(p.places + 8 + 8 * c);
-        o[0] = make_int4(a.b, a.h, a.rt, a.split);
-        o[1] = make_int4(q0 + (a.rt << p.rules.lg_tpr), min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, 0, 0);
+        int4 item = make_int4(0, 0, 0, 0);
+        int pieces = 0;
+        if (a.split) {
+            Seq q;
+            int q0, lo, hi;
+            bool bad;
+            Walk::lengths(p, a.b, q, q0, bad);
+            chunk::tiles(p.rules, q, a.rt, lo, hi);
+            // positions on the line: where the item may first be cut, and its end
+            const int64_t x = chunk::share_start(U, n, c), first = x - (a.tile - lo), end = first + (hi - lo);
+            if (chunk::share_start(U, n, c - 1) <= first) {
+                pieces = 2;
+                while (c + pieces - 1 < n && chunk::share_start(U, n, c + pieces - 1) < end)
+                    ++pieces;
+            }
+            item = make_int4(q0 + (a.rt << p.rules.lg_tpr),
+                             min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, a.h, 0);
+        }
+        p.places[8 + c] = pieces;
+        reinterpret_cast<int4 *>(p.places + p.items_at)[c] = item;
     }
     return true;
 }
@@ -1099,7 +1114,9 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         constexpr uint32_t Q_PANEL = TILE_M * 128;
         const uint32_t idesc_s = umma_idesc(BF && !F8 ? 1u : 0u, 0u, TILE);
         const uint32_t idesc_o = umma_idesc(C::PBF ? 1u : 0u, 1u, D);
-        const uint32_t tm = __shfl_sync(FULL_MASK, tmem, 0), el = elect_lane();
+        // (an allocation of all of tensor memory starts at its first column)
+        constexpr uint32_t tm = 0;
+        const uint32_t el = elect_lane();
         const uint64_t dq = umma_desc_sw128(smem_addr(sQ), 16, 1024);
         const uint64_t dk = umma_desc_sw128(smem_addr(sK), 16, C::GROUP8);
         const uint64_t dv = umma_desc_sw128(smem_addr(sV), 1024, C::GROUP8);
@@ -1113,8 +1130,12 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             return __all_sync(FULL_MASK, wait(bar, parity));
         };
         for (uint32_t item = 0; ok && take(item); ++item) {
-            const bool both = shared_rows(c);
-            const int nt0 = group_tiles(p, c, 0), nt1 = group_tiles(p, c, 1);
+            // (shuffled, so that what follows from them is known to be the warp's and is worked
+            // out in uniform registers)
+            const bool both = __shfl_sync(FULL_MASK, (int)shared_rows(c), 0) != 0;
+            const int nt0 = __shfl_sync(FULL_MASK, group_tiles(p, c, 0), 0);
+            const int nt1 = __shfl_sync(FULL_MASK, group_tiles(p, c, 1), 0);
+            const int tiles = __shfl_sync(FULL_MASK, c.t1 - c.t0, 0);
             int s_left = nt0 + nt1;
             if (!(ok = wait_all(q_full, item)))
                 break;
@@ -1128,8 +1149,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 if (s >= nt)
                     continue;
                 const bool more = s + 1 < nt;
-                const uint32_t k = gt + tile_at(c, g, s), slot = k % NS;
-                const uint32_t k1 = gt + tile_at(c, g, s + 1), slot1 = k1 % NS;
+                const uint32_t k = gt + (both ? 2 * s + g : s), slot = k % NS;
+                const uint32_t k1 = k + (both ? 2 : 1), slot1 = k1 % NS;
                 if ((s >= 0 && !wait_all(&v_full[slot], k / NS)) ||
                     (more && !wait_all(&k_full[slot1], k1 / NS))) {
                     ok = false;
@@ -1181,7 +1202,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         umma_commit_elected(el, q_empty);
                 }
             }
-            gt += c.t1 - c.t0;
+            gt += tiles;
             done(item);
         }
         // every issued MMA has finished before tensor memory is released
@@ -1205,88 +1226,83 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     }
 }
 
-// Items that were cut: the states of an item's pieces joined, a warp a row, in the order of
-// the keys.  A warp takes (share c, row) pairs; the row of the item that share c starts within
-// is joined where c is the first such share.
+// Items that were cut: the states of an item's pieces joined in the order of the keys, four
+// rows a warp, eight lanes a row.  Warps count off the shares that an item to join is noted
+// with, so that those without cost a look at a word each, and take their rows in turn.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
                                                          int item_rows, int per, float v_scale)
 {
     grid_dependency_wait();
     grid_dependents_launch();
-    const int n = p.places[0], lane = threadIdx.x & 31;
-    const int warps = gridDim.x * 8;
+    const int n = p.places[0], lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
+    const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
     const int64_t state = (int64_t)item_rows * (D + 2);
-    const int4 *place = reinterpret_cast<const int4 *>(p.places + 8);      // two a share
-    constexpr int W = D / 32;
-    for (int k = blockIdx.x * 8 + (threadIdx.x >> 5); k < (n - 1) * per; k += warps) {
-        const int c = k / per + 1, row = k - (c - 1) * per;
-        const int4 at = place[2 * c], more = place[2 * c + 1];             // b, h, row tile, split; token, rows
-        // lanes look at the shares from c - 1 on: those that start within the item
-        int pieces = 1;
-        bool first = true;
-        for (int s0 = c - 1; s0 < n; s0 += 32) {
-            const int s = s0 + lane;
-            bool in = false;
-            if (s < n) {
-                const int4 o = place[2 * s];
-                in = o.x == at.x && o.y == at.y && o.z == at.z && o.w != 0;
+    constexpr int W = D / 32;                              // float4s of a lane
+    int base = 0;                                          // units of the shares looked at
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        const int mine = s0 + lane < n ? p.places[8 + s0 + lane] : 0;
+        const unsigned some = __ballot_sync(FULL_MASK, mine > 0);
+        const int units = __popc(some) * per;
+        // this warp's units among them: `per` of four rows for each share
+        for (int u = warp < base % warps ? base - base % warps + warps + warp : base - base % warps + warp;
+             u < base + units; u += warps) {
+            const int k = (u - base) / per, row = ((u - base) - k * per) * 4 + sub;
+            const int src = __fns(some, 0, k + 1);         // the k-th share's lane
+            const int pieces = __shfl_sync(FULL_MASK, mine, src), c = s0 + src;
+            const int4 item = reinterpret_cast<const int4 *>(p.places + p.items_at)[c];
+            if (row - sub >= item.y)
+                continue;
+            const bool valid = row < item.y;
+            // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
+            const float *start = p.part + (2 * (int64_t)(c - 1) + 1) * state;
+            auto piece = [&](int i) -> const float * {
+                return i == 0 ? start : start + (2 * (int64_t)i - 1) * state;
+            };
+            const int64_t sum_at = item_rows * D + 2 * row, o_at = (int64_t)row * D + 4 * j;
+            float m = -INFINITY;
+            for (int i = j; i < pieces; i += 8) {
+                const float2 s = valid ? *reinterpret_cast<const float2 *>(piece(i) + sum_at)
+                                       : make_float2(0.0f, 0.0f);
+                m = s.y != 0.0f ? fmaxf(m, s.x) : m;
             }
-            unsigned here = __ballot_sync(FULL_MASK, in);
-            if (s0 == c - 1) {
-                first = !(here & 1);
-                here |= 1;                                                 // (as if: counted in `pieces`)
-            }
-            const int run = here == FULL_MASK ? 32 : __ffs(~here) - 1;
-            pieces += run - (s0 == c - 1 ? 1 : 0);
-            if (run < 32)
-                break;
-        }
-        if (!at.w || !first || row >= more.y)
-            continue;
-        // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
-        const float *start = p.part + (2 * (int64_t)(c - 1) + 1) * state;
-        auto piece = [&](int i) -> const float * {
-            return i == 0 ? start : start + (2 * (int64_t)i - 1) * state;
-        };
-        float m = -INFINITY;
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 s = *reinterpret_cast<const float2 *>(piece(i) + item_rows * D + 2 * row);
-            if (s.y != 0.0f)
-                m = fmaxf(m, s.x);
-        }
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, d));
-        float acc[W] = {}, l = 0.0f;
+            for (int d = 4; d >= 1; d >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, d));
+            if (!valid)
+                continue;                                  // (no shuffles from here on)
+            float acc[4 * W] = {}, l = 0.0f;
 #pragma unroll 4
-        for (int i = 0; i < pieces; ++i) {
-            const float *s = piece(i);
-            const float2 ml = *reinterpret_cast<const float2 *>(s + item_rows * D + 2 * row);
-            float x[W];
-            if constexpr (W == 4) {
-                const float4 o = *reinterpret_cast<const float4 *>(s + (int64_t)row * D + lane * W);
-                x[0] = o.x; x[1] = o.y; x[2] = o.z; x[3] = o.w;
-            } else {
-                const float2 o = *reinterpret_cast<const float2 *>(s + (int64_t)row * D + lane * W);
-                x[0] = o.x; x[1] = o.y;
-            }
-            // (a piece that has none of the row's keys in sight wrote no sum)
-            const float w = ml.y == 0.0f || ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
-            l = fmaf(w, ml.y, l);
+            for (int i = 0; i < pieces; ++i) {
+                const float *s = piece(i);
+                const float2 ml = *reinterpret_cast<const float2 *>(s + sum_at);
+                float4 o[W];
 #pragma unroll
-            for (int d = 0; d < W; ++d)
-                acc[d] = ml.y == 0.0f ? acc[d] : fmaf(w, x[d], acc[d]);
+                for (int q = 0; q < W; ++q)
+                    o[q] = *reinterpret_cast<const float4 *>(s + o_at + 32 * q);
+                // (a piece that has none of the row's keys in sight may have written no O)
+                const bool none = ml.y == 0.0f;
+                const float w = none || ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+                l = fmaf(w, ml.y, l);
+#pragma unroll
+                for (int q = 0; q < W; ++q) {
+                    acc[4 * q] = none ? acc[4 * q] : fmaf(w, o[q].x, acc[4 * q]);
+                    acc[4 * q + 1] = none ? acc[4 * q + 1] : fmaf(w, o[q].y, acc[4 * q + 1]);
+                    acc[4 * q + 2] = none ? acc[4 * q + 2] : fmaf(w, o[q].z, acc[4 * q + 2]);
+                    acc[4 * q + 3] = none ? acc[4 * q + 3] : fmaf(w, o[q].w, acc[4 * q + 3]);
+                }
+            }
+            const float inv = l == 0.0f ? 0.0f : v_scale / l;
+            T *out = static_cast<T *>(p.out) +
+                     ((int64_t)(item.x + (row >> p.lg_g)) * p.num_q_heads + (item.z << p.lg_g) +
+                      (row & ((1 << p.lg_g) - 1))) * D + 4 * j;
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+                *reinterpret_cast<uint2 *>(out + 32 * q) =
+                    make_uint2(pack2<T>(acc[4 * q] * inv, acc[4 * q + 1] * inv),
+                               pack2<T>(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
         }
-        const float inv = l == 0.0f ? 0.0f : v_scale / l;
-        T *out = static_cast<T *>(p.out) +
-                 ((int64_t)(more.x + (row >> p.lg_g)) * p.num_q_heads + (at.y << p.lg_g) +
-                  (row & ((1 << p.lg_g) - 1))) * D + lane * W;
-        if constexpr (W == 4)
-            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc[0] * inv, acc[1] * inv),
-                                                         pack2<T>(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(out) = pack2<T>(acc[0] * inv, acc[1] * inv);
+        base += units;
     }
 }
 
@@ -1346,7 +1362,7 @@ int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
         return PKV_ERR_CUDA;
     if (sms > 1 && launch_pdl(chunk_join_kernel<D, T>, dim3((unsigned)(4 * sms)), dim3(256),
                               0, s, p, (int)C::ROWS,
-                              (int)std::min<int64_t>(C::ROWS, (int64_t)p.max_q_len << p.lg_g), F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
+                              (int)((std::min<int64_t>(C::ROWS, (int64_t)p.max_q_len << p.lg_g) + 3) / 4), F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
         return PKV_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1355,9 +1371,12 @@ int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
 // softmax groups in turn), else 256.
 int item_rows(int max_q_len, int G) { return (int64_t)max_q_len * G <= TILE_M ? TILE_M : 2 * TILE_M; }
 
+int items_at(const pkv_pool *pool) { return (8 + std::max(1, pool->num_sms) + 3) / 4 * 4; }
+
 size_t places_bytes(const pkv_pool *pool)
 {
-    return ((size_t)(8 + 8 * std::max(1, pool->num_sms)) * 4 + 255) / 256 * 256;
+    // a word a share, and 16 bytes
+    return ((size_t)items_at(pool) * 4 + (size_t)16 * std::max(1, pool->num_sms) + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -1390,6 +1409,7 @@ int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num
     p.visible = visible;
     p.out = out;
     p.places = static_cast<int32_t *>(workspace);
+    p.items_at = items_at(pool);
     p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + places_bytes(pool));
     p.err = pool->d_err;
     p.batch = batch;
