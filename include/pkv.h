@@ -868,8 +868,8 @@ size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_he
  *              calls that run concurrently.
  *
  * Scores and sums in fp32; the weights enter the second product rounded to q's type (over
- * F8 caches to bf16, and for fp16 q in two parts), which moves an output by about as much as its own
- * rounding does.  An F16 or BF16 row of V that is not finite makes the outputs of its own
+ * F8 caches to fp16, relative to the row's largest weight times its block's scale), which moves an
+ * output by about as much as its own rounding does.  An F16 or BF16 row of V that is not finite makes the outputs of its own
  * sequence's earlier tokens in the same call unspecified (those of the same 32 to 256 tokens),
  * an F8 cache's values are finite.  Pools: F16, BF16, F8 (others
  * PKV_ERR_UNSUPPORTED).  Lengths out of range (n_b > max_q_len or n_b > 64 with `visible`

@@ -65,29 +65,26 @@ struct ChunkParams {
 // four that bring and convert tiles, the MMA warp, and the one for pieces and q.
 template <int D, bool F8, bool BF, int NQ>
 struct Cfg {
-    // threads a row of a softmax group: two halve the time from S to P, which the tensor cores
-    // wait for; over an 8-bit cache the registers are wanted for the conversion
-    static constexpr int HT = 1;
     static constexpr int ROWS = NQ * TILE_M;
     static constexpr int Q_BYTES = TILE_M * D * 2;                       // one half
     static constexpr int KV_BYTES = TILE * D * 2;
     // ring slots: what shared memory holds
-    static constexpr int NS = D == 64 ? 4 : NQ == 1 ? 3 : 2;
-    // tiles' scales of K: read until the tile's softmax, when NS + 1 tiles more may be there
+    static constexpr int NS = D == 64 ? 4 : NQ == 1 && !F8 ? 3 : 2;
+    // tiles' scales: read until the tile's softmax, when NS + 1 tiles more may be there
     static constexpr int RING = 8;
     static_assert(RING >= NS + 2, "scales in use");
     static constexpr int OFF_K = NQ * Q_BYTES;
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
-    static constexpr int OFF_ML = OFF_V + NS * KV_BYTES;                 // what threads of a row exchange
-    static constexpr int XM1 = HT == 2 ? 2 * TILE_M : 0;                 // the second group's slots
-    static constexpr int OFF_SC = OFF_ML + (XM1 + 2 * TILE_M) * 4;       // [RING][16] scales of K
-    static constexpr int OFF_QE = OFF_SC + (F8 ? RING * 16 * 4 : 0);     // q's exponents, two pieces
+    static constexpr int OFF_ML = OFF_V + NS * KV_BYTES;                 // the second group's states
+    // [RING][2][16]: scales of K, exponents of V's
+    static constexpr int OFF_SC = OFF_ML + (F8 ? 3 : 2) * TILE_M * 4;
+    static constexpr int OFF_QE = OFF_SC + (F8 ? RING * 32 * 4 : 0);     // q's exponents, two pieces
     static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * TILE_M : 0);
     static constexpr int PIECES = 4;                                     // handed out and not done
-    static constexpr int NBARS = 4 * NS + 8 + 6 + 2 * PIECES + (HT == 2 ? 8 : 0);
+    static constexpr int NBARS = 4 * NS + 8 + 6 + 2 * PIECES;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;                 // tensor memory's address, flag, pieces
     static constexpr int SMEM_BYTES = OFF_MISC + 224;
-    static constexpr int W0 = 8 * HT;                                    // the first warp behind the groups
+    static constexpr int W0 = 8;                                         // the first warp behind the groups
     static constexpr int W_MMA = F8 ? W0 + 4 : W0 + 3, W_FEED = F8 ? W0 + 5 : W0 + 2;
     static constexpr int CONSUMERS = W0 + (F8 ? 5 : 3);                  // warps that a piece is for
     static constexpr bool QCONV = F8 && BF;
@@ -96,17 +93,15 @@ struct Cfg {
     // warps behind them, and the last four (the shares add up to what was there at launch)
     static constexpr int REGS = F8 ? 128 : 168;
     static constexpr int R_SOFT = F8 ? 152 : 216, R_2 = F8 ? 128 : 72, R_3 = F8 ? 80 : 0;
-    static_assert(2 * HT * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
+    static_assert(2 * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
     static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
     // a K or V tile: eight rows of 64 columns are 1024 bytes (128-byte swizzled); a group of
     // eight rows holds its panels one after the other, so that one tensor copy brings
     // a block's whole rows (two of 64 columns each cost the warp that issues them
     // twice as long, more than a tile's time on the tensor cores)
     static constexpr int GROUP8 = 1024 * (D / 64);
-    // P in one 16-bit part, rounded as the output is; over an 8-bit cache P is bf16, for
-    // its range, and in two parts where the output is fp16
-    static constexpr bool PBF = F8 || BF;
-    static constexpr bool SPLIT = F8 && !BF;
+    // P in the caches' 16-bit type; over an 8-bit cache, whose codes become fp16, in fp16
+    static constexpr bool PBF = BF && !F8;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -332,23 +327,6 @@ __device__ __forceinline__ void codes_to_half(const uint4 &w, uint4 &lo, uint4 &
     f8x4_to_half2(w.w, hi.z, hi.w);
 }
 
-// The same times a power of two, as bf16 (exact: four significant bits).
-__device__ __forceinline__ uint32_t scaled_bf16(uint32_t h2, float f)
-{
-    const float2 x = half2_to_float2(h2);
-    float a = x.x, b = x.y;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "f"(f));
-    return pack2<__nv_bfloat16>(a, b);
-}
-__device__ __forceinline__ uint4 scaled_bf16(const uint4 &h, float f)
-{
-    return make_uint4(scaled_bf16(h.x, f), scaled_bf16(h.y, f), scaled_bf16(h.z, f),
-                      scaled_bf16(h.w, f));
-}
-
 // Chunks 2j and 2j + 1 of a row: the second panel's lanes write their odd one first, so that
 // eight lanes' stores fall on all banks.
 template <int D>
@@ -360,26 +338,15 @@ __device__ __forceinline__ void put_chunks(unsigned char *tile, int row, int j, 
     *reinterpret_cast<uint4 *>(tile + tile_off<D>(row, 2 * j + 1 - odd)) = odd ? lo : hi;
 }
 
-// V of an 8-bit cache enters P V times 2^-16 (its largest values are beyond bf16's
-// otherwise; its smallest stay normal), and the quotient is multiplied back.
-constexpr int V_SHIFT = 16;
-
 // fp16 weights are taken times 2^7: the running maximum moves when a score is 2^8 above it, so
 // they stay below 2^15, and weights down to 2^-21 of the largest keep all their bits.
 constexpr float P_SHIFT = 7.0f;
 
-constexpr uint32_t WAIT_TRIES = 1u << 22;
+// O over an 8-bit cache is kept times 2^-16 outside of tensor memory (the sum over many keys
+// of values near fp32's largest is beyond it; their quotient by the weights' sum is not).
+constexpr int V_SHIFT = 16;
 
-__device__ __forceinline__ float ld_shared(uint32_t addr)
-{
-    float x;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-    return x;
-}
-__device__ __forceinline__ void st_shared(uint32_t addr, float x)
-{
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
+constexpr uint32_t WAIT_TRIES = 1u << 22;
 
 // Row r of a half of q (bf16, as the tensor copy left it) -> fp16 times 2^-e in place, the
 // row's largest magnitude in [2^14, 2^15); returns e.
@@ -436,15 +403,15 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *sQ = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
-    float *xm = reinterpret_cast<float *>(smem + C::OFF_ML);
+    float *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
     float *k_sc = reinterpret_cast<float *>(smem + C::OFF_SC);
     signed char *q_exp = reinterpret_cast<signed char *>(smem + C::OFF_QE);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *k_empty = k_full + NS, *v_full = k_empty + NS, *v_empty = v_full + NS;
     uint64_t *s_full = v_empty + NS, *p_full = s_full + 2, *o_done = p_full + 2, *o_free = o_done + 2;
     uint64_t *q_full = o_free + 2, *q_empty = q_full + 1, *ml_full = q_empty + 1, *ml_free = ml_full + 1;
-    uint64_t *drain = ml_free + 1, *pair = drain + 1;
-    uint64_t *pc_full = pair + (C::HT == 2 ? 8 : 0), *pc_empty = pc_full + C::PIECES, *q_raw = pc_empty + C::PIECES;
+    uint64_t *drain = ml_free + 1;
+    uint64_t *pc_full = drain + 1, *pc_empty = pc_full + C::PIECES, *q_raw = pc_empty + C::PIECES;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Place *places = reinterpret_cast<Place *>(smem + C::OFF_MISC + 16);
@@ -465,12 +432,10 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&s_full[g], 1);
-            mbar_init(&p_full[g], 4 * C::HT);      // (a lane a warp arrives)
+            mbar_init(&p_full[g], 4);      // (a lane a warp arrives)
             mbar_init(&o_done[g], 1);
-            mbar_init(&o_free[g], 4 * C::HT);
+            mbar_init(&o_free[g], 4);
         }
-        for (int i = 0; C::HT == 2 && i < 8; ++i)
-            mbar_init(&pair[i], 2);
         mbar_init(q_full, C::QCONV ? 8 : 1);
         mbar_init(q_raw, 1);
         for (int i = 0; i < C::PIECES; ++i) {
@@ -478,8 +443,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             mbar_init(&pc_empty[i], C::CONSUMERS);
         }
         mbar_init(q_empty, 1);
-        mbar_init(ml_full, 4 * C::HT);
-        mbar_init(ml_free, 4 * C::HT);
+        mbar_init(ml_full, 4);
+        mbar_init(ml_free, 4);
         mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_fence_init();
@@ -519,39 +484,19 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     else
         fewer_registers<F8 ? C::R_3 : 24>();
     if (warp < W0) {
-        // ================= softmax: group g, HT threads a row, each its share of a tile's
-        // keys and of the output's columns
-        constexpr int HT = C::HT, CW = TILE / HT, OW = D / HT;
-        const int g = warp / (4 * HT), hf = warp / 4 % HT, quad = warp & 3;
+        // ================= softmax: group g, one thread a row
+        const int g = warp >> 2, quad = warp & 3;
         const int r = quad * 32 + lane;
-        const uint32_t t_row = tmem + g * C::GROUP_COLS + ((uint32_t)(quad * 32) << 16);
-        const uint32_t t_s = t_row + hf * CW;
-        const uint32_t t_o = t_row + TILE + hf * OW;
-        const uint32_t mine = smem_addr(xm + g * C::XM1 + hf * TILE_M + r);
-        const uint32_t other = HT == 2 ? mine ^ (TILE_M * 4) : mine;
-        // the parities of the phases that come next, of s_full, o_done, ml_full, the row's pair
-        // and (group 0) the second group's o_done; and (group 1) whether its slots of xm
-        // are being read
+        const uint32_t t_s = tmem + g * C::GROUP_COLS + ((uint32_t)(quad * 32) << 16), t_o = t_s + TILE;
+        // the parities of the phases that come next, of s_full, o_done, ml_full and (group 0)
+        // the second group's o_done; and (group 1) whether its state is being read
         uint32_t ph = 0;
-        constexpr uint32_t P_S = 1, P_O = 2, P_ML = 4, P_X = 8, P_O1 = 16, LENT = 32;
+        constexpr uint32_t P_S = 1, P_O = 2, P_ML = 4, P_O1 = 8, LENT = 16;
         int gt = 0;                                // the CTA's tiles so far
         auto phase = [&](uint64_t *bar, uint32_t bit) -> bool {
             const bool ok = __all_sync(FULL_MASK, wait(bar, (ph & bit) ? 1u : 0u));
             ph ^= bit;
             return ok;
-        };
-        // what both threads of a row say, to each other
-        auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(pair + g * 4 + quad);
-            return phase(pair + g * 4 + quad, P_X);
-        };
-        auto read_back = [&]() -> bool {           // the first group has read what was lent
-            if (!(ph & LENT))
-                return true;
-            ph ^= LENT;
-            return __all_sync(FULL_MASK, wait(ml_free, (ph & P_ML) ? 0u : 1u));
         };
         for (uint32_t item = 0; take(item); ++item) {
             const bool both = shared_rows(c);
@@ -564,7 +509,11 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             const int from = p.rules.window > 0 ? pos - p.rules.window + 1 : 0;
             const uint64_t *bits_at = p.visible + (p.visible && valid ? c.tok + (row >> p.lg_g) : 0);
             const int nt = group_tiles(p, c, g);
-            float m_run = -INFINITY, l_run = 0.0f, rs = p.scale_log2;
+            // The running maximum and sum; and over an 8-bit cache, where a block's V has a
+            // scale of 2^E, the running maximum of score + E: what P (p 2^E) is taken
+            // relative to, so that fp16 holds all that matters to this row however far apart
+            // the scales are.
+            float m_run = -INFINITY, l_run = 0.0f, x_run = -INFINITY, rs = p.scale_log2;
             if constexpr (C::QCONV) {
                 // bf16 q over an 8-bit cache becomes fp16 times a power of two a row (K's
                 // codes are fp16; what a row's small values lose is below 2^-38 of its
@@ -592,15 +541,13 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 if (warp_live) {
                     if (C::QCONV && both && g == 1 && s == 0)
                         rs *= pow2_f32(q_exp[(item & 1) * TILE_M + r]);
-                    // a tile's factor for eight keys: an 8-bit cache's scale, the row's
-                    // own and the softmax's
-                    const float *fac = k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 16 + hf * (CW / 8);
+                    const float *fac = k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 32;
                     const bool masked = __any_sync(
                         FULL_MASK, tb + TILE - 1 > lim || tb < from ||
                                        (p.visible && tb + TILE > c.base));
-                    // keys in sight among the 32 from this thread's c0 on
+                    // keys in sight among the 32 from c0 on
                     auto in_sight = [&](int c0) -> uint32_t {
-                        const int k0 = tb + hf * CW + c0, u = lim - k0, d = from - k0;
+                        const int k0 = tb + c0, u = lim - k0, d = from - k0;
                         uint32_t w = u >= 31 ? 0xffffffffu : u < 0 ? 0u : (2u << u) - 1u;
                         if (d > 0)
                             w = d < 32 ? w & (0xffffffffu << d) : 0u;
@@ -614,11 +561,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         return w;
                     };
-                    // Half of the scores, then their maximum under way while the others come;
-                    // over an 8-bit cache (whose conversion wants registers too) one half
-                    // after the other, the second one read again for its weights.
-                    constexpr int HW = CW / 2, KEEP = F8 ? HW : CW;
-                    float v[KEEP], mx = -INFINITY;
+                    constexpr int HW = TILE / 2;
                     auto hide = [&](float *x, int h0) {
                         if (masked) {
 #pragma unroll
@@ -630,69 +573,22 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                             }
                         }
                     };
-                    auto highest = [&](const float *x, int h0) {
-                        if constexpr (F8) {
-#pragma unroll
-                            for (int k = 0; k < HW / 8; ++k)
-                                mx = fmaxf(mx, max3f(max3f(x[8 * k], x[8 * k + 1], x[8 * k + 2]),
-                                                     max3f(x[8 * k + 3], x[8 * k + 4], x[8 * k + 5]),
-                                                     fmaxf(x[8 * k + 6], x[8 * k + 7])) *
-                                                   (fac[h0 / 8 + k] * rs));
-                        } else {
-                            float t[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                            for (int j = 4; j < HW; j += 8)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    t[k] = j + 4 < HW ? max3f(t[k], x[j + k], x[j + 4 + k])
-                                                      : fmaxf(t[k], x[j + k]);
-                            mx = fmaxf(mx, max3f(fmaxf(t[0], t[1]), t[2], t[3]));
-                        }
-                    };
-                    if constexpr (F8) {
-                        tmem_ld_begin<HW>(t_s + HW, v);
-                        tmem_ld_end<HW>(v);
-                        hide(v, HW);
-                        highest(v, HW);
-                        tmem_ld_begin<HW>(t_s, v);
-                        tmem_ld_end<HW>(v);
-                        hide(v, 0);
-                        highest(v, 0);
-                    } else {
-                        tmem_ld_begin<HW>(t_s, v);
-                        tmem_ld_end<HW>(v);
-                        tmem_ld_begin<HW>(t_s + HW, v + KEEP - HW);
-                        hide(v, 0);
-                        highest(v, 0);
-                        tmem_ld_end<HW>(v + KEEP - HW);
-                        hide(v + KEEP - HW, HW);
-                        highest(v + KEEP - HW, HW);
-                        mx *= rs;                  // scale > 0: the maximum commutes
-                    }
-                    if constexpr (HT == 2) {
-                        // the row's maximum; and from here on both have read their scores, over
-                        // which the weights go.  (The slots' last reader was done before
-                        // this S was multiplied, but at an item's end.)
-                        if (!read_back())
-                            goto softmax_done;
-                        st_shared(mine, mx);
-                        if (!meet())
-                            goto softmax_done;
-                        mx = fmaxf(mx, ld_shared(other));
-                    }
-                    // The running maximum moves only when a score exceeds it by more than
+                    // The running maxima move only when a score exceeds them by more than
                     // 2^8 (or is the first in sight): below that the weights stay <= 2^8, and
                     // the quotient by the sum of the same weights is unchanged.
-                    const bool move = mx > m_run + 8.0f;
-                    const float m_new = move ? mx : m_run;
-                    const float corr = !move ? 1.0f : m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_new);
-                    m_run = m_new;
-                    // O is idle here: the P V of the previous tile finished before this S
-                    // did, the next one waits for p_full
-                    if (s > 0 && __any_sync(FULL_MASK, move)) {
+                    auto moved = [&](float &run, float mx) -> float {
+                        const float was = run;
+                        run = mx > was + 8.0f ? mx : was;
+                        return run == was ? 1.0f : was == -INFINITY ? 0.0f : ex2_approx(was - run);
+                    };
+                    // O is idle at this point: the P V of the previous tile finished before
+                    // this S did, the next one waits for p_full
+                    auto rescale = [&](float corr) {
+                        if (s == 0 || !__any_sync(FULL_MASK, corr != 1.0f))
+                            return;
                         // (rare: few registers rather than few loads)
 #pragma unroll 1
-                        for (int c0 = 0; c0 < OW; c0 += 8) {
+                        for (int c0 = 0; c0 < D; c0 += 8) {
                             float o[8];
                             uint32_t w[8];
                             tmem_ld_begin<8>(t_o + c0, o);
@@ -702,67 +598,140 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                                 w[j] = __float_as_uint(o[j] * corr);
                             tmem_st8(t_o + c0, w);
                         }
-                    }
-                    // weights, their sum, and P over the S columns: of each 64 keys the 16-bit
-                    // pairs in 32 columns, their low parts (where there are two) in the next
-                    // 32.  Eight keys a step: the exponents of one eight, the exponentials of
-                    // the one before, the rounding and summing of the one before that, so
-                    // that the three units that they run on work at once.
-                    const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_new == -INFINITY ? 0.0f : m_new);
-                    float sum[4] = {};
+                    };
                     using PT = typename std::conditional<C::PBF, __nv_bfloat16, __half>::type;
-                    auto weigh = [&](float *x, int h0, uint32_t t_p) {   // 64 keys
-                        constexpr int E = 64 / 8;
-                        uint32_t w[8], wl[8];
+                    float mx = -INFINITY;
+                    if constexpr (!F8) {
+                        // half of the scores, then their maximum under way while the others come
+                        float v[TILE];
+                        auto highest = [&](const float *x) {
+                            float t[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                            for (int j = 4; j < HW; j += 8)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    t[k] = j + 4 < HW ? max3f(t[k], x[j + k], x[j + 4 + k])
+                                                      : fmaxf(t[k], x[j + k]);
+                            mx = fmaxf(mx, max3f(fmaxf(t[0], t[1]), t[2], t[3]));
+                        };
+                        tmem_ld_begin<HW>(t_s, v);
+                        tmem_ld_end<HW>(v);
+                        tmem_ld_begin<HW>(t_s + HW, v + HW);
+                        hide(v, 0);
+                        highest(v);
+                        tmem_ld_end<HW>(v + HW);
+                        hide(v + HW, HW);
+                        highest(v + HW);
+                        const float corr = moved(m_run, mx * rs);   // (scale > 0: the maximum commutes)
+                        rescale(corr);
+                        // Weights, their sum, and P over the S columns: of each 64 keys the
+                        // 16-bit pairs in 32 columns.  Eight keys a step: the exponents of one
+                        // eight, the exponentials of the one before, the rounding and summing
+                        // of the one before that, so that the three units that they run on
+                        // work at once.
+                        const float off = (C::PBF ? 0.0f : P_SHIFT) - (m_run == -INFINITY ? 0.0f : m_run);
+                        float sum[4] = {};
+                        constexpr int E = TILE / 8;
+                        uint32_t w[8];
 #pragma unroll
                         for (int i = 0; i < E + 2; ++i) {
-                            if (i < E) {
-                                const float f = F8 ? fac[h0 / 8 + i] * rs : rs;
+                            if (i < E)
 #pragma unroll
                                 for (int j = 8 * i; j < 8 * i + 8; j += 2)
-                                    fma2_bc(x[j], x[j + 1], f, off);
-                            }
+                                    fma2_bc(v[j], v[j + 1], rs, off);
                             if (i >= 1 && i <= E)
 #pragma unroll
                                 for (int j = 8 * i - 8; j < 8 * i; ++j)
-                                    x[j] = ex2_approx(x[j]);
+                                    v[j] = ex2_approx(v[j]);
                             if (i >= 2) {
-                                const float *y = x + 8 * i - 16;
-                                const int at = (i - 2) % 2 * 4;
+                                const float *y = v + 8 * i - 16;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    w[at + j] = pack2<PT>(y[2 * j], y[2 * j + 1]);
-                                    if constexpr (C::SPLIT) {
-                                        const float2 h = unpack2<PT>(w[at + j]);
-                                        float r0 = y[2 * j], r1 = y[2 * j + 1];
-                                        add2(r0, r1, -h.x, -h.y);
-                                        wl[at + j] = pack2<PT>(r0, r1);
-                                    }
-                                }
+                                for (int j = 0; j < 4; ++j)
+                                    w[(i & 1) * 4 + j] = pack2<PT>(y[2 * j], y[2 * j + 1]);
                                 add2(sum[0], sum[1], y[0], y[1]);
                                 add2(sum[2], sum[3], y[2], y[3]);
                                 add2(sum[0], sum[1], y[4], y[5]);
                                 add2(sum[2], sum[3], y[6], y[7]);
-                                if ((i - 2) % 2 == 1) {
-                                    const uint32_t col = t_p + (i - 2) / 2 * 8;
-                                    tmem_st8(col, w);
-                                    if constexpr (C::SPLIT)
-                                        tmem_st8(col + 32, wl);
+                                if (i & 1)
+                                    tmem_st8(t_s + (i - 2) / 8 * 64 + (i - 2) % 8 / 2 * 8, w);
+                            }
+                        }
+                        l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    } else {
+                        // One half of the scores after the other, read again for their weights:
+                        // the conversion wants the registers, and the instruction cache the
+                        // loops.  A factor for eight keys: K's scale, the row's own and the
+                        // softmax's (at least the smallest normal number: -inf times it is -inf).
+                        float v[HW], mv = -INFINITY;
+                        auto factor = [&](int k) { return fmaxf(fac[k] * rs, 0x1p-126f); };
+#pragma unroll 1
+                        for (int h0 = 0; h0 < TILE; h0 += HW) {
+                            tmem_ld_begin<HW>(t_s + h0, v);
+                            tmem_ld_end<HW>(v);
+                            hide(v, h0);
+#pragma unroll
+                            for (int k = 0; k < HW / 8; ++k) {
+                                const float *x = v + 8 * k;
+                                const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
+                                                      fmaxf(x[6], x[7])) * factor(h0 / 8 + k);
+                                mx = fmaxf(mx, a);
+                                mv = fmaxf(mv, a + fac[16 + h0 / 8 + k]);
+                            }
+                        }
+                        l_run *= moved(m_run, mx);
+                        rescale(moved(x_run, mv));
+                        const float x0 = x_run == -INFINITY ? 0.0f : x_run;
+                        // The sum of p: of P = p 2^(E + 7 - x), by eights, times 2^-E and
+                        // 2^(x - 7 - m).  (Where V's scales reach so high that fp32 does not
+                        // hold the P of keys with small ones, of p itself.)
+                        const float up = x_run == -INFINITY ? 0.0f : ex2_approx(x_run - P_SHIFT - m_run);
+                        const bool far = __any_sync(FULL_MASK, x_run - m_run > 11.0f);
+                        float lt = 0.0f;
+#pragma unroll 1
+                        for (int h0 = 0; h0 < TILE; h0 += HW) {
+                            tmem_ld_begin<HW>(t_s + h0, v);
+                            tmem_ld_end<HW>(v);
+                            hide(v, h0);
+                            if (far) {
+                                const float m0 = m_run == -INFINITY ? 0.0f : m_run;
+#pragma unroll
+                                for (int j = 0; j < HW; ++j)
+                                    l_run += ex2_approx(fmaf(v[j], factor((h0 + j) / 8), -m0));
+                            }
+                            constexpr int E = HW / 8;
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < E + 2; ++i) {      // (steps as above)
+                                if (i < E) {
+                                    const float f = factor(h0 / 8 + i);
+                                    const float off = fac[16 + h0 / 8 + i] + (P_SHIFT - x0);
+#pragma unroll
+                                    for (int j = 8 * i; j < 8 * i + 8; j += 2)
+                                        fma2_bc(v[j], v[j + 1], f, off);
+                                }
+                                if (i >= 1 && i <= E)
+#pragma unroll
+                                    for (int j = 8 * i - 8; j < 8 * i; ++j)
+                                        v[j] = ex2_approx(v[j]);
+                                if (i >= 2) {
+                                    float *y = v + 8 * i - 16;
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        w[(i & 1) * 4 + j] = pack2<PT>(y[2 * j], y[2 * j + 1]);
+                                    add2(y[0], y[1], y[2], y[3]);
+                                    add2(y[4], y[5], y[6], y[7]);
+                                    add2(y[0], y[1], y[4], y[5]);
+                                    lt = fmaf(y[0] + y[1],
+                                              pow2_f32(-(int)fac[16 + h0 / 8 + i - 2]), lt);
+                                    if (i & 1)
+                                        tmem_st8(t_s + h0 + (i - 2) / 2 * 8, w);
                                 }
                             }
                         }
-                    };
-                    weigh(v, 0, t_s);
-                    if constexpr (F8) {
-                        tmem_ld_begin<HW>(t_s + HW, v);
-                        tmem_ld_end<HW>(v);
-                        hide(v, HW);
-                        weigh(v, HW, t_s + HW);
-                    } else if constexpr (HT == 1) {
-                        weigh(v + KEEP - HW, HW, t_s + HW);
+                        if (!far)
+                            l_run = fmaf(lt, up, l_run);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                     tc_fence_before();
                 }
                 __syncwarp();
@@ -775,64 +744,57 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             const int nt1 = both ? group_tiles(p, c, 1) : 0;
             if (nt > 0 && !phase(&o_done[g], P_O))
                 goto softmax_done;
-            if (HT == 2 && warp_live && nt > 0) {  // (nothing reads the maxima any more: O is done)
-                if (!read_back())
-                    goto softmax_done;
-                st_shared(mine, l_run);
-                if (!meet())
-                    goto softmax_done;
-                l_run += ld_shared(other);
-                if (!meet())                       // both have read
-                    goto softmax_done;
-            }
+            // O to units of p: over an 8-bit cache it holds P's, and V_SHIFT below
+            float a0 = !F8 ? 1.0f : x_run == -INFINITY ? 0.0f
+                                  : ex2_approx(x_run - m_run - (P_SHIFT + V_SHIFT)), a1 = 0.0f;
             if (g == 1 && both) {
                 // hand the state over: the first group reads it and this group's O
                 if (nt > 0) {
-                    if (!read_back())
+                    if ((ph & LENT) && !__all_sync(FULL_MASK, wait(ml_free, (ph & P_ML) ? 0u : 1u)))
                         goto softmax_done;
-                    if (hf == 0)
-                        xm[C::XM1 + r] = l_run;
-                    if (hf == HT - 1)
-                        xm[C::XM1 + TILE_M + r] = m_run;
+                    ml[r] = l_run;
+                    ml[TILE_M + r] = m_run;
+                    if (F8)
+                        ml[2 * TILE_M + r] = a0;
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(ml_full);
-                    ph ^= P_ML | LENT;
+                    ph = (ph ^ P_ML) | LENT;
                 }
                 done(item);
                 continue;
             }
-            float a0 = 1.0f, a1 = 0.0f;
             if (g == 0 && !both)
                 ph ^= P_O1;                        // (the second group waits for its own)
             if (nt1 > 0) {
                 if (!phase(&o_done[1], P_O1) || !phase(ml_full, P_ML))
                     goto softmax_done;
-                const float l1 = xm[C::XM1 + r], n1 = xm[C::XM1 + TILE_M + r];
+                const float l1 = ml[r], n1 = ml[TILE_M + r], b1 = F8 ? ml[2 * TILE_M + r] : 1.0f;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(ml_free);
                 const float m = fmaxf(m_run, n1);
-                a0 = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m);
-                a1 = n1 == -INFINITY ? 0.0f : ex2_approx(n1 - m);
+                const float w0 = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m);
+                const float w1 = n1 == -INFINITY ? 0.0f : ex2_approx(n1 - m);
+                a0 *= w0;
+                a1 = b1 * w1;
                 m_run = m;
-                l_run = l_run * a0 + l1 * a1;
+                l_run = l_run * w0 + l1 * w1;
             }
             tc_fence_after();
             if (warp_live) {
-                const float vs = F8 ? (float)(1 << V_SHIFT) : 1.0f;
                 if (c.kind == 0) {
-                    const float inv = l_run == 0.0f ? 0.0f : vs / l_run;
+                    const float inv = l_run == 0.0f ? 0.0f : (F8 ? (float)(1 << V_SHIFT) : 1.0f) / l_run;
                     a0 *= inv;
                     a1 *= inv;
                 }
                 T *out = static_cast<T *>(p.out) +
                          ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
-                          (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D + hf * OW;
+                          (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D;
                 float *states = p.part + ((int64_t)blockIdx.x * 2 + (c.kind == 2)) * C::ROWS * (D + 2);
-                float *part = states + (int64_t)row * D + hf * OW;
+                float *part = states + (int64_t)row * D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < OW; c0 += 32) {
+                for (int c0 = 0; c0 < D; c0 += 32) {
                     float o[32];
                     if (nt > 0) {
                         tmem_ld32(t_o + c0, o);
@@ -863,7 +825,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                                 make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                 }
-                if (c.kind && valid && hf == 0)
+                if (c.kind && valid)
                     *reinterpret_cast<float2 *>(states + C::ROWS * D + 2 * row) = make_float2(m_run, l_run);
             }
             tc_fence_before();
@@ -949,8 +911,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             done(item);
         }
     } else if (F8 && warp < W0 + 4) {
-        // ================= bring and convert tiles of an 8-bit cache: K's codes to fp16, V's
-        // values to bf16; this warp's 32 rows.  The codes come through registers, a tile ahead
+        // ================= bring and convert tiles of an 8-bit cache: codes to fp16, this
+        // warp's 32 rows.  The codes come through registers, a tile ahead
         // (through shared memory they would take as much of its bandwidth again as the
         // converted tiles' writing does, and room for a slot of each).
         const int w0 = (warp - W0) * 32, H = p.num_kv_heads;
@@ -1023,8 +985,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             for (int t = c.t0; t < c.t1; ++t, ++gt) {
                 const int slot = gt % NS;
                 const uint32_t count = count1;
-                const float kf = pow2_f32(block_exponent(ks));
-                const float vf = pow2_f32(block_exponent(vs) - V_SHIFT);
+                const float kf = pow2_f32(block_exponent(ks)), ve = (float)block_exponent(vs);
                 ids = ids1;
                 ids1 = block_of(t + 2);
                 scales(ids);
@@ -1032,8 +993,11 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 // K
                 if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&k_empty[slot], gt / NS + 1))))
                     break;
-                if (lane < 4)
-                    k_sc[(gt & (C::RING - 1)) * 16 + (w0 >> 3) + lane] = kf;
+                if (lane < 4) {
+                    float *sc = k_sc + (gt & (C::RING - 1)) * 32 + (w0 >> 3) + lane;
+                    sc[0] = kf;
+                    sc[16] = ve;
+                }
                 unsigned char *dst = sK + slot * C::KV_BYTES;
                 clear(kd, count);
 #pragma unroll
@@ -1054,10 +1018,9 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 clear(vd, count);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const float f = __shfl_sync(FULL_MASK, vf, (i * RPI) >> 3);
                     uint4 lo, hi;
                     codes_to_half(vd[i], lo, hi);
-                    put_chunks<D>(dst, w0 + i * RPI + rr, j, scaled_bf16(lo, f), scaled_bf16(hi, f));
+                    put_chunks<D>(dst, w0 + i * RPI + rr, j, lo, hi);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -1112,7 +1075,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         // eight rows behind both.  A step of 16 along the contraction is 32 bytes into S's
         // rows, 16 rows of V.
         constexpr uint32_t Q_PANEL = TILE_M * 128;
-        const uint32_t idesc_s = umma_idesc(BF && !F8 ? 1u : 0u, 0u, TILE);
+        const uint32_t idesc_s = umma_idesc(C::PBF ? 1u : 0u, 0u, TILE);
         const uint32_t idesc_o = umma_idesc(C::PBF ? 1u : 0u, 1u, D);
         // (an allocation of all of tensor memory starts at its first column)
         constexpr uint32_t tm = 0;
@@ -1177,9 +1140,6 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         const uint32_t pa = base + ks / 4 * 64 + ks % 4 * 8;
                         umma_f16_ta_elected(el, base + TILE, pa, vb + ks * (C::GROUP8 / 8), v_hi,
                                             idesc_o, s > 0 || ks > 0 ? 1u : 0u);
-                        if (C::SPLIT)
-                            umma_f16_ta_elected(el, base + TILE, pa + 32, vb + ks * (C::GROUP8 / 8),
-                                                v_hi, idesc_o, 1u);
                     }
                     if (both || g == 1)            // the tile's last reader
                         umma_commit_elected(el, &v_empty[slot]);
@@ -1248,7 +1208,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
         for (int u = warp < base % warps ? base - base % warps + warps + warp : base - base % warps + warp;
              u < base + units; u += warps) {
             const int k = (u - base) / per, row = ((u - base) - k * per) * 4 + sub;
-            const int src = __fns(some, 0, k + 1);         // the k-th share's lane
+            // the k-th share's lane
+            const int src = __ffs(__ballot_sync(FULL_MASK, mine > 0 && __popc(some & ((1u << lane) - 1)) == k)) - 1;
             const int pieces = __shfl_sync(FULL_MASK, mine, src), c = s0 + src;
             const int4 item = reinterpret_cast<const int4 *>(p.places + p.items_at)[c];
             if (row - sub >= item.y)

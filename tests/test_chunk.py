@@ -121,14 +121,14 @@ def reference(s, scale, window=0):
     scale sum_d |q_d k_d| (an MMA may truncate), plus its roundings to the log2 domain: e =
     (D / 16 + 4) 2^-22 a, and 2^-22 for the exponential.  Numerator and denominator each carry
     that and their own accumulations, n / 16 + 15 roundings of 2^-22.  A weight enters the product
-    rounded to u: half a step of the type (two bf16 parts of an fp16 q over e4m3: 2^-16); as fp16,
-    times 2^7 below the running maximum's 2^8, a weight is off by 2^-32 of the largest at
-    least.  The quotient is rounded once more, to the output's type, half a step."""
+    rounded to u: half a step of q's type, and over e4m3 of fp16 (what the codes are multiplied
+    as); as fp16, times 2^7 below the running maximum's 2^8, a weight (times its block's scale)
+    is off by 2^-32 of the largest at least.  The quotient is rounded once more, to the output's type, half a step."""
     H, D, G = s["H"], s["D"], s["hq"] // s["H"]
     out = torch.full((s["T"], s["hq"], D), math.nan, dtype=torch.float64)
     lim = torch.zeros_like(out)
     u_out = HALF_STEP[s["dtype"]]
-    u_p = u_out if s["kv"] != "f8" or s["dtype"] == "bf16" else 2.0 ** -16
+    u_p = u_out if s["kv"] != "f8" else HALF_STEP["f16"]
     for b, (L, n) in enumerate(zip(s["lens"], s["new"])):
         if n == 0:
             continue
