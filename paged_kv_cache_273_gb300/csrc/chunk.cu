@@ -51,6 +51,7 @@ struct ChunkParams {
     int32_t *places;              // [0]: shares; from [8] on a share's pieces to join; from
                                   // [items_at] on their item: token, rows, KV head
     int items_at;
+    uint32_t share_step;          // 2^32 / the grid's CTAs
     float *part;                  // 2 states a CTA: that of its first piece, and of its last
     unsigned int *err;
     int batch, num_tokens, max_q_len, num_q_heads, num_kv_heads, lg_g;
@@ -228,7 +229,7 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
     // first the sum, then the two places (one body, for the instruction cache's sake)
 #pragma unroll 1
     for (int k = -1; k < 2; ++k) {
-        int64_t x = k < 0 ? -1 : chunk::share_start(U, n, c + k) - before;
+        int64_t x = k < 0 ? -1 : chunk::share_start(U, n, c + k, gridDim.x, p.share_step) - before;
         if (k >= 0 && (x < 0 || x >= mine))
             continue;
         int64_t sum = 0;
@@ -278,33 +279,15 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
             places[1] = e;
         }
     }
+    if (tid == 0)
+        sums[NT / 32] = U;
     __syncthreads();
-    if (tid == 0) {
-        // for the joining: the item that this share starts within, if it is the first to do so,
-        // its pieces, its first token and its rows
-        const Place &a = places[0];
-        int4 item = make_int4(0, 0, 0, 0);
-        int pieces = 0;
-        if (a.split) {
-            Seq q;
-            int q0, lo, hi;
-            bool bad;
-            Walk::lengths(p, a.b, q, q0, bad);
-            chunk::tiles(p.rules, q, a.rt, lo, hi);
-            // positions on the line: where the item may first be cut, and its end
-            const int64_t x = chunk::share_start(U, n, c), first = x - (a.tile - lo), end = first + (hi - lo);
-            if (chunk::share_start(U, n, c - 1) <= first) {
-                pieces = 2;
-                while (c + pieces - 1 < n && chunk::share_start(U, n, c + pieces - 1) < end)
-                    ++pieces;
-            }
-            item = make_int4(q0 + (a.rt << p.rules.lg_tpr),
-                             min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, a.h, 0);
-        }
-        p.places[8 + c] = pieces;
-        reinterpret_cast<int4 *>(p.places + p.items_at)[c] = item;
-    }
     return true;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // One block's rows (or 128 of them) of one KV head, from its group `y` of eight on.
@@ -316,6 +299,34 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
         " [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
+}
+
+// For the joining (one thread, of a warp that is done): the item that this share starts within,
+// if the share is the first to do so, its pieces, its first token and its rows.
+__device__ __forceinline__ void note_item(const ChunkParams &p, const Place &a, int64_t U)
+{
+    const int c = blockIdx.x, n = chunk::shares(U, gridDim.x);
+    int4 item = make_int4(0, 0, 0, 0);
+    int pieces = 0;
+    if (a.split) {
+        Seq q;
+        int q0, lo, hi;
+        bool bad;
+        Walk::lengths(p, a.b, q, q0, bad);
+        chunk::tiles(p.rules, q, a.rt, lo, hi);
+        auto start = [&](int k) { return chunk::share_start(U, n, k, gridDim.x, p.share_step); };
+        // positions on the line: where the item may first be cut, and its end
+        const int64_t first = start(c) - (a.tile - lo), end = first + (hi - lo);
+        if (start(c - 1) <= first) {
+            pieces = 2;
+            while (c + pieces - 1 < n && start(c + pieces - 1) < end)
+                ++pieces;
+        }
+        item = make_int4(q0 + (a.rt << p.rules.lg_tpr),
+                         min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, a.h, 0);
+    }
+    p.places[8 + c] = pieces;
+    reinterpret_cast<int4 *>(p.places + p.items_at)[c] = item;
 }
 
 // 16 e4m3 codes -> 16 fp16 values (exact), as two 16-byte chunks.
@@ -419,10 +430,19 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     Piece *pieces = reinterpret_cast<Piece *>(smem + C::OFF_MISC + 16);    // (over the two above)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        prefetch_map(&p.tm_q);
+        if (!F8) {
+            prefetch_map(&p.tm_k);
+            prefetch_map(&p.tm_v);
+        }
+    }
     grid_dependency_wait();
     grid_dependents_launch();
     if (!find_share<C::NT>(p, places, sums))
         return;
+    const Place begin = places[0];
+    const int64_t line = sums[C::NT / 32];
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&k_full[i], F8 ? 4 : 2);
@@ -791,8 +811,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 T *out = static_cast<T *>(p.out) +
                          ((int64_t)(c.tok + (row >> p.lg_g)) * p.num_q_heads +
                           (c.h << p.lg_g) + (row & ((1 << p.lg_g) - 1))) * D;
+                // a state: of each four columns all rows' side by side, then maxima and sums
                 float *states = p.part + ((int64_t)blockIdx.x * 2 + (c.kind == 2)) * C::ROWS * (D + 2);
-                float *part = states + (int64_t)row * D;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float o[32];
@@ -821,7 +841,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4 *>(part + c0 + 4 * j) =
+                            *reinterpret_cast<float4 *>(states + ((c0 / 4 + j) * C::ROWS + row) * 4) =
                                 make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
                 }
@@ -910,6 +930,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             }
             done(item);
         }
+        if (is_k && lane == 0)
+            note_item(p, begin, line);
     } else if (F8 && warp < W0 + 4) {
         // ================= bring and convert tiles of an 8-bit cache: codes to fp16, this
         // warp's 32 rows.  The codes come through registers, a tile ahead
@@ -1030,6 +1052,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             }
             done(item);
         }
+        if (warp == W0 && lane == 0)
+            note_item(p, begin, line);
     } else if (warp == C::W_FEED) {
         // ================= hand out the share's pieces, one ahead of the one whose q is
         // brought (once the last S before has read its own)
@@ -1186,84 +1210,69 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     }
 }
 
-// Items that were cut: the states of an item's pieces joined in the order of the keys, four
-// rows a warp, eight lanes a row.  Warps count off the shares that an item to join is noted
-// with, so that those without cost a look at a word each, and take their rows in turn.
+// Items that were cut: the states of an item's pieces joined in the order of the keys, eight
+// columns of 32 rows a warp, a lane a row.  Warps count off the shares that an item to join is
+// noted with, so that those without cost a look at a word each, and take their units in turn.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
-                                                         int item_rows, int per, float v_scale)
+                                                         int item_rows, int row_blocks, float v_scale)
 {
     grid_dependency_wait();
     grid_dependents_launch();
-    const int n = p.places[0], lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
+    const int n = p.places[0], lane = threadIdx.x & 31;
     const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
     const int64_t state = (int64_t)item_rows * (D + 2);
-    constexpr int W = D / 32;                              // float4s of a lane
-    int base = 0;                                          // units of the shares looked at
+    constexpr int CG = D / 8;                              // groups of eight columns
+    const int per = row_blocks * CG;                       // units of an item
+    int u = warp;                                          // this warp's next unit, from here on
     for (int s0 = 0; s0 < n; s0 += 32) {
         const int mine = s0 + lane < n ? p.places[8 + s0 + lane] : 0;
         const unsigned some = __ballot_sync(FULL_MASK, mine > 0);
         const int units = __popc(some) * per;
-        // this warp's units among them: `per` of four rows for each share
-        for (int u = warp < base % warps ? base - base % warps + warps + warp : base - base % warps + warp;
-             u < base + units; u += warps) {
-            const int k = (u - base) / per, row = ((u - base) - k * per) * 4 + sub;
+        for (; u < units; u += warps) {
+            const int k = u / per, v = u - k * per;
+            const int row = v / CG * 32 + lane, col = v % CG;
             // the k-th share's lane
             const int src = __ffs(__ballot_sync(FULL_MASK, mine > 0 && __popc(some & ((1u << lane) - 1)) == k)) - 1;
             const int pieces = __shfl_sync(FULL_MASK, mine, src), c = s0 + src;
             const int4 item = reinterpret_cast<const int4 *>(p.places + p.items_at)[c];
-            if (row - sub >= item.y)
-                continue;
-            const bool valid = row < item.y;
+            if (row >= item.y)
+                continue;                                  // (no exchange from here on)
             // piece i: the last state of share c - 1, then the first ones of c, c + 1, ..
             const float *start = p.part + (2 * (int64_t)(c - 1) + 1) * state;
             auto piece = [&](int i) -> const float * {
                 return i == 0 ? start : start + (2 * (int64_t)i - 1) * state;
             };
-            const int64_t sum_at = item_rows * D + 2 * row, o_at = (int64_t)row * D + 4 * j;
-            float m = -INFINITY;
-            for (int i = j; i < pieces; i += 8) {
-                const float2 s = valid ? *reinterpret_cast<const float2 *>(piece(i) + sum_at)
-                                       : make_float2(0.0f, 0.0f);
-                m = s.y != 0.0f ? fmaxf(m, s.x) : m;
+            float m = -INFINITY, l = 0.0f, acc[8] = {};
+#pragma unroll 4
+            for (int i = 0; i < pieces; ++i) {
+                const float2 ml = *reinterpret_cast<const float2 *>(piece(i) + item_rows * D + 2 * row);
+                m = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
             }
-#pragma unroll
-            for (int d = 4; d >= 1; d >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, d));
-            if (!valid)
-                continue;                                  // (no shuffles from here on)
-            float acc[4 * W] = {}, l = 0.0f;
 #pragma unroll 4
             for (int i = 0; i < pieces; ++i) {
                 const float *s = piece(i);
-                const float2 ml = *reinterpret_cast<const float2 *>(s + sum_at);
-                float4 o[W];
-#pragma unroll
-                for (int q = 0; q < W; ++q)
-                    o[q] = *reinterpret_cast<const float4 *>(s + o_at + 32 * q);
+                const float2 ml = *reinterpret_cast<const float2 *>(s + item_rows * D + 2 * row);
+                const float4 o0 = *reinterpret_cast<const float4 *>(s + (2 * col * item_rows + row) * 4);
+                const float4 o1 = *reinterpret_cast<const float4 *>(s + ((2 * col + 1) * item_rows + row) * 4);
                 // (a piece that has none of the row's keys in sight may have written no O)
                 const bool none = ml.y == 0.0f;
                 const float w = none || ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
                 l = fmaf(w, ml.y, l);
+                const float x[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
 #pragma unroll
-                for (int q = 0; q < W; ++q) {
-                    acc[4 * q] = none ? acc[4 * q] : fmaf(w, o[q].x, acc[4 * q]);
-                    acc[4 * q + 1] = none ? acc[4 * q + 1] : fmaf(w, o[q].y, acc[4 * q + 1]);
-                    acc[4 * q + 2] = none ? acc[4 * q + 2] : fmaf(w, o[q].z, acc[4 * q + 2]);
-                    acc[4 * q + 3] = none ? acc[4 * q + 3] : fmaf(w, o[q].w, acc[4 * q + 3]);
-                }
+                for (int d = 0; d < 8; ++d)
+                    acc[d] = none ? acc[d] : fmaf(w, x[d], acc[d]);
             }
             const float inv = l == 0.0f ? 0.0f : v_scale / l;
             T *out = static_cast<T *>(p.out) +
                      ((int64_t)(item.x + (row >> p.lg_g)) * p.num_q_heads + (item.z << p.lg_g) +
-                      (row & ((1 << p.lg_g) - 1))) * D + 4 * j;
-#pragma unroll
-            for (int q = 0; q < W; ++q)
-                *reinterpret_cast<uint2 *>(out + 32 * q) =
-                    make_uint2(pack2<T>(acc[4 * q] * inv, acc[4 * q + 1] * inv),
-                               pack2<T>(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
+                      (row & ((1 << p.lg_g) - 1))) * D + 8 * col;
+            *reinterpret_cast<uint4 *>(out) =
+                make_uint4(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv),
+                           pack2<T>(acc[4] * inv, acc[5] * inv), pack2<T>(acc[6] * inv, acc[7] * inv));
         }
-        base += units;
+        u -= units;
     }
 }
 
@@ -1323,7 +1332,7 @@ int launch_chunk_t(const pkv_pool *pool, const ChunkParams &p, cudaStream_t s)
         return PKV_ERR_CUDA;
     if (sms > 1 && launch_pdl(chunk_join_kernel<D, T>, dim3((unsigned)(4 * sms)), dim3(256),
                               0, s, p, (int)C::ROWS,
-                              (int)((std::min<int64_t>(C::ROWS, (int64_t)p.max_q_len << p.lg_g) + 3) / 4), F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
+                              (int)((std::min<int64_t>(C::ROWS, (int64_t)p.max_q_len << p.lg_g) + 31) / 32), F8 ? (float)(1 << V_SHIFT) : 1.0f) != cudaSuccess)
         return PKV_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1371,6 +1380,7 @@ int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num
     p.out = out;
     p.places = static_cast<int32_t *>(workspace);
     p.items_at = items_at(pool);
+    p.share_step = chunk::share_step(std::max(1, pool->num_sms));
     p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + places_bytes(pool));
     p.err = pool->d_err;
     p.batch = batch;

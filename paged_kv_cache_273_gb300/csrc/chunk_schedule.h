@@ -104,8 +104,15 @@ PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x, int64_t c)
 {
     Place p;
     p.b = b;
-    p.h = (int)(x / c);
-    x -= p.h * c;
+    // x / c, by an estimate that is put right (a division of 64-bit integers is a hundred
+    // instructions, and the start of a kernel waits for all of those that it runs)
+    int64_t h = (int64_t)((float)x / (float)c);
+    while (h * c > x)
+        --h;
+    while ((h + 1) * c <= x)
+        ++h;
+    p.h = (int)h;
+    x -= h * c;
     int a = 0, e = row_tiles(r, q) - 1;               // the last row tile that starts by x
     int64_t before = 0;                               // and the cost before it
     while (a < e) {
@@ -127,19 +134,31 @@ PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x, int64_t c)
     return p;
 }
 
-// Shares for a line of length U on `ctas` CTAs: none of them shorter than MIN_SHARE
+// Shares for a line of length U on `ctas` CTAs: equal ones, but none shorter than MIN_SHARE
 // (a share of a tile or two costs more in its start and in the joining of its state
 // than it saves).
 constexpr int MIN_SHARE = 4;
 PKV_HD int shares(int64_t U, int ctas)
 {
-    const int64_t n = U / MIN_SHARE;
-    return n < 1 ? 1 : n < ctas ? (int)n : ctas;
+    return U >= (int64_t)MIN_SHARE * ctas ? ctas : U < MIN_SHARE ? 1 : (int)(U / MIN_SHARE);
 }
-PKV_HD int64_t share_start(int64_t U, int n, int c)
+// 2^32 / ctas, rounded up: what share_start multiplies by instead of dividing.
+inline uint32_t share_step(int ctas) { return (uint32_t)((((uint64_t)1 << 32) + ctas - 1) / ctas); }
+
+// Where share c of n (or the line's end, c = n) starts.
+PKV_HD int64_t share_start(int64_t U, int n, int c, int ctas, uint32_t step)
 {
-    // U c / n without a product beyond 64 bits
-    return U / n * c + U % n * c / n;
+    if (c >= n)
+        return U;
+    if (n < ctas)
+        return (int64_t)c * MIN_SHARE;
+    // U c step / 2^32: the product c step is below 2^32 for c < ctas
+    const uint64_t f = (uint64_t)c * step;
+#if defined(__CUDA_ARCH__)
+    return (int64_t)__umul64hi((uint64_t)U, f << 32);
+#else
+    return (int64_t)(((unsigned __int128)(uint64_t)U * f) >> 32);
+#endif
 }
 
 }  // namespace chunk
