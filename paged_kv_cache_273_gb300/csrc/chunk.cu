@@ -1111,7 +1111,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         const uint32_t q_hi = (uint32_t)(dq >> 32), k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
         // per group, a bit each: the parity of p_full's and o_free's next phase, and whether O
         // holds an earlier piece's
-        uint32_t gt = 0, p_par = 0, of_par = 0, used = 0;
+        uint32_t gt = 0, p_par = 0, of_par = 0, used = 0, k_seen = 0, v_seen = 0;
         bool ok = true;
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(FULL_MASK, wait(bar, parity));
@@ -1138,10 +1138,16 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 const bool more = s + 1 < nt;
                 const uint32_t k = gt + (both ? 2 * s + g : s), slot = k % NS;
                 const uint32_t k1 = k + (both ? 2 : 1), slot1 = k1 % NS;
-                if ((s >= 0 && !wait_all(&v_full[slot], k / NS)) ||
-                    (more && !wait_all(&k_full[slot1], k1 / NS))) {
-                    ok = false;
-                    break;
+                // (a tile that both groups read is waited for once)
+                if (s >= 0 && (int)(k - v_seen) >= 0) {
+                    if (!(ok = wait_all(&v_full[slot], k / NS)))
+                        break;
+                    v_seen = k + 1;
+                }
+                if (more && (int)(k1 - k_seen) >= 0) {
+                    if (!(ok = wait_all(&k_full[slot1], k1 / NS)))
+                        break;
+                    k_seen = k1 + 1;
                 }
                 const uint32_t base = tm + g * C::GROUP_COLS;
                 if (s >= 0) {
