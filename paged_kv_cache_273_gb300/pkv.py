@@ -246,6 +246,8 @@ class Pool:
         self.num_kv_heads = num_kv_heads
         self.head_dim = head_dim
         self.kv_dtype = kv_dtype
+        self.cache_shape = (num_blocks, num_kv_heads, block_size,
+                            head_dim // 2 if kv_dtype == PKV_I4 else head_dim)
 
     def close(self):
         if self.handle:
@@ -814,7 +816,9 @@ class RopePlan:
             raise ValueError("layout must be one of %s" % ", ".join(ROPE_LAYOUTS))
         self.freqs = torch.from_numpy(freqs.view(np.int64).copy()).to(device)
         self.rot_dim, self.layout, self.magnitude = 2 * freqs.size, layout, magnitude
+        self.device = self.freqs.get_device()
         self.struct = Rope(self.freqs.data_ptr(), self.rot_dim, ROPE_LAYOUTS[layout], magnitude)
+        self.ref = ctypes.byref(self.struct)
 
 
 def rope_plan(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "plain",
@@ -826,26 +830,51 @@ def rope_plan(rot_dim: int, base: float = 10000.0, layout: str = "half", scaling
     return RopePlan(freqs, mag, layout, device)
 
 
-def _head_rows(name: str, t, dtype, heads, head_dim):
-    """The pointer and token stride of rows [T, heads, head_dim] whose heads lie side by side:
-    a contiguous tensor, or a slice of one projection's output."""
-    _shaped(name, t, dtype, (None, heads, head_dim))
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    T, H, D = t.shape
+# The current device's number without torch.cuda's own checks, where this torch has it (as
+# _raw_stream: the calls below cost the host about as much as a small batch costs the GPU).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _elsewhere(name: str, dev: int):
+    raise ValueError("%s must be on the current device (cuda:%d)" % (name, dev))
+
+
+def _flat(name: str, t, dtype, shape, dev: int) -> int:
+    """The pointer of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape:
+        _shaped(name, t, dtype, shape)
+    if t.get_device() != dev:
+        _elsewhere(name, dev)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _head_rows(name: str, t, dtype, shape, dev: int):
+    """The pointer and token stride of rows [T, heads, D] whose heads lie side by side: a
+    contiguous tensor, or a slice of one projection's output."""
+    if t.dtype is not dtype or t.shape != shape:
+        _shaped(name, t, dtype, shape)
+    T, H, D = shape
     if T == 0 or H == 0:
         return 0, H * D
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if t.get_device() != dev:
+        _elsewhere(name, dev)
+    step, head, one = t.stride()
+    if one != 1 or (head != D and H > 1):
         raise ValueError("%s: a token's heads must lie side by side" % name)
-    return t.data_ptr(), t.stride(0) if T > 1 else max(t.stride(0), H * D)
+    return t.data_ptr(), step if T > 1 else max(step, H * D)
 
 
-def _on_current(*tensors) -> None:
-    """Kernels run on the current device: raise for a tensor on another."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError("expected tensors on the current device (cuda:%d)" % cur)
+def _scales_of(pool: Pool, k_scales, v_scales, dev: int):
+    """Pointers of an 8-bit float pool's scales (others have none here)."""
+    if pool.kv_dtype != PKV_F8:
+        return None, None
+    if k_scales is None or v_scales is None:
+        raise ValueError("8-bit float pools need k_scales and v_scales")
+    shape = (pool.num_blocks, pool.num_kv_heads)
+    return (_flat("k_scales", k_scales, _F32, shape, dev),
+            _flat("v_scales", v_scales, _F32, shape, dev))
 
 
 def kv_rope_rotate(rope: RopePlan, x, positions, out=None, transposed: bool = False,
@@ -853,19 +882,25 @@ def kv_rope_rotate(rope: RopePlan, x, positions, out=None, transposed: bool = Fa
     """Rotate the heads x [T, heads, D] to their positions (see include/pkv.h), into `out`
     (default: a new tensor; x itself: in place), which is returned.  x and out may be slices
     of wider rows.  transposed: the rotation's gradient."""
-    if x.dim() != 3 or x.dtype not in PKV_DTYPE:
+    dt = x.dtype
+    if x.dim() != 3 or dt not in PKV_DTYPE:
         raise ValueError("x must be [T, heads, D] of float32, float16 or bfloat16")
-    T, H, D = x.shape
+    shape = x.shape
+    T, H, D = shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    xp, xs = _head_rows("x", x, x.dtype, H, D)
-    op, os_ = _head_rows("out", out, x.dtype, H, D)
-    _shaped("out", out, x.dtype, (T, H, D))
-    _shaped("positions", positions, _I32, (T,))
-    _on_current(x, out, positions, rope.freqs)
-    _check(load().kv_rope_rotate(ctypes.byref(rope.struct), xp, xs, PKV_DTYPE[x.dtype], H, D,
-                                 _dptr(positions), T, int(transposed), op, os_,
-                                 _stream(stream)), "kv_rope_rotate")
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev = _current_device()
+    xp, xs = _head_rows("x", x, dt, shape, dev)
+    op, os_ = _head_rows("out", out, dt, shape, dev)
+    pos = _flat("positions", positions, _I32, (T,), dev)
+    if rope.device != dev:
+        _elsewhere("rope", dev)
+    st = load().kv_rope_rotate(rope.ref, xp, xs, PKV_DTYPE[dt], H, D, pos, T,
+                               1 if transposed else 0, op, os_, _stream(stream))
+    if st < 0:
+        raise PkvError(st, "kv_rope_rotate")
     return out
 
 
@@ -874,37 +909,37 @@ def kv_rope_append(pool: Pool, rope: RopePlan, q, k, v, positions, slot_mapping,
     """Rotate q [T, Hq, D] into q_out and K [T, Hkv, D] into the cache, V beside it, in one
     kernel (see include/pkv.h).  q, k and v may be slices of one projection's output; q None:
     K and V only."""
-    if k.dtype not in PKV_DTYPE:
-        raise ValueError("unsupported k dtype %s" % k.dtype)
-    H, D, T = pool.num_kv_heads, pool.head_dim, k.shape[0]
-    kp, ks = _head_rows("k", k, k.dtype, H, D)
-    vp, vs = _head_rows("v", v, k.dtype, H, D)
-    _shaped("v", v, k.dtype, (T, H, D))
-    _shaped("positions", positions, _I32, (T,))
-    _shaped("slot_mapping", slot_mapping, _I32, (T,))
-    qp = qs = op = os_ = Hq = 0
+    dt = k.dtype
+    if dt not in PKV_DTYPE:
+        raise ValueError("unsupported k dtype %s" % dt)
+    if not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    T, H, D = k.shape[0], pool.num_kv_heads, pool.head_dim
+    dev = _current_device()
+    rows = (T, H, D)
+    kp, ks = _head_rows("k", k, dt, rows, dev)
+    vp, vs = _head_rows("v", v, dt, rows, dev)
+    qp = op = None
+    qs = os_ = Hq = 0
     if q is not None:
-        _shaped("q", q, k.dtype, (T, None, D))
+        if q.dim() != 3:
+            _shaped("q", q, dt, (T, None, D))
         Hq = q.shape[1]
-        qp, qs = _head_rows("q", q, k.dtype, Hq, D)
-        _shaped("q_out", q_out, k.dtype, (T, Hq, D))
-        op, os_ = _head_rows("q_out", q_out, k.dtype, Hq, D)
-        _on_current(q, q_out)
-    _on_current(k, v, positions, slot_mapping, rope.freqs)
-    _cache_of(pool, k_cache, v_cache)
-    _check_scales(pool, k_scales, v_scales)
-    _check(load().kv_rope_append(pool.handle, ctypes.byref(rope.struct), qp, qs, kp, ks, vp, vs,
-                                 PKV_DTYPE[k.dtype], Hq, _dptr(positions), _dptr(slot_mapping), T,
-                                 op, os_, _dptr(k_cache), _dptr(v_cache), _dptr(k_scales),
-                                 _dptr(v_scales), _stream(stream)), "kv_rope_append")
-
-
-def _cache_of(pool: Pool, *caches) -> None:
-    """Raise unless these are caches of the pool's shape and type."""
-    shape = (pool.num_blocks, pool.num_kv_heads, pool.block_size, pool.head_dim)
-    for c in caches:
-        if c.shape != shape or c.dtype is not TORCH_DTYPE[pool.kv_dtype]:
-            _shaped("a cache", c, TORCH_DTYPE[pool.kv_dtype], shape)
+        rows = (T, Hq, D)
+        qp, qs = _head_rows("q", q, dt, rows, dev)
+        op, os_ = _head_rows("q_out", q_out, dt, rows, dev)
+    if rope.device != dev:
+        _elsewhere("rope", dev)
+    cache, ct = pool.cache_shape, TORCH_DTYPE[pool.kv_dtype]
+    ksp, vsp = _scales_of(pool, k_scales, v_scales, dev)
+    st = load().kv_rope_append(pool.handle, rope.ref, qp, qs, kp, ks, vp, vs, PKV_DTYPE[dt], Hq,
+                               _flat("positions", positions, _I32, (T,), dev),
+                               _flat("slot_mapping", slot_mapping, _I32, (T,), dev), T, op, os_,
+                               _flat("k_cache", k_cache, ct, cache, dev),
+                               _flat("v_cache", v_cache, ct, cache, dev), ksp, vsp,
+                               _stream(stream))
+    if st < 0:
+        raise PkvError(st, "kv_rope_append")
 
 
 # ------------------------------------------------------------- chunks of new tokens
@@ -928,25 +963,34 @@ def paged_chunk_attention(pool: Pool, q, k_cache, v_cache, block_tables, q_start
     q_start[b] .. q_start[b + 1], over its cached rows (see include/pkv.h): causal, in a sliding
     `window`, or (`visible`, int64 [num_tokens]) with the drafted tokens' own masks.  out is
     of q's shape and type."""
-    if q.dtype not in PKV_DTYPE:
-        raise ValueError("unsupported q dtype %s" % q.dtype)
-    T, B = q.shape[0], seq_lens.numel()
-    _shaped("q", q, q.dtype, (T, None, pool.head_dim))
-    _shaped("out", out, q.dtype, tuple(q.shape))
-    _shaped("seq_lens", seq_lens, _I32, (B,))
-    _shaped("q_start", q_start, _I32, (B + 1,))
-    _rows("block_tables", block_tables, B)
-    _cache_of(pool, k_cache, v_cache)
-    _check_scales(pool, k_scales, v_scales)
-    if visible is not None:
-        _shaped("visible", visible, torch.int64, (T,))
-    _on_current(q, out, k_cache, workspace, visible)
-    _check(load().paged_chunk_attention(
-        pool.handle, _dptr(q), PKV_DTYPE[q.dtype], q.shape[1], T, _dptr(k_cache), _dptr(v_cache),
-        _dptr(k_scales), _dptr(v_scales), _dptr(block_tables), block_tables.shape[1],
-        _dptr(q_start), _dptr(seq_lens), B, int(max_q_len), int(window), _dptr(visible),
-        float(scale), _dptr(out), _dptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "paged_chunk_attention")
+    dt = q.dtype
+    if dt not in PKV_DTYPE:
+        raise ValueError("unsupported q dtype %s" % dt)
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [num_tokens, Hq, D]")
+    shape, dev = q.shape, _current_device()
+    T, Hq, D = shape
+    B = seq_lens.numel()
+    if D != pool.head_dim:
+        _shaped("q", q, dt, (T, None, pool.head_dim))
+    if block_tables.dim() != 2:
+        _rows("block_tables", block_tables, B)
+    most = block_tables.shape[1]
+    cache, ct = pool.cache_shape, TORCH_DTYPE[pool.kv_dtype]
+    ksp, vsp = _scales_of(pool, k_scales, v_scales, dev)
+    if workspace.get_device() != dev:
+        _elsewhere("workspace", dev)
+    st = load().paged_chunk_attention(
+        pool.handle, _flat("q", q, dt, shape, dev), PKV_DTYPE[dt], Hq, T,
+        _flat("k_cache", k_cache, ct, cache, dev), _flat("v_cache", v_cache, ct, cache, dev), ksp,
+        vsp, _flat("block_tables", block_tables, _I32, (B, most), dev), most,
+        _flat("q_start", q_start, _I32, (B + 1,), dev),
+        _flat("seq_lens", seq_lens, _I32, (B,), dev), B, max_q_len, window,
+        None if visible is None else _flat("visible", visible, torch.int64, (T,), dev), scale,
+        _flat("out", out, dt, shape, dev), _dptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    if st < 0:
+        raise PkvError(st, "paged_chunk_attention")
 
 
 def pkv_selftest_wait_timeout(pool: Pool, stream=None) -> None:
