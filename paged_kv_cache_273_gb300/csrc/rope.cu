@@ -39,9 +39,16 @@ struct RopeParams {
     float magnitude;
     float sign;                   // -1: the transposed rotation
     int slices;                   // threads that share a token's heads, for each unit
-    int row_ctas;                 // CTAs of rotated rows (the others: runs of an 8-bit float cache)
-    int chunk;                    // tokens a warp looks for runs in
+    int run_ctas;                 // CTAs of an 8-bit float cache's runs (the others: rotated rows)
+    int every;                    // one of them among so many CTAs
+    int parts;                    // of them, to a chunk of tokens: 8 (K or V, head)s each
+    int chunk;                    // tokens that are looked at for runs
 };
+
+// Tokens whose sines and cosines a CTA of runs keeps in shared memory: those of its chunk and
+// of a run that goes on behind it (of blocks of up to 32 tokens; of larger ones the tokens
+// behind are worked out by each warp).
+constexpr int TABLE_TOKENS = 64;
 
 // A unit: V pairs of channels, in two 16-byte chunks at elements a and b of the
 // head.  Halves: the chunks are V channels of either half.  Interleaved: they are
@@ -114,14 +121,14 @@ __device__ __forceinline__ uint4 put_row16(const float (&x)[4])
                       __float_as_uint(x[3]));
 }
 
-// Cosines and sines (times the magnitude) of a unit's pairs at position p.  The
+// Cosines and sines (times the magnitude) of V pairs, or of a unit's, at a position.  The
 // angle's top 32 bits, as a signed fraction of a turn, are good to 2^-33 turns: 7e-10
 // in a sine, below fp32's rounding of it.
 template <int V>
-__device__ __forceinline__ void turns(const RopeParams &p, int u, int32_t pos, float (&c)[V],
-                                      float (&s)[V])
+__device__ __forceinline__ void turns_at(const RopeParams &p, int pair, int32_t pos, float (&c)[V],
+                                         float (&s)[V])
 {
-    const uint64_t *f = p.freqs + u * V;
+    const uint64_t *f = p.freqs + pair;
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
         const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(f + i);
@@ -135,6 +142,13 @@ __device__ __forceinline__ void turns(const RopeParams &p, int u, int32_t pos, f
             s[i + j] = sn * (p.magnitude * p.sign);
         }
     }
+}
+
+template <int V>
+__device__ __forceinline__ void turns(const RopeParams &p, int u, int32_t pos, float (&c)[V],
+                                      float (&s)[V])
+{
+    turns_at<V>(p, u * V, pos, c, s);
 }
 
 // The unit's pairs in xa, xb (its two chunks), rotated in place.
@@ -165,11 +179,11 @@ __device__ __forceinline__ void turn(float (&xa)[V], float (&xb)[V], const float
 // Heads of one token, unit by unit: q's to q_out and, over a cache of T itself
 // (HEADS_KV), K's and V's to their slot.
 template <typename T, int D, bool IL, bool HEADS_KV>
-__device__ __forceinline__ void rope_rows(const RopeParams &p)
+__device__ __forceinline__ void rope_rows(const RopeParams &p, int cta)
 {
     using U = Unit<T, D>;
     constexpr int V = U::V, UNROLL = 4;
-    const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t g = (int64_t)cta * blockDim.x + threadIdx.x;
     const int u = (int)(g % U::N);
     const int64_t rest = g / U::N;
     const int64_t t = rest / p.slices;
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const __grid_constant__ 
 {
     grid_dependency_wait();
     grid_dependents_launch();
-    rope_rows<T, D, IL, HEADS_KV>(p);
+    rope_rows<T, D, IL, HEADS_KV>(p, blockIdx.x);
 }
 
 // K or V rows of one run into an 8-bit float cache, by one warp: as kv_append does
@@ -253,8 +267,8 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const __grid_constant__ 
 // rows of a run of up to 16 stay in registers between the maximum and the codes;
 // of a longer run they are read and rotated twice.
 template <typename T, int D, bool IL>
-__device__ __forceinline__ void rope_run(const RopeParams &p, bool is_v, int h, int64_t t,
-                                         int blk, int off, int n)
+__device__ __forceinline__ void rope_run(const RopeParams &p, const float2 *table, int64_t t0,
+                                         bool is_v, int h, int64_t t, int blk, int off, int n)
 {
     using U = Unit<T, D>;
     constexpr int V = U::V, RPI = 32 / U::N, ROWS = 16, NR = ROWS / RPI;
@@ -286,7 +300,17 @@ __device__ __forceinline__ void rope_run(const RopeParams &p, bool is_v, int h, 
             get_row16(wb[i], xb[i], T());
             if (turned && k < n) {
                 float c[V], s[V];
-                turns<V>(p, u, p.positions[t + k], c, s);
+                const int row = (int)(t - t0) + k;
+                if (row < TABLE_TOKENS) {
+                    const float4 *w = reinterpret_cast<const float4 *>(table + row * (p.rot / 2) + u * V);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        const float4 f = w[e];
+                        c[2 * e] = f.x; s[2 * e] = f.y; c[2 * e + 1] = f.z; s[2 * e + 1] = f.w;
+                    }
+                } else {
+                    turns<V>(p, u, p.positions[t + k], c, s);
+                }
                 turn<V, IL>(xa[i], xb[i], c, s);
             }
         }
@@ -339,27 +363,44 @@ __device__ __forceinline__ void rope_run(const RopeParams &p, bool is_v, int h, 
     }
 }
 
-// One launch for both: the first row_ctas CTAs rotate q, in the others a warp takes
-// (chunk of tokens, K or V, head).
+// One launch for both: in some CTAs a warp takes runs of a chunk of tokens for one (K or
+// V, head), the others rotate q.  They are spread evenly over the grid, so that the arithmetic of
+// the runs goes beside the rows' memory traffic.  A chunk's sines and cosines are worked
+// out once for all its heads.
 template <typename T, int D, bool IL>
 __global__ void __launch_bounds__(256, 2) rope_append_f8_kernel(const __grid_constant__ RopeParams p)
 {
+    extern __shared__ __align__(16) float2 table[];        // [TABLE_TOKENS][rot / 2]: cosine, sine
     grid_dependency_wait();
     grid_dependents_launch();
-    if ((int)blockIdx.x < p.row_ctas) {
-        rope_rows<T, D, IL, false>(p);
+    // every `every`-th CTA until there are run_ctas of them
+    const int cta = (int)blockIdx.x, run = cta / p.every;
+    if (run * p.every != cta || run >= p.run_ctas) {
+        rope_rows<T, D, IL, false>(p, cta - min(p.run_ctas, run + 1));
         return;
     }
-    const int H = p.num_kv_heads;
-    const int64_t w = ((int64_t)(blockIdx.x - p.row_ctas) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t chunk = w / (2 * H);
-    if (chunk * p.chunk >= p.num_tokens)
+    const int H = p.num_kv_heads, warp = threadIdx.x >> 5;
+    const int64_t chunk = run / p.parts, t0 = chunk * p.chunk;
+    const int r0 = (int)(run - chunk * p.parts) * 8;
+    if (r0 < H) {                                          // (K among them)
+        const int pairs = p.rot / 2;
+        const int rows = (int)min((int64_t)min(TABLE_TOKENS, p.chunk + p.block_size - 1),
+                                  p.num_tokens - t0);
+        for (int i = threadIdx.x; i < rows * pairs / 2; i += 256) {
+            const int row = 2 * i / pairs, pair = 2 * i - row * pairs;
+            float c[2], s[2];
+            turns_at<2>(p, pair, p.positions[t0 + row], c, s);
+            *reinterpret_cast<float4 *>(table + 2 * i) = make_float4(c[0], s[0], c[1], s[1]);
+        }
+    }
+    __syncthreads();
+    const int r = r0 + warp;
+    if (r >= 2 * H)
         return;
-    const int r = (int)(w - chunk * 2 * H);
     const bool is_v = r >= H;
-    for_runs(p.slots, chunk * p.chunk, p.chunk, p.num_tokens, p.block_size, p.num_slots, r == 0,
-             p.err, [&](int64_t t, int blk, int off, int n) {
-                 rope_run<T, D, IL>(p, is_v, is_v ? r - H : r, t, blk, off, n);
+    for_runs(p.slots, t0, p.chunk, p.num_tokens, p.block_size, p.num_slots, r == 0, p.err,
+             [&](int64_t t, int blk, int off, int n) {
+                 rope_run<T, D, IL>(p, table, t0, is_v, is_v ? r - H : r, t, blk, off, n);
              });
 }
 
@@ -393,14 +434,17 @@ int launch_f8(RopeParams &p, int num_sms, cudaStream_t s)
 {
     p.slices = p.num_q_heads ? head_slices(p.num_tokens, Unit<T, D>::N, p.num_q_heads, num_sms) : 0;
     const int64_t rows = (p.num_tokens * Unit<T, D>::N * p.slices + 255) / 256;
-    // as kv_append: a token a warp while that keeps the warps few, else 32
+    // as kv_append: a token at a time while that keeps the warps few, else 32
     p.chunk = p.num_tokens * 2 * p.num_kv_heads <= (int64_t)num_sms * 64 ? 1 : 32;
-    const int64_t runs = ((p.num_tokens + p.chunk - 1) / p.chunk * 2 * p.num_kv_heads + 7) / 8;
+    p.parts = (2 * p.num_kv_heads + 7) / 8;
+    const int64_t runs = (p.num_tokens + p.chunk - 1) / p.chunk * p.parts;
     if (rows + runs > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
-    p.row_ctas = (int)rows;
+    p.run_ctas = (int)runs;
+    p.every = (int)((rows + runs) / runs);
+    const size_t smem = (size_t)TABLE_TOKENS * (p.rot / 2) * sizeof(float2);   // at most 32 KB
     const cudaError_t e = launch_pdl(rope_append_f8_kernel<T, D, IL>, dim3((unsigned)(rows + runs)),
-                                     dim3(256), 0, s, p);
+                                     dim3(256), smem, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
