@@ -856,7 +856,7 @@ size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_he
  *   q_start    device int32 [batch + 1], non-decreasing, q_start[0] >= 0 and
  *              q_start[batch] <= num_tokens; rows of `out` behind the last sequence's (and
  *              before the first's) are left as they were.
- *   seq_lens   device int32 [batch], seq_lens[b] >= n_b.
+ *   seq_lens   device int32 [batch], n_b <= seq_lens[b] <= 2^30.
  *   max_q_len  >= every n_b (sizes the items of work; host value, no device read).
  *   window     0: none.
  *   visible    device uint64 [num_tokens] or NULL: bit j of token i's word: i sees new token

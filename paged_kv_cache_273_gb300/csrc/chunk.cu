@@ -128,6 +128,9 @@ struct Piece {
                            // -1: no more pieces
 };
 
+// Rows that a sequence may have: positions of a tile's keys stay below 2^31.
+constexpr int MAX_LEN = 1 << 30;
+
 struct Walk {
     Place at, end;
     Seq q;
@@ -141,7 +144,7 @@ struct Walk {
         const int64_t n = (int64_t)p.q_start[b + 1] - q0;
         const int L = p.seq_lens[b];
         bad = n < 0 || (n > 0 && (q0 < 0 || n > p.max_q_len || q0 + n > p.num_tokens || L < n ||
-                                  (int64_t)L > (int64_t)p.max_blocks * p.block_size ||
+                                  (int64_t)L > (int64_t)p.max_blocks * p.block_size || L > MAX_LEN ||
                                   (p.rules.tree && n > 64)));
         q.n = bad ? 0 : (int)n;
         q.L = L;
