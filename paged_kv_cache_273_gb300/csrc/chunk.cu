@@ -63,7 +63,8 @@ struct ChunkParams {
 
 // Warps: the softmax groups; then, of a 16-bit cache, one that brings K, one V, one that
 // hands out the pieces and brings their q, and one that issues the MMAs; of an 8-bit cache,
-// four that bring and convert tiles, the MMA warp, and the one for pieces and q.
+// four that bring and convert tiles, the MMA warp, the one for pieces and q, and one that
+// brings the tiles' scales.
 template <int D, bool F8, bool BF, int NQ>
 struct Cfg {
     static constexpr int ROWS = NQ * TILE_M;
@@ -77,9 +78,10 @@ struct Cfg {
     static constexpr int OFF_K = NQ * Q_BYTES;
     static constexpr int OFF_V = OFF_K + NS * KV_BYTES;
     static constexpr int OFF_ML = OFF_V + NS * KV_BYTES;                 // the second group's states
-    // [RING][2][16]: scales of K, exponents of V's
+    // [RING][FAC / 16][16]: scales of K, exponents of V's, and two to minus these
+    static constexpr int FAC = 48;
     static constexpr int OFF_SC = OFF_ML + (F8 ? 3 : 2) * TILE_M * 4;
-    static constexpr int OFF_QE = OFF_SC + (F8 ? RING * 32 * 4 : 0);     // q's exponents, two pieces
+    static constexpr int OFF_QE = OFF_SC + (F8 ? RING * FAC * 4 : 0);     // q's exponents, two pieces
     static constexpr int OFF_BAR = OFF_QE + (F8 ? 2 * TILE_M : 0);
     static constexpr int PIECES = 4;                                     // handed out and not done
     static constexpr int NBARS = 4 * NS + 8 + 6 + 2 * PIECES;
@@ -87,13 +89,14 @@ struct Cfg {
     static constexpr int SMEM_BYTES = OFF_MISC + 224;
     static constexpr int W0 = 8;                                         // the first warp behind the groups
     static constexpr int W_MMA = F8 ? W0 + 4 : W0 + 3, W_FEED = F8 ? W0 + 5 : W0 + 2;
-    static constexpr int CONSUMERS = W0 + (F8 ? 5 : 3);                  // warps that a piece is for
+    static constexpr int W_SCALES = W0 + 6;                              // of an 8-bit cache
+    static constexpr int CONSUMERS = W0 + (F8 ? 6 : 3);                  // warps that a piece is for
     static constexpr bool QCONV = F8 && BF;
     static constexpr int NT = 32 * (F8 ? W0 + 8 : W0 + 4);
     // registers of a thread: at launch, and from then on in the softmax groups, the four
     // warps behind them, and the last four (the shares add up to what was there at launch)
     static constexpr int REGS = F8 ? 128 : 168;
-    static constexpr int R_SOFT = F8 ? 152 : 216, R_2 = F8 ? 128 : 72, R_3 = F8 ? 80 : 0;
+    static constexpr int R_SOFT = F8 ? 168 : 216, R_2 = F8 ? 112 : 72, R_3 = F8 ? 64 : 0;
     static_assert(2 * R_SOFT + R_2 + R_3 <= NT / 128 * REGS, "registers");
     static constexpr int GROUP_COLS = 256;                               // S, then O, of a group
     // a K or V tile: eight rows of 64 columns are 1024 bytes (128-byte swizzled); a group of
@@ -360,7 +363,7 @@ constexpr float P_SHIFT = 7.0f;
 // of values near fp32's largest is beyond it; their quotient by the weights' sum is not).
 constexpr int V_SHIFT = 16;
 
-constexpr uint32_t WAIT_TRIES = 1u << 22;
+constexpr uint32_t WAIT_TRIES = 1u << 18;
 
 // Row r of a half of q (bf16, as the tensor copy left it) -> fp16 times 2^-e in place, the
 // row's largest magnitude in [2^14, 2^15); returns e.
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     const int64_t line = sums[C::NT / 32];
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&k_full[i], F8 ? 4 : 2);
+            mbar_init(&k_full[i], F8 ? 5 : 2);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], F8 ? 4 : 2);
             mbar_init(&v_empty[i], 1);
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 if (warp_live) {
                     if (C::QCONV && both && g == 1 && s == 0)
                         rs *= pow2_f32(q_exp[(item & 1) * TILE_M + r]);
-                    const float *fac = k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * 32;
+                    const float *fac = k_sc + ((gt + tile_at(c, g, s)) & (C::RING - 1)) * C::FAC;
                     const bool masked = __any_sync(
                         FULL_MASK, tb + TILE - 1 > lim || tb < from ||
                                        (p.visible && tb + TILE > c.base));
@@ -681,24 +684,33 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         }
                         l_run = l_run * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                     } else {
-                        // One half of the scores after the other, read again for their weights:
-                        // the conversion wants the registers, and the instruction cache the
-                        // loops.  A factor for eight keys: K's scale, the row's own and the
-                        // softmax's (at least the smallest normal number: -inf times it is -inf).
+                        // One half of the scores after the other, the first one read again for its
+                        // weights: registers are the conversion's too, and both halves written
+                        // out (929 us rather than 880) take more of the instruction cache.
+                        // A factor for eight keys: K's scale, the row's own and the softmax's
+                        // (at least the smallest normal number: -inf times it is -inf).
                         float v[HW], mv = -INFINITY;
-                        auto factor = [&](int k) { return fmaxf(fac[k] * rs, 0x1p-126f); };
-#pragma unroll 1
+                        auto factor = [&](float ks) { return fmaxf(ks * rs, 0x1p-126f); };
+                        auto eight = [&](float (&f)[8], int at) {
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4)
+                                *reinterpret_cast<float4 *>(f + k) = *reinterpret_cast<const float4 *>(fac + at + k);
+                        };
+#pragma unroll
                         for (int h0 = 0; h0 < TILE; h0 += HW) {
                             tmem_ld_begin<HW>(t_s + h0, v);
+                            float kf[8], ve[8];
+                            eight(kf, h0 / 8);
+                            eight(ve, 16 + h0 / 8);
                             tmem_ld_end<HW>(v);
                             hide(v, h0);
 #pragma unroll
                             for (int k = 0; k < HW / 8; ++k) {
                                 const float *x = v + 8 * k;
                                 const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]),
-                                                      fmaxf(x[6], x[7])) * factor(h0 / 8 + k);
+                                                      fmaxf(x[6], x[7])) * factor(kf[k]);
                                 mx = fmaxf(mx, a);
-                                mv = fmaxf(mv, a + fac[16 + h0 / 8 + k]);
+                                mv = fmaxf(mv, a + ve[k]);
                             }
                         }
                         l_run *= moved(m_run, mx);
@@ -711,23 +723,28 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                         const bool far = __any_sync(FULL_MASK, x_run - m_run > 11.0f);
                         float lt = 0.0f;
 #pragma unroll 1
-                        for (int h0 = 0; h0 < TILE; h0 += HW) {
-                            tmem_ld_begin<HW>(t_s + h0, v);
-                            tmem_ld_end<HW>(v);
-                            hide(v, h0);
+                        for (int h0 = TILE - HW; h0 >= 0; h0 -= HW) {
+                            float kf[8], ve[8];
+                            eight(kf, h0 / 8);
+                            eight(ve, 16 + h0 / 8);
+                            if (h0 < TILE - HW) {          // (the last half is there)
+                                tmem_ld_begin<HW>(t_s + h0, v);
+                                tmem_ld_end<HW>(v);
+                                hide(v, h0);
+                            }
                             if (far) {
                                 const float m0 = m_run == -INFINITY ? 0.0f : m_run;
 #pragma unroll
                                 for (int j = 0; j < HW; ++j)
-                                    l_run += ex2_approx(fmaf(v[j], factor((h0 + j) / 8), -m0));
+                                    l_run += ex2_approx(fmaf(v[j], factor(kf[j / 8]), -m0));
                             }
                             constexpr int E = HW / 8;
                             uint32_t w[8];
 #pragma unroll
                             for (int i = 0; i < E + 2; ++i) {      // (steps as above)
                                 if (i < E) {
-                                    const float f = factor(h0 / 8 + i);
-                                    const float off = fac[16 + h0 / 8 + i] + (P_SHIFT - x0);
+                                    const float f = factor(kf[i]);
+                                    const float off = ve[i] + (P_SHIFT - x0);
 #pragma unroll
                                     for (int j = 8 * i; j < 8 * i + 8; j += 2)
                                         fma2_bc(v[j], v[j + 1], f, off);
@@ -744,8 +761,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                                     add2(y[0], y[1], y[2], y[3]);
                                     add2(y[4], y[5], y[6], y[7]);
                                     add2(y[0], y[1], y[4], y[5]);
-                                    lt = fmaf(y[0] + y[1],
-                                              pow2_f32(-(int)fac[16 + h0 / 8 + i - 2]), lt);
+                                    lt = fmaf(y[0] + y[1], fac[32 + h0 / 8 + i - 2], lt);
                                     if (i & 1)
                                         tmem_st8(t_s + h0 + (i - 2) / 2 * 8, w);
                                 }
@@ -937,9 +953,11 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             note_item(p, begin, line);
     } else if (F8 && warp < W0 + 4) {
         // ================= bring and convert tiles of an 8-bit cache: codes to fp16, this
-        // warp's 32 rows.  The codes come through registers, a tile ahead
-        // (through shared memory they would take as much of its bandwidth again as the
-        // converted tiles' writing does, and room for a slot of each).
+        // warp's 32 rows.  The codes come through registers, asked for when the tile before
+        // (V before the next K, K before V) has been converted: through shared memory they
+        // would take as much of its bandwidth again as the converted tiles' writing does, and
+        // room for a slot of each.  K and V take turns in one copy of the code: with one for each,
+        // whose loads had twice as long, pieces of prompts took 914 us rather than 880.
         const int w0 = (warp - W0) * 32, H = p.num_kv_heads;
         constexpr int LPR = D / 16, RPI = 32 / LPR, NI = 32 / RPI;  // lanes a row, rows at once
         const int rr = lane / LPR, j = lane % LPR;
@@ -978,85 +996,84 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
                 }
                 return count;
             };
-            uint4 kd[NI], vd[NI];
-            auto bring = [&](uint4 (&d)[NI], const unsigned char *cache) {
+            uint4 d[NI];
+            auto bring = [&](const unsigned char *cache) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
                     d[i] = *reinterpret_cast<const uint4 *>(cache + at[i / (NI / 4)] +
                                                             i % (NI / 4) * 4 * D);
             };
-            auto clear = [&](uint4 (&d)[NI], uint32_t count) {
-                if (__all_sync(FULL_MASK, count == (1u << NI) - 1u))
-                    return;
-#pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    if (!((count >> i) & 1))
-                        d[i] = make_uint4(0u, 0u, 0u, 0u);
-            };
             int32_t ids = block_of(c.t0), ids1 = block_of(c.t0 + 1);
-            float ks = 1.0f, vs = 1.0f;            // lane q's blocks' scales
-            auto scales = [&](int32_t blk) {
-                const int64_t sc = (int64_t)(good(blk) ? blk : 0) * H + c.h;
-                ks = p.k_scales[sc];
-                vs = p.v_scales[sc];
-                if (blk != -2 && !good(blk))
-                    atomicOr(p.err, PKV_EBIT_BLOCK);
-            };
-            uint32_t count1 = find(c.t0, ids);
-            scales(ids);
-            bring(kd, kc);
-            bring(vd, vc);
+            uint32_t count = find(c.t0, ids);
+            bring(kc);
+            // K and V in turn: one copy of the code
 #pragma unroll 1
-            for (int t = c.t0; t < c.t1; ++t, ++gt) {
+            for (int u = 2 * c.t0; u < 2 * c.t1; ++u) {
+                const bool is_v = u & 1;
                 const int slot = gt % NS;
-                const uint32_t count = count1;
-                const float kf = pow2_f32(block_exponent(ks)), ve = (float)block_exponent(vs);
-                ids = ids1;
-                ids1 = block_of(t + 2);
-                scales(ids);
-                count1 = find(t + 1, ids);
-                // K
-                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&k_empty[slot], gt / NS + 1))))
+                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait((is_v ? v_empty : k_empty) + slot, gt / NS + 1))))
                     break;
-                if (lane < 4) {
-                    float *sc = k_sc + (gt & (C::RING - 1)) * 32 + (w0 >> 3) + lane;
-                    sc[0] = kf;
-                    sc[16] = ve;
+                unsigned char *dst = (is_v ? sV : sK) + slot * C::KV_BYTES;
+                if (!__all_sync(FULL_MASK, count == (1u << NI) - 1u)) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (!((count >> i) & 1))
+                            d[i] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                unsigned char *dst = sK + slot * C::KV_BYTES;
-                clear(kd, count);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     uint4 lo, hi;
-                    codes_to_half(kd[i], lo, hi);
+                    codes_to_half(d[i], lo, hi);
                     put_chunks<D>(dst, w0 + i * RPI + rr, j, lo, hi);
                 }
+                if (is_v) {
+                    ids = ids1;
+                    ids1 = block_of((u >> 1) + 2);
+                    count = find((u >> 1) + 1, ids);
+                    ++gt;
+                }
+                bring(is_v ? kc : vc);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&k_full[slot]);
-                bring(kd, kc);
-                // V
-                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&v_empty[slot], gt / NS + 1))))
-                    break;
-                dst = sV + slot * C::KV_BYTES;
-                clear(vd, count);
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    uint4 lo, hi;
-                    codes_to_half(vd[i], lo, hi);
-                    put_chunks<D>(dst, w0 + i * RPI + rr, j, lo, hi);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&v_full[slot]);
-                bring(vd, vc);
+                    mbar_arrive((is_v ? v_full : k_full) + slot);
             }
             done(item);
         }
         if (warp == W0 && lane == 0)
             note_item(p, begin, line);
+    } else if (F8 && warp == C::W_SCALES) {
+        // ================= a tile's scales, lane l those of its rows 8 l .. 8 l + 7: loaded
+        // before the tile's slot is free.  (By the warps that convert, between their own
+        // loads, it took 901 us rather than 879, and one token of 131072 rows 145 rather than 140.)
+        const int H = p.num_kv_heads;
+        uint32_t gt = 0;
+        bool ok = true;
+        for (uint32_t item = 0; ok && take(item); ++item) {
+            const int32_t *table = p.tables + (int64_t)c.b * p.max_blocks;
+            for (int t = c.t0; t < c.t1; ++t, ++gt) {
+                const int pos0 = t * TILE + 8 * (lane & 15);
+                const int first = pos0 & ~(p.block_size - 1);
+                const bool in = pos0 <= c.last && first + p.block_size > c.sight;
+                const int32_t blk = in ? table[pos0 >> p.bs_log2] : 0;
+                const bool good = blk >= 0 && blk < p.num_blocks;
+                const int64_t at = (int64_t)(good ? blk : 0) * H + c.h;
+                const float kf = pow2_f32(block_exponent(p.k_scales[at]));
+                const int ve = block_exponent(p.v_scales[at]);
+                if (!good)
+                    atomicOr(p.err, PKV_EBIT_BLOCK);
+                if (!(ok = __all_sync(FULL_MASK, gt < NS || wait(&k_empty[gt % NS], gt / NS + 1))))
+                    break;
+                float *sc = k_sc + (gt & (C::RING - 1)) * C::FAC + (lane & 15);
+                sc[0] = kf;
+                sc[16] = (float)ve;
+                sc[32] = pow2_f32(-ve);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&k_full[gt % NS]);
+            }
+            done(item);
+        }
     } else if (warp == C::W_FEED) {
         // ================= hand out the share's pieces, one ahead of the one whose q is
         // brought (once the last S before has read its own)
