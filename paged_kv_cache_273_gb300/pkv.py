@@ -980,6 +980,8 @@ def paged_chunk_attention(pool: Pool, q, k_cache, v_cache, block_tables, q_start
     ksp, vsp = _scales_of(pool, k_scales, v_scales, dev)
     if workspace.get_device() != dev:
         _elsewhere("workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     st = load().paged_chunk_attention(
         pool.handle, _flat("q", q, dt, shape, dev), PKV_DTYPE[dt], Hq, T,
         _flat("k_cache", k_cache, ct, cache, dev), _flat("v_cache", v_cache, ct, cache, dev), ksp,

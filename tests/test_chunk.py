@@ -381,3 +381,116 @@ def test_gpu_nothing_to_do():
     s = make([10, 20], [0, 0], 4, 2, 64, 16, "f16", "f16")
     out = run(s, 0.125)
     assert pkv.pkv_check_error(s["pool"]) == pkv.PKV_OK and bool((out == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    ([33, 1, 700] * 340, [1, 1, 2] * 340, 1, 1, 64, 16, "f16", "f16"),       # more sequences than threads
+    ([33, 1, 700] * 340, [1, 0, 2] * 340, 4, 1, 128, 16, "bf16", "f8"),
+    ([70000], [1], 4, 1, 64, 64, "bf16", "bf16"),                            # one item in more than 32 shares
+    ([90001, 5], [3, 5], 8, 1, 128, 16, "f16", "f8"),
+    ([40000, 300], [200, 300], 2, 1, 64, 32, "f16", "f16"),
+], ids=["many", "many_f8", "long", "long_f8", "long_256"])
+def test_gpu_many_and_long(case):
+    s = make(*case)
+    check(s, run(s, 1.0 / math.sqrt(s["D"])))
+    check(s, run(s, 1.0 / math.sqrt(s["D"]), 100), 100)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["bf16", "f8"])
+def test_gpu_keys_not_finite_where_masked(kv):
+    """K rows of NaN and infinity change no output of a token that does not see them."""
+    s = make([300, 90], [40, 90], 4, 2, 64, 16, "bf16", kv, gap=0)
+    want = run(s, 0.125)
+    g = s["bt"].long()
+    new = 290                                          # the first sequence's position from which K is spoilt
+    if kv == "f8":
+        c = s["kc"].view(torch.uint8)
+        for p in range(new, 300):
+            c[g[0, p // 16], :, p % 16] = 0x7f if p % 2 else 0xff
+    else:
+        for p in range(new, 300):
+            s["kc"][g[0, p // 16], :, p % 16] = [math.nan, math.inf, -math.inf][p % 3]
+    got = run(s, 0.125)
+    assert pkv.pkv_check_error(s["pool"]) == pkv.PKV_OK
+    keep = torch.tensor(list(range(30)) + list(range(40, 130)), device=DEV)
+    assert torch.equal(got[keep], want[keep])
+    # in a tree: token 0's row is seen by nobody but itself
+    t = make([200], [6], 4, 2, 64, 16, "bf16", kv, gap=0, tree=[1, 2, 6, 14, 30, 62])
+    want = run(t, 0.125)
+    b, off = int(t["bt"][0, 194 // 16]), 194 % 16
+    t["kc"].view(torch.uint8)[b, :, off] = 0x7f         # (0x7f7f is no NaN of bf16, but 3.4e38)
+    assert torch.equal(run(t, 0.125)[1:], want[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["f16", "f8"])
+def test_gpu_shared_blocks_and_a_sequence_twice(kv):
+    """Two sequences on the same blocks, and one as long as another's prefix."""
+    s = make([200, 200, 200], [20, 20, 9], 8, 2, 128, 16, "f16", kv, gap=0)
+    s["bt"][1], s["bt"][2] = s["bt"][0], s["bt"][0]
+    s["lens"][2] = 50
+    check(s, run(s, 0.1), scale=0.1)
+    s["q"][20:40] = s["q"][:20]
+    out = run(s, 0.1)
+    n = s["start"]
+    assert bool(((out[:20].double() - out[20:40].double()).abs() <= 2 * reference(s, 0.1)[1][:20].to(DEV)).all())
+
+
+@pytest.mark.gpu
+def test_gpu_two_calls_at_once():
+    """Two streams, a workspace each: the bits of the calls one after the other."""
+    a = make([20000, 100], [20, 9], 8, 2, 128, 16, "bf16", "bf16", gap=0)
+    b = make([9000] * 3, [200, 30, 64], 8, 1, 64, 16, "f16", "f8", gap=0)
+    wa, wb = run(a, 0.09), run(b, 0.125)
+    args = []
+    for s, n in ((a, 20), (b, 200)):
+        args.append((s["q"].to(DEV), s["bt"].to(DEV), i32(s["start"]), i32(s["lens"]), pkv.alloc_chunk_workspace(s["pool"], len(s["lens"]), 8, n)))
+    oa, ob = torch.zeros_like(wa), torch.zeros_like(wb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        q, bt, st, ln, ws = args[0]
+        pkv.paged_chunk_attention(a["pool"], q, a["kc"], a["vc"], bt, st, ln, 0.09, oa, ws, 20, stream=sa)
+        q, bt, st, ln, ws = args[1]
+        pkv.paged_chunk_attention(b["pool"], q, b["kc"], b["vc"], bt, st, ln, 0.125, ob, ws, 200, b["ks"], b["vs"], stream=sb)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+@pytest.mark.gpu
+def test_gpu_a_larger_limit_of_new_tokens():
+    """max_q_len above every sequence's own count, and far above."""
+    s = make([200, 64, 1000], [8, 3, 1], 8, 2, 64, 16, "bf16", "bf16")
+    for max_q in (8, 9, 17, 1000, 2 ** 31 - 1):
+        check(s, run(s, 0.125, max_q=max_q), scale=0.125)
+
+
+def test_tensors_elsewhere_are_refused():
+    s = pkv.kv_block_pool_init(8, 16, 2, 64, pkv.PKV_BF16)
+    x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        pkv.paged_chunk_attention(s, x, None, None, None, None, None, 0.1, x, None, 3)
+
+
+@pytest.mark.gpu
+def test_gpu_binding_refusals():
+    s = make([20], [3], 4, 2, 64, 16, "bf16", "bf16", gap=0)
+    pool, q, bt, st, ln = s["pool"], s["q"].to(DEV), s["bt"].to(DEV), i32(s["start"]), i32(s["lens"])
+    out, ws = torch.zeros_like(q), pkv.alloc_chunk_workspace(s["pool"], 1, 4, 3)
+
+    def call(q=q, kc=s["kc"], vc=s["vc"], bt=bt, st=st, ln=ln, out=out, ws=ws, **kw):
+        pkv.paged_chunk_attention(pool, q, kc, vc, bt, st, ln, 0.1, out, ws, 3, **kw)
+    call()
+    one = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    for kw in (dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)), dict(kc=s["kc"].half()), dict(vc=s["vc"][:1]),
+               dict(kc=s["kc"].cpu()), dict(bt=bt.long()), dict(bt=bt[:0]), dict(bt=bt[:, ::2]), dict(st=st[:1]), dict(st=st.cpu()), dict(ln=ln.float()),
+               dict(out=out.float()), dict(out=out[:2]), dict(out=out.cpu()), dict(ws=ws.cpu()), dict(ws=one.expand(ws.numel())),
+               dict(visible=torch.zeros(2, dtype=torch.int64, device=DEV)), dict(visible=torch.zeros(3, dtype=torch.int32, device=DEV))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(pkv.PkvError):
+        call(ws=ws[:ws.numel() - 16])
+    torch.cuda.synchronize()
+    assert pkv.pkv_check_error(pool) == pkv.PKV_OK
