@@ -803,8 +803,8 @@ int kv_rope_rotate(const pkv_rope *rope, const void *x, int64_t x_stride, pkv_dt
  *              not looked at).
  *   positions  device int32 [T], the angle's position (apart from the slot, so drafted
  *              tokens of a tree may share one).
- *   slot_mapping  device int32 [T].  A token with a slot < 0 is skipped altogether:
- *              its row of q_out stays as it was.
+ *   slot_mapping  device int32 [T], no slot twice.  A token with a slot < 0 is skipped
+ *              altogether: its row of q_out stays as it was.
  *   q_out      device rows of in_dtype, q_out_stride apart ([T][Hq][D] with
  *              q_out_stride = Hq * D is what the attention takes); may be q itself with
  *              the same stride, and overlaps nothing else.
@@ -868,10 +868,11 @@ size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_he
  *              calls that run concurrently.
  *
  * Scores and sums in fp32; the weights enter the second product rounded to q's type (over
- * F8 caches to fp16, relative to the row's largest weight times its block's scale), which moves an
- * output by about as much as its own rounding does.  An F16 or BF16 row of V that is not finite makes the outputs of its own
- * sequence's earlier tokens in the same call unspecified (those of the same 32 to 256 tokens),
- * an F8 cache's values are finite.  Pools: F16, BF16, F8 (others
+ * F8 caches to fp16, relative to the row's largest weight times its block's scale), which
+ * moves an output by about as much as its own rounding does.  Masked rows of K may hold
+ * anything; an F16 or BF16 row of V that is not finite makes the outputs of tokens of its
+ * sequence that do not see it unspecified too, where they read a row less than 128 from it.
+ * (An F8 cache's values are finite.)  `out` overlaps no input.  Pools: F16, BF16, F8 (others
  * PKV_ERR_UNSUPPORTED).  Lengths out of range (n_b > max_q_len or n_b > 64 with `visible`
  * among them) set PKV_ERR_BAD_INDEX and that sequence's rows of `out` are left as they
  * were; a block id outside the pool sets it too and its rows are read as zeros.  Table

@@ -16,11 +16,14 @@
 // Within a CTA two softmax groups of 128 threads, a thread a row, alternate on the
 // tensor cores.  Of an item of more than 128 rows each group has its own rows, and both read
 // each K and V tile; of a smaller one both have the same rows, and every other
-// key tile each: their two states are joined at the piece's end, through tensor memory.
+// key tile each: the first group joins the two states at the piece's end, out of tensor memory.
 //
 // Bound: few new tokens read K and V once for n G rows, so memory is the floor (n G below
 // about 290 rows of 16-bit keys, half that of e4m3); long pieces are bound by the tensor cores
-// and the exponentials.
+// and by the softmax between a group's two products.  Measured on a GB300 (a call in a
+// captured chain, both kernels): 8 drafted tokens each of 16 sequences' 271 MB of rows 56 us
+// (4.8 TB/s); whole prompts of 550 GFLOP 435 us (1.26 PFLOP/s, the tensor cores 55% busy); pieces over
+// e4m3 of 756 GFLOP 880 us (0.86 PFLOP/s, 45%); 32 tokens of 64 heads over 131000 e4m3 rows 140 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -117,7 +120,7 @@ __device__ __forceinline__ uint32_t tile_off(int r, int ch)
                       (((ch & 7) ^ (r & 7)) << 4));
 }
 
-// The share's walk over its items' pieces.
+// What a share does of an item.
 struct Piece {
     int b, h;
     int tok;               // first token, as a row of q
@@ -134,6 +137,7 @@ struct Piece {
 // Rows that a sequence may have: positions of a tile's keys stay below 2^31.
 constexpr int MAX_LEN = 1 << 30;
 
+// The share's walk over its items' pieces.
 struct Walk {
     Place at, end;
     Seq q;
@@ -397,8 +401,8 @@ __device__ __forceinline__ int halve_row(unsigned char *q, int r)
     return e;
 }
 
-// Wait for a phase, with a limit in tries (each lets the warp sleep for a while: some
-// seconds in all), or until another role has given up.  Kept short: it is inlined at every wait.
+// Wait for a phase, with a limit in tries (each lets the warp sleep for a while: about a
+// second in all), or until another role has given up.  Kept short: it is inlined at every wait.
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                         unsigned int *err)
 {
@@ -1239,6 +1243,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
 // Items that were cut: the states of an item's pieces joined in the order of the keys, eight
 // columns of 32 rows a warp, a lane a row.  Warps count off the shares that an item to join is
 // noted with, so that those without cost a look at a word each, and take their units in turn.
+// Bound by latency: 6 us of a call with its launch where the states are 128 rows, 14 where they
+// are 256 (152 cut items' 20 MB of fp32 states).
 template <int D, typename T>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
                                                          int item_rows, int row_blocks, float v_scale)
