@@ -1244,7 +1244,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
 // columns of 32 rows a warp, a lane a row.  Warps count off the shares that an item to join is
 // noted with, so that those without cost a look at a word each, and take their units in turn.
 // Bound by latency: 6 us of a call with its launch where the states are 128 rows, 14 where they
-// are 256 (152 cut items' 20 MB of fp32 states).
+// are 256 (two states a CTA then: 40 MB written and read, mostly in L2).
 template <int D, typename T>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkParams p,
                                                          int item_rows, int row_blocks, float v_scale)

@@ -15,7 +15,7 @@
 // halves) of one token through several heads, so that its sines and cosines are
 // computed once for them.  Measured on a GB300: prompts of 32 + 8 heads rotated, 671 MB, 116 us
 // (5.8 TB/s); q, K and V of prompts to q_out and an fp16 cache, 806 MB, 120 us (6.7 TB/s); 64 + 8 + 8
-// heads into e4m3, 1.5 GB, 254 us; a decode step's 2 to 5 us, a launch's time.
+// heads into e4m3, 1.5 GB, 258 us; a decode step's 2 to 5 us, a launch's time.
 #include <cuda_runtime.h>
 
 #include "blocks_common.cuh"
@@ -124,8 +124,9 @@ __device__ __forceinline__ uint4 put_row16(const float (&x)[4])
 }
 
 // Cosines and sines (times the magnitude) of V pairs, or of a unit's, at a position.  The
-// angle's top 32 bits, as a signed fraction of a turn, are good to 2^-33 turns: 7e-10
-// in a sine, below fp32's rounding of it.
+// angle is taken as a number of quarter turns and a rest of at most an eighth, 32 bits of it
+// (2^-35 turns: 2e-10 in a sine): rounded to fp32 the rest is within 2.4e-8, half a step of a
+// sine's own (a fraction of a whole turn would be off by four times that).
 template <int V>
 __device__ __forceinline__ void turns_at(const RopeParams &p, int pair, int32_t pos, float (&c)[V],
                                          float (&s)[V])
@@ -137,11 +138,13 @@ __device__ __forceinline__ void turns_at(const RopeParams &p, int pair, int32_t 
         const uint64_t t[2] = {w.x * (uint64_t)(int64_t)pos, w.y * (uint64_t)(int64_t)pos};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float x = (float)(int32_t)(uint32_t)(t[j] >> 32) * 0x1p-31f;   // half turns
+            const uint32_t n = ((uint32_t)(t[j] >> 32) + 0x20000000u) >> 30;     // quarters, 0..3
+            const float x = (float)(int32_t)(uint32_t)(t[j] >> 30) * 0x1p-33f;   // half turns
             float sn, cs;
             sincospif(x, &sn, &cs);
-            c[i + j] = cs * p.magnitude;
-            s[i + j] = sn * (p.magnitude * p.sign);
+            const uint32_t a = __float_as_uint(n & 1 ? sn : cs), b = __float_as_uint(n & 1 ? cs : sn);
+            c[i + j] = __uint_as_float(a ^ ((n + 1) & 2) << 30) * p.magnitude;
+            s[i + j] = __uint_as_float(b ^ (n & 2) << 30) * (p.magnitude * p.sign);
         }
     }
 }
