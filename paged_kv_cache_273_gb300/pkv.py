@@ -51,7 +51,8 @@ SYMBOLS = ("pkv_status_string", "kv_block_pool_init", "kv_block_pool_destroy", "
            "paged_decode_attention_noalloc", "paged_decode_step", "kv_device_reserve",
            "kv_device_release", "kv_bounds_append", "kv_bounds_copy", "paged_sparse_workspace_bytes",
            "paged_decode_attention_sparse", "kv_rope_frequencies", "kv_rope_rotate",
-           "kv_rope_append", "paged_chunk_workspace_bytes", "paged_chunk_attention", "pkv_selftest_wait_timeout", "pkv_check_error")
+           "kv_rope_append", "paged_chunk_workspace_bytes", "paged_chunk_attention",
+           "pkv_selftest_wait_timeout", "pkv_check_error")
 
 
 class StepLayout(ctypes.Structure):
@@ -881,13 +882,16 @@ def kv_rope_rotate(rope: RopePlan, x, positions, out=None, transposed: bool = Fa
                    stream=None):
     """Rotate the heads x [T, heads, D] to their positions (see include/pkv.h), into `out`
     (default: a new tensor; x itself: in place), which is returned.  x and out may be slices
-    of wider rows.  transposed: the rotation's gradient."""
+    of wider rows.  transposed: the rotation's gradient (autograd does not follow the call).
+    With a stream of its own the call needs `out`: a new tensor would be the current stream's."""
     dt = x.dtype
     if x.dim() != 3 or dt not in PKV_DTYPE:
         raise ValueError("x must be [T, heads, D] of float32, float16 or bfloat16")
     shape = x.shape
     T, H, D = shape
     if out is None:
+        if stream is not None:
+            raise ValueError("a call on a stream of its own needs out")
         out = torch.empty(shape, dtype=dt, device=x.device)
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")

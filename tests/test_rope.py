@@ -438,3 +438,22 @@ def test_gpu_empty_calls():
     assert pkv.pkv_check_error(s["pool"]) == pkv.PKV_OK
     with pytest.raises(ValueError):
         pkv.kv_rope_rotate(plan, torch.zeros(2, 64, 4, dtype=torch.float16, device=DEV).transpose(1, 2), i32([0, 1]))
+
+
+@pytest.mark.gpu
+def test_gpu_rotate_on_a_stream_of_its_own():
+    """Into a given tensor; a new one would be the current stream's."""
+    plan = pkv.rope_plan(64)
+    x = torch.randn(500, 4, 64, device=DEV)
+    pos = i32(list(range(500)))
+    want = pkv.kv_rope_rotate(plan, x, pos)
+    out, stream = torch.zeros_like(x), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        pkv.kv_rope_rotate(plan, x, pos, stream=stream)
+    assert pkv.kv_rope_rotate(plan, x, pos, out, stream=stream) is out
+    stream.synchronize()
+    assert torch.equal(out, want)
+    with torch.cuda.stream(stream):                    # the current stream: a new tensor is its own
+        assert torch.equal(pkv.kv_rope_rotate(plan, x, pos), want)
+    stream.synchronize()
