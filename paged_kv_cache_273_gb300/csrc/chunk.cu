@@ -137,6 +137,9 @@ struct Piece {
 // Rows that a sequence may have: positions of a tile's keys stay below 2^31.
 constexpr int MAX_LEN = 1 << 30;
 
+// What a wait for the end of a piece may take for each of its tiles, beside WAIT_LIMIT_NS.
+constexpr uint64_t TILE_LIMIT_NS = 1 << 17;
+
 // The share's walk over its items' pieces.
 struct Walk {
     Place at, end;
@@ -367,8 +370,6 @@ constexpr float P_SHIFT = 7.0f;
 // of values near fp32's largest is beyond it; their quotient by the weights' sum is not).
 constexpr int V_SHIFT = 16;
 
-constexpr uint32_t WAIT_TRIES = 1u << 18;
-
 // Row r of a half of q (bf16, as the tensor copy left it) -> fp16 times 2^-e in place, the
 // row's largest magnitude in [2^14, 2^15); returns e.
 template <int D>
@@ -399,20 +400,6 @@ __device__ __forceinline__ int halve_row(unsigned char *q, int r)
         *at(ch) = make_uint4(v[0], v[1], v[2], v[3]);
     }
     return e;
-}
-
-// Wait for a phase, with a limit in tries (each lets the warp sleep for a while: about a
-// second in all), or until another role has given up.  Kept short: it is inlined at every wait.
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned int *err)
-{
-    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries)
-        if ((tries & 1023) == 0 && (*abort_flag || tries >= WAIT_TRIES)) {
-            *abort_flag = 1;
-            atomicOr(err, PKV_EBIT_TIMEOUT);
-            return false;
-        }
-    return true;
 }
 
 template <int D, bool F8, bool BF, int NQ>
@@ -489,9 +476,9 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // A wait that runs out raises the error bit once and makes every role stop.
+    // Every role but the one that hands out the pieces waits for a few tiles' work at most.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return wait_on(bar, parity & 1, abort_flag, p.err);
+        return mbar_wait_or_abort(bar, parity & 1, abort_flag);
     };
     Piece c;
     // The item-th piece, and when this warp is done with it.
@@ -1084,12 +1071,24 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
         Walk walk;
         walk.start(p, places);
         __syncwarp();                              // (places lie where the pieces go)
+        // A wait for the end of a piece: as long as its tiles take (1 to 4 us each), so its limit
+        // grows with the tiles handed out.  Should another role hang, that role's own limit
+        // ends this wait too.
+        int64_t tiles = 0;
+        auto wait_piece = [&](uint64_t *bar, uint32_t parity) -> bool {
+            const bool ok = mbar_wait_bounded(bar, parity & 1, abort_flag,
+                                              WAIT_LIMIT_NS + (uint64_t)tiles * TILE_LIMIT_NS);
+            if (!ok)
+                *abort_flag = 1;
+            return __all_sync(FULL_MASK, ok);
+        };
         auto hand_out = [&](uint32_t item, bool more) -> bool {
             const uint32_t slot = item % C::PIECES;
-            if (item >= C::PIECES &&
-                !__all_sync(FULL_MASK, wait(&pc_empty[slot], item / C::PIECES + 1)))
+            if (item >= C::PIECES && !wait_piece(&pc_empty[slot], item / C::PIECES + 1))
                 return false;
-            if (!more)
+            if (more)
+                tiles += c.t1 - c.t0;
+            else
                 c.kind = -1;
             if (lane == 0) {
                 pieces[slot] = c;
@@ -1103,7 +1102,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             more = walk.next(p, c);
             if (!(ok = hand_out(item + 1, more)))
                 break;
-            if (item > 0 && !(ok = __all_sync(FULL_MASK, wait(q_empty, item - 1))))
+            if (item > 0 && !(ok = wait_piece(q_empty, item - 1)))
                 break;
             if (lane == 0) {
                 uint64_t *bar = C::QCONV ? q_raw : q_full;
@@ -1229,6 +1228,8 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     tc_fence_before();
     __syncthreads();
     if (*abort_flag) {
+        if (tid == 0)
+            atomicOr(p.err, PKV_EBIT_TIMEOUT);
         // copies in flight land before the shared memory is another CTA's
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000) {

@@ -86,7 +86,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
 // returns false) after WAIT_LIMIT_NS, or at once when *abort is set by any
 // thread of the CTA; the caller then records the timeout and winds down.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity,
-                                                  volatile int *abort)
+                                                  volatile int *abort,
+                                                  uint64_t limit = WAIT_LIMIT_NS)
 {
     if (mbar_try_wait(bar, parity))
         return true;
@@ -97,7 +98,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
         if ((it & 63u) == 0) {
             if (*abort)
                 return false;
-            if (globaltimer_ns() - t0 > WAIT_LIMIT_NS)
+            if (globaltimer_ns() - t0 > limit)
                 return false;
         }
     }

@@ -350,6 +350,28 @@ __device__ __forceinline__ void tmem_ld_end<64>(float *v)
                  : "memory");
 }
 
+// mbar_wait_bounded for kernels that are short of room in the instruction cache, where this is
+// inlined at every wait: the clock's low word (it turns over after four times the limit, and
+// is looked at every 64 tries of 4 us at most), and a wait that runs out makes the other roles
+// stop, so that one place at the kernel's end can report it.
+__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity,
+                                                   volatile int *abort_flag)
+{
+    uint32_t t0 = 0;
+    for (uint32_t tries = 1; !mbar_try_wait(bar, parity); ++tries)
+        if ((tries & 63u) == 0) {
+            uint32_t now;
+            asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+            if (t0 == 0u)
+                t0 = now;
+            if (now - t0 > (uint32_t)WAIT_LIMIT_NS || *abort_flag) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    return true;
+}
+
 // The registers a thread of this warpgroup may use from here on (all four warps of it call
 // this; the shares of a block's warpgroups add up to no more than it was launched with).
 template <int N> __device__ __forceinline__ void more_registers()
