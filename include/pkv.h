@@ -870,9 +870,11 @@ size_t paged_chunk_workspace_bytes(const pkv_pool *pool, int batch, int num_q_he
  * Scores and sums in fp32; the weights enter the second product rounded to q's type (over
  * F8 caches to fp16, relative to the row's largest weight times its block's scale), which
  * moves an output by about as much as its own rounding does.  Masked rows of K may hold
- * anything; an F16 or BF16 row of V that is not finite makes the outputs of tokens of its
- * sequence that do not see it unspecified too, where they read a row less than 128 from it.
- * (An F8 cache's values are finite.)  `out` overlaps no input.  Pools: F16, BF16, F8 (others
+ * anything.  A row of V that is not finite (an F8 cache's are finite where the appended values
+ * were) makes the outputs unspecified not only of the tokens that see it, but also of tokens of
+ * its sequence up to 254 positions before it, with `window` of those whose window starts up
+ * to 382 positions behind it, and with `visible`, where it is a new token's, of all of the
+ * sequence's.  `out` overlaps no input.  Pools: F16, BF16, F8 (others
  * PKV_ERR_UNSUPPORTED).  Lengths out of range (n_b > max_q_len or n_b > 64 with `visible`
  * among them) set PKV_ERR_BAD_INDEX and that sequence's rows of `out` are left as they
  * were; a block id outside the pool sets it too and its rows are read as zeros.  Table
