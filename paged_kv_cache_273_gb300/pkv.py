@@ -928,6 +928,8 @@ def kv_rope_append(pool: Pool, rope: RopePlan, q, k, v, positions, slot_mapping,
     if q is not None:
         if q.dim() != 3:
             _shaped("q", q, dt, (T, None, D))
+        if q_out is None:
+            raise ValueError("q needs q_out")
         Hq = q.shape[1]
         rows = (T, Hq, D)
         qp, qs = _head_rows("q", q, dt, rows, dev)
