@@ -864,7 +864,7 @@ def _head_rows(name: str, t, dtype, shape, dev: int):
     step, head, one = t.stride()
     if one != 1 or (head != D and H > 1):
         raise ValueError("%s: a token's heads must lie side by side" % name)
-    return t.data_ptr(), step if T > 1 else max(step, H * D)
+    return t.data_ptr(), step if T > 1 else H * D      # (one token has no next one to be apart from)
 
 
 def _scales_of(pool: Pool, k_scales, v_scales, dev: int):
