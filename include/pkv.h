@@ -760,7 +760,7 @@ typedef struct {
  *               (high - low), 0, 1).
  * magnitude is 1 but for PARTS.  PKV_ERR_INVALID for a null pointer, base < 1 (PARTS:
  * <= 1), factor <= 0, and for PARTS and WAVELENGTH trained_len < 1, low <= 0 or high <=
- * low, or a value that is not finite; PKV_ERR_UNSUPPORTED for a rot_dim that is not one
+ * low, or a value or a theta_i that is not finite; PKV_ERR_UNSUPPORTED for a rot_dim that is not one
  * of 16, 32, .. 128.
  */
 int kv_rope_frequencies(int rot_dim, double base, pkv_rope_scaling scaling, double factor,

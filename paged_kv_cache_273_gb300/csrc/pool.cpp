@@ -996,6 +996,8 @@ int kv_rope_frequencies(int rot_dim, double base, pkv_rope_scaling scaling, doub
             const double s = std::min(1.0, std::max(0.0, (trained_len * f / tau - low) / (high - low)));
             theta = f / factor * (1.0 - s) + f * s;
         }
+        if (!std::isfinite(theta))         // a factor next to nothing
+            return PKV_ERR_INVALID;
         // a fraction of a turn in units of 2^-64 (whole turns make no difference at
         // whole positions)
         const double turn = theta / tau, part = std::ldexp(turn - std::floor(turn), 64);
