@@ -429,7 +429,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         prefetch_map(&p.tm_q);
-        if (!F8) {
+        if (!F8 && p.box_rows >= 8) {              // (blocks of 4 rows have no map)
             prefetch_map(&p.tm_k);
             prefetch_map(&p.tm_v);
         }
