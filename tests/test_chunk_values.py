@@ -63,3 +63,35 @@ def test_gpu_values_not_finite_in_a_tree(kv):
         sees = [r < 136 or bool((w >> (r - 136)) & 1) for w in s["tree"][:64]]
         assert not bool(torch.isfinite(got[:64][torch.tensor(sees, device=DEV)]).any()), r
     assert pkv.pkv_check_error(s["pool"]) == pkv.PKV_OK
+
+
+def _far_apart(dtype, shift):
+    """Blocks whose V scales differ by up to 2^60, all times 2^shift; keys of one size."""
+    s = C.make([500, 1200], [20, 3], 8, 2, 128, 16, dtype, "f8", seed=5, spread=30)
+    s["k"], one = s["k"] / s["ks"].double().cpu()[:, :, None, None] * 2.0 ** -7, torch.full_like(s["ks"], 2.0 ** -7)
+    s["ks"] = one
+    s["v"], s["vs"] = s["v"] * 2.0 ** shift, s["vs"] * 2.0 ** shift
+    return s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,shift", [("f16", 0), ("f16", -12), ("f16", -24), ("f16", -34), ("bf16", 0), ("bf16", 80), ("bf16", -50)])
+def test_gpu_f8_scales_far_apart_to_the_bound(dtype, shift):
+    """Every output to its bound; in fp16 those beyond its largest number are infinite, and those
+    within their bound of it either."""
+    s = _far_apart(dtype, shift)
+    scale = 1.0 / math.sqrt(128)
+    out = C.run(s, scale)
+    assert pkv.pkv_check_error(s["pool"]) == pkv.PKV_OK
+    y, lim = C.reference(s, scale)
+    n = s["start"][-1]
+    y, lim, got = y[:n], lim[:n], out[:n].double().cpu()
+    # half a step above the largest number is where rounding goes to infinity
+    border = 65520.0 if dtype == "f16" else float("inf")
+    small, large = y.abs() + lim < border, y.abs() - lim > border
+    if dtype == "f16" and shift <= -24:
+        assert bool(small.all())                       # (nothing is left out where all are in range)
+    err = (got - y).abs()
+    assert bool((err[small] <= lim[small]).all()), float((err[small] / lim[small]).max())
+    assert torch.equal(got[large], torch.where(y > 0, math.inf, -math.inf).double()[large])
+    assert bool((out[n:] == 7).all())
