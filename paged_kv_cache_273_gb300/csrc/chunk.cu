@@ -46,7 +46,7 @@ using chunk::TILE;
 struct ChunkParams {
     CUtensorMap tm_q;             // q [T][Hq][D]: boxes of 64 columns x G heads x 128 / G tokens
     CUtensorMap tm_k, tm_v;       // 16-bit caches: boxes of box_rows whole rows
-    const void *q, *k_cache, *v_cache;
+    const void *k_cache, *v_cache;
     const float *k_scales, *v_scales;
     const int32_t *tables, *q_start, *seq_lens;
     const uint64_t *visible;
@@ -1401,7 +1401,6 @@ int launch_chunk(const pkv_pool *pool, const void *q, pkv_dtype q_dtype, int num
     ChunkParams p{};
     const int G = num_q_heads / pool->num_kv_heads;
     const bool f8 = pool->kv_dtype == PKV_F8, bf = q_dtype == PKV_BF16;
-    p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.k_scales = static_cast<const float *>(k_scales);
