@@ -125,8 +125,8 @@ __device__ __forceinline__ uint4 put_row16(const float (&x)[4])
 
 // Cosines and sines (times the magnitude) of V pairs, or of a unit's, at a position.  The
 // angle is taken as a number of quarter turns and a rest of at most an eighth, 32 bits of it
-// (2^-35 turns: 2e-10 in a sine): rounded to fp32 the rest is within 2.4e-8, half a step of a
-// sine's own (a fraction of a whole turn would be off by four times that).
+// (cut off below 2^-34 turns: 3.7e-10 in a sine): rounded to fp32 the rest is within 2.4e-8, half
+// a step of a sine's own (a fraction of a whole turn would be off by four times that).
 template <int V>
 __device__ __forceinline__ void turns_at(const RopeParams &p, int pair, int32_t pos, float (&c)[V],
                                          float (&s)[V])
