@@ -38,10 +38,12 @@ namespace pkv {
 namespace {
 
 using namespace dev;
+using chunk::Piece;
 using chunk::Place;
 using chunk::Rules;
 using chunk::Seq;
 using chunk::TILE;
+using chunk::Walk;
 
 struct ChunkParams {
     CUtensorMap tm_q;             // q [T][Hq][D]: boxes of 64 columns x G heads x 128 / G tokens
@@ -120,95 +122,25 @@ __device__ __forceinline__ uint32_t tile_off(int r, int ch)
                       (((ch & 7) ^ (r & 7)) << 4));
 }
 
-// What a share does of an item.
-struct Piece {
-    int b, h;
-    int tok;               // first token, as a row of q
-    int rows;
-    int first, last;       // positions of the first token and of the last key in sight
-    int sight;             // first key in sight of any row
-    int base;              // cached rows before the new tokens (L - n)
-    int len;               // L
-    int t0, t1;            // key tiles
-    int kind;              // 0: the whole item; 1: not from its start; 2: from its start, not to its end;
-                           // -1: no more pieces
-};
-
 // Rows that a sequence may have: positions of a tile's keys stay below 2^31.
 constexpr int MAX_LEN = 1 << 30;
 
 // What a wait for the end of a piece may take for each of its tiles, beside WAIT_LIMIT_NS.
 constexpr uint64_t TILE_LIMIT_NS = 1 << 17;
 
-// The share's walk over its items' pieces.
-struct Walk {
-    Place at, end;
-    Seq q;
-    int q0;
-
-    // Sequence b's lengths; false if it has no work.
-    __device__ __forceinline__ static bool lengths(const ChunkParams &p, int b, Seq &q, int &q0,
-                                                   bool &bad)
-    {
-        q0 = p.q_start[b];
-        const int64_t n = (int64_t)p.q_start[b + 1] - q0;
-        const int L = p.seq_lens[b];
-        bad = n < 0 || (n > 0 && (q0 < 0 || n > p.max_q_len || q0 + n > p.num_tokens || L < n ||
-                                  (int64_t)L > (int64_t)p.max_blocks * p.block_size || L > MAX_LEN ||
-                                  (p.rules.tree && n > 64)));
-        q.n = bad ? 0 : (int)n;
-        q.L = L;
-        return q.n > 0;
-    }
-
-    __device__ __forceinline__ void start(const ChunkParams &p, const Place *places)
-    {
-        at = places[0];
-        end = places[1];
-        bool bad;
-        if (at.b < p.batch)
-            lengths(p, at.b, q, q0, bad);
-    }
-
-    __device__ __forceinline__ bool next(const ChunkParams &p, Piece &c)
-    {
-        const bool last_item = at.b == end.b && at.h == end.h && at.rt == end.rt;
-        if (at.b >= p.batch || (last_item && at.tile >= end.tile))
-            return false;
-        int lo, hi;
-        chunk::tiles(p.rules, q, at.rt, lo, hi);
-        chunk::span(p.rules, q, at.rt, c.first, c.last);
-        c.b = at.b;
-        c.h = at.h;
-        c.tok = q0 + (at.rt << p.rules.lg_tpr);
-        c.rows = min(1 << p.rules.lg_tpr, q.n - (at.rt << p.rules.lg_tpr)) << p.lg_g;
-        c.sight = p.rules.window > 0 ? max(0, c.first - p.rules.window + 1) : 0;
-        c.base = q.L - q.n;
-        c.len = q.L;
-        c.t0 = at.tile;
-        c.t1 = last_item ? end.tile : hi;
-        c.kind = c.t0 > lo ? 1 : c.t1 < hi ? 2 : 0;
-        if (last_item) {
-            at.tile = end.tile;
-            return true;
-        }
-        if (++at.rt == chunk::row_tiles(p.rules, q)) {
-            at.rt = 0;
-            if (++at.h == p.num_kv_heads) {
-                at.h = 0;
-                bool bad;
-                do
-                    ++at.b;
-                while (at.b < p.batch && !lengths(p, at.b, q, q0, bad));
-                if (at.b >= p.batch)
-                    return true;
-            }
-        }
-        chunk::tiles(p.rules, q, at.rt, lo, hi);
-        at.tile = lo;
-        return true;
-    }
-};
+// Sequence b's lengths; false if it has no work.
+__device__ __forceinline__ bool lengths(const ChunkParams &p, int b, Seq &q, int &q0, bool &bad)
+{
+    q0 = p.q_start[b];
+    const int64_t n = (int64_t)p.q_start[b + 1] - q0;
+    const int L = p.seq_lens[b];
+    bad = n < 0 || (n > 0 && (q0 < 0 || n > p.max_q_len || q0 + n > p.num_tokens || L < n ||
+                              (int64_t)L > (int64_t)p.max_blocks * p.block_size || L > MAX_LEN ||
+                              (p.rules.tree && n > 64)));
+    q.n = bad ? 0 : (int)n;
+    q.L = L;
+    return q.n > 0;
+}
 
 // What a group does of a piece: its rows, and its s-th key tile.
 __device__ __forceinline__ bool shared_rows(const Piece &c) { return c.rows <= TILE_M; }
@@ -251,7 +183,7 @@ __device__ __forceinline__ bool find_share(const ChunkParams &p, Place *places, 
             Seq q;
             int q0;
             bool bad;
-            if (Walk::lengths(p, b, q, q0, bad)) {
+            if (lengths(p, b, q, q0, bad)) {
                 const int64_t one = chunk::cost_of(p.rules, q), cost = p.num_kv_heads * one;
                 if (k >= 0 && x < sum + cost) {
                     places[k] = chunk::place_in(p.rules, q, b, x - sum, one);
@@ -323,18 +255,10 @@ __device__ __forceinline__ void note_item(const ChunkParams &p, const Place &a, 
     int pieces = 0;
     if (a.split) {
         Seq q;
-        int q0, lo, hi;
+        int q0;
         bool bad;
-        Walk::lengths(p, a.b, q, q0, bad);
-        chunk::tiles(p.rules, q, a.rt, lo, hi);
-        auto start = [&](int k) { return chunk::share_start(U, n, k, gridDim.x, p.share_step); };
-        // positions on the line: where the item may first be cut, and its end
-        const int64_t first = start(c) - (a.tile - lo), end = first + (hi - lo);
-        if (start(c - 1) <= first) {
-            pieces = 2;
-            while (c + pieces - 1 < n && start(c + pieces - 1) < end)
-                ++pieces;
-        }
+        lengths(p, a.b, q, q0, bad);
+        pieces = chunk::pieces_to_join(p.rules, q, a, U, n, c, gridDim.x, p.share_step);
         item = make_int4(q0 + (a.rt << p.rules.lg_tpr),
                          min(1 << p.rules.lg_tpr, q.n - (a.rt << p.rules.lg_tpr)) << p.lg_g, a.h, 0);
     }
@@ -1068,8 +992,12 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     } else if (warp == C::W_FEED) {
         // ================= hand out the share's pieces, one ahead of the one whose q is
         // brought (once the last S before has read its own)
+        auto seq = [&](int b, Seq &q, int &q0) {
+            bool bad;
+            return lengths(p, b, q, q0, bad);
+        };
         Walk walk;
-        walk.start(p, places);
+        walk.start(p.batch, places, seq);
         __syncwarp();                              // (places lie where the pieces go)
         // A wait for the end of a piece: as long as its tiles take (1 to 4 us each), so its limit
         // grows with the tiles handed out.  Should another role hang, that role's own limit
@@ -1096,10 +1024,10 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
             }
             return true;
         };
-        bool more = walk.next(p, c), ok = hand_out(0, more);
+        bool more = walk.next(p.rules, p.batch, p.num_kv_heads, p.lg_g, c, seq), ok = hand_out(0, more);
         for (uint32_t item = 0; ok && more; ++item) {
             const int halves = shared_rows(c) ? 1 : 2, y = c.h << p.lg_g, z = c.tok;
-            more = walk.next(p, c);
+            more = walk.next(p.rules, p.batch, p.num_kv_heads, p.lg_g, c, seq);
             if (!(ok = hand_out(item + 1, more)))
                 break;
             if (item > 0 && !(ok = wait_piece(q_empty, item - 1)))

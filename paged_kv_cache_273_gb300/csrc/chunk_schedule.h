@@ -161,5 +161,95 @@ PKV_HD int64_t share_start(int64_t U, int n, int c, int ctas, uint32_t step)
 #endif
 }
 
+// What a share does of an item.
+struct Piece {
+    int b, h;
+    int tok;               // first token, as a row of q
+    int rows;
+    int first, last;       // positions of the first token and of the last key in sight
+    int sight;             // first key in sight of any row
+    int base;              // cached rows before the new tokens (L - n)
+    int len;               // L
+    int t0, t1;            // key tiles
+    int kind;              // 0: the whole item; 1: not from its start; 2: from its start, not to its end;
+                           // -1: no more pieces
+};
+
+// A share's walk over its items' pieces.  `lengths(b, q, q0)`: sequence b's, and its first token
+// as a row of q; false if it has no work.
+struct Walk {
+    Place at, end;
+    Seq q;
+    int q0;
+
+    template <typename F>
+    PKV_HD void start(int batch, const Place *places, F lengths)
+    {
+        at = places[0];
+        end = places[1];
+        if (at.b < batch)
+            lengths(at.b, q, q0);
+    }
+
+    template <typename F>
+    PKV_HD bool next(const Rules &r, int batch, int num_kv_heads, int lg_g, Piece &c, F lengths)
+    {
+        const bool last_item = at.b == end.b && at.h == end.h && at.rt == end.rt;
+        if (at.b >= batch || (last_item && at.tile >= end.tile))
+            return false;
+        const int tok = at.rt << r.lg_tpr, tpr = 1 << r.lg_tpr;
+        int lo, hi;
+        tiles(r, q, at.rt, lo, hi);
+        span(r, q, at.rt, c.first, c.last);
+        c.b = at.b;
+        c.h = at.h;
+        c.tok = q0 + tok;
+        c.rows = (q.n - tok < tpr ? q.n - tok : tpr) << lg_g;
+        c.sight = r.window > 0 && c.first - r.window + 1 > 0 ? c.first - r.window + 1 : 0;
+        c.base = q.L - q.n;
+        c.len = q.L;
+        c.t0 = at.tile;
+        c.t1 = last_item ? end.tile : hi;
+        c.kind = c.t0 > lo ? 1 : c.t1 < hi ? 2 : 0;
+        if (last_item) {
+            at.tile = end.tile;
+            return true;
+        }
+        if (++at.rt == row_tiles(r, q)) {
+            at.rt = 0;
+            if (++at.h == num_kv_heads) {
+                at.h = 0;
+                do
+                    ++at.b;
+                while (at.b < batch && !lengths(at.b, q, q0));
+                if (at.b >= batch)
+                    return true;
+            }
+        }
+        tiles(r, q, at.rt, lo, hi);
+        at.tile = lo;
+        return true;
+    }
+};
+
+// Share c starts within an item, at place `a` (a.split): how many pieces the item has if c is the
+// first share to start within it, else 0.  Its first piece is then share c - 1's last, the others
+// the first ones of shares c, c + 1, ..  (A share leaves at most two states: that of its
+// first piece, kind 1, and that of its last, kind 2.)
+PKV_HD int pieces_to_join(const Rules &r, const Seq &q, const Place &a, int64_t U, int n, int c,
+                          int ctas, uint32_t step)
+{
+    int lo, hi;
+    tiles(r, q, a.rt, lo, hi);
+    // positions on the line: where the item may first be cut, and its end
+    const int64_t first = share_start(U, n, c, ctas, step) - (a.tile - lo), end = first + (hi - lo);
+    if (share_start(U, n, c - 1, ctas, step) > first)
+        return 0;
+    int pieces = 2;
+    while (c + pieces - 1 < n && share_start(U, n, c + pieces - 1, ctas, step) < end)
+        ++pieces;
+    return pieces;
+}
+
 }  // namespace chunk
 }  // namespace pkv
