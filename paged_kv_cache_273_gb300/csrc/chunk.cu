@@ -22,8 +22,9 @@
 // about 290 rows of 16-bit keys, half that of e4m3); long pieces are bound by the tensor cores
 // and by the softmax between a group's two products.  Measured on a GB300 (a call in a
 // captured chain, both kernels): 8 drafted tokens each of 16 sequences' 271 MB of rows 56 us
-// (4.8 TB/s); whole prompts of 550 GFLOP 435 us (1.26 PFLOP/s, the tensor cores 55% busy); pieces over
-// e4m3 of 756 GFLOP 880 us (0.86 PFLOP/s, 45%); 32 tokens of 64 heads over 131000 e4m3 rows 140 us.
+// (4.8 TB/s); whole prompts of 550 GFLOP 435 to 453 us on several GPUs (1.21 to 1.26 PFLOP/s, the tensor
+// cores 55% busy); pieces over e4m3 of 756 GFLOP 880 us (0.86 PFLOP/s, 45%); 32 tokens of 64 heads over
+// 131000 e4m3 rows 140 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -109,7 +110,11 @@ struct Cfg {
     // a block's whole rows (two of 64 columns each cost the warp that issues them
     // twice as long, more than a tile's time on the tensor cores)
     static constexpr int GROUP8 = 1024 * (D / 64);
-    // P in the caches' 16-bit type; over an 8-bit cache, whose codes become fp16, in fp16
+    // P in the caches' 16-bit type; over an 8-bit cache, whose codes become fp16, in fp16.  One
+    // rounding of a weight, no second part for the rest: it moves an output by about what the
+    // output's own rounding to q's type does (bf16 2.1e-3 of its size rather than 1.6e-3, fp16
+    // 2.7e-4 rather than 2.1e-4), and P V of two parts would add half as many MMAs again
+    // (prefill.cu, whose fp32 output shows the rest, takes 717 us for these prompts).
     static constexpr bool PBF = BF && !F8;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
@@ -960,7 +965,7 @@ __global__ void __launch_bounds__((Cfg<D, F8, BF, NQ>::NT), 1)
     } else if (F8 && warp == C::W_SCALES) {
         // ================= a tile's scales, lane l those of its rows 8 l .. 8 l + 7: loaded
         // before the tile's slot is free.  (By the warps that convert, between their own
-        // loads, it took 901 us rather than 879, and one token of 131072 rows 145 rather than 140.)
+        // loads, pieces took 901 us rather than 879, and 32 tokens over 131000 rows 145 rather than 140.)
         const int H = p.num_kv_heads;
         uint32_t gt = 0;
         bool ok = true;

@@ -4,7 +4,9 @@
 // rows, tpr = rows / G tokens of all G query heads of the KV head.  It covers the key
 // tiles (of 128) from the first that its first token sees to the last that its last
 // one does.  Items are numbered by sequence, KV head, row tile; an item costs its tiles
-// and ITEM_COST more for its q, its first tile's latency and its output.  The costs end
+// and ITEM_COST more for its q, its first tile's latency and its output.  (A tile counts the
+// same whatever rows the item has: shares of batches of long pieces and single tokens are
+// equal in tiles, not in time.)  The costs end
 // to end are a line that is cut into equal shares; a cut within an item falls between two of its
 // tiles.  Where a position of the line falls is worked out in closed form, so a CTA
 // finds its share without looking at other CTAs' items.  Host and device.
@@ -22,6 +24,8 @@ namespace pkv {
 namespace chunk {
 
 constexpr int TILE = 128, LG_TILE = 7;   // keys of a tile
+// Measured with 0, 1, 2 and 4: 768 items of up to 16 tiles 91, 73, 66, 66 us; whole prompts 474,
+// 449, 443, 452; drafts, one long sequence, pieces and windows the same within 2%.
 constexpr int ITEM_COST = 2;
 
 struct Rules {
@@ -136,7 +140,9 @@ PKV_HD Place place_in(const Rules &r, const Seq &q, int b, int64_t x, int64_t c)
 
 // Shares for a line of length U on `ctas` CTAs: equal ones, but none shorter than MIN_SHARE
 // (a share of a tile or two costs more in its start and in the joining of its state
-// than it saves).
+// than it saves).  Measured with 2, 4, 8 and 16: 8 tokens of 8 KV heads over 500 rows 13.2, 14.4, 17.9,
+// 24.2 us, over 2000 rows 16.8, 16.3, 18.8, 24.9, over 8000 rows 27.5, 24.4, 22.0, 32.0; calls
+// whose shares are longer anyway are the same.
 constexpr int MIN_SHARE = 4;
 PKV_HD int shares(int64_t U, int ctas)
 {
