@@ -894,10 +894,10 @@ int paged_chunk_attention(const pkv_pool *pool, const void *q, pkv_dtype q_dtype
 
 /*
  * pkv_selftest_wait_timeout — a check of the failure path of the library's
- * bounded device waits (not part of the method).  Launches one kernel whose
- * single waiting thread waits, the way every mbarrier wait in this library
- * does, on a phase that nothing completes; after the wait's time limit
- * (about one second) it records a timeout in the pool's error word and
+ * bounded device waits (not part of the method).  Launches one kernel of which
+ * two threads wait, in the two forms of this library's mbarrier waits, on
+ * phases that nothing completes; when both have given up, after the waits' time
+ * limit (about one second), it records a timeout in the pool's error word and
  * returns.  The next pkv_check_error() then returns PKV_ERR_TIMEOUT and the
  * device stays usable.  Returns PKV_OK when the kernel was launched,
  * PKV_ERR_INVALID for a null pool, PKV_ERR_CUDA without a device.
