@@ -83,7 +83,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity)
 }
 
 // Wait until the phase with the given parity has completed.  Gives up (and
-// returns false) after WAIT_LIMIT_NS, or at once when *abort is set by any
+// returns false) after `limit` ns, or at once when *abort is set by any
 // thread of the CTA; the caller then records the timeout and winds down.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity,
                                                   volatile int *abort,
